@@ -1,0 +1,99 @@
+// The integer logic of the paged attention kernels on the host: which part of
+// which unit each CTA takes, and where a position lies in the cache.
+#include <cstring>
+
+#include "paged.cuh"
+
+using namespace mha;
+
+namespace {
+PagedProblem problem(const int32_t *starts, const int32_t *lens, const int32_t *table, int B, int T,
+                     int H, int Hkv, int hpu, int tb, int causal, int pages, int page_shift,
+                     int max_pages, int layout) {
+  PagedProblem p;
+  std::memset(&p, 0, sizeof p);
+  p.batch = PagedBatch{starts, lens, table, B, T, pages, 1 << page_shift, page_shift, max_pages,
+                       layout};
+  p.H = H;
+  p.Hkv = Hkv;
+  p.group = H / Hkv;
+  p.hpu = hpu;
+  p.hblocks = (p.group + hpu - 1) / hpu;
+  p.tb = tb;
+  p.causal = causal;
+  p.rows = hpu * tb;
+  return p;
+}
+}  // namespace
+
+// What paged_span finds, by a plain search.
+static PagedSpan span_of(const PagedProblem &p, int cta, int grid) {
+  long long total = 0, units = 0;
+  for (int b = 0; b < p.batch.B; ++b) {
+    const PagedSeq s = paged_seq(p.batch, b);
+    units += paged_units(p, s);
+    total += static_cast<long long>(paged_units(p, s)) * paged_unit_cost(p, s);
+  }
+  PagedSpan sp = paged_stretch(total, units, cta, grid);
+  sp.b = p.batch.B;
+  sp.u = 0;
+  sp.s = total;
+  long long s = 0;
+  for (int b = 0; b < p.batch.B && sp.lo < total; ++b) {
+    const PagedSeq q = paged_seq(p.batch, b);
+    const long long cost = paged_unit_cost(p, q), whole = cost * paged_units(p, q);
+    if (sp.lo < s + whole) {
+      sp.b = b;
+      sp.s = s;
+      sp.u = static_cast<int>((sp.lo - s) / cost);
+      break;
+    }
+    s += whole;
+  }
+  return sp;
+}
+
+// Rows of (cta, b, i0, i1, h0, heads, kv, nt, t0, t1, slot or -1); returns their number.
+extern "C" int parts(const int32_t *starts, const int32_t *lens, int B, int T, int H, int Hkv,
+                     int hpu, int tb, int causal, int page_shift, int max_pages, int grid,
+                     int32_t *out, int most) {
+  const PagedProblem p =
+      problem(starts, lens, nullptr, B, T, H, Hkv, hpu, tb, causal, 0, page_shift, max_pages, 0);
+  int n = 0;
+  for (int c = 0; c < grid; ++c) {
+    PagedWalk w;
+    w.begin(p, span_of(p, c, grid));
+    PagedPart part;
+    while (w.next(p, part)) {
+      if (n == most) return -1;
+      const int32_t row[11] = {c,       part.b,  part.i0, part.i1,
+                               part.h0, part.heads, part.kv, part.nt,
+                               part.t0, part.t1, paged_split(part) ? paged_slot(part) : -1};
+      std::memcpy(out + 11 * n++, row, sizeof row);
+    }
+  }
+  return n;
+}
+
+extern "C" long long cell(const int32_t *table, int pages, int page_shift, int max_pages,
+                          int layout, int b, int pos, int head, int heads) {
+  const PagedProblem p =
+      problem(nullptr, nullptr, table, 0, 0, 1, 1, 1, 1, 1, pages, page_shift, max_pages, layout);
+  return paged_cell(p.batch, b, pos, head, heads);
+}
+
+extern "C" void seq(const int32_t *starts, const int32_t *lens, int T, int page_shift,
+                    int max_pages, int b, int32_t *out) {
+  const PagedProblem p =
+      problem(starts, lens, nullptr, 1, T, 1, 1, 1, 1, 1, 0, page_shift, max_pages, 0);
+  const PagedSeq s = paged_seq(p.batch, b);
+  out[0] = s.q0;
+  out[1] = s.n;
+  out[2] = s.len;
+  out[3] = s.base;
+}
+
+extern "C" int seq_of_row(const int32_t *starts, int B, int T, int t) {
+  const PagedProblem p = problem(starts, nullptr, nullptr, B, T, 1, 1, 1, 1, 1, 0, 4, 0, 0);
+  return paged_seq_of_row(p.batch, t);
+}

@@ -8,6 +8,10 @@ kernel.  Masks: causal, key padding, query padding (see include/mha.h).
 attention) and the [B, L, H, d] layout; ``mha_sublayer_fwd`` runs the whole
 multi-head sublayer (projections with biases on ``mha_linear_fwd``'s tensor-core
 kernel, attention, output projection).
+
+For generation from a paged key/value cache and for the layers around it:
+``mha_qk_norm_rope_fwd`` / ``_bwd`` (per-head norm and position rotation),
+``mha_paged_append`` and ``mha_paged_fwd`` (see include/mha_paged.h).
 """
 from .mha import (MHA_DTYPE_BF16, MHA_DTYPE_F32, MHA_ERR_CUDA, MHA_ERR_INVALID_ARGUMENT,
                   MHA_ERR_TIMEOUT, MHA_ERR_UNSUPPORTED, MHA_MASK_CAUSAL, MHA_MASK_KEY_PADDING,
@@ -17,6 +21,10 @@ from .mha import (MHA_DTYPE_BF16, MHA_DTYPE_F32, MHA_ERR_CUDA, MHA_ERR_INVALID_A
                   mha_linear_fwd,
                   mha_sublayer_fwd, mha_sublayer_fwd_static, mha_sublayer_workspace_size,
                   mha_bwd, mha_bwd_workspace_size, mha_status_string, mha_version)
+from .paged import (MHA_ROPE_HALVES, MHA_ROPE_INTERLEAVED, PAGED_PATH_NAMES, mha_paged_append,
+                    mha_paged_fwd, mha_paged_path, mha_paged_workspace_size,
+                    mha_qk_norm_rope_bwd, mha_qk_norm_rope_bwd_workspace_size,
+                    mha_qk_norm_rope_fwd, rope_inv_freq)
 
 __all__ = ["mha_fwd", "mha_fwd_ex", "mha_fwd_lse", "mha_linear_fwd", "mha_sublayer_fwd", "mha_bwd",
            "mha_bwd_workspace_size",
@@ -27,4 +35,7 @@ __all__ = ["mha_fwd", "mha_fwd_ex", "mha_fwd_lse", "mha_linear_fwd", "mha_sublay
            "MHA_ERR_UNSUPPORTED", "MHA_ERR_CUDA", "MHA_ERR_TIMEOUT", "MHA_DTYPE_F32",
            "MHA_DTYPE_BF16", "MHA_MASK_NONE", "MHA_MASK_CAUSAL", "MHA_MASK_KEY_PADDING",
            "MHA_MASK_QUERY_PADDING", "MHA_MASK_CAUSAL_TAIL", "MHA_LAYOUT_BHSD",
-           "MHA_LAYOUT_BSHD"]
+           "MHA_LAYOUT_BSHD", "MHA_ROPE_HALVES", "MHA_ROPE_INTERLEAVED", "PAGED_PATH_NAMES",
+           "mha_qk_norm_rope_fwd", "mha_qk_norm_rope_bwd", "mha_qk_norm_rope_bwd_workspace_size",
+           "mha_paged_append", "mha_paged_fwd", "mha_paged_path", "mha_paged_workspace_size",
+           "rope_inv_freq"]

@@ -17,7 +17,8 @@ LIB = os.path.join(BUILD, "libmha.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["mha_api.cu", "attn_f32_simt.cu", "attn_short_tc.cu", "attn_long_tc.cu", "attn_decode_tc.cu",
-           "attn_bwd_simt.cu", "attn_bwd_tc.cu", "linear_tc.cu"]
+           "attn_bwd_simt.cu", "attn_bwd_tc.cu", "linear_tc.cu", "paged_api.cu", "qk_rope.cu",
+           "paged_simt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", CSRC, "-I", INCLUDE]
@@ -32,7 +33,7 @@ def nvcc() -> str:
 
 def _deps_mtime() -> float:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "mha.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 

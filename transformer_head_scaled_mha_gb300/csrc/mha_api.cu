@@ -12,6 +12,7 @@
 
 #include "../../include/mha.h"
 #include "common.cuh"
+#include "host.cuh"
 
 namespace mha {
 namespace {
@@ -44,6 +45,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sms[kMaxDevices];
 
+}  // namespace
+
 int sm_count(int dev) {
   if (dev < 0 || dev >= kMaxDevices) return 0;
   int v = g_sms[dev].load(std::memory_order_relaxed);
@@ -52,6 +55,8 @@ int sm_count(int dev) {
   g_sms[dev].store(v, std::memory_order_relaxed);
   return v;
 }
+
+namespace {
 
 // ---- per-context caches ----------------------------------------------------
 // Device addresses of the module's symbols, and whether a kernel's attributes
@@ -131,9 +136,11 @@ void *symbol_ptr(const void *symbol) {
   return v;
 }
 
+}  // namespace
+
 int *status_ptr() { return static_cast<int *>(symbol_ptr(reinterpret_cast<const void *>(&g_status))); }
 
-}  // namespace
+uint64_t wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
 
 cudaError_t set_smem_once(const void *kernel, int bytes) {
   const unsigned long long ctx = current_ctx_id();
@@ -152,6 +159,8 @@ int next_pow2(int x) {
   while (r < x) r <<= 1;
   return r;
 }
+
+}  // namespace
 
 // 4-D view (d, L, heads, B) of a contiguous bf16 tensor in either layout,
 // 128-byte swizzle; box (64, box_rows, box_heads, 1)
@@ -174,6 +183,8 @@ bool make_map(CUtensorMap *map, const void *base, int d, int L, int heads, int B
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 // 2-D view (cols, rows) of a row-major bf16 matrix, 128-byte swizzle
 bool make_map_2d(CUtensorMap *map, const void *base, int cols, int rows, int box_cols,
@@ -209,11 +220,15 @@ bool make_map_slabs(CUtensorMap *map, const void *base, int cols, int rows, int 
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
   if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
 }
+
+namespace {
 
 // Validates and picks a path; returns a non-negative Path or -(mha_status).
 int select_path(int B, int H, int H_kv, int Lq, int Lk, int dk, int dv, int mask, int dtype) {

@@ -1,0 +1,348 @@
+// Definitions shared by the operators of include/mha_paged.h: the ragged batch
+// and the paged cache as the kernels see them, and the split of attention work
+// over CTAs.
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+// The logic that turns lengths and tables into work is plain integer code and
+// also compiles for the host, where its tests run.
+#define MHA_HD __host__ __device__ __forceinline__
+
+namespace mha {
+
+// ---- norm and rotation of head rows (qk_rope.cu) ---------------------------
+constexpr int kRopeHalves = 0;
+constexpr int kRopeInterleaved = 1;
+
+// The ragged batch and its cache (include/mha_paged.h, "Ragged batches").
+struct PagedBatch {
+  const int32_t *q_starts, *kv_lengths, *block_table;
+  int B, T;
+  int num_pages, page_size, page_shift, max_pages;  // page_size = 1 << page_shift
+  int layout;                                       // of the cache
+};
+
+struct RopeArgs {
+  const void *q, *k, *v;  // v only when appending
+  void *q_out, *k_out, *v_out;  // appending: k_out, v_out are the caches
+  const void *q_weight, *k_weight;  // nullptr: that tensor is not normed
+  const float *inv_freq;
+  const int32_t *positions;  // [B, L] or nullptr (not appending)
+  int B, H, Hkv, L;          // not appending: token t = (t / L, t % L)
+  int tokens;                // B * L, or the batch's T
+  int rotary, layout, style;
+  float eps;
+  PagedBatch batch;  // appending
+  // backward: q, k the forward's inputs, dq_out, dk_out the incoming gradients
+  const void *dq_out, *dk_out;
+  float *partial;  // [CTAs, 2, d] sums of the weights' gradients
+  float *dq_weight, *dk_weight;
+};
+
+// CTAs of the backward kernel at most (rows of RopeArgs::partial)
+constexpr int kRopeBwdMaxCtas = 1216;
+
+cudaError_t launch_rope_fwd(const RopeArgs &a, int d, int dtype, bool append, int num_sms,
+                            cudaStream_t stream);
+cudaError_t launch_rope_bwd(const RopeArgs &a, int d, int dtype, int num_sms, cudaStream_t stream);
+
+// ---- attention over the cache ----------------------------------------------
+constexpr int kPagedTile = 128;     // keys per tile: the unit that work is split by
+constexpr int kPagedMaxCtas = 608;  // CTAs that may hold partial sums
+
+// A unit of attention work: `tb` consecutive new tokens of one sequence times
+// `hpu` query heads of one key/value head's group.  Row r of a unit is head
+// r / tb of its heads, token r % tb of its tokens.
+struct PagedProblem {
+  PagedBatch batch;
+  int H, Hkv, group;  // group = H / Hkv
+  int hpu, hblocks;   // query heads per unit; units that cover a group's heads
+  int tb;             // tokens per unit
+  int causal;
+  float scale_log2;  // scale * log2(e)
+  const void *q, *k, *v;
+  void *out;
+  // Sums of units whose keys several CTAs share: slot s of CTA c holds `rows`
+  // rows of d fp32 (unnormalised output) and, behind them all, (max, sum) pairs
+  float *part;
+  int32_t *meta;  // [CTAs][kPagedMeta]
+  int rows;       // rows of a slot
+  int *status;
+  uint64_t wait_ns;
+};
+
+// meta words of a CTA: which parts of split units it holds.  Slot 0 holds a part
+// that continues a unit begun by the CTA before, slot 1 the first part of a
+// unit that the CTAs behind it continue.
+constexpr int kPagedMeta = 8;
+constexpr int kMetaFlags = 0;  // kPart* bits
+constexpr int kMetaSeq = 1, kMetaTok = 2, kMetaHead = 3;  // unit of slot 0: sequence, first token
+                                                          // in it, first query head
+constexpr int kPartContinues = 1;  // slot 0 is used
+constexpr int kPartEnds = 2;       // ... and holds the unit's last keys
+constexpr int kPartBegins = 4;     // slot 1 is used
+
+// Sequence b of a batch: its first row, new tokens, cached length (what the
+// block table can hold of it) and the position of its first new token.
+struct PagedSeq {
+  int q0, n, len, base;
+};
+
+MHA_HD PagedSeq paged_seq(const PagedBatch &p, int b) {
+  PagedSeq s;
+  const int a = p.q_starts[b], e = p.q_starts[b + 1], l = p.kv_lengths[b];
+  s.q0 = min(max(a, 0), p.T);
+  s.n = min(max(e, s.q0), p.T) - s.q0;
+  const int full = max(l, 0);
+  const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
+  s.len = static_cast<int>(min(static_cast<long long>(full), cap));
+  s.base = full - s.n;
+  return s;
+}
+
+// Keys that tokens [i0, i1) of a sequence may read, at most.
+MHA_HD int paged_kv_end(const PagedSeq &s, int i1, int causal) {
+  if (!causal) return s.len;
+  return max(min(s.base + i1, s.len), 0);
+}
+
+// Sequence of row t: the last one that starts at or before it; -1 when the row
+// belongs to none.
+MHA_HD int paged_seq_of_row(const PagedBatch &p, int t) {
+  int lo = 0, hi = p.B;  // q_starts[lo] <= t < q_starts[hi], if the arrays are in order
+  if (p.B <= 0 || t < p.q_starts[0] || t >= p.q_starts[p.B]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.q_starts[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---- the split of the units' keys over CTAs --------------------------------
+// Units are laid on a line, each taking kUnitCost + 2 * tiles (half tiles: a
+// unit's own work -- queries, sums, output -- costs about 1.5 tiles), sequence
+// by sequence; within a sequence by head, then token block.  CTA c of G takes
+// the stretch [c X / G, (c + 1) X / G) of the line, X its length; a unit's keys
+// are cut where a stretch ends inside it, unless that leaves a part of under
+// kMinPart tiles.  G is at most the grid, and no larger than leaves every CTA
+// kMinStretch or, if that is more, one unit each.
+constexpr int kUnitCost = 3;
+constexpr int kMinPart = 2;
+constexpr int kMinStretch = 2 * 4;
+
+// tiles of a unit before offset x (> 0) of its stretch on the line
+MHA_HD int paged_cut(long long x, int nt) {
+  if (x <= 0) return 0;
+  const long long t = (x - kUnitCost + 1) >> 1;
+  if (t < kMinPart) return 0;
+  if (t > nt - kMinPart) return nt;
+  return static_cast<int>(t);
+}
+
+// A CTA's place on the line: its first unit and where its stretch begins and ends.
+struct PagedSpan {
+  long long lo, hi;  // the stretch
+  long long s;       // where sequence b's first unit begins
+  int b;             // sequence of the first unit
+  int u;             // its number within the sequence
+  int ctas;          // G
+};
+
+// The stretch of CTA `cta` of `grid` on a line of length `total` with `units` units.
+MHA_HD PagedSpan paged_stretch(long long total, long long units, int cta, int grid) {
+  PagedSpan sp;
+  const long long by_work = total / kMinStretch;
+  const long long most = by_work > units ? by_work : units;
+  sp.ctas = static_cast<int>(most < 1 ? 1 : (most < grid ? most : grid));
+  // total * cta / ctas without the product of the two
+  const long long each = total / sp.ctas, over = total % sp.ctas;
+  sp.lo = cta < sp.ctas ? each * cta + over * cta / sp.ctas : total;
+  sp.hi = cta < sp.ctas ? each * (cta + 1) + over * (cta + 1) / sp.ctas : total;
+  sp.s = total;
+  sp.b = sp.u = 0;
+  return sp;
+}
+
+MHA_HD int paged_units(const PagedProblem &p, const PagedSeq &s) {
+  return p.Hkv * p.hblocks * ((s.n + p.tb - 1) / p.tb);
+}
+// length on the line of each unit of a sequence (the last token block's)
+MHA_HD int paged_unit_cost(const PagedProblem &p, const PagedSeq &s) {
+  return kUnitCost + 2 * ((paged_kv_end(s, s.n, p.causal) + kPagedTile - 1) / kPagedTile);
+}
+
+// The span of CTA `cta` of `grid`; all threads of the block call it (kThreads of
+// them), `scratch` holds 40 long longs in shared memory, every thread gets the
+// answer.  Ends with a __syncthreads.
+template <int kThreads>
+__device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long long *scratch) {
+  constexpr int kWarps = (kThreads + 31) / 32;
+  static_assert(kWarps <= 16, "scratch size");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.batch.B + kThreads - 1) / kThreads;
+  const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch.B), b1 = min(b0 + per, p.batch.B);
+  long long mine = 0, units = 0;
+  for (int b = b0; b < b1; ++b) {
+    const PagedSeq s = paged_seq(p.batch, b);
+    const long long nu = paged_units(p, s);
+    units += nu;
+    mine += nu * paged_unit_cost(p, s);
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+  }
+  if (lane == 31) {
+    scratch[warp] = inc;
+    scratch[16 + warp] = units;
+  }
+  __syncthreads();
+  long long before = 0, total = 0, all_units = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+    all_units += scratch[16 + w];
+  }
+  PagedSpan sp = paged_stretch(total, all_units, cta, grid);
+  const long long first = before + inc - mine;
+  if (sp.lo < total && sp.lo >= first && sp.lo < first + mine) {  // one thread of the block
+    long long s = first;
+    int b = b0;
+    long long cost = 1;
+    for (;; ++b) {
+      const PagedSeq q = paged_seq(p.batch, b);
+      cost = paged_unit_cost(p, q);
+      const long long whole = cost * paged_units(p, q);
+      if (sp.lo < s + whole) break;
+      s += whole;
+    }
+    scratch[32] = s;
+    scratch[33] = b;
+    scratch[34] = (sp.lo - s) / cost;
+  }
+  if (threadIdx.x == 0 && sp.lo >= total) {
+    scratch[32] = total;
+    scratch[33] = p.batch.B;
+    scratch[34] = 0;
+  }
+  __syncthreads();
+  sp.s = scratch[32];
+  sp.b = static_cast<int>(scratch[33]);
+  sp.u = static_cast<int>(scratch[34]);
+  return sp;
+}
+
+// One CTA's share of a unit: tiles [t0, t1) of its nt.
+struct PagedPart {
+  PagedSeq seq;
+  int b;        // sequence
+  int kv;       // key/value head
+  int h0;       // first query head
+  int heads;    // query heads (the last block of a group may have fewer)
+  int i0, i1;   // tokens of the sequence
+  int kv_end;   // keys that any of its rows may read
+  int nt, t0, t1;
+};
+
+// Walks the parts of a CTA's span in order.  Every thread may keep its own.
+struct PagedWalk {
+  PagedSpan sp;
+  PagedSeq seq;
+  int b, u, units, cost;
+  long long s;  // where sequence b's first unit begins
+
+  MHA_HD void load(const PagedProblem &p) {
+    if (b >= p.batch.B) return;
+    seq = paged_seq(p.batch, b);
+    units = paged_units(p, seq);
+    cost = paged_unit_cost(p, seq);
+  }
+  MHA_HD void begin(const PagedProblem &p, const PagedSpan &span) {
+    sp = span;
+    b = sp.b;
+    u = sp.u;
+    s = sp.s;
+    units = 0;
+    cost = 0;
+    load(p);
+  }
+  // The next part; false when the span is done.
+  MHA_HD bool next(const PagedProblem &p, PagedPart &part) {
+    for (;;) {
+      while (b < p.batch.B && u >= units) {
+        s += static_cast<long long>(units) * cost;
+        ++b;
+        u = 0;
+        load(p);
+      }
+      if (b >= p.batch.B) return false;
+      const long long at = s + static_cast<long long>(u) * cost;
+      if (at >= sp.hi) return false;
+      const int blocks = (seq.n + p.tb - 1) / p.tb;
+      const int hb = u / blocks, blk = u - hb * blocks;
+      ++u;
+      part.seq = seq;
+      part.b = b;
+      part.kv = hb / p.hblocks;
+      const int hin = (hb - part.kv * p.hblocks) * p.hpu;
+      part.h0 = part.kv * p.group + hin;
+      part.heads = min(p.hpu, p.group - hin);
+      part.i0 = blk * p.tb;
+      part.i1 = min(part.i0 + p.tb, seq.n);
+      part.kv_end = paged_kv_end(seq, part.i1, p.causal);
+      part.nt = (part.kv_end + kPagedTile - 1) / kPagedTile;
+      part.t0 = paged_cut(sp.lo - at, part.nt);
+      part.t1 = sp.hi < at + cost ? paged_cut(sp.hi - at, part.nt) : part.nt;
+      if (part.nt == 0) {  // nothing to attend to: zeros, by the CTA that holds its beginning
+        if (at >= sp.lo) return true;
+        continue;
+      }
+      if (part.t1 > part.t0) return true;
+    }
+  }
+};
+
+MHA_HD bool paged_split(const PagedPart &part) {
+  return part.t0 > 0 || part.t1 < part.nt;
+}
+// slot of a split part
+MHA_HD int paged_slot(const PagedPart &part) { return part.t0 > 0 ? 0 : 1; }
+
+// one slot: rows x d sums, then rows x (max, sum)
+MHA_HD size_t paged_slot_floats(int rows, int d) {
+  return static_cast<size_t>(rows) * (d + 2);
+}
+MHA_HD float *paged_slot_ptr(const PagedProblem &p, int d, int cta, int slot) {
+  return p.part + (static_cast<size_t>(cta) * 2 + slot) * paged_slot_floats(p.rows, d);
+}
+
+// Number of the cell [page, head, offset] of position pos in the cache, in rows
+// of d; -1 when the position lies in no page.
+MHA_HD long long paged_cell(const PagedBatch &p, int b, int pos, int head,
+                                                int heads) {
+  if (pos < 0) return -1;
+  const int pi = pos >> p.page_shift;
+  if (pi >= p.max_pages) return -1;
+  const int id = p.block_table[static_cast<size_t>(b) * p.max_pages + pi];
+  if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) return -1;
+  const int off = pos & (p.page_size - 1);
+  return p.layout == kLayoutBHSD
+             ? ((static_cast<long long>(id) * heads + head) << p.page_shift) + off
+             : ((static_cast<long long>(id) << p.page_shift) + off) * heads + head;
+}
+
+cudaError_t launch_paged_simt(const PagedProblem &p, int d, int dtype, int grid,
+                              cudaStream_t stream);
+// joins the parts of split units
+cudaError_t launch_paged_merge(const PagedProblem &p, int d, int dtype, int grid,
+                               cudaStream_t stream);
+
+}  // namespace mha
