@@ -3,6 +3,7 @@
 // over CTAs.
 #pragma once
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -339,6 +340,11 @@ MHA_HD long long paged_cell(const PagedBatch &p, int b, int pos, int head,
              : ((static_cast<long long>(id) << p.page_shift) + off) * heads + head;
 }
 
+// bf16, at most 16 rows per unit: maps over q (d, T, H, 1) with box (64, tb, hpu, 1)
+// and over the caches (d, page_size, H_kv, num_pages) with box
+// (64, min(page_size, 128), 1, 1)
+cudaError_t launch_paged_few(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                             const PagedProblem &p, int d, int grid, cudaStream_t stream);
 cudaError_t launch_paged_simt(const PagedProblem &p, int d, int dtype, int grid,
                               cudaStream_t stream);
 // joins the parts of split units

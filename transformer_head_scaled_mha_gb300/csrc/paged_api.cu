@@ -125,7 +125,8 @@ int paged_path(int B, int T, int H, int H_kv, int d, int max_q, int dtype) {
   if (static_cast<long long>(T) * H > 0x7fffffffLL || static_cast<long long>(B) * H > 0x7fffffffLL)
     return -MHA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0 || H == 0) return kNone;
-  return kSimt;
+  if (dtype == MHA_DTYPE_F32) return kSimt;
+  return static_cast<long long>(H / H_kv) * max_q <= 16 ? kFew : kSimt;
 }
 
 Units units_of(int path, int group, int max_q) {
@@ -408,8 +409,24 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   p.status = dev.status;
   p.wait_ns = wait_limit_ns();
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const int grid = std::min(u.ctas, 3 * dev.sms);
-  cudaError_t err = launch_paged_simt(p, d, dtype, grid, stream);
+  int grid = std::min(u.ctas, 3 * dev.sms);
+  cudaError_t err = cudaSuccess;
+  if (path == kSimt) {
+    err = launch_paged_simt(p, d, dtype, grid, stream);
+  } else {
+    grid = std::min(u.ctas, dev.sms);
+    CUtensorMap qm, km, vm;
+    const int box = std::min(page_size, kPagedTile);
+    // a cache without pages is never read: any valid map will do
+    const bool none = num_pages == 0;
+    const void *kb = none ? q : k_cache, *vb = none ? q : v_cache;
+    const int pages = none ? 1 : num_pages;
+    if (!make_map(&qm, q, d, T, H, 1, kLayoutBSHD, u.tb, u.hpu) ||
+        !make_map(&km, kb, d, page_size, H_kv, pages, layout, box, 1) ||
+        !make_map(&vm, vb, d, page_size, H_kv, pages, layout, box, 1))
+      return MHA_ERR_CUDA;
+    err = launch_paged_few(qm, km, vm, p, d, grid, stream);
+  }
   if (err == cudaSuccess) err = launch_paged_merge(p, d, dtype, grid, stream);
   return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
