@@ -28,28 +28,28 @@ PagedProblem problem(const int32_t *starts, const int32_t *lens, const int32_t *
 
 // What paged_span finds, by a plain search.
 static PagedSpan span_of(const PagedProblem &p, int cta, int grid) {
-  long long total = 0, units = 0;
+  long long one = 0, units = 0;
   for (int b = 0; b < p.batch.B; ++b) {
     const PagedSeq s = paged_seq(p.batch, b);
-    units += paged_units(p, s);
-    total += static_cast<long long>(paged_units(p, s)) * paged_unit_cost(p, s);
+    units += paged_blocks(p, s);
+    one += static_cast<long long>(paged_blocks(p, s)) * paged_unit_cost(p, s);
   }
-  PagedSpan sp = paged_stretch(total, units, cta, grid);
-  sp.b = p.batch.B;
-  sp.u = 0;
-  sp.s = total;
+  const int hbs = p.Hkv * p.hblocks;
+  PagedSpan sp = paged_stretch(one * hbs, units * hbs, cta, grid);
   long long s = 0;
-  for (int b = 0; b < p.batch.B && sp.lo < total; ++b) {
-    const PagedSeq q = paged_seq(p.batch, b);
-    const long long cost = paged_unit_cost(p, q), whole = cost * paged_units(p, q);
-    if (sp.lo < s + whole) {
-      sp.b = b;
-      sp.s = s;
-      sp.u = static_cast<int>((sp.lo - s) / cost);
-      break;
+  for (int hb = 0; hb < hbs; ++hb)
+    for (int b = 0; b < p.batch.B; ++b) {
+      const PagedSeq q = paged_seq(p.batch, b);
+      const long long cost = paged_unit_cost(p, q), whole = cost * paged_blocks(p, q);
+      if (sp.lo >= s && sp.lo < s + whole) {
+        sp.hb = hb;
+        sp.b = b;
+        sp.s = s;
+        sp.u = static_cast<int>((sp.lo - s) / cost);
+        return sp;
+      }
+      s += whole;
     }
-    s += whole;
-  }
   return sp;
 }
 

@@ -125,12 +125,17 @@ MHA_HD int paged_seq_of_row(const PagedBatch &p, int t) {
 
 // ---- the split of the units' keys over CTAs --------------------------------
 // Units are laid on a line, each taking kUnitCost + 2 * tiles (half tiles: a
-// unit's own work -- queries, sums, output -- costs about 1.5 tiles), sequence
-// by sequence; within a sequence by head, then token block.  CTA c of G takes
-// the stretch [c X / G, (c + 1) X / G) of the line, X its length; a unit's keys
-// are cut where a stretch ends inside it, unless that leaves a part of under
+// unit's own work -- queries, sums, output -- costs about 1.5 tiles): head block
+// by head block, for each all sequences, for each its token blocks.  CTA c of G
+// takes the stretch [c X / G, (c + 1) X / G) of the line, X its length; a unit's
+// keys are cut where a stretch ends inside it, unless that leaves a part of under
 // kMinPart tiles.  G is at most the grid, and no larger than leaves every CTA
 // kMinStretch or, if that is more, one unit each.
+//
+// Heads come first because every head's piece of the line is alike: with G a
+// multiple of the head blocks, the CTAs of different heads read the same positions
+// at about the same time, and in the [page, position, head, d] layout those lie
+// side by side in memory.
 constexpr int kUnitCost = 3;
 constexpr int kMinPart = 2;
 constexpr int kMinStretch = 2 * 4;
@@ -144,12 +149,13 @@ MHA_HD int paged_cut(long long x, int nt) {
   return static_cast<int>(t);
 }
 
-// A CTA's place on the line: its first unit and where its stretch begins and ends.
+// A CTA's place on the line: where its stretch begins and ends, and its first unit.
 struct PagedSpan {
   long long lo, hi;  // the stretch
-  long long s;       // where sequence b's first unit begins
-  int b;             // sequence of the first unit
-  int u;             // its number within the sequence
+  long long s;       // where the first unit's sequence begins (this head block's units of it)
+  int hb;            // head block of the first unit
+  int b;             // its sequence
+  int u;             // its token block
   int ctas;          // G
 };
 
@@ -164,13 +170,12 @@ MHA_HD PagedSpan paged_stretch(long long total, long long units, int cta, int gr
   sp.lo = cta < sp.ctas ? each * cta + over * cta / sp.ctas : total;
   sp.hi = cta < sp.ctas ? each * (cta + 1) + over * (cta + 1) / sp.ctas : total;
   sp.s = total;
-  sp.b = sp.u = 0;
+  sp.hb = sp.b = sp.u = 0;
   return sp;
 }
 
-MHA_HD int paged_units(const PagedProblem &p, const PagedSeq &s) {
-  return p.Hkv * p.hblocks * ((s.n + p.tb - 1) / p.tb);
-}
+// token blocks of a sequence: its units of one head block
+MHA_HD int paged_blocks(const PagedProblem &p, const PagedSeq &s) { return (s.n + p.tb - 1) / p.tb; }
 // length on the line of each unit of a sequence (the last token block's)
 MHA_HD int paged_unit_cost(const PagedProblem &p, const PagedSeq &s) {
   return kUnitCost + 2 * ((paged_kv_end(s, s.n, p.causal) + kPagedTile - 1) / kPagedTile);
@@ -186,10 +191,10 @@ __device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long l
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.batch.B + kThreads - 1) / kThreads;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch.B), b1 = min(b0 + per, p.batch.B);
-  long long mine = 0, units = 0;
+  long long mine = 0, units = 0;  // of one head block
   for (int b = b0; b < b1; ++b) {
     const PagedSeq s = paged_seq(p.batch, b);
-    const long long nu = paged_units(p, s);
+    const long long nu = paged_blocks(p, s);
     units += nu;
     mine += nu * paged_unit_cost(p, s);
   }
@@ -205,39 +210,40 @@ __device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long l
     scratch[16 + warp] = units;
   }
   __syncthreads();
-  long long before = 0, total = 0, all_units = 0;
+  long long before = 0, one = 0, all_units = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += scratch[w];
-    total += scratch[w];
+    one += scratch[w];
     all_units += scratch[16 + w];
   }
-  PagedSpan sp = paged_stretch(total, all_units, cta, grid);
-  const long long first = before + inc - mine;
-  if (sp.lo < total && sp.lo >= first && sp.lo < first + mine) {  // one thread of the block
+  const int hbs = p.Hkv * p.hblocks;
+  PagedSpan sp = paged_stretch(one * hbs, all_units * hbs, cta, grid);
+  const bool any = sp.lo < one * hbs;
+  const int hb = any ? static_cast<int>(sp.lo / one) : hbs;
+  const long long at = any ? sp.lo - hb * one : 0, first = before + inc - mine;
+  if (any && at >= first && at < first + mine) {  // one thread of the block
     long long s = first;
     int b = b0;
     long long cost = 1;
     for (;; ++b) {
       const PagedSeq q = paged_seq(p.batch, b);
       cost = paged_unit_cost(p, q);
-      const long long whole = cost * paged_units(p, q);
-      if (sp.lo < s + whole) break;
+      const long long whole = cost * paged_blocks(p, q);
+      if (at < s + whole) break;
       s += whole;
     }
     scratch[32] = s;
     scratch[33] = b;
-    scratch[34] = (sp.lo - s) / cost;
-  }
-  if (threadIdx.x == 0 && sp.lo >= total) {
-    scratch[32] = total;
-    scratch[33] = p.batch.B;
-    scratch[34] = 0;
+    scratch[34] = (at - s) / cost;
   }
   __syncthreads();
-  sp.s = scratch[32];
-  sp.b = static_cast<int>(scratch[33]);
-  sp.u = static_cast<int>(scratch[34]);
+  sp.hb = hb;
+  if (any) {
+    sp.s = hb * one + scratch[32];
+    sp.b = static_cast<int>(scratch[33]);
+    sp.u = static_cast<int>(scratch[34]);
+  }
   return sp;
 }
 
@@ -253,51 +259,52 @@ struct PagedPart {
   int nt, t0, t1;
 };
 
-// Walks the parts of a CTA's span in order.  Every thread may keep its own.
+// Walks the parts of a CTA's span in order.
 struct PagedWalk {
   PagedSpan sp;
-  PagedSeq seq;
-  int b, u, units, cost;
-  long long s;  // where sequence b's first unit begins
+  PagedSeq seq, ahead;  // sequence b, and the one behind it (read early)
+  int hb, b, u, blocks, cost;
+  long long s;  // where this head block's units of sequence b begin
 
-  MHA_HD void load(const PagedProblem &p) {
-    if (b >= p.batch.B) return;
-    seq = paged_seq(p.batch, b);
-    units = paged_units(p, seq);
+  MHA_HD void take(const PagedProblem &p, const PagedSeq &q) {
+    seq = q;
+    blocks = paged_blocks(p, seq);
     cost = paged_unit_cost(p, seq);
+    ahead = paged_seq(p.batch, b + 1 < p.batch.B ? b + 1 : 0);
   }
   MHA_HD void begin(const PagedProblem &p, const PagedSpan &span) {
     sp = span;
+    hb = sp.hb;
     b = sp.b;
     u = sp.u;
     s = sp.s;
-    units = 0;
-    cost = 0;
-    load(p);
+    if (sp.lo < sp.hi) take(p, paged_seq(p.batch, b));
   }
   // The next part; false when the span is done.
   MHA_HD bool next(const PagedProblem &p, PagedPart &part) {
     for (;;) {
-      while (b < p.batch.B && u >= units) {
-        s += static_cast<long long>(units) * cost;
-        ++b;
+      if (s >= sp.hi) return false;
+      while (u >= blocks) {
+        s += static_cast<long long>(blocks) * cost;
+        if (s >= sp.hi) return false;
         u = 0;
-        load(p);
+        if (++b == p.batch.B) {
+          b = 0;
+          if (++hb >= p.Hkv * p.hblocks) return false;  // lengths changed meanwhile
+        }
+        take(p, ahead);
       }
-      if (b >= p.batch.B) return false;
       const long long at = s + static_cast<long long>(u) * cost;
       if (at >= sp.hi) return false;
-      const int blocks = (seq.n + p.tb - 1) / p.tb;
-      const int hb = u / blocks, blk = u - hb * blocks;
-      ++u;
       part.seq = seq;
       part.b = b;
       part.kv = hb / p.hblocks;
       const int hin = (hb - part.kv * p.hblocks) * p.hpu;
       part.h0 = part.kv * p.group + hin;
-      part.heads = min(p.hpu, p.group - hin);
-      part.i0 = blk * p.tb;
-      part.i1 = min(part.i0 + p.tb, seq.n);
+      part.heads = p.group - hin < p.hpu ? p.group - hin : p.hpu;
+      part.i0 = u * p.tb;
+      part.i1 = seq.n - part.i0 < p.tb ? seq.n : part.i0 + p.tb;
+      ++u;
       part.kv_end = paged_kv_end(seq, part.i1, p.causal);
       part.nt = (part.kv_end + kPagedTile - 1) / kPagedTile;
       part.t0 = paged_cut(sp.lo - at, part.nt);
@@ -342,9 +349,10 @@ MHA_HD long long paged_cell(const PagedBatch &p, int b, int pos, int head,
 
 // bf16, at most 16 rows per unit: maps over q (d, T, H, 1) with box (64, tb, hpu, 1)
 // and over the caches (d, page_size, H_kv, num_pages) with box
-// (64, min(page_size, 128), 1, 1)
+// (64, min(page_size, 128), 1, 1); lowers `grid` to the CTAs it launches
 cudaError_t launch_paged_few(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                             const PagedProblem &p, int d, int grid, cudaStream_t stream);
+                             const PagedProblem &p, int d, int &grid, int num_sms,
+                             cudaStream_t stream);
 cudaError_t launch_paged_simt(const PagedProblem &p, int d, int dtype, int grid,
                               cudaStream_t stream);
 // joins the parts of split units

@@ -414,7 +414,7 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   if (path == kSimt) {
     err = launch_paged_simt(p, d, dtype, grid, stream);
   } else {
-    grid = std::min(u.ctas, dev.sms);
+    grid = u.ctas;
     CUtensorMap qm, km, vm;
     const int box = std::min(page_size, kPagedTile);
     // a cache without pages is never read: any valid map will do
@@ -425,7 +425,7 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
         !make_map(&km, kb, d, page_size, H_kv, pages, layout, box, 1) ||
         !make_map(&vm, vb, d, page_size, H_kv, pages, layout, box, 1))
       return MHA_ERR_CUDA;
-    err = launch_paged_few(qm, km, vm, p, d, grid, stream);
+    err = launch_paged_few(qm, km, vm, p, d, grid, dev.sms, stream);
   }
   if (err == cudaSuccess) err = launch_paged_merge(p, d, dtype, grid, stream);
   return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;

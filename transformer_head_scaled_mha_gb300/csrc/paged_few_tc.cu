@@ -3,8 +3,7 @@
 //
 // A part of work (paged.cuh) is R <= 16 query rows of one key/value head -- its
 // group's query heads times a few tokens -- against some 128-key tiles.  Each key
-// and value is read once, so the kernel is bound by HBM.  Persistent CTAs, one
-// per SM, take equal stretches of all sequences' tiles, cutting a sequence's keys
+// and value is read once, so the kernel is bound by HBM.  Persistent CTAs take equal stretches of all sequences' tiles, cutting a sequence's keys
 // where a stretch ends; paged_merge_kernel joins the cut ones.
 //
 // Scores are computed transposed, keys on the 128 TMEM lanes, so that a thread
@@ -16,7 +15,8 @@
 //                        maximum moves only when it grows by more than 2^8
 //                        (numerator and denominator share it), and O is rescaled
 //                        in TMEM when it does; partial row sums per thread
-//   P -> smem (bf16)     rounded to nearest: weights in [0, 2^8], 2^-8 relative
+//   P -> smem (bf16)     up to 8 rows as a sum of two bf16; 9 to 16 rows rounded to
+//                        one (2^-8 relative)
 //   O^T += V_j^T P^T     A = the V tile read MN-major.  d = 64: both 64-key halves
 //                        of the tile in one product, M rows 0..63 the first
 //                        half's values and 64..127 the second's, N = 32 the first
@@ -37,6 +37,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "common.cuh"
@@ -56,17 +57,27 @@ constexpr int kMaxSlots = 6;
 constexpr int kDescs = 4;  // part descriptions in flight
 constexpr uint32_t kBarSoftmax = 1;
 
-template <int D>
+// d = 64 up to 8 rows: half the ring and two CTAs per SM, whose waits (for a
+// part's first tile, its output) fall into each other's work.
+template <int D, int RP>
 struct Cfg {
+  static constexpr int kCtas = D == 64 && RP <= 8 ? 2 : 1;  // per SM
   static constexpr int kSlabs = D / 64;
   static constexpr int kBlkBytes = 128 * 128;           // [128 rows x 64] swizzle block
   static constexpr int kTileBytes = kSlabs * kBlkBytes;  // a K or V tile
   static constexpr int kSlotBytes = 2 * kTileBytes;      // ring slot: K tile, V tile
-  static constexpr int kSlots = D == 128 ? 3 : 6;
-  static constexpr int kQBlk = kN * 128;                 // [16 rows x 64] of Q or P
+  static constexpr int kSlots = D == 128 || kCtas == 2 ? 3 : 6;
+  static constexpr int kQBlk = kN * 128;  // [16 rows x 64] of Q
   static constexpr int kQBytes = kSlabs * kQBlk;
-  static constexpr int kPBytes = 2 * kQBlk;              // 16 rows x 128 keys
-  static constexpr int kPvN = D == 64 ? 32 : 16;
+  // Up to 8 rows the weights go in as two bf16, the rounded weight and what the
+  // rounding left (2^-17 relative together), in rows of the product that would
+  // otherwise be padding: row r and row r + kLo.
+  static constexpr bool kTwo = RP <= 8;
+  static constexpr int kLo = D == 64 && RP <= 4 ? 4 : 8;
+  static constexpr int kPRows = D == 64 && RP <= 4 ? 8 : 16;  // rows of P per 64-key half
+  static constexpr int kPHalf = kPRows * 128;
+  static constexpr int kPBytes = 2 * kPHalf;
+  static constexpr int kPvN = D == 64 ? 2 * kPRows : 16;
   static constexpr int kPvSteps = D == 64 ? 4 : 8;
   // A's second M block: d = 64, the tile's keys 64..127 (64 rows down);
   // d = 128, value dims 64..127 (the next swizzle block)
@@ -87,10 +98,11 @@ struct Desc {
   int slot;         // of its sums; -1: the part is a whole unit
 };
 
+template <int RP>
 struct __align__(16) Shared {
-  float red[2][4][kN];  // per-warp tile maxima, double-buffered by tile
-  float lsum[4][kN];    // per-warp row sums
-  float xo[kN][64];     // d = 64: the second key half's partial output
+  float red[2][4][RP];  // per-warp tile maxima, double-buffered by tile
+  float lsum[4][RP];    // per-warp row sums
+  float xo[RP][64];     // d = 64: the second key half's partial output
   long long scratch[40];
   Desc desc[kDescs];
   uint32_t present[kMaxSlots];  // pages of the slot's tile that were loaded
@@ -105,11 +117,11 @@ struct __align__(16) Shared {
   int abort_flag;
 };
 
-template <int D>
+template <int D, int RP>
 constexpr size_t smem_bytes() {
-  using C = Cfg<D>;
+  using C = Cfg<D, RP>;
   return 1024 + static_cast<size_t>(C::kSlots) * C::kSlotBytes + 2 * C::kQBytes + 2 * C::kPBytes +
-         sizeof(Shared);
+         sizeof(Shared<RP>);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -130,7 +142,8 @@ struct FewMaps {
 
 // Waits for description n and copies it (a whole warp of a reading role); false
 // when there are no more parts, or when the wait was given up (then !ok).
-__device__ __forceinline__ bool take_desc(Shared *sh, int n, Desc &d, uint64_t limit, bool &ok) {
+template <int RP>
+__device__ __forceinline__ bool take_desc(Shared<RP> *sh, int n, Desc &d, uint64_t limit, bool &ok) {
   volatile int *abort_flag = &sh->abort_flag;
   ok = mbar_wait_warp(&sh->desc_full[n % kDescs], (n / kDescs) & 1, abort_flag, limit);
   if (!ok) return false;
@@ -141,16 +154,16 @@ __device__ __forceinline__ bool take_desc(Shared *sh, int n, Desc &d, uint64_t l
 }
 
 template <int D, int RP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
     paged_few_tc_kernel(const __grid_constant__ FewMaps maps, const PagedProblem p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, RP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *ring = smem;                              // kSlots (K tile, V tile)
   uint8_t *qbuf = ring + C::kSlots * C::kSlotBytes;  // 2 Q buffers
   uint8_t *pbuf = qbuf + 2 * C::kQBytes;             // 2 P buffers
-  Shared *sh = reinterpret_cast<Shared *>(pbuf + 2 * C::kPBytes);
+  Shared<RP> *sh = reinterpret_cast<Shared<RP> *>(pbuf + 2 * C::kPBytes);
   volatile int *abort_flag = &sh->abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -359,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t db0 = smem_desc_sw128(smem_addr(pbuf + (t & 1) * C::kPBytes), 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < C::kPvSteps; ++kk) {
-            // d = 64: P rows 0..31 (both halves) per step; d = 128: 16 rows,
-            // the second 64 keys kQBlk further
-            const uint32_t pb = D == 64 ? kk * 32 : (kk >> 2) * C::kQBlk + (kk & 3) * 32;
+            // d = 64: the P rows of both halves per step; d = 128: 16 rows, the
+            // second 64 keys kPHalf further
+            const uint32_t pb = D == 64 ? kk * 32 : (kk >> 2) * C::kPHalf + (kk & 3) * 32;
             tc_mma_ss(d_tmem, da0 + ((kk * 16 * 128) >> 4), db0 + (pb >> 4), idesc_o,
                       (j > 0 || kk > 0) ? 1u : 0u);
           }
@@ -385,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     // O^T lanes: d = 128, value dim k; d = 64, value dim k % 64 of the first
     // (warps 0-1) or second (warps 2-3) key half's partial output
-    const int o_col = D == 64 && warp >= 2 ? kN : 0;
+    const int o_col = D == 64 && warp >= 2 ? C::kPRows : 0;
     const int vdim = D == 64 ? (k & 63) : k;
     const bool stores = D == 128 || warp < 2;  // threads that write output
     const int box_shift = min(p.batch.page_shift, 7);
@@ -478,13 +491,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool okr = mbar_wait_warp(&sh->pv_done[u & 1], (u >> 1) & 1, abort_flag, p.wait_ns);
           if (okr) {
             tc_fence_after();
-            uint32_t o[RP];
             const uint32_t ta = tmem + lane_base + 2 * kN + (oi & 1) * C::kOCols + o_col;
-            tmem_ld_cols(ta, o);
-            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < RP; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[c]);
-            tmem_st_cols(ta, o);
+            for (int two = 0; two < (C::kTwo ? 2 : 1); ++two) {
+              uint32_t o[RP];
+              tmem_ld_cols(ta + two * C::kLo, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < RP; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[c]);
+              tmem_st_cols(ta + two * C::kLo, o);
+            }
             tmem_wait_st();
           }
           ok = okr;
@@ -492,15 +508,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P buffer t % 2 held P_{t-2}: its product must be done reading it
         if (t >= 2 && ok)
           ok = mbar_wait_warp(&sh->pv_done[t & 1], ((t - 2) >> 1) & 1, abort_flag, p.wait_ns);
-        // row r of P_t: keys of this tile, bf16, 128B-swizzled rows; the
-        // second 64 keys in the second 2 KB (rows 16..31 of the d = 64 product)
-        const uint32_t pb = smem_addr(pbuf + (t & 1) * C::kPBytes) + (k >> 6) * C::kQBlk;
+        // row r of P_t: keys of this tile, bf16, 128B-swizzled rows; the second
+        // 64 keys kPHalf further (the second half of the d = 64 product's rows)
+        const uint32_t pb = smem_addr(pbuf + (t & 1) * C::kPBytes) + (k >> 6) * C::kPHalf;
         const uint32_t kc = static_cast<uint32_t>(k & 63);
+        auto p_at = [&](int r) { return pb + r * 128 + (((kc >> 3) ^ (r & 7)) << 4) + (kc & 7) * 2; };
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
           const float pr = ex2_approx(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
           l[r] += pr;
-          st_shared_u16(pb + r * 128 + (((kc >> 3) ^ (r & 7)) << 4) + (kc & 7) * 2, bf16_bits(pr));
+          const uint16_t hi = bf16_bits(pr);
+          st_shared_u16(p_at(r), hi);
+          if (C::kTwo)
+            st_shared_u16(p_at(r + C::kLo),
+                          bf16_bits(pr - __uint_as_float(static_cast<uint32_t>(hi) << 16)));
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -523,8 +544,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t o[RP];
       if (oke) {
         tc_fence_after();
-        tmem_ld_cols(tmem + lane_base + 2 * kN + (oi & 1) * C::kOCols + o_col, o);
-        tmem_wait_ld();
+        const uint32_t ta = tmem + lane_base + 2 * kN + (oi & 1) * C::kOCols + o_col;
+        tmem_ld_cols(ta, o);
+        if (C::kTwo) {
+          uint32_t lo[RP];
+          tmem_ld_cols(ta + C::kLo, lo);
+          tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < RP; ++r)
+            o[r] = __float_as_uint(__uint_as_float(o[r]) + __uint_as_float(lo[r]));
+        } else {
+          tmem_wait_ld();
+        }
         if (D == 64 && warp >= 2) {
 #pragma unroll
           for (int r = 0; r < RP; ++r) sh->xo[r][vdim] = __uint_as_float(o[r]);
@@ -582,10 +613,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, int RP>
-cudaError_t launch_impl(const FewMaps &maps, const PagedProblem &p, int grid, cudaStream_t stream) {
-  static_assert(smem_bytes<D>() <= 232448, "shared memory budget");
-  static_assert(Cfg<D>::kSlots <= kMaxSlots, "ring size");
-  constexpr size_t kSmem = smem_bytes<D>();
+cudaError_t launch_impl(const FewMaps &maps, const PagedProblem &p, int &grid, int num_sms,
+                        cudaStream_t stream) {
+  using C = Cfg<D, RP>;
+  constexpr size_t kSmem = smem_bytes<D, RP>();
+  // 1 KB per CTA is the system's
+  static_assert(C::kCtas * (kSmem + 1024) <= 233472, "shared memory budget");
+  static_assert(C::kSlots <= kMaxSlots, "ring size");
+  grid = std::min(grid, C::kCtas * num_sms);
   const cudaError_t e = set_smem_once(
       reinterpret_cast<const void *>(paged_few_tc_kernel<D, RP>), static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
@@ -603,22 +638,25 @@ cudaError_t launch_impl(const FewMaps &maps, const PagedProblem &p, int grid, cu
 }
 
 template <int D>
-cudaError_t launch_rows(const FewMaps &maps, const PagedProblem &p, int grid, cudaStream_t stream) {
+cudaError_t launch_rows(const FewMaps &maps, const PagedProblem &p, int &grid, int num_sms,
+                        cudaStream_t stream) {
   const int R = p.hpu * p.tb;
-  if (R <= 1) return launch_impl<D, 1>(maps, p, grid, stream);
-  if (R <= 2) return launch_impl<D, 2>(maps, p, grid, stream);
-  if (R <= 4) return launch_impl<D, 4>(maps, p, grid, stream);
-  if (R <= 8) return launch_impl<D, 8>(maps, p, grid, stream);
-  return launch_impl<D, 16>(maps, p, grid, stream);
+  if (R <= 1) return launch_impl<D, 1>(maps, p, grid, num_sms, stream);
+  if (R <= 2) return launch_impl<D, 2>(maps, p, grid, num_sms, stream);
+  if (R <= 4) return launch_impl<D, 4>(maps, p, grid, num_sms, stream);
+  if (R <= 8) return launch_impl<D, 8>(maps, p, grid, num_sms, stream);
+  return launch_impl<D, 16>(maps, p, grid, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_few(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                             const PagedProblem &p, int d, int grid, cudaStream_t stream) {
+                             const PagedProblem &p, int d, int &grid, int num_sms,
+                             cudaStream_t stream) {
   if (p.hpu * p.tb > kN) return cudaErrorInvalidValue;
   const FewMaps maps{q, k, v};
-  return d == 128 ? launch_rows<128>(maps, p, grid, stream) : launch_rows<64>(maps, p, grid, stream);
+  return d == 128 ? launch_rows<128>(maps, p, grid, num_sms, stream)
+                  : launch_rows<64>(maps, p, grid, num_sms, stream);
 }
 
 }  // namespace mha
