@@ -22,6 +22,7 @@ PagedProblem problem(const int32_t *starts, const int32_t *lens, const int32_t *
   p.tb = tb;
   p.causal = causal;
   p.rows = hpu * tb;
+  p.min_stretch = 4;
   return p;
 }
 }  // namespace
@@ -31,24 +32,27 @@ static PagedSpan span_of(const PagedProblem &p, int cta, int grid) {
   long long one = 0, units = 0;
   for (int b = 0; b < p.batch.B; ++b) {
     const PagedSeq s = paged_seq(p.batch, b);
-    units += paged_blocks(p, s);
-    one += static_cast<long long>(paged_blocks(p, s)) * paged_unit_cost(p, s);
+    for (int u = 0; u < paged_blocks(p, s); ++u, ++units)
+      one += paged_unit_cost(p, s, paged_blocks(p, s), u);
   }
   const int hbs = p.Hkv * p.hblocks;
-  PagedSpan sp = paged_stretch(one * hbs, units * hbs, cta, grid);
+  PagedSpan sp = paged_stretch(one * hbs, units * hbs, cta, grid, p.min_stretch);
   long long s = 0;
   for (int hb = 0; hb < hbs; ++hb)
     for (int b = 0; b < p.batch.B; ++b) {
       const PagedSeq q = paged_seq(p.batch, b);
-      const long long cost = paged_unit_cost(p, q), whole = cost * paged_blocks(p, q);
-      if (sp.lo >= s && sp.lo < s + whole) {
-        sp.hb = hb;
-        sp.b = b;
-        sp.s = s;
-        sp.u = static_cast<int>((sp.lo - s) / cost);
-        return sp;
+      const int blocks = paged_blocks(p, q);
+      sp.s = s;
+      for (int u = 0; u < blocks; ++u) {
+        const long long cost = paged_unit_cost(p, q, blocks, u);
+        if (sp.lo >= s && sp.lo < s + cost) {
+          sp.hb = hb;
+          sp.b = b;
+          sp.u = u;
+          return sp;
+        }
+        s += cost;
       }
-      s += whole;
     }
   return sp;
 }
@@ -96,4 +100,24 @@ extern "C" void seq(const int32_t *starts, const int32_t *lens, int T, int page_
 extern "C" int seq_of_row(const int32_t *starts, int B, int T, int t) {
   const PagedProblem p = problem(starts, nullptr, nullptr, B, T, 1, 1, 1, 1, 1, 0, 4, 0, 0);
   return paged_seq_of_row(p.batch, t);
+}
+
+// Units of a sequence: their lengths' prefix sums by the closed form, and the unit
+// at each boundary; returns 0 when they agree with sums and a plain search.
+extern "C" int unit_sums(const int32_t *starts, const int32_t *lens, int T, int tb, int causal,
+                         int page_shift, int max_pages) {
+  const PagedProblem p =
+      problem(starts, lens, nullptr, 1, T, 1, 1, 1, tb, causal, 0, page_shift, max_pages, 0);
+  const PagedSeq s = paged_seq(p.batch, 0);
+  const int blocks = paged_blocks(p, s);
+  long long sum = 0;
+  for (int u = 0; u < blocks; ++u) {
+    const long long cost = paged_unit_cost(p, s, blocks, u);
+    if (paged_cost_before(p, s, blocks, u) != sum) return 1 + u;
+    if (cost < kUnitCost) return -1;
+    if (paged_unit_at(p, s, blocks, sum) != u || paged_unit_at(p, s, blocks, sum + cost - 1) != u)
+      return -2 - u;
+    sum += cost;
+  }
+  return paged_cost_before(p, s, blocks, blocks) == sum ? 0 : -100;
 }

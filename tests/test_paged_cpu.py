@@ -171,7 +171,8 @@ def test_paged_fwd_rejects_before_launch(mha):
 def test_paged_path_and_workspace_sizes(mha):
     path, size = mha.mha_paged_path, mha.mha_paged_workspace_size
     assert path(0, 4, 8, 8, 64, 1, 16, 1) == 0
-    assert path(4, 4, 8, 8, 64, 1, 16, 0) == 1
+    assert path(4, 4, 8, 8, 64, 1, 16, 0) == 1 and path(4, 4, 32, 4, 64, 2, 16, 1) == 2
+    assert path(4, 9, 32, 4, 64, 3, 16, 1) == 3 and path(4, 9, 32, 4, 64, 3, 16, 0) == 1
     assert path(4, 4, 8, 3, 64, 1, 16, 1) == -1
     assert path(4, 4, 8, 8, 64, 0, 16, 1) == -1
     assert path(4, 4, 8, 8, 64, 1, 24, 1) == -1
@@ -405,6 +406,26 @@ def test_empty_units_are_taken_once(host):
     check_split(host, [0, 3, 3, 9], [0, 0, 2], 4, 2, 2, 8, 0, 4, 0, 5)
     rows = all_parts(host, [0, 0, 0], [5, 7], 4, 2, 2, 8, 1, 4, 4, 5)
     assert len(rows) == 0
+
+
+def test_unit_lengths_have_their_closed_form(host):
+    rng = np.random.default_rng(5)
+    for _ in range(3000):
+        n = int(rng.choice([0, 1, 7, 130, 3000]))
+        ln = int(rng.integers(0, int(rng.choice([2, 400, 5000])) + 1))
+        max_pages = int(rng.choice([0, 3, 400]))
+        (a, ap), (l, lp) = i32([0, n]), i32([ln])
+        for causal in (0, 1):
+            assert host.unit_sums(ap, lp, n, int(rng.integers(1, 300)), causal, 4, max_pages) == 0
+
+
+@pytest.mark.parametrize("causal", [0, 1])
+def test_chunks_are_split_evenly(host, causal):
+    # units of 256 rows: a long prompt from its beginning, and chunks behind caches
+    load = check_split(host, [0, 8192], [8192], 16, 16, 1, 256, causal, 7, 64, 152)
+    assert load.max() <= 1.25 * load.sum() / 152
+    load = check_split(host, [0, 512, 600, 601], [4096, 3000, 2500], 32, 8, 4, 64, causal, 6, 64, 152)
+    assert load.max() <= 1.4 * load.sum() / 152
 
 
 def test_lengths_out_of_range_are_clamped(host):

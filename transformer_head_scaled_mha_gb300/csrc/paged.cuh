@@ -52,7 +52,8 @@ cudaError_t launch_rope_bwd(const RopeArgs &a, int d, int dtype, int num_sms, cu
 
 // ---- attention over the cache ----------------------------------------------
 constexpr int kPagedTile = 128;     // keys per tile: the unit that work is split by
-constexpr int kPagedMaxCtas = 608;  // CTAs that may hold partial sums
+constexpr int kPagedMaxCtas = 608;      // CTAs that may hold partial sums, at most 16 rows per unit
+constexpr int kPagedManyMaxCtas = 192;  // ... 256 rows per unit
 
 // A unit of attention work: `tb` consecutive new tokens of one sequence times
 // `hpu` query heads of one key/value head's group.  Row r of a unit is head
@@ -63,6 +64,7 @@ struct PagedProblem {
   int hpu, hblocks;   // query heads per unit; units that cover a group's heads
   int tb;             // tokens per unit
   int causal;
+  int min_stretch;   // tiles of work below which a CTA is not worth having
   float scale_log2;  // scale * log2(e)
   const void *q, *k, *v;
   void *out;
@@ -124,26 +126,27 @@ MHA_HD int paged_seq_of_row(const PagedBatch &p, int t) {
 }
 
 // ---- the split of the units' keys over CTAs --------------------------------
-// Units are laid on a line, each taking kUnitCost + 2 * tiles (half tiles: a
-// unit's own work -- queries, sums, output -- costs about 1.5 tiles): head block
-// by head block, for each all sequences, for each its token blocks.  CTA c of G
-// takes the stretch [c X / G, (c + 1) X / G) of the line, X its length; a unit's
-// keys are cut where a stretch ends inside it, unless that leaves a part of under
-// kMinPart tiles.  G is at most the grid, and no larger than leaves every CTA
-// kMinStretch or, if that is more, one unit each.
+// Units are laid on a line, each as long as its work (in 1/256 of a key tile):
+// head block by head block, for each all sequences, for each its token blocks.
+// CTA c of G takes the stretch [c X / G, (c + 1) X / G) of the line, X its length;
+// a unit's keys are cut where a stretch ends inside it, unless that leaves a part
+// of under kMinPart tiles.  G is at most the grid, and no larger than leaves every
+// CTA `min_stretch` tiles or, if that is more, one unit each.
 //
 // Heads come first because every head's piece of the line is alike: with G a
 // multiple of the head blocks, the CTAs of different heads read the same positions
 // at about the same time, and in the [page, position, head, d] layout those lie
-// side by side in memory.
-constexpr int kUnitCost = 3;
+// side by side in memory (66 -> 58 us on 256 sequences of 128 to 1024 keys, 8
+// heads, d 64).
+constexpr int kTileCost = 256;
+// a unit's own work -- queries, sums, output -- costs about 1.5 tiles
+constexpr int kUnitCost = kTileCost * 3 / 2;
 constexpr int kMinPart = 2;
-constexpr int kMinStretch = 2 * 4;
 
-// tiles of a unit before offset x (> 0) of its stretch on the line
+// tiles of a unit before offset x (> 0) of its piece of the line
 MHA_HD int paged_cut(long long x, int nt) {
   if (x <= 0) return 0;
-  const long long t = (x - kUnitCost + 1) >> 1;
+  const long long t = (x - kUnitCost + kTileCost / 2) / kTileCost;
   if (t < kMinPart) return 0;
   if (t > nt - kMinPart) return nt;
   return static_cast<int>(t);
@@ -152,7 +155,7 @@ MHA_HD int paged_cut(long long x, int nt) {
 // A CTA's place on the line: where its stretch begins and ends, and its first unit.
 struct PagedSpan {
   long long lo, hi;  // the stretch
-  long long s;       // where the first unit's sequence begins (this head block's units of it)
+  long long s;       // where this head block's units of the first unit's sequence begin
   int hb;            // head block of the first unit
   int b;             // its sequence
   int u;             // its token block
@@ -160,9 +163,10 @@ struct PagedSpan {
 };
 
 // The stretch of CTA `cta` of `grid` on a line of length `total` with `units` units.
-MHA_HD PagedSpan paged_stretch(long long total, long long units, int cta, int grid) {
+MHA_HD PagedSpan paged_stretch(long long total, long long units, int cta, int grid,
+                               int min_stretch) {
   PagedSpan sp;
-  const long long by_work = total / kMinStretch;
+  const long long by_work = total / (static_cast<long long>(min_stretch) * kTileCost);
   const long long most = by_work > units ? by_work : units;
   sp.ctas = static_cast<int>(most < 1 ? 1 : (most < grid ? most : grid));
   // total * cta / ctas without the product of the two
@@ -176,9 +180,45 @@ MHA_HD PagedSpan paged_stretch(long long total, long long units, int cta, int gr
 
 // token blocks of a sequence: its units of one head block
 MHA_HD int paged_blocks(const PagedProblem &p, const PagedSeq &s) { return (s.n + p.tb - 1) / p.tb; }
-// length on the line of each unit of a sequence (the last token block's)
-MHA_HD int paged_unit_cost(const PagedProblem &p, const PagedSeq &s) {
-  return kUnitCost + 2 * ((paged_kv_end(s, s.n, p.causal) + kPagedTile - 1) / kPagedTile);
+// Length on the line of unit u of a sequence: exact in tiles when the sequence has
+// one token block; else linear in its keys (half a tile for the last, ragged one),
+// so that sums over units have a closed form.
+MHA_HD int paged_blocks_end(const PagedProblem &p, const PagedSeq &s, int u) {
+  const long long i1 = static_cast<long long>(u + 1) * p.tb;
+  return i1 < s.n ? static_cast<int>(i1) : s.n;
+}
+MHA_HD long long paged_unit_cost(const PagedProblem &p, const PagedSeq &s, int blocks, int u) {
+  const long long keys = paged_kv_end(s, paged_blocks_end(p, s, u), p.causal);
+  if (blocks == 1) return kUnitCost + (keys + kPagedTile - 1) / kPagedTile * kTileCost;
+  return kUnitCost + kTileCost / 2 + keys * (kTileCost / kPagedTile);
+}
+// Length of the units before u (0 <= u <= blocks) of a sequence.
+MHA_HD long long paged_cost_before(const PagedProblem &p, const PagedSeq &s, int blocks, int u) {
+  if (blocks <= 1) return u > 0 ? paged_unit_cost(p, s, blocks, 0) : 0;
+  const long long fixed = kUnitCost + kTileCost / 2, per_key = kTileCost / kPagedTile;
+  if (!p.causal) return u * (fixed + per_key * s.len);
+  // units before the last see base + (v + 1) tb keys, held to [0, len]
+  const long long full = u < blocks ? u : blocks - 1;
+  const long long tb = p.tb, base = s.base, len = s.len;
+  long long lo = base < 0 ? -base / tb : 0;  // units that see nothing
+  if (lo > full) lo = full;
+  long long hi = len - base > 0 ? (len - base - 1) / tb : 0;  // ... and from here on, all of len
+  if (hi > full) hi = full;
+  if (hi < lo) hi = lo;
+  long long keys = (hi - lo) * base + tb * ((hi - lo) * (hi + lo + 1) / 2) + (full - hi) * len;
+  if (u == blocks) keys += paged_kv_end(s, s.n, 1);
+  return u * fixed + per_key * keys;
+}
+
+// The unit of a sequence whose piece of the line holds offset x.
+MHA_HD int paged_unit_at(const PagedProblem &p, const PagedSeq &s, int blocks, long long x) {
+  int lo = 0, hi = blocks;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (paged_cost_before(p, s, blocks, mid) <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
 // The span of CTA `cta` of `grid`; all threads of the block call it (kThreads of
@@ -196,7 +236,7 @@ __device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long l
     const PagedSeq s = paged_seq(p.batch, b);
     const long long nu = paged_blocks(p, s);
     units += nu;
-    mine += nu * paged_unit_cost(p, s);
+    mine += paged_cost_before(p, s, static_cast<int>(nu), static_cast<int>(nu));
   }
   long long inc = mine;
 #pragma unroll
@@ -218,24 +258,24 @@ __device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long l
     all_units += scratch[16 + w];
   }
   const int hbs = p.Hkv * p.hblocks;
-  PagedSpan sp = paged_stretch(one * hbs, all_units * hbs, cta, grid);
+  PagedSpan sp = paged_stretch(one * hbs, all_units * hbs, cta, grid, p.min_stretch);
   const bool any = sp.lo < one * hbs;
   const int hb = any ? static_cast<int>(sp.lo / one) : hbs;
   const long long at = any ? sp.lo - hb * one : 0, first = before + inc - mine;
   if (any && at >= first && at < first + mine) {  // one thread of the block
     long long s = first;
-    int b = b0;
-    long long cost = 1;
-    for (;; ++b) {
+    for (int b = b0;; ++b) {
       const PagedSeq q = paged_seq(p.batch, b);
-      cost = paged_unit_cost(p, q);
-      const long long whole = cost * paged_blocks(p, q);
-      if (at < s + whole) break;
+      const int nu = paged_blocks(p, q);
+      const long long whole = paged_cost_before(p, q, nu, nu);
+      if (at < s + whole || b + 1 >= b1) {
+        scratch[32] = s;
+        scratch[33] = b;
+        scratch[34] = paged_unit_at(p, q, nu, at - s);
+        break;
+      }
       s += whole;
     }
-    scratch[32] = s;
-    scratch[33] = b;
-    scratch[34] = (at - s) / cost;
   }
   __syncthreads();
   sp.hb = hb;
@@ -263,13 +303,12 @@ struct PagedPart {
 struct PagedWalk {
   PagedSpan sp;
   PagedSeq seq, ahead;  // sequence b, and the one behind it (read early)
-  int hb, b, u, blocks, cost;
-  long long s;  // where this head block's units of sequence b begin
+  int hb, b, u, blocks;
+  long long at;  // where unit u begins
 
   MHA_HD void take(const PagedProblem &p, const PagedSeq &q) {
     seq = q;
     blocks = paged_blocks(p, seq);
-    cost = paged_unit_cost(p, seq);
     ahead = paged_seq(p.batch, b + 1 < p.batch.B ? b + 1 : 0);
   }
   MHA_HD void begin(const PagedProblem &p, const PagedSpan &span) {
@@ -277,25 +316,24 @@ struct PagedWalk {
     hb = sp.hb;
     b = sp.b;
     u = sp.u;
-    s = sp.s;
-    if (sp.lo < sp.hi) take(p, paged_seq(p.batch, b));
+    at = sp.hi;
+    if (sp.lo < sp.hi) {
+      take(p, paged_seq(p.batch, b));
+      at = sp.s + paged_cost_before(p, seq, blocks, u);
+    }
   }
   // The next part; false when the span is done.
   MHA_HD bool next(const PagedProblem &p, PagedPart &part) {
     for (;;) {
-      if (s >= sp.hi) return false;
+      if (at >= sp.hi) return false;
       while (u >= blocks) {
-        s += static_cast<long long>(blocks) * cost;
-        if (s >= sp.hi) return false;
         u = 0;
-        if (++b == p.batch.B) {
+        if (++b >= p.batch.B) {
           b = 0;
           if (++hb >= p.Hkv * p.hblocks) return false;  // lengths changed meanwhile
         }
         take(p, ahead);
       }
-      const long long at = s + static_cast<long long>(u) * cost;
-      if (at >= sp.hi) return false;
       part.seq = seq;
       part.b = b;
       part.kv = hb / p.hblocks;
@@ -303,14 +341,16 @@ struct PagedWalk {
       part.h0 = part.kv * p.group + hin;
       part.heads = p.group - hin < p.hpu ? p.group - hin : p.hpu;
       part.i0 = u * p.tb;
-      part.i1 = seq.n - part.i0 < p.tb ? seq.n : part.i0 + p.tb;
-      ++u;
+      part.i1 = paged_blocks_end(p, seq, u);
       part.kv_end = paged_kv_end(seq, part.i1, p.causal);
       part.nt = (part.kv_end + kPagedTile - 1) / kPagedTile;
-      part.t0 = paged_cut(sp.lo - at, part.nt);
-      part.t1 = sp.hi < at + cost ? paged_cut(sp.hi - at, part.nt) : part.nt;
+      const long long from = at;
+      at += paged_unit_cost(p, seq, blocks, u);
+      ++u;
+      part.t0 = paged_cut(sp.lo - from, part.nt);
+      part.t1 = sp.hi < at ? paged_cut(sp.hi - from, part.nt) : part.nt;
       if (part.nt == 0) {  // nothing to attend to: zeros, by the CTA that holds its beginning
-        if (at >= sp.lo) return true;
+        if (from >= sp.lo) return true;
         continue;
       }
       if (part.t1 > part.t0) return true;
@@ -353,8 +393,12 @@ MHA_HD long long paged_cell(const PagedBatch &p, int b, int pos, int head,
 cudaError_t launch_paged_few(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                              const PagedProblem &p, int d, int &grid, int num_sms,
                              cudaStream_t stream);
-cudaError_t launch_paged_simt(const PagedProblem &p, int d, int dtype, int grid,
-                              cudaStream_t stream);
+// bf16, 256 rows per unit: maps over q with box (64, tb / 2, hpu, 1), over the caches
+// as above
+cudaError_t launch_paged_many(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                              const PagedProblem &p, int d, int grid, cudaStream_t stream);
+// fp32, at most 16 rows per unit
+cudaError_t launch_paged_simt(const PagedProblem &p, int d, int grid, cudaStream_t stream);
 // joins the parts of split units
 cudaError_t launch_paged_merge(const PagedProblem &p, int d, int dtype, int grid,
                                cudaStream_t stream);

@@ -126,17 +126,17 @@ int paged_path(int B, int T, int H, int H_kv, int d, int max_q, int dtype) {
     return -MHA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0 || H == 0) return kNone;
   if (dtype == MHA_DTYPE_F32) return kSimt;
-  return static_cast<long long>(H / H_kv) * max_q <= 16 ? kFew : kSimt;
+  return static_cast<long long>(H / H_kv) * max_q <= 16 ? kFew : kMany;
 }
 
 Units units_of(int path, int group, int max_q) {
-  (void)path;
   Units u;
-  u.hpu = std::min(group, 16);
+  const int rows = path == kMany ? 128 : 16;  // of a tile
+  u.hpu = std::min(group, rows);
   u.hblocks = (group + u.hpu - 1) / u.hpu;
-  u.tb = std::min(16 / u.hpu, max_q);
+  u.tb = path == kMany ? 2 * (rows / u.hpu) : std::min(rows / u.hpu, max_q);
   u.rows = u.hpu * u.tb;
-  u.ctas = kPagedMaxCtas;
+  u.ctas = path == kMany ? kPagedManyMaxCtas : kPagedMaxCtas;
   return u;
 }
 
@@ -409,23 +409,29 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   p.status = dev.status;
   p.wait_ns = wait_limit_ns();
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  int grid = std::min(u.ctas, 3 * dev.sms);
+  p.min_stretch = 4;
+  int grid = u.ctas;
   cudaError_t err = cudaSuccess;
   if (path == kSimt) {
-    err = launch_paged_simt(p, d, dtype, grid, stream);
+    grid = std::min(u.ctas, 3 * dev.sms);
+    err = launch_paged_simt(p, d, grid, stream);
   } else {
-    grid = u.ctas;
     CUtensorMap qm, km, vm;
     const int box = std::min(page_size, kPagedTile);
     // a cache without pages is never read: any valid map will do
     const bool none = num_pages == 0;
     const void *kb = none ? q : k_cache, *vb = none ? q : v_cache;
     const int pages = none ? 1 : num_pages;
-    if (!make_map(&qm, q, d, T, H, 1, kLayoutBSHD, u.tb, u.hpu) ||
+    if (!make_map(&qm, q, d, T, H, 1, kLayoutBSHD, path == kMany ? u.tb / 2 : u.tb, u.hpu) ||
         !make_map(&km, kb, d, page_size, H_kv, pages, layout, box, 1) ||
         !make_map(&vm, vb, d, page_size, H_kv, pages, layout, box, 1))
       return MHA_ERR_CUDA;
-    err = launch_paged_few(qm, km, vm, p, d, grid, dev.sms, stream);
+    if (path == kMany) {
+      grid = std::min(grid, dev.sms);
+      err = launch_paged_many(qm, km, vm, p, d, grid, stream);
+    } else {
+      err = launch_paged_few(qm, km, vm, p, d, grid, dev.sms, stream);
+    }
   }
   if (err == cudaSuccess) err = launch_paged_merge(p, d, dtype, grid, stream);
   return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;

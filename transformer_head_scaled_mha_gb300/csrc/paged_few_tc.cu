@@ -53,20 +53,20 @@ constexpr int kBN = kPagedTile;
 constexpr int kN = 16;               // query rows per score product
 constexpr uint32_t kTmemCols = 128;  // S0 S1 (kN each), O0 O1 (kOCols each)
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kMaxSlots = 6;
+constexpr int kMaxSlots = 3;
 constexpr int kDescs = 4;  // part descriptions in flight
 constexpr uint32_t kBarSoftmax = 1;
 
-// d = 64 up to 8 rows: half the ring and two CTAs per SM, whose waits (for a
-// part's first tile, its output) fall into each other's work.
+// d = 64: half the ring and two CTAs per SM, whose waits (for a part's first tile,
+// its output, a lone softmax warp's latencies) fall into each other's work.
 template <int D, int RP>
 struct Cfg {
-  static constexpr int kCtas = D == 64 && RP <= 8 ? 2 : 1;  // per SM
+  static constexpr int kCtas = D == 64 ? 2 : 1;  // per SM
   static constexpr int kSlabs = D / 64;
   static constexpr int kBlkBytes = 128 * 128;           // [128 rows x 64] swizzle block
   static constexpr int kTileBytes = kSlabs * kBlkBytes;  // a K or V tile
   static constexpr int kSlotBytes = 2 * kTileBytes;      // ring slot: K tile, V tile
-  static constexpr int kSlots = D == 128 || kCtas == 2 ? 3 : 6;
+  static constexpr int kSlots = 3;
   static constexpr int kQBlk = kN * 128;  // [16 rows x 64] of Q
   static constexpr int kQBytes = kSlabs * kQBlk;
   // Up to 8 rows the weights go in as two bf16, the rounded weight and what the
@@ -100,9 +100,8 @@ struct Desc {
 
 template <int RP>
 struct __align__(16) Shared {
-  float red[2][4][RP];  // per-warp tile maxima, double-buffered by tile
+  float4 red[2][RP];    // tile maxima of the four warps, double-buffered by tile
   float lsum[4][RP];    // per-warp row sums
-  float xo[RP][64];     // d = 64: the second key half's partial output
   long long scratch[40];
   Desc desc[kDescs];
   uint32_t present[kMaxSlots];  // pages of the slot's tile that were loaded
@@ -124,15 +123,29 @@ constexpr size_t smem_bytes() {
          sizeof(Shared<RP>);
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Maxima of R values (R rows, one value of each per lane) over the warp: halves of
+// the rows change hands at each step, so R - 1 + log2(32 / R) shuffles serve all
+// rows (5 R row by row).  Lane l ends with row l / (32 / R).
+template <int R>
+__device__ __forceinline__ float rows_max(float (&v)[R], int lane) {
+  int bit = 16;
+#pragma unroll
+  for (int h = R / 2; h > 0; h >>= 1, bit >>= 1) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float give = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
+      v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+    }
+  }
+  for (; bit > 0; bit >>= 1) v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
+  return v[0];
 }
 
 struct FewMaps {
@@ -462,11 +475,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
                 st_shared_v4(v + (c >> 3) * C::kBlkBytes + (((c ^ k) & 7) << 4), 0, 0, 0, 0);
             }
           }
+          float v[RP];
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            const float v = warp_max(x[r]);
-            if (lane == 0) sh->red[t & 1][warp][r] = v;
-          }
+          for (int r = 0; r < RP; ++r) v[r] = x[r];
+          const float top = rows_max(v, lane);
+          if (lane % (32 / RP) == 0)
+            reinterpret_cast<float *>(&sh->red[t & 1][lane / (32 / RP)])[warp] = top;
         }
         ok = named_barrier_and(kBarSoftmax, kSoftmaxThreads, ok && okw);
         if (!ok) break;
@@ -475,8 +489,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
         bool rescale = false;
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-          const float tm = fmaxf(fmaxf(sh->red[t & 1][0][r], sh->red[t & 1][1][r]),
-                                 fmaxf(sh->red[t & 1][2][r], sh->red[t & 1][3][r]));
+          const float4 w = sh->red[t & 1][r];
+          const float tm = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
           const bool up = tm > m[r] + kRescaleThreshold;
           const bool moved = up && m[r] != -INFINITY;
           alpha[r] = moved ? ex2_approx(m[r] - tm) : 1.f;
@@ -541,6 +555,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
       }
       const int u = t - 1;
       const bool oke = mbar_wait_warp(&sh->pv_done[u & 1], (u >> 1) & 1, abort_flag, p.wait_ns);
+      // d = 64: the second key half's output goes through the P buffer of the last
+      // tile, which its product has read
+      float *xo = reinterpret_cast<float *>(pbuf + (u & 1) * C::kPBytes);
       uint32_t o[RP];
       if (oke) {
         tc_fence_after();
@@ -558,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
         }
         if (D == 64 && warp >= 2) {
 #pragma unroll
-          for (int r = 0; r < RP; ++r) sh->xo[r][vdim] = __uint_as_float(o[r]);
+          for (int r = 0; r < RP; ++r) xo[r * 64 + vdim] = __uint_as_float(o[r]);
         }
       }
       tc_fence_before();
@@ -574,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
           if (r < R && h < d.heads && i < d.tokens) {
             const float lt = (sh->lsum[0][r] + sh->lsum[1][r]) + (sh->lsum[2][r] + sh->lsum[3][r]);
             float acc = __uint_as_float(o[r]);
-            if (D == 64) acc += sh->xo[r][vdim];
+            if (D == 64) acc += xo[r * 64 + vdim];
             if (sums != nullptr) {
               sums[r * D + vdim] = acc;
               if (k == 0) {
@@ -591,8 +608,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
           }
         }
       }
-      // lsum and xo are rewritten only after the next part's first tile
-      // barrier, which every thread reaches after the reads above
+      // lsum and that P buffer are rewritten only after the next part's first
+      // tile barrier, which every thread reaches after the reads above
     }
   }
 
@@ -618,6 +635,7 @@ cudaError_t launch_impl(const FewMaps &maps, const PagedProblem &p, int &grid, i
   using C = Cfg<D, RP>;
   constexpr size_t kSmem = smem_bytes<D, RP>();
   // 1 KB per CTA is the system's
+  static_assert(RP * 64 * sizeof(float) <= C::kPBytes, "output of a key half in a P buffer");
   static_assert(C::kCtas * (kSmem + 1024) <= 233472, "shared memory budget");
   static_assert(C::kSlots <= kMaxSlots, "ring size");
   grid = std::min(grid, C::kCtas * num_sms);

@@ -1,4 +1,4 @@
-// Attention over a paged key/value cache on the CUDA cores (FFMA, no TF32), and
+// Attention over a paged fp32 key/value cache on the CUDA cores (FFMA, no TF32), and
 // the joining of split units that every paged attention kernel uses.
 //
 // A CTA of four warps walks its parts (paged.cuh): R <= 16 query rows of one
@@ -36,8 +36,6 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
 
@@ -50,7 +48,7 @@ struct Smem {
   long long scratch[40];
 };
 
-template <typename T, int D, int RP>
+template <int D, int RP>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem p) {
   constexpr int kC = D / 32;  // output columns of a lane
   static_assert(sizeof(float) * kRows * D <= sizeof(float) * kKeys * (D + 4), "warp sums fit");
@@ -64,8 +62,9 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
   walk.begin(p, span);
   PagedPart part;
   int flags = 0, mseq = 0, mtok = 0, mhead = 0;
-  const T *kc = static_cast<const T *>(p.k), *vc = static_cast<const T *>(p.v);
-  T *out = static_cast<T *>(p.out);
+  const float *q = static_cast<const float *>(p.q);
+  const float *kc = static_cast<const float *>(p.k), *vc = static_cast<const float *>(p.v);
+  float *out = static_cast<float *>(p.out);
   while (walk.next(p, part)) {
     __syncthreads();  // the part before has read q and the warps' sums
     for (int e = threadIdx.x; e < RP * D; e += kThreads) {
@@ -73,8 +72,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
       const int h = r / p.tb, i = part.i0 + r % p.tb;
       float x = 0.f;
       if (h < part.heads && i < part.i1)
-        x = to_f32(static_cast<const T *>(
-            p.q)[(static_cast<long long>(part.seq.q0 + i) * p.H + part.h0 + h) * D + c]);
+        x = q[(static_cast<long long>(part.seq.q0 + i) * p.H + part.h0 + h) * D + c];
       sm.q[r][c] = x;
     }
     __syncthreads();
@@ -102,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
         const long long at = __shfl_sync(0xffffffffu, cell, j);
 #pragma unroll
         for (int c = 0; c < kC; ++c)
-          sm.k[warp][j][c * 32 + lane] = at >= 0 ? to_f32(kc[at * D + c * 32 + lane]) : 0.f;
+          sm.k[warp][j][c * 32 + lane] = at >= 0 ? kc[at * D + c * 32 + lane] : 0.f;
       }
       __syncwarp();
       float s[RP];
@@ -136,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
         const long long at = __shfl_sync(0xffffffffu, cell, j);
         float v[kC];
 #pragma unroll
-        for (int c = 0; c < kC; ++c) v[c] = at >= 0 ? to_f32(vc[at * D + c * 32 + lane]) : 0.f;
+        for (int c = 0; c < kC; ++c) v[c] = at >= 0 ? vc[at * D + c * 32 + lane] : 0.f;
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
           const float pr = sm.p[warp][j][r];
@@ -183,8 +181,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
           slot[p.rows * D + 2 * r + 1] = lt;
         }
       } else {
-        store_as(out + (static_cast<long long>(part.seq.q0 + i) * p.H + part.h0 + h) * D + c,
-                 lt > 0.f ? o / lt : 0.f);
+        out[(static_cast<long long>(part.seq.q0 + i) * p.H + part.h0 + h) * D + c] =
+            lt > 0.f ? o / lt : 0.f;
       }
     }
     if (split) {
@@ -208,24 +206,25 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
 }
 
 // CTA (c, y): if CTA c + 1 of the attention kernel holds the second part of a unit,
-// rows y, y + gridDim.y, ... of that unit are joined from its parts, in the order
-// of their keys.  A unit may have as many parts as there are CTAs, so lanes look at
-// different parts for the last part, the maximum and the sum, and groups of D
-// threads take every kGroups-th part of the output; a loop over the parts one
-// after the other would wait for memory once per part (13 of the 22 us of one
-// token over 8192 keys, d 128).
-constexpr int kMergeThreads = 256;
-template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedProblem p, int ctas) {
-  constexpr int kGroups = kMergeThreads / D;
-  __shared__ float sums[kGroups][D];
+// that unit's rows are joined from its parts, in the order of their keys.  kSplit of
+// the eight warps share a row: each takes every kSplit-th part, its lanes d / 32
+// columns each.  With few rows a unit may have as many parts as there are CTAs, and
+// a warp that went through them alone would wait for memory over and over (13 of the
+// 22 us of one token over 8192 keys, d 128); with 256 rows there are few parts.
+constexpr int kMergeWarps = 8;
+template <typename T, int D, int kSplit>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    paged_merge_kernel(const PagedProblem p, int ctas) {
+  constexpr int kC = D / 32;
+  constexpr int kRowsAtOnce = kMergeWarps / kSplit;
+  __shared__ float sums[kMergeWarps][D];
   griddep_launch_dependents();
   griddep_wait();
   const int c = blockIdx.x + 1;
   const int32_t *meta = p.meta + static_cast<size_t>(c) * kPagedMeta;
   if (!(meta[kMetaFlags] & kPartContinues) || !(meta[kMetaFlags - kPagedMeta] & kPartBegins)) return;
-  const int lane = threadIdx.x & 31;
-  const int col = threadIdx.x % D, group = threadIdx.x / D;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int share = warp % kSplit;
   int last = c;  // the parts are slot 1 of CTA c - 1 and slot 0 of CTAs c .. last
   for (int at = c; at < ctas; at += 32) {
     const int k = min(at + lane, ctas - 1);
@@ -239,36 +238,52 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
   const PagedSeq seq = paged_seq(p.batch, meta[kMetaSeq]);
   const int i0 = meta[kMetaTok], h0 = meta[kMetaHead];
   const int heads = min(p.hpu, p.group - h0 % p.group);
-  for (int r = blockIdx.y; r < p.rows; r += gridDim.y) {
+  for (int r0 = blockIdx.y * kRowsAtOnce; r0 < p.rows; r0 += gridDim.y * kRowsAtOnce) {
+    const int r = r0 + warp / kSplit;
     const int h = r / p.tb, i = i0 + r % p.tb;
-    if (h >= heads || i >= seq.n) continue;
-    const size_t ml = static_cast<size_t>(p.rows) * D + 2 * r;  // (max, sum) of the row in a slot
-    float m = -INFINITY, l = 0.f;
-    for (int k = c - 1 + lane; k <= last; k += 32) {
-      const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
-      const float mk = slot[ml], lk = slot[ml + 1];
-      const float mn = fmaxf(m, mk), use = mn == -INFINITY ? 0.f : mn;
-      l = l * ex2_approx(m - use) + lk * ex2_approx(mk - use);
-      m = mn;
-    }
-    const float top = warp_max(m), use = top == -INFINITY ? 0.f : top;
-    l = warp_sum(l * ex2_approx(m - use));
-    float o = 0.f;
-#pragma unroll 4
-    for (int k = c - 1 + group; k <= last; k += kGroups) {
-      const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
-      o = fmaf(slot[static_cast<size_t>(r) * D + col], ex2_approx(slot[ml] - use), o);
-    }
-    sums[group][col] = o;
-    __syncthreads();
-    if (group == 0) {
+    const bool row = r < p.rows && h < heads && i < seq.n;
+    float o[kC], m = -INFINITY, l = 0.f, use = 0.f;
 #pragma unroll
-      for (int g = 1; g < kGroups; ++g) o += sums[g][col];
-      store_as(static_cast<T *>(p.out) +
-                   (static_cast<long long>(seq.q0 + i) * p.H + h0 + h) * D + col,
-               l > 0.f ? o / l : 0.f);
+    for (int e = 0; e < kC; ++e) o[e] = 0.f;
+    if (row) {
+      const size_t ml = static_cast<size_t>(p.rows) * D + 2 * r;  // (max, sum) in a slot
+      for (int k = c - 1 + lane; k <= last; k += 32) {
+        const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
+        const float mk = slot[ml], lk = slot[ml + 1];
+        const float mn = fmaxf(m, mk), u = mn == -INFINITY ? 0.f : mn;
+        l = l * ex2_approx(m - u) + lk * ex2_approx(mk - u);
+        m = mn;
+      }
+      const float top = warp_max(m);
+      use = top == -INFINITY ? 0.f : top;
+      l = warp_sum(l * ex2_approx(m - use));
+#pragma unroll 4
+      for (int k = c - 1 + share; k <= last; k += kSplit) {
+        const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
+        const float f = ex2_approx(slot[ml] - use);
+#pragma unroll
+        for (int e = 0; e < kC; ++e)
+          o[e] = fmaf(slot[static_cast<size_t>(r) * D + e * 32 + lane], f, o[e]);
+      }
     }
-    __syncthreads();
+    if (kSplit > 1) {
+#pragma unroll
+      for (int e = 0; e < kC; ++e) sums[warp][e * 32 + lane] = o[e];
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kC; ++e) {
+        o[e] = 0.f;
+#pragma unroll
+        for (int g = 0; g < kSplit; ++g) o[e] += sums[warp - share + g][e * 32 + lane];
+      }
+      __syncthreads();
+    }
+    if (row && share == 0) {
+      T *to = static_cast<T *>(p.out) +
+              (static_cast<long long>(seq.q0 + i) * p.H + h0 + h) * D + lane;
+#pragma unroll
+      for (int e = 0; e < kC; ++e) store_as(to + e * 32, l > 0.f ? o[e] / l : 0.f);
+    }
   }
 }
 
@@ -288,42 +303,49 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, int smem, cu
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename T, int D, int RP>
+template <int D, int RP>
 cudaError_t simt(const PagedProblem &p, int grid, cudaStream_t stream) {
-  const cudaError_t e = set_smem_once(
-      reinterpret_cast<const void *>(paged_simt_kernel<T, D, RP>), sizeof(Smem<D>));
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(paged_simt_kernel<D, RP>),
+                                      sizeof(Smem<D>));
   if (e != cudaSuccess) return e;
-  return launch(paged_simt_kernel<T, D, RP>, dim3(grid), kThreads, sizeof(Smem<D>), stream, p);
+  return launch(paged_simt_kernel<D, RP>, dim3(grid), kThreads, sizeof(Smem<D>), stream, p);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t simt_rows(const PagedProblem &p, int grid, cudaStream_t stream) {
   const int R = p.hpu * p.tb;
-  if (R <= 1) return simt<T, D, 1>(p, grid, stream);
-  if (R <= 4) return simt<T, D, 4>(p, grid, stream);
-  return simt<T, D, 16>(p, grid, stream);
+  if (R <= 1) return simt<D, 1>(p, grid, stream);
+  if (R <= 4) return simt<D, 4>(p, grid, stream);
+  return simt<D, 16>(p, grid, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_simt(const PagedProblem &p, int d, int dtype, int grid,
-                              cudaStream_t stream) {
+cudaError_t launch_paged_simt(const PagedProblem &p, int d, int grid, cudaStream_t stream) {
   if (p.hpu * p.tb > kRows) return cudaErrorInvalidValue;
-  if (dtype == 0)
-    return d == 64 ? simt_rows<float, 64>(p, grid, stream) : simt_rows<float, 128>(p, grid, stream);
-  return d == 64 ? simt_rows<__nv_bfloat16, 64>(p, grid, stream)
-                 : simt_rows<__nv_bfloat16, 128>(p, grid, stream);
+  return d == 64 ? simt_rows<64>(p, grid, stream) : simt_rows<128>(p, grid, stream);
 }
+
+namespace {
+
+template <typename T, int D>
+cudaError_t merge(const PagedProblem &p, int grid, cudaStream_t stream) {
+  if (p.rows <= 16)
+    return launch(paged_merge_kernel<T, D, kMergeWarps>, dim3(grid - 1, p.rows), kMergeWarps * 32,
+                  0, stream, p, grid);
+  return launch(paged_merge_kernel<T, D, 1>, dim3(grid - 1, 8), kMergeWarps * 32, 0, stream, p,
+                grid);
+}
+
+}  // namespace
 
 cudaError_t launch_paged_merge(const PagedProblem &p, int d, int dtype, int grid,
                                cudaStream_t stream) {
   if (grid < 2) return cudaSuccess;
-  const dim3 g(grid - 1, p.rows < 16 ? p.rows : 16);
   if (dtype == 0)
-    return d == 64 ? launch(paged_merge_kernel<float, 64>, g, kMergeThreads, 0, stream, p, grid)
-                   : launch(paged_merge_kernel<float, 128>, g, kMergeThreads, 0, stream, p, grid);
-  return d == 64 ? launch(paged_merge_kernel<__nv_bfloat16, 64>, g, kMergeThreads, 0, stream, p, grid)
-                 : launch(paged_merge_kernel<__nv_bfloat16, 128>, g, kMergeThreads, 0, stream, p, grid);
+    return d == 64 ? merge<float, 64>(p, grid, stream) : merge<float, 128>(p, grid, stream);
+  return d == 64 ? merge<__nv_bfloat16, 64>(p, grid, stream)
+                 : merge<__nv_bfloat16, 128>(p, grid, stream);
 }
 
 }  // namespace mha
