@@ -204,6 +204,9 @@ class Fake:
     def dim(self):
         return len(self.shape)
 
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
     def is_contiguous(self):
         return self._contiguous
 

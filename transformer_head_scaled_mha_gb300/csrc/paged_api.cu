@@ -413,7 +413,7 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   int grid = u.ctas;
   cudaError_t err = cudaSuccess;
   if (path == kSimt) {
-    grid = std::min(u.ctas, 3 * dev.sms);
+    grid = std::min(u.ctas, (d == 64 ? 2 : 1) * dev.sms);  // CTAs that run at a time
     err = launch_paged_simt(p, d, grid, stream);
   } else {
     CUtensorMap qm, km, vm;
@@ -433,6 +433,10 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
       err = launch_paged_few(qm, km, vm, p, d, grid, dev.sms, stream);
     }
   }
-  if (err == cudaSuccess) err = launch_paged_merge(p, d, dtype, grid, stream);
+  // a unit is cut only when both parts have kMinPart tiles: not where the block
+  // table has no room for them
+  const long long most = static_cast<long long>(max_pages) * page_size;
+  if (err == cudaSuccess && most > (2 * kMinPart - 1) * kPagedTile)
+    err = launch_paged_merge(p, d, dtype, grid, stream);
   return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }

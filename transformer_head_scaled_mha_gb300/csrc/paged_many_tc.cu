@@ -165,6 +165,96 @@ __device__ __noinline__ void rescale_p16(uint32_t taddr, float f) {
   tmem_st16(taddr, r);
 }
 
+// N lanes with N 16-byte pieces of a row each: lane l ends with piece l of all N
+// rows (v[k]: of lane k's), so that N lanes store N x 16 bytes side by side.  Storing
+// each lane's own row instead touches 32 lines per instruction.
+template <int N>
+__device__ __forceinline__ void swap_rows(uint4 (&v)[N], int lane) {
+#pragma unroll
+  for (int s = N / 2; s > 0; s >>= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (k & s) continue;
+      const uint4 give = up ? v[k] : v[k + s];
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, s);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, s);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, s);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, s);
+      if (up) v[k] = got;
+      else v[k + s] = got;
+    }
+  }
+}
+
+// Stores the warp's 32 rows of O (TMEM o0 times a0, plus TMEM o1 times a1): as fp32
+// to rows `mine` of a slot of sums, or as bf16 to rows `mine` of out (-1: no row of
+// ours).  kNoTmem stands for zeros; `none`: this lane's row is zeros whatever TMEM
+// holds.
+constexpr uint32_t kNoTmem = 0xffffffffu;
+template <int D>
+__device__ __forceinline__ void store_rows(uint32_t o0, uint32_t o1, float a0, float a1, bool none,
+                                           int mine, float *slot, uint16_t *out, int lane) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    uint32_t o[32];
+    if (o0 != kNoTmem) {
+      tmem_ld32(o0 + c0, o);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      o[e] = o0 == kNoTmem || none ? 0u : __float_as_uint(__uint_as_float(o[e]) * a0);
+    if (o1 != kNoTmem) {
+#pragma unroll
+      for (int hf = 0; hf < 32; hf += 16) {
+        uint32_t t[16];
+        tmem_ld16(o1 + c0 + hf, t);
+        tmem_wait_ld();
+        if (!none) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[hf + e] =
+                __float_as_uint(fmaf(__uint_as_float(t[e]), a1, __uint_as_float(o[hf + e])));
+        }
+      }
+    }
+    if (slot != nullptr) {
+      uint4 f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        f[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      swap_rows(f, lane);
+      slot += (lane & 7) * 4 + c0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int to = __shfl_sync(0xffffffffu, mine, (lane & 24) + k);
+        if (to >= 0) st_global_v4(slot + static_cast<size_t>(to) * D, f[k]);
+      }
+      slot -= (lane & 7) * 4 + c0;
+    } else {
+      uint4 q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * e]),
+                             __uint_as_float(o[8 * k + 2 * e + 1]));
+        q[k] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+      swap_rows(q, lane);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int to = __shfl_sync(0xffffffffu, mine, (lane & 28) + k);
+        if (to >= 0)
+          st_global_v4(out + static_cast<size_t>(to) * D + c0 + (lane & 3) * 8, q[k]);
+      }
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_many_tc_kernel(const __grid_constant__ ManyMaps maps, const PagedProblem p) {
@@ -672,60 +762,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       parts[0] += d.both ? cnt > 0 : d.tiles0 > 0;
       parts[1] += d.both ? join : d.tiles > 0;
-      float *sums = nullptr;
       const int unit_row = head * p.tb + i;
-      if (d.slot >= 0) {
-        float *slot = paged_slot_ptr(p, D, blockIdx.x, d.slot);
-        sums = slot + static_cast<size_t>(unit_row) * D;
-        if (row) {
-          float *ml = slot + static_cast<size_t>(p.rows) * D + 2 * unit_row;
-          ml[0] = m_use;
-          ml[1] = l_run;
-        }
+      float *slot = d.slot >= 0 ? paged_slot_ptr(p, D, blockIdx.x, d.slot) : nullptr;
+      if (slot != nullptr && row) {
+        float *ml = slot + static_cast<size_t>(p.rows) * D + 2 * unit_row;
+        ml[0] = m_use;
+        ml[1] = l_run;
       }
       const bool none = l_run == 0.f;  // nothing attended to: +0.0
-      const float inv = d.slot >= 0 ? 1.f : (none ? 0.f : 1.f / l_run);
-      if (live_warp) {
-#pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t o[32];
-          if (cnt > 0) {
-            tmem_ld32(o_tmem + ch * 32, o);
-            tmem_wait_ld();
-          }
-          float a = f0 * inv;
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = cnt == 0 || none ? 0u : __float_as_uint(__uint_as_float(o[e]) * a);
-          if (join) {
-            uint32_t o1[32];
-            tmem_ld32(o_tmem + 128 + ch * 32, o1);
-            tmem_wait_ld();
-            a = f1 * inv;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!none)
-                o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), a, __uint_as_float(o[e])));
-          }
-          if (row) {
-            if (sums != nullptr) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                st_global_v4(sums + ch * 32 + e, make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint4 v;
-                v.x = pack_bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
-                v.y = pack_bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                v.z = pack_bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
-                v.w = pack_bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
-                st_global_v4(out + out_row * D + ch * 32 + e, v);
-              }
-            }
-          }
-        }
-      }
+      const float inv = slot != nullptr ? 1.f : (none ? 0.f : 1.f / l_run);
+      const int mine = row ? (slot != nullptr ? unit_row : static_cast<int>(out_row)) : -1;
+      if (live_warp)
+        store_rows<D>(cnt > 0 ? o_tmem : kNoTmem, join ? o_tmem + 128 : kNoTmem,
+                      none ? 0.f : f0 * inv, none ? 0.f : f1 * inv, none, mine, slot, out, lane);
       tc_fence_before();
       if (cnt > 0) mbar_arrive(&sh->o_free[w]);
       if (join) mbar_arrive(&sh->o_free[1]);  // warpgroup 1's, with its statistics

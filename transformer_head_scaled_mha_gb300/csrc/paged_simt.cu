@@ -6,8 +6,10 @@
 // of each tile, a key per lane: scores of all R rows against the lane's key
 // (keys staged in shared memory, rows padded by 16 bytes so that lanes read
 // without conflicts; queries broadcast), an online softmax per warp, then the
-// value rows, each lane owning d / 32 output columns.  The warps' sums are
-// joined once per part.
+// value rows, each lane owning d / 32 output columns.  Keys and values are copied
+// to shared memory without registers (cp.async): the next tile's keys while this
+// one's softmax and values are worked on, its values while the next scores are, so
+// a warp always has a tile in flight.  The warps' sums are joined once per part.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -39,10 +41,23 @@ __device__ __forceinline__ float warp_sum(float x) {
 __device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
 
+// 16 bytes global -> shared, or zeros
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t saddr, const void *gptr, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(saddr), "l"(gptr),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+// all but the last N groups of this thread's copies are complete
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int D>
 struct Smem {
   float q[kRows][D];
-  float k[kWarps][kKeys][D + 4];  // later the warps' sums
+  float k[kWarps][kKeys][D + 4];
+  float v[kWarps][kKeys][D];  // at a part's end the warps' sums
   float p[kWarps][kKeys][kRows];
   float m[kWarps][kRows], l[kWarps][kRows];
   long long scratch[40];
@@ -51,7 +66,7 @@ struct Smem {
 template <int D, int RP>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem p) {
   constexpr int kC = D / 32;  // output columns of a lane
-  static_assert(sizeof(float) * kRows * D <= sizeof(float) * kKeys * (D + 4), "warp sums fit");
+  static_assert(kRows <= kKeys, "a warp's sums fit where its values were");
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
   griddep_launch_dependents();
@@ -87,21 +102,33 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
       const int i = part.i0 + r % p.tb;
       lim[r] = paged_kv_end(part.seq, i + 1, p.causal);
     }
-    for (int t = part.t0; t < part.t1; ++t) {
-      const int key0 = t * kPagedTile + warp * kKeys;
-      if (key0 >= part.kv_end) break;
-      const int key = key0 + lane;
-      const long long cell =
-          key < part.kv_end ? paged_cell(p.batch, part.b, key, part.kv, p.Hkv) : -1;
-      __syncwarp();
-      // the warp's key rows, zeros where there is none
+    // a warp's keys of tile t: the cache rows, one per lane (-1: none)
+    auto cell_of = [&](int t) -> long long {
+      const int key = t * kPagedTile + warp * kKeys + lane;
+      return t < part.t1 && key < part.kv_end ? paged_cell(p.batch, part.b, key, part.kv, p.Hkv)
+                                              : -1;
+    };
+    // copies those rows, zeros where there is none; 16 bytes per lane
+    auto copy = [&](const float *cache, float *to, int stride, long long cell) {
+      constexpr int kPer = D / 4, kAtOnce = 32 / kPer;  // lanes per row, rows at once
+      const int c = (lane % kPer) * 4;
 #pragma unroll 8
-      for (int j = 0; j < kKeys; ++j) {
-        const long long at = __shfl_sync(0xffffffffu, cell, j);
-#pragma unroll
-        for (int c = 0; c < kC; ++c)
-          sm.k[warp][j][c * 32 + lane] = at >= 0 ? kc[at * D + c * 32 + lane] : 0.f;
+      for (int j = 0; j < kKeys; j += kAtOnce) {
+        const int row = j + lane / kPer;
+        const long long at = __shfl_sync(0xffffffffu, cell, row);
+        cp_async16_or_zero(smem_addr(to + row * stride + c), cache + (at < 0 ? 0 : at) * D + c,
+                           at >= 0);
       }
+      cp_async_commit();
+    };
+    float *kw = &sm.k[warp][0][0], *vw = &sm.v[warp][0][0];
+    long long cell = cell_of(part.t0);
+    copy(kc, kw, D + 4, cell);
+    copy(vc, vw, D, cell);
+    for (int t = part.t0; t < part.t1; ++t) {
+      const int key = t * kPagedTile + warp * kKeys + lane;
+      const long long next = cell_of(t + 1);
+      cp_async_wait<1>();  // this tile's keys (its values may be on their way)
       __syncwarp();
       float s[RP];
 #pragma unroll
@@ -115,6 +142,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
           s[r] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[r]))));
         }
       }
+      __syncwarp();
+      copy(kc, kw, D + 4, next);
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
         const float x = cell >= 0 && key < lim[r] ? s[r] * p.scale_log2 : -INFINITY;
@@ -128,13 +157,13 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
         for (int c = 0; c < kC; ++c) acc[r][c] *= alpha;
         sm.p[warp][lane][r] = pr;
       }
+      cp_async_wait<1>();  // this tile's values
       __syncwarp();
 #pragma unroll 4
       for (int j = 0; j < kKeys; ++j) {
-        const long long at = __shfl_sync(0xffffffffu, cell, j);
         float v[kC];
 #pragma unroll
-        for (int c = 0; c < kC; ++c) v[c] = at >= 0 ? vc[at * D + c * 32 + lane] : 0.f;
+        for (int c = 0; c < kC; ++c) v[c] = sm.v[warp][j][c * 32 + lane];
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
           const float pr = sm.p[warp][j][r];
@@ -142,10 +171,14 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
           for (int c = 0; c < kC; ++c) acc[r][c] = fmaf(pr, v[c], acc[r][c]);
         }
       }
+      __syncwarp();
+      copy(vc, vw, D, next);
+      cell = next;
     }
-    // join the warps: each leaves its sums where its keys were
+    cp_async_wait<0>();
+    // join the warps: each leaves its sums where its values were
     __syncwarp();
-    float *mine = &sm.k[warp][0][0];
+    float *mine = vw;
 #pragma unroll
     for (int r = 0; r < RP; ++r) {
       const float lw = warp_sum(l[r]);
@@ -172,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2_approx(sm.m[w][r] - use);
         lt = fmaf(sm.l[w][r], f, lt);
-        o = fmaf(sm.k[w][0][r * D + c], f, o);
+        o = fmaf(sm.v[w][0][r * D + c], f, o);
       }
       if (split) {
         slot[r * D + c] = o;

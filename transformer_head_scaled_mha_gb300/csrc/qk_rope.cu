@@ -7,10 +7,11 @@
 //   (y_a, y_b) = (n_a c - n_b s, n_a s + n_b c),  c, s = cos, sin(p f_i)
 //
 // Bound: HBM (about 10 flop per element against 2 x 2 bytes).  d * sizeof(T) / 16
-// lanes hold a row, 16 bytes each, so a row is read and written once with wide
-// accesses and its sums are shuffles within those lanes.  A CTA takes `tb` tokens
-// and walks their heads; the angles of a token are formed once, into shared
-// memory, and serve all its heads.
+// lanes hold a row, 16 bytes each in two pieces, so a row is read and written once and its sums are shuffles within those lanes.  A CTA takes `tb` tokens
+// and walks their heads, queries then keys (then values); the angles of a token are
+// formed once, into shared memory, and serve all its heads.  The first rows are on
+// their way before the angles are formed, and every row's load is issued kAhead
+// rows before it is needed.
 //
 // Angles: with the frequency in turns as a 64-bit binary fraction F =
 // frac(f / 2 pi) 2^64, the position times F modulo 2^64 is the angle's fraction of
@@ -30,10 +31,11 @@ namespace mha {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;  // tokens of a CTA at most
+constexpr int kMaxTokens = 16;  // tokens of a CTA at most
 
+// 16 bytes of a row, as a lane holds them: two pieces of 8 bytes.
 template <typename T>
-struct Vec;  // 16 bytes of a row
+struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
@@ -65,15 +67,17 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// A plain 16-byte load that the compiler may not move to the read-only path: a
-// row may be overwritten in place.
-__device__ __forceinline__ uint4 ld16(const void *p) {
+// Plain loads that the compiler may not move to the read-only path: a row may be
+// overwritten in place.
+__device__ __forceinline__ uint4 ld8x2(const void *lo, const void *hi) {
   uint4 v;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(lo) : "memory");
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.z), "=r"(v.w) : "l"(hi) : "memory");
   return v;
+}
+__device__ __forceinline__ void st8x2(void *lo, void *hi, uint4 v) {
+  asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(lo), "r"(v.x), "r"(v.y) : "memory");
+  asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(hi), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // frequency i as a 64-bit fraction of a turn per position
@@ -100,48 +104,30 @@ __device__ __forceinline__ Rows rows_of(int layout, int t, int heads, int L, int
   return {(static_cast<long long>(b) * heads * L + l) * d, static_cast<long long>(L) * d};
 }
 
-// What one thread holds of the rotation: its kN elements' factors.  out = x * c +
-// partner * s, the sign of s included.
-template <typename T, int D>
-struct Lane {
-  static constexpr int kN = Vec<T>::kN;
-  float c[kN], s[kN];
-  int partner;  // lane of the row's group that holds the other element of each pair
-  bool on;      // its elements are rotated (rotary is a multiple of 16: all or none are)
-
-  __device__ __forceinline__ void set(const float2 *cs, int col, int lane, int rotary, int style,
-                                      bool back) {
-    const int half = rotary >> 1;
-    partner = lane;
-    const int e0 = col * kN;
-    on = e0 < rotary;
-    if (style == kRopeHalves && on) partner = e0 < half ? lane + half / kN : lane - half / kN;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int e = e0 + i;
-      c[i] = 1.f;
-      s[i] = 0.f;
-      if (on) {
-        const bool first = style == kRopeHalves ? e < half : (e & 1) == 0;
-        const float2 v = cs[style == kRopeHalves ? (e < half ? e : e - half) : e >> 1];
-        c[i] = v.x;
-        s[i] = first != back ? -v.y : v.y;
-      }
-    }
+// A lane's place in a row.  Both elements of a rotated pair belong to one lane:
+// with MHA_ROPE_HALVES lane l of the rotated ones holds a piece of kN / 2 elements
+// from each half, pair i being elements (i, i + kN / 2) of the lane's kN; otherwise
+// the pieces lie side by side and pair i is (2 i, 2 i + 1).
+template <typename T, int kStyle>
+struct Place {
+  static constexpr int kN = Vec<T>::kN, kPairs = kN / 2;
+  int lo, hi;  // first elements of the two pieces
+  int freq;    // first pair's frequency
+  bool on;     // rotated (rotary is a multiple of 16: all of a lane's pairs are, or none)
+  __device__ __forceinline__ Place(int col, int rotary) {
+    on = col * kN < rotary;
+    freq = col * kPairs;
+    lo = kStyle == kRopeHalves && on ? col * kPairs : col * kN;
+    hi = kStyle == kRopeHalves && on ? (rotary >> 1) + col * kPairs : col * kN + kPairs;
   }
-  __device__ __forceinline__ void rotate(float (&x)[kN], int style) const {
-    float o[kN];
-    if (style == kRopeHalves) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], partner);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) o[i] = x[i ^ 1];
-    }
-    if (!on) return;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) x[i] = fmaf(o[i], s[i], x[i] * c[i]);
+  static __device__ __forceinline__ constexpr int a(int i) {
+    return kStyle == kRopeHalves ? i : 2 * i;
   }
+  static __device__ __forceinline__ constexpr int b(int i) {
+    return kStyle == kRopeHalves ? i + kPairs : 2 * i + 1;
+  }
+  __device__ __forceinline__ uint4 load(const T *row) const { return ld8x2(row + lo, row + hi); }
+  __device__ __forceinline__ void store(T *row, uint4 v) const { st8x2(row + lo, row + hi, v); }
 };
 
 template <int kLanes>
@@ -151,249 +137,316 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Norms and rotates `heads` rows of one token, every `hstep`-th from `h0`; all
-// lanes of the warp call it (`live`: this lane's row group has a token).  kBatch
-// rows are loaded before the first is stored.
-template <typename T, int D, bool kCopy>
-__device__ __forceinline__ void process_rows(const T *src, Rows in, T *dst, Rows to, int heads,
-                                             int h0, int hstep, bool live, const T *weight,
-                                             float eps, const Lane<T, D> &rot, int style,
-                                             bool rotates, int col) {
-  constexpr int kN = Vec<T>::kN, kLanes = D / kN, kBatch = 4;
-  float w[kN];
-  if (!kCopy && weight != nullptr) Vec<T>::unpack(ld16(weight + col * kN), w);
-  const int rounds = (heads + hstep - 1) / hstep;  // the same for all lanes: shuffles inside
-  for (int j = 0; j < rounds; j += kBatch) {
-    uint4 raw[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int h = h0 + (j + i) * hstep;
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (live && h < heads) raw[i] = ld16(src + in.base + h * in.step + col * kN);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int h = h0 + (j + i) * hstep;
-      if (!kCopy) {
-        if (j + i >= rounds) break;
-        float x[kN];
-        Vec<T>::unpack(raw[i], x);
-        if (weight != nullptr) {
-          float sq = 0.f;
-#pragma unroll
-          for (int e = 0; e < kN; ++e) sq = fmaf(x[e], x[e], sq);
-          const float r = rsqrtf(row_sum<kLanes>(sq) * (1.f / D) + eps);
-#pragma unroll
-          for (int e = 0; e < kN; ++e) x[e] = x[e] * r * w[e];
-        }
-        if (rotates) rot.rotate(x, style);
-        raw[i] = Vec<T>::pack(x);
-      }
-      if (live && h < heads) st_global_v4(dst + to.base + h * to.step + col * kN, raw[i]);
-    }
-  }
-}
-
 struct TokenInfo {
   long long cell;  // appending: cache row of head 0, or -1
   int pos;
   int live;
 };
 
-template <typename T, int D, bool kAppend>
+template <typename T, int D, int kStyle, bool kAppend>
 __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a, int tb) {
-  constexpr int kN = Vec<T>::kN, kLanes = D / kN, kSlots = kThreads / kLanes;
+  using P = Place<T, kStyle>;
+  constexpr int kN = Vec<T>::kN, kPairs = kN / 2, kLanes = D / kN, kSlots = kThreads / kLanes;
+  constexpr int kAhead = 4;
   __shared__ float2 cs[kMaxTokens][D / 2];
   __shared__ unsigned long long turns[D / 2];
   __shared__ TokenInfo info[kMaxTokens];
   griddep_launch_dependents();
+  const int col = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
+  const int tok = slot % tb, h0 = slot / tb, hstep = kSlots / tb;
+  const int t0 = blockIdx.x * tb, t = t0 + tok;
+  const P place(col, a.rotary);
+  const int rounds_q = (a.H + hstep - 1) / hstep, rounds_k = (a.Hkv + hstep - 1) / hstep;
+  const int rows = rounds_q + (kAppend ? 2 : 1) * rounds_k;
+  const int layout = kAppend ? kLayoutBSHD : a.layout;
+  const Rows rq = rows_of(layout, t, a.H, a.L, D), rk = rows_of(layout, t, a.Hkv, a.L, D);
+  // element offsets of a slot's first row and between its rows
+  const long long q0 = rq.base + h0 * rq.step, dq = hstep * rq.step;
+  const long long k0 = rk.base + h0 * rk.step, dk = hstep * rk.step;
+  // where the next row to load lies
+  const T *src = static_cast<const T *>(a.q) + q0;
+  int lj = 0, lh = h0;
+  auto load = [&]() {
+    if (lj == rounds_q || (kAppend && lj == rounds_q + rounds_k)) {
+      src = static_cast<const T *>(lj == rounds_q ? a.k : a.v) + k0;
+      lh = h0;
+    }
+    const bool q = lj < rounds_q;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (lj < rows && t < a.tokens && lh < (q ? a.H : a.Hkv)) v = place.load(src);
+    src += q ? dq : dk;
+    lh += hstep;
+    ++lj;
+    return v;
+  };
   griddep_wait();
-  const int t0 = blockIdx.x * tb;
+  uint4 raw[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) raw[i] = load();
   const int half = a.rotary >> 1;
   if (threadIdx.x >= kThreads - half) {
     const int f = threadIdx.x - (kThreads - half);
     turns[f] = turn_fraction(a.inv_freq[f]);
   }
   if (threadIdx.x < tb) {
-    const int t = t0 + threadIdx.x;
+    const int u = t0 + threadIdx.x;
     TokenInfo ti{-1, 0, 0};
-    if (t < a.tokens) {
+    if (u < a.tokens) {
       if (kAppend) {
-        const int b = paged_seq_of_row(a.batch, t);
+        const int b = paged_seq_of_row(a.batch, u);
         if (b >= 0) {
           // tokens up to the sequence's end count back from its length
           const int end = min(a.batch.q_starts[b + 1], a.tokens);
           ti.live = 1;
-          ti.pos = max(a.batch.kv_lengths[b], 0) - (end - t);
+          ti.pos = max(a.batch.kv_lengths[b], 0) - (end - u);
           ti.cell = paged_cell(a.batch, b, ti.pos, 0, a.Hkv);
         }
       } else {
         ti.live = 1;
-        ti.pos = a.positions != nullptr ? a.positions[t] : t % a.L;
+        ti.pos = a.positions != nullptr ? a.positions[u] : u % a.L;
       }
     }
     info[threadIdx.x] = ti;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < tb * half; i += kThreads) {
-    const int tok = i / half, f = i - tok * half;
-    cs[tok][f] = angle_cos_sin(info[tok].pos, turns[f]);
+    const int k = i / half, f = i - k * half;
+    cs[k][f] = angle_cos_sin(info[k].pos, turns[f]);
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const int col = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
-  const int tok = slot % tb, h0 = slot / tb, hstep = kSlots / tb;
-  const int t = t0 + tok;
   const bool live = info[tok].live != 0;
-  Lane<T, D> rot;
-  rot.set(cs[tok], col, lane, a.rotary, a.style, false);
-  const int layout = kAppend ? kLayoutBSHD : a.layout;
-  if (a.H > 0) {
-    const Rows r = rows_of(layout, t, a.H, a.L, D);
-    process_rows<T, D, false>(static_cast<const T *>(a.q), r, static_cast<T *>(a.q_out), r, a.H,
-                              h0, hstep, live, static_cast<const T *>(a.q_weight), a.eps, rot,
-                              a.style, half > 0, col);
+  const long long cell = info[tok].cell;
+  float c[kPairs], s[kPairs];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const float2 v = place.on ? cs[tok][place.freq + i] : make_float2(1.f, 0.f);
+    c[i] = v.x;
+    s[i] = v.y;
   }
-  if (a.Hkv > 0) {
-    const Rows r = rows_of(layout, t, a.Hkv, a.L, D);
-    Rows to = r;
-    bool kept = live;
-    if (kAppend) {
-      kept = live && info[tok].cell >= 0;
-      to.base = info[tok].cell * D;
-      to.step = a.batch.layout == kLayoutBHSD ? static_cast<long long>(a.batch.page_size) * D : D;
+  // where the row goes, and this tensor's factors: y_a = r (a ca - b sb),
+  // y_b = r (a sa + b cb), with the weight in them
+  T *dst = static_cast<T *>(a.q_out) + q0;
+  long long step = dq;
+  int h = h0, heads = a.H;
+  bool writes = live, normed = false, copies = false;
+  float ca[kPairs], sb[kPairs], sa[kPairs], cb[kPairs];
+  for (int j0 = 0; j0 < rows; j0 += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i;
+      if (j >= rows) break;
+      uint4 v = raw[i];
+      raw[i] = load();
+      if (j == 0 || j == rounds_q || (kAppend && j == rounds_q + rounds_k)) {
+        const bool q = j < rounds_q;
+        copies = kAppend && j == rounds_q + rounds_k;
+        if (!q) {
+          h = h0;
+          heads = a.Hkv;
+          dst = static_cast<T *>(copies ? a.v_out : a.k_out);
+          if (kAppend) {
+            const long long per = a.batch.layout == kLayoutBHSD
+                                      ? static_cast<long long>(a.batch.page_size) * D
+                                      : D;
+            writes = live && cell >= 0;
+            dst += cell * D + h0 * per;
+            step = hstep * per;
+          } else {
+            dst += k0;
+            step = dk;
+          }
+        }
+        const T *weight = static_cast<const T *>(q ? a.q_weight : a.k_weight);
+        normed = weight != nullptr && !copies;
+        float w[kN];
+        if (normed) Vec<T>::unpack(place.load(weight), w);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+          const float wa = normed ? w[P::a(e)] : 1.f, wb = normed ? w[P::b(e)] : 1.f;
+          ca[e] = c[e] * wa;
+          sb[e] = s[e] * wb;
+          sa[e] = s[e] * wa;
+          cb[e] = c[e] * wb;
+        }
+      }
+      if (!kAppend || !copies) {
+        float y[kN];
+        Vec<T>::unpack(v, y);
+        float r = 1.f;
+        if (normed) {
+          float sq = 0.f;
+#pragma unroll
+          for (int e = 0; e < kN; ++e) sq = fmaf(y[e], y[e], sq);
+          r = rsqrtf(row_sum<kLanes>(sq) * (1.f / D) + a.eps);
+        }
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+          const float ya = y[P::a(e)], yb = y[P::b(e)];
+          float oa = ya * ca[e], ob = yb * cb[e];
+          if (place.on) {  // outside the rotation an infinity must not meet a factor of 0
+            oa = fmaf(-yb, sb[e], oa);
+            ob = fmaf(ya, sa[e], ob);
+          }
+          y[P::a(e)] = oa * r;
+          y[P::b(e)] = ob * r;
+        }
+        v = Vec<T>::pack(y);
+      }
+      if (writes && h < heads) place.store(dst, v);
+      dst += step;
+      h += hstep;
     }
-    process_rows<T, D, false>(static_cast<const T *>(a.k), r, static_cast<T *>(a.k_out), to, a.Hkv,
-                              h0, hstep, kept, static_cast<const T *>(a.k_weight), a.eps, rot,
-                              a.style, half > 0, col);
-    if (kAppend)
-      process_rows<T, D, true>(static_cast<const T *>(a.v), r, static_cast<T *>(a.v_out), to,
-                               a.Hkv, h0, hstep, kept, nullptr, 0.f, rot, a.style, false, col);
   }
 }
 
-// Gradients of `heads` rows of one token; adds this lane's share of the weight's
-// gradient to dw.
-template <typename T, int D>
-__device__ __forceinline__ void process_rows_bwd(const T *x_in, const T *dy, T *dx, Rows r,
-                                                 int heads, int h0, int hstep, bool live,
-                                                 const T *weight, float eps,
-                                                 const Lane<T, D> &rot, int style, bool rotates,
-                                                 int col, float (&dw)[Vec<T>::kN]) {
-  constexpr int kN = Vec<T>::kN, kLanes = D / kN, kBatch = 2;
-  float w[kN];
-  const bool normed = weight != nullptr;
-  if (normed) Vec<T>::unpack(ld16(weight + col * kN), w);
-  const int rounds = (heads + hstep - 1) / hstep;
-  for (int j = 0; j < rounds; j += kBatch) {
-    uint4 rx[kBatch], rg[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int h = h0 + (j + i) * hstep;
-      rx[i] = rg[i] = make_uint4(0, 0, 0, 0);
-      if (live && h < heads) {
-        const long long at = r.base + h * r.step + col * kN;
-        rg[i] = ld16(dy + at);
-        if (normed) rx[i] = ld16(x_in + at);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int h = h0 + (j + i) * hstep;
-      if (j + i >= rounds) break;
-      float g[kN];
-      Vec<T>::unpack(rg[i], g);
-      if (rotates) rot.rotate(g, style);
-      if (normed) {
-        float x[kN], sq = 0.f, dot = 0.f;
-        Vec<T>::unpack(rx[i], x);
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-          sq = fmaf(x[e], x[e], sq);
-          dot = fmaf(g[e] * w[e], x[e], dot);
-        }
-        sq = row_sum<kLanes>(sq);
-        dot = row_sum<kLanes>(dot);
-        const float inv = rsqrtf(sq * (1.f / D) + eps);
-        const float mean = dot * inv * (1.f / D);  // mean of (w g) (x inv)
-        // an absent row adds nothing (its inv may be infinite)
-        const float add = live && h < heads ? inv : 0.f;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-          dw[e] = fmaf(g[e], x[e] * add, dw[e]);
-          g[e] = inv * (g[e] * w[e] - x[e] * inv * mean);
-        }
-      }
-      if (live && h < heads) st_global_v4(dx + r.base + h * r.step + col * kN, Vec<T>::pack(g));
-    }
-  }
-}
-
-template <typename T, int D>
+template <typename T, int D, int kStyle>
 __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeArgs a, int tb) {
-  constexpr int kN = Vec<T>::kN, kLanes = D / kN, kSlots = kThreads / kLanes;
+  using P = Place<T, kStyle>;
+  constexpr int kN = Vec<T>::kN, kPairs = kN / 2, kLanes = D / kN, kSlots = kThreads / kLanes;
+  constexpr int kAhead = 2;
   __shared__ float2 cs[kMaxTokens][D / 2];
   __shared__ unsigned long long turns[D / 2];
   __shared__ float sums[kSlots][D];
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31;
   const int col = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
   const int tok = slot % tb, h0 = slot / tb, hstep = kSlots / tb;
   const int half = a.rotary >> 1;
-  float dqw[kN], dkw[kN];
+  const P place(col, a.rotary);
+  const int rounds_q = (a.H + hstep - 1) / hstep;
+  const int rows = rounds_q + (a.Hkv + hstep - 1) / hstep;
+  // this lane's share of the weights' gradients: of the tensor at hand, and of the other
+  float dw[kN], other[kN];
 #pragma unroll
-  for (int e = 0; e < kN; ++e) dqw[e] = dkw[e] = 0.f;
+  for (int e = 0; e < kN; ++e) dw[e] = other[e] = 0.f;
   if (threadIdx.x < half) turns[threadIdx.x] = turn_fraction(a.inv_freq[threadIdx.x]);
-  __syncthreads();
   const int tiles = (a.tokens + tb - 1) / tb;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int t0 = tile * tb;
+    const int t0 = tile * tb, t = t0 + tok;
+    const Rows rq = rows_of(a.layout, t, a.H, a.L, D), rk = rows_of(a.layout, t, a.Hkv, a.L, D);
+    long long from = rq.base + h0 * rq.step, to = from;  // next row to load, to store
+    int lj = 0, lh = h0, h = h0;
+    uint4 raw_x[kAhead], raw_g[kAhead];
+    auto load = [&](int i) {
+      if (lj == rounds_q) {
+        from = rk.base + h0 * rk.step;
+        lh = h0;
+      }
+      const bool q = lj < rounds_q;
+      raw_x[i] = raw_g[i] = make_uint4(0, 0, 0, 0);
+      if (lj < rows && t < a.tokens && lh < (q ? a.H : a.Hkv)) {
+        raw_g[i] = place.load(static_cast<const T *>(q ? a.dq_out : a.dk_out) + from);
+        if ((q ? a.q_weight : a.k_weight) != nullptr)
+          raw_x[i] = place.load(static_cast<const T *>(q ? a.q : a.k) + from);
+      }
+      from += hstep * (q ? rq.step : rk.step);
+      lh += hstep;
+      ++lj;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i);
+    __syncthreads();  // the tile before has read cs; turns are written
     for (int i = threadIdx.x; i < tb * half; i += kThreads) {
       const int k = i / half, f = i - k * half;
-      const int t = min(t0 + k, a.tokens - 1);
-      const int pos = a.positions != nullptr ? a.positions[t] : t % a.L;
+      const int u = min(t0 + k, a.tokens - 1);
+      const int pos = a.positions != nullptr ? a.positions[u] : u % a.L;
       cs[k][f] = angle_cos_sin(pos, turns[f]);
     }
     __syncthreads();
-    const int t = t0 + tok;
-    const bool live = t < a.tokens;
-    Lane<T, D> rot;
-    rot.set(cs[tok], col, lane, a.rotary, a.style, true);
-    if (a.H > 0)
-      process_rows_bwd<T, D>(static_cast<const T *>(a.q), static_cast<const T *>(a.dq_out),
-                             static_cast<T *>(a.q_out), rows_of(a.layout, t, a.H, a.L, D), a.H, h0,
-                             hstep, live, static_cast<const T *>(a.q_weight), a.eps, rot, a.style,
-                             half > 0, col, dqw);
-    if (a.Hkv > 0)
-      process_rows_bwd<T, D>(static_cast<const T *>(a.k), static_cast<const T *>(a.dk_out),
-                             static_cast<T *>(a.k_out), rows_of(a.layout, t, a.Hkv, a.L, D), a.Hkv,
-                             h0, hstep, live, static_cast<const T *>(a.k_weight), a.eps, rot,
-                             a.style, half > 0, col, dkw);
-    __syncthreads();  // cs is rewritten by the next tile
+    float c[kPairs], s[kPairs], w[kN];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const float2 v = place.on ? cs[tok][place.freq + i] : make_float2(1.f, 0.f);
+      c[i] = v.x;
+      s[i] = v.y;
+    }
+    bool normed = false;
+    auto turn = [&]() {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        const float v = dw[e];
+        dw[e] = other[e];
+        other[e] = v;
+      }
+    };
+    for (int j0 = 0; j0 < rows; j0 += kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = j0 + i;
+        if (j >= rows) break;
+        const bool q = j < rounds_q;
+        if (j == rounds_q) {
+          to = rk.base + h0 * rk.step;
+          h = h0;
+          turn();
+        }
+        if (j == 0 || j == rounds_q) {
+          const T *weight = static_cast<const T *>(q ? a.q_weight : a.k_weight);
+          normed = weight != nullptr;
+          if (normed) Vec<T>::unpack(place.load(weight), w);
+        }
+        float g[kN], x[kN];
+        Vec<T>::unpack(raw_g[i], g);
+        Vec<T>::unpack(raw_x[i], x);
+        load(i);
+        const bool is = t < a.tokens && h < (q ? a.H : a.Hkv);
+        if (place.on) {
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) {
+            const float ga = g[P::a(e)], gb = g[P::b(e)];
+            g[P::a(e)] = fmaf(gb, s[e], ga * c[e]);
+            g[P::b(e)] = fmaf(-ga, s[e], gb * c[e]);
+          }
+        }
+        if (normed) {
+          float sq = 0.f, dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < kN; ++e) {
+            sq = fmaf(x[e], x[e], sq);
+            dot = fmaf(g[e] * w[e], x[e], dot);
+          }
+          sq = row_sum<kLanes>(sq);
+          dot = row_sum<kLanes>(dot);
+          const float inv = rsqrtf(sq * (1.f / D) + a.eps);
+          const float mean = dot * inv * (1.f / D);  // mean of (w g) (x inv)
+          const float add = is ? inv : 0.f;  // an absent row adds nothing (its inv may be infinite)
+#pragma unroll
+          for (int e = 0; e < kN; ++e) {
+            dw[e] = fmaf(g[e], x[e] * add, dw[e]);
+            g[e] = inv * (g[e] * w[e] - x[e] * inv * mean);
+          }
+        }
+        if (is) place.store(static_cast<T *>(q ? a.q_out : a.k_out) + to, Vec<T>::pack(g));
+        to += hstep * (q ? rq.step : rk.step);
+        h += hstep;
+      }
+    }
+    if (rounds_q < rows) turn();  // q's again
   }
   // this CTA's sums over its row slots, in a fixed order
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if ((which == 0 ? a.q_weight : a.k_weight) == nullptr) continue;
+    __syncthreads();
 #pragma unroll
-    for (int e = 0; e < kN; ++e) sums[slot][col * kN + e] = which == 0 ? dqw[e] : dkw[e];
+    for (int e = 0; e < kN; ++e)
+      sums[slot][(e < kPairs ? place.lo : place.hi) + e % kPairs] = which == 0 ? dw[e] : other[e];
     __syncthreads();
     if (threadIdx.x < D) {
       float v = 0.f;
 #pragma unroll
-      for (int s = 0; s < kSlots; ++s) v += sums[s][threadIdx.x];
+      for (int k = 0; k < kSlots; ++k) v += sums[k][threadIdx.x];
       a.partial[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + threadIdx.x] = v;
     }
-    __syncthreads();
   }
 }
 
 // dweight = sum of the CTAs' partial sums: CTA (x, y) takes columns 32 x .. + 31 of
-// tensor y, warp w the rows w, w + 8, ...
-__global__ void __launch_bounds__(256) rope_dweight_kernel(const float *partial, int rows, int d,
-                                                           float *dq_weight, float *dk_weight) {
-  __shared__ float sums[8][32];
+// tensor y, warp w the rows w, w + 32, ...
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32)
+    rope_dweight_kernel(const float *partial, int rows, int d, float *dq_weight, float *dk_weight) {
+  __shared__ float sums[kSumWarps][32];
   griddep_launch_dependents();
   griddep_wait();
   float *out = blockIdx.y == 0 ? dq_weight : dk_weight;
@@ -401,14 +454,15 @@ __global__ void __launch_bounds__(256) rope_dweight_kernel(const float *partial,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-#pragma unroll 4
-  for (int r = warp; r < rows; r += 8) v += partial[(static_cast<size_t>(r) * 2 + blockIdx.y) * d + c];
+#pragma unroll 8
+  for (int r = warp; r < rows; r += kSumWarps)
+    v += partial[(static_cast<size_t>(r) * 2 + blockIdx.y) * d + c];
   sums[warp][lane] = v;
   __syncthreads();
   if (warp == 0) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += sums[w][lane];
+    for (int w = 0; w < kSumWarps; ++w) s += sums[w][lane];
     out[c] = s;
   }
 }
@@ -428,45 +482,69 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Tokens per CTA: four share a CTA when that still leaves every SM several CTAs.
-int tokens_per_cta(int tokens, int num_sms) { return tokens >= 16 * num_sms ? kMaxTokens : 1; }
-
-template <typename T, int D>
-cudaError_t fwd(const RopeArgs &a, bool append, int num_sms, cudaStream_t stream) {
-  const int tb = tokens_per_cta(a.tokens, num_sms);
-  const dim3 grid((a.tokens + tb - 1) / tb);
-  return append ? launch(rope_fwd_kernel<T, D, true>, grid, kThreads, stream, a, tb)
-                : launch(rope_fwd_kernel<T, D, false>, grid, kThreads, stream, a, tb);
+// Tokens per CTA: more share a CTA, and its angles' latency, while a row slot has
+// fewer than 8 rows and the SMs keep several CTAs each.
+int tokens_per_cta(int tokens, int heads, int slots, int num_sms) {
+  int tb = 1;
+  while (tb < std::min(kMaxTokens, slots) && tb * heads < 8 * slots &&
+         tokens / (2 * tb) >= 4 * num_sms)
+    tb *= 2;
+  return tb;
 }
 
 template <typename T, int D>
+constexpr int slots() {
+  return kThreads / (D / Vec<T>::kN);
+}
+
+template <typename T, int D, int kStyle>
+cudaError_t fwd(const RopeArgs &a, bool append, int num_sms, cudaStream_t stream) {
+  const int tb = tokens_per_cta(a.tokens, a.H + (append ? 2 : 1) * a.Hkv, slots<T, D>(), num_sms);
+  const dim3 grid((a.tokens + tb - 1) / tb);
+  return append ? launch(rope_fwd_kernel<T, D, kStyle, true>, grid, kThreads, stream, a, tb)
+                : launch(rope_fwd_kernel<T, D, kStyle, false>, grid, kThreads, stream, a, tb);
+}
+
+template <typename T, int D, int kStyle>
 cudaError_t bwd(const RopeArgs &a, int num_sms, cudaStream_t stream) {
-  const int tb = tokens_per_cta(a.tokens, num_sms);
+  const int tb = tokens_per_cta(a.tokens, a.H + a.Hkv, slots<T, D>(), num_sms);
   const int grid = std::min({(a.tokens + tb - 1) / tb, 4 * num_sms, kRopeBwdMaxCtas});
   cudaError_t e = cudaSuccess;
-  if (grid > 0) e = launch(rope_bwd_kernel<T, D>, dim3(grid), kThreads, stream, a, tb);
+  if (grid > 0) e = launch(rope_bwd_kernel<T, D, kStyle>, dim3(grid), kThreads, stream, a, tb);
   if (e == cudaSuccess && (a.dq_weight != nullptr || a.dk_weight != nullptr))
-    e = launch(rope_dweight_kernel, dim3(D / 32, 2), 256, stream,
+    e = launch(rope_dweight_kernel, dim3(D / 32, 2), kSumWarps * 32, stream,
                static_cast<const float *>(a.partial), grid, D, a.dq_weight, a.dk_weight);
   return e;
+}
+
+template <typename T, int D>
+cudaError_t rope(const RopeArgs &a, int mode, int num_sms, cudaStream_t stream) {
+  if (a.style == kRopeHalves)
+    return mode < 2 ? fwd<T, D, kRopeHalves>(a, mode == 1, num_sms, stream)
+                    : bwd<T, D, kRopeHalves>(a, num_sms, stream);
+  return mode < 2 ? fwd<T, D, kRopeInterleaved>(a, mode == 1, num_sms, stream)
+                  : bwd<T, D, kRopeInterleaved>(a, num_sms, stream);
+}
+
+// mode: 0 forward, 1 append, 2 backward
+cudaError_t rope_of(const RopeArgs &a, int d, int dtype, int mode, int num_sms,
+                    cudaStream_t stream) {
+  if (dtype == 0)
+    return d == 64 ? rope<float, 64>(a, mode, num_sms, stream)
+                   : rope<float, 128>(a, mode, num_sms, stream);
+  return d == 64 ? rope<__nv_bfloat16, 64>(a, mode, num_sms, stream)
+                 : rope<__nv_bfloat16, 128>(a, mode, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_fwd(const RopeArgs &a, int d, int dtype, bool append, int num_sms,
                             cudaStream_t stream) {
-  if (dtype == 0)
-    return d == 64 ? fwd<float, 64>(a, append, num_sms, stream)
-                   : fwd<float, 128>(a, append, num_sms, stream);
-  return d == 64 ? fwd<__nv_bfloat16, 64>(a, append, num_sms, stream)
-                 : fwd<__nv_bfloat16, 128>(a, append, num_sms, stream);
+  return rope_of(a, d, dtype, append ? 1 : 0, num_sms, stream);
 }
 
 cudaError_t launch_rope_bwd(const RopeArgs &a, int d, int dtype, int num_sms, cudaStream_t stream) {
-  if (dtype == 0)
-    return d == 64 ? bwd<float, 64>(a, num_sms, stream) : bwd<float, 128>(a, num_sms, stream);
-  return d == 64 ? bwd<__nv_bfloat16, 64>(a, num_sms, stream)
-                 : bwd<__nv_bfloat16, 128>(a, num_sms, stream);
+  return rope_of(a, d, dtype, 2, num_sms, stream);
 }
 
 }  // namespace mha

@@ -10,7 +10,7 @@ import contextlib
 import ctypes
 
 from .mha import (MHA_DTYPE_BF16, MHA_DTYPE_F32, MHA_LAYOUT_BHSD, MHA_LAYOUT_BSHD,
-                  MHA_MASK_CAUSAL_TAIL, MHA_OK, MhaError, _workspace_bytes, lib)
+                  MHA_MASK_CAUSAL_TAIL, MHA_OK, MhaError, lib)
 
 MHA_ROPE_HALVES, MHA_ROPE_INTERLEAVED = 0, 1
 PAGED_PATH_NAMES = {0: "none", 1: "paged_simt", 2: "paged_few_tc", 3: "paged_many_tc"}
@@ -66,9 +66,13 @@ def _layout_of(layout: str) -> int:
     raise ValueError("layout must be 'bhsd' or 'bshd'")
 
 
+# These checks run on every call of a generation step, where they weigh as much as
+# the kernels: plain attribute reads, the device by its number (-1: not CUDA).
 def _like(name, t, ref, shape):
-    """A tensor of the call: contiguous, on ref's device, of ref's dtype and ``shape``."""
-    if t.shape != shape or t.dtype != ref.dtype or t.device != ref.device or not t.is_cuda or \
+    """Address of a tensor of the call: contiguous, on ref's device, of ref's dtype
+    and ``shape``."""
+    dev = t.get_device()
+    if t.shape != shape or t.dtype != ref.dtype or dev < 0 or dev != ref.get_device() or \
             not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s CUDA tensor of shape %s on %s"
                          % (name, ref.dtype, tuple(shape), ref.device))
@@ -76,14 +80,24 @@ def _like(name, t, ref, shape):
 
 
 def _array(name, t, ref, dtype, shape):
-    """An int32 or float32 array of the call, or None; its address."""
+    """Address of an int32 or float32 array of the call, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != ref.device or not t.is_cuda or \
+    dev = t.get_device()
+    if t.shape != shape or t.dtype != dtype or dev < 0 or dev != ref.get_device() or \
             not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s CUDA tensor of shape %s on %s"
                          % (name, dtype, tuple(shape), ref.device))
     return t.data_ptr()
+
+
+def _scratch(t, ref):
+    """(address, bytes) of a workspace, or (None, 0)."""
+    if t is None:
+        return None, 0
+    if t.get_device() < 0 or t.get_device() != ref.get_device() or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _weight(name, t, ref):
@@ -110,20 +124,27 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
-def _call(name, device, stream, args):
+def _call(name, ref, stream, args):
     import torch
-    fn = getattr(lib, name)
+    dev = ref.get_device()
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = _current_stream(dev)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, handle)
+    if torch.cuda.current_device() == dev:
+        st = getattr(lib, name)(*args, handle)
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, handle)
+        with torch.cuda.device(dev):
+            st = getattr(lib, name)(*args, handle)
     if st != MHA_OK:
         raise MhaError(st, name)
+
+
+def _current_stream(dev: int) -> int:
+    """Handle of torch's current stream on device ``dev``."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public call's time
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _head_rows(q, k, layout):
@@ -171,7 +192,7 @@ def mha_qk_norm_rope_fwd(q, k, q_out=None, k_out=None, *, q_weight=None, k_weigh
             _weight("k_weight", k_weight, ref),
             _array("positions", positions, ref, torch.int32, (B, L)), freq, B, H, Hkv, L, d,
             rotary, lay, int(bool(interleaved)), float(eps), dtype)
-    _call("mha_qk_norm_rope_fwd", ref.device, stream, args)
+    _call("mha_qk_norm_rope_fwd", ref, stream, args)
     return q_out, k_out
 
 
@@ -198,15 +219,16 @@ def mha_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq=None, dk=None, dq_weight=None,
     weights = q_weight is not None or k_weight is not None
     if q_weight is None and dq_weight is not None or k_weight is None and dk_weight is not None:
         raise ValueError("dq_weight and dk_weight go with q_weight and k_weight")
-    with _on(stream, ref.device):
-        dq = torch.empty_like(dq_out) if dq is None and dq_out is not None else dq
-        dk = torch.empty_like(dk_out) if dk is None and dk_out is not None else dk
-        new = lambda: torch.empty(d, dtype=torch.float32, device=ref.device)  # noqa: E731
-        dq_weight = new() if dq_weight is None and q_weight is not None else dq_weight
-        dk_weight = new() if dk_weight is None and k_weight is not None else dk_weight
-        if workspace is None and weights:
-            workspace = torch.empty(max(mha_qk_norm_rope_bwd_workspace_size(d), 1),
-                                    dtype=torch.uint8, device=ref.device)
+    if any(t is None for t in (dq, dk, dq_weight, dk_weight, workspace)):
+        with _on(stream, ref.device):
+            dq = torch.empty_like(dq_out) if dq is None and dq_out is not None else dq
+            dk = torch.empty_like(dk_out) if dk is None and dk_out is not None else dk
+            new = lambda: torch.empty(d, dtype=torch.float32, device=ref.device)  # noqa: E731
+            dq_weight = new() if dq_weight is None and q_weight is not None else dq_weight
+            dk_weight = new() if dk_weight is None and k_weight is not None else dk_weight
+            if workspace is None and weights:
+                workspace = torch.empty(max(mha_qk_norm_rope_bwd_workspace_size(d), 1),
+                                        dtype=torch.uint8, device=ref.device)
     addr = lambda name, t, shape: None if t is None else _like(name, t, ref, shape)  # noqa: E731
     for name, x, w, shape in (("q", q, q_weight, qs), ("k", k, k_weight, ks)):
         if x is None and w is not None and 0 not in shape:
@@ -219,9 +241,8 @@ def mha_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq=None, dk=None, dq_weight=None,
             _weight("q_weight", q_weight, ref), _weight("k_weight", k_weight, ref),
             _array("positions", positions, ref, torch.int32, (B, L)), freq, B, H, Hkv, L, d,
             rotary, lay, int(bool(interleaved)), float(eps), dtype,
-            workspace.data_ptr() if workspace is not None else None,
-            _workspace_bytes(workspace, ref.device) if workspace is not None else 0)
-    _call("mha_qk_norm_rope_bwd", ref.device, stream, args)
+            *_scratch(workspace, ref))
+    _call("mha_qk_norm_rope_bwd", ref, stream, args)
     return dq, dk, dq_weight, dk_weight
 
 
@@ -279,7 +300,7 @@ def mha_paged_append(q, k, v, k_cache, v_cache, q_out=None, *, q_starts, kv_leng
             _weight("q_weight", q_weight, k), _weight("k_weight", k_weight, k), freq, *arrays, B, T,
             H, Hkv, d, pages, page, max_pages, rotary, lay, int(bool(interleaved)), float(eps),
             dtype)
-    _call("mha_paged_append", k.device, stream, args)
+    _call("mha_paged_append", k, stream, args)
     return q_out
 
 
@@ -326,6 +347,6 @@ def mha_paged_fwd(q, k_cache, v_cache, out=None, *, q_starts, kv_lengths, block_
         scale = float(d) ** -0.5
     args = (_like("q", q, q, (T, H, d)), kc, vc, _like("out", out, q, (T, H, d)), *arrays, B, T, H,
             Hkv, d, max_q, pages, page, max_pages, lay, int(mask_kind), float(scale), dtype,
-            workspace.data_ptr(), _workspace_bytes(workspace, q.device))
-    _call("mha_paged_fwd", q.device, stream, args)
+            *_scratch(workspace, q))
+    _call("mha_paged_fwd", q, stream, args)
     return out
