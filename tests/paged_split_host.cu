@@ -97,11 +97,6 @@ extern "C" void seq(const int32_t *starts, const int32_t *lens, int T, int page_
   out[3] = s.base;
 }
 
-extern "C" int seq_of_row(const int32_t *starts, int B, int T, int t) {
-  const PagedProblem p = problem(starts, nullptr, nullptr, B, T, 1, 1, 1, 1, 1, 0, 4, 0, 0);
-  return paged_seq_of_row(p.batch, t);
-}
-
 // Units of a sequence: their lengths' prefix sums by the closed form, and the unit
 // at each boundary; returns 0 when they agree with sums and a plain search.
 extern "C" int unit_sums(const int32_t *starts, const int32_t *lens, int T, int tb, int causal,

@@ -85,7 +85,7 @@ def test_rope_rejects_before_launch(mha):
                dict(qw=P[4] + 4), dict(qo=P[0] + 16), dict(qo=P[1]), dict(ko=P[0]),
                dict(ko=P[2] + 64), dict(qo=P[6]), dict(ko=P[7]), dict(qo=P[4]), dict(qo=P[5])):
         assert rope_fwd(mha, **kw) == E_ARG, kw
-    for kw in (dict(d=96), dict(d=256), dict(rot=24), dict(B=1 << 16, L=1 << 15),
+    for kw in (dict(d=96), dict(d=256), dict(rot=24), dict(B=1 << 16, L=1 << 15), dict(B=1, L=(1 << 31) - 1000),
                dict(H=1 << 30, Hkv=0, B=1 << 10, L=1 << 20)):
         assert rope_fwd(mha, **kw) == E_UNS, kw
     for kw in (dict(B=0), dict(L=0), dict(H=0, Hkv=0)):
@@ -448,21 +448,6 @@ def test_lengths_out_of_range_are_clamped(host):
     assert seq([0, 5], [2 ** 31 - 1], 10) == [0, 5, 64, 2 ** 31 - 6]
     assert seq([0, 5], [30], 10, max_pages=0) == [0, 5, 0, 25]
     assert seq([-2 ** 31, 2 ** 31 - 1], [2 ** 31 - 1], 10, 2 ** 31 - 1)[:3] == [0, 10, 2 ** 31 - 1]
-
-
-def test_rows_find_their_sequence(host):
-    starts = [2, 2, 5, 5, 5, 9, 9]
-    (a, ap) = i32(starts)
-    got = [host.seq_of_row(ap, 6, 12, t) for t in range(12)]
-    assert got == [-1, -1, 1, 1, 1, 4, 4, 4, 4, -1, -1, -1]
-    assert host.seq_of_row(ap, 0, 12, 3) == -1
-    rng = np.random.default_rng(0)
-    for _ in range(200):  # any numbers: the sequence found holds the row, by its own limits
-        st = rng.integers(-5, 20, 7)
-        (a, ap) = i32(st)
-        for t in range(15):
-            b = host.seq_of_row(ap, 6, 15, t)
-            assert b == -1 or (0 <= b < 6 and st[b] <= t < st[b + 1])
 
 
 def test_cells_of_bad_pages_are_absent(host):

@@ -375,6 +375,33 @@ def test_append_and_attend_agree_on_positions_outside_the_rows():
     assert kc.float().abs().sum() == k.float().abs().sum()
 
 
+@pytest.mark.parametrize("B", [1, 2, 31, 32, 33, 700, 1500])
+def test_every_row_finds_its_sequence(B):
+    # ragged and empty sequences, rows of none: each key tells where it should lie
+    import torch
+    import transformer_head_scaled_mha_gb300 as mha
+    rng = np.random.default_rng(B)
+    n = rng.integers(0, 4, B) * rng.integers(0, 2, B)
+    n[rng.integers(0, B)] += 3
+    starts = (2 + np.concatenate([[0], np.cumsum(n)])).astype(np.int32)
+    T = int(starts[-1]) + 3
+    lens = (n + rng.integers(0, 40, B)).astype(np.int32)
+    table = rng.permutation(B * 4).reshape(B, 4).astype(np.int32)
+    k = torch.arange(1, T + 1, device="cuda", dtype=torch.float32)[:, None, None].expand(T, 1, 64)
+    k = k.contiguous()
+    kc, vc = (torch.zeros(B * 4, 16, 1, 64, device="cuda") for _ in range(2))
+    mha.mha_paged_append(None, k, k, kc, vc, q_starts=dev(starts), kv_lengths=dev(lens),
+                         block_table=dev(table), layout="bshd")
+    want = np.zeros((B * 4, 16))
+    for b in range(B):
+        for i in range(n[b]):
+            p = lens[b] - n[b] + i
+            want[table[b, p // 16], p % 16] = 1 + starts[b] + i
+    for c in (kc, vc):
+        c = c.cpu().numpy()
+        assert np.all(c == c[..., :1]) and np.array_equal(c[:, :, 0, 0], want)
+
+
 # ---------------------------------------------------------------------------
 # a run of them together
 # ---------------------------------------------------------------------------

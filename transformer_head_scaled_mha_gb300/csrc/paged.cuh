@@ -112,19 +112,6 @@ MHA_HD int paged_kv_end(const PagedSeq &s, int i1, int causal) {
   return max(min(s.base + i1, s.len), 0);
 }
 
-// Sequence of row t: the last one that starts at or before it; -1 when the row
-// belongs to none.
-MHA_HD int paged_seq_of_row(const PagedBatch &p, int t) {
-  int lo = 0, hi = p.B;  // q_starts[lo] <= t < q_starts[hi], if the arrays are in order
-  if (p.B <= 0 || t < p.q_starts[0] || t >= p.q_starts[p.B]) return -1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.q_starts[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 // ---- the split of the units' keys over CTAs --------------------------------
 // Units are laid on a line, each as long as its work (in 1/256 of a key tile):
 // head block by head block, for each all sequences, for each its token blocks.

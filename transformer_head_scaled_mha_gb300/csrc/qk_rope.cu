@@ -6,12 +6,14 @@
 //   n = x w / sqrt(mean x^2 + eps)          (skipped without a weight)
 //   (y_a, y_b) = (n_a c - n_b s, n_a s + n_b c),  c, s = cos, sin(p f_i)
 //
-// Bound: HBM (about 10 flop per element against 2 x 2 bytes).  d * sizeof(T) / 16
-// lanes hold a row, 16 bytes each in two pieces, so a row is read and written once and its sums are shuffles within those lanes.  A CTA takes `tb` tokens
-// and walks their heads, queries then keys (then values); the angles of a token are
-// formed once, into shared memory, and serve all its heads.  The first rows are on
-// their way before the angles are formed, and every row's load is issued kAhead
-// rows before it is needed.
+// Bound: HBM (about 10 flop per element against 2 x 2 bytes), then the instructions
+// issued per row.  d * sizeof(T) / 16 lanes hold a row, 16 bytes each in two pieces,
+// so a row is read and written once and its sums are shuffles within those lanes;
+// a warp holds 1, 2 or 4 rows at a time.  A warp takes one token, or a share of its
+// rows, forms the token's angles once, in registers, and walks the token's heads,
+// queries then keys (then values), four warp-rows in flight.  No shared memory and
+// no barrier: what a CTA-wide table of angles costs in waiting and bookkeeping is
+// more than computing an angle per lane and token.
 //
 // Angles: with the frequency in turns as a 64-bit binary fraction F =
 // frac(f / 2 pi) 2^64, the position times F modulo 2^64 is the angle's fraction of
@@ -30,8 +32,9 @@
 namespace mha {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 16;  // tokens of a CTA at most
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kFwdCtas = 3, kBwdCtas = 2;  // per SM
 
 // 16 bytes of a row, as a lane holds them: two pieces of 8 bytes.
 template <typename T>
@@ -67,6 +70,27 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
+// Two fp32 in one 64-bit register, multiplied and added by one instruction: the
+// backward's rows are bound by instructions issued (65 -> 59 us on 8192 tokens of
+// 32 + 8 heads, d 128; the forward gains nothing and spills).  Subnormal values are
+// kept.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return a + b;
+}
+
 // Plain loads that the compiler may not move to the read-only path: a row may be
 // overwritten in place.
 __device__ __forceinline__ uint4 ld8x2(const void *lo, const void *hi) {
@@ -80,10 +104,20 @@ __device__ __forceinline__ void st8x2(void *lo, void *hi, uint4 v) {
   asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(hi), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// frequency i as a 64-bit fraction of a turn per position
+// frac(f / 2 pi) 2^64 for f = m 2^e: m times 2^66 / 2 pi (rounded to 64 bits), shifted
 __device__ __forceinline__ unsigned long long turn_fraction(float f) {
-  const double t = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
-  return static_cast<unsigned long long>((t - floor(t)) * 18446744073709551616.0);
+  constexpr unsigned long long k = 11743562013128004906ull;  // 2^66 / (2 pi)
+  const uint32_t bits = __float_as_uint(f);
+  const int exp = (bits >> 23) & 255;
+  const unsigned long long m = (bits & 0x7fffffu) | (exp != 0 ? 0x800000u : 0u);
+  const int right = 2 - ((exp != 0 ? exp : 1) - 150);  // bits to drop of the 88-bit product
+  const unsigned long long lo = m * k, hi = __umul64hi(m, k);
+  unsigned long long v;
+  if (right >= 128) v = 0;
+  else if (right >= 64) v = hi >> (right - 64);
+  else if (right > 0) v = (hi << (64 - right)) | (lo >> right);
+  else v = right > -64 ? lo << -right : 0;
+  return (bits >> 31) != 0 ? 0 - v : v;
 }
 
 __device__ __forceinline__ float2 angle_cos_sin(int pos, unsigned long long fraction) {
@@ -104,30 +138,71 @@ __device__ __forceinline__ Rows rows_of(int layout, int t, int heads, int L, int
   return {(static_cast<long long>(b) * heads * L + l) * d, static_cast<long long>(L) * d};
 }
 
-// A lane's place in a row.  Both elements of a rotated pair belong to one lane:
-// with MHA_ROPE_HALVES lane l of the rotated ones holds a piece of kN / 2 elements
+// How the kernels see the rotation: the two styles for any rotary_dim, and halves
+// over the whole head, where the pieces' distance is a constant.
+enum Style { kHalves = 0, kInterleaved = 1, kWholeHalves = 2 };
+
+// A lane's place in a row, and its elements as kTwos packed twos of first elements a
+// and of second elements b of its pairs.  Both elements of a rotated pair belong to
+// one lane: with halves lane l of the rotated ones holds a piece of kN / 2 elements
 // from each half, pair i being elements (i, i + kN / 2) of the lane's kN; otherwise
 // the pieces lie side by side and pair i is (2 i, 2 i + 1).
-template <typename T, int kStyle>
+template <typename T, int D, int kStyle>
 struct Place {
-  static constexpr int kN = Vec<T>::kN, kPairs = kN / 2;
-  int lo, hi;  // first elements of the two pieces
-  int freq;    // first pair's frequency
-  bool on;     // rotated (rotary is a multiple of 16: all of a lane's pairs are, or none)
+  static constexpr int kN = Vec<T>::kN, kPairs = kN / 2, kTwos = kPairs / 2;
+  int lo;     // first element of the first piece
+  int apart;  // from there to the second piece
+  int freq;   // first pair's frequency
+  bool on;    // rotated (rotary is a multiple of 16: all of a lane's pairs are, or none)
   __device__ __forceinline__ Place(int col, int rotary) {
-    on = col * kN < rotary;
+    on = kStyle == kWholeHalves || col * kN < rotary;
     freq = col * kPairs;
-    lo = kStyle == kRopeHalves && on ? col * kPairs : col * kN;
-    hi = kStyle == kRopeHalves && on ? (rotary >> 1) + col * kPairs : col * kN + kPairs;
+    lo = kStyle != kInterleaved && on ? col * kPairs : col * kN;
+    apart = kStyle == kWholeHalves ? D / 2
+                                   : (kStyle == kHalves && on ? rotary >> 1 : kPairs);
+    if (kStyle == kInterleaved) apart = kPairs;
   }
+  __device__ __forceinline__ uint4 load(const T *row) const {
+    return ld8x2(row + lo, row + lo + apart);
+  }
+  __device__ __forceinline__ void store(T *row, uint4 v) const {
+    st8x2(row + lo, row + lo + apart, v);
+  }
+  // which of the lane's elements pair i's are
   static __device__ __forceinline__ constexpr int a(int i) {
-    return kStyle == kRopeHalves ? i : 2 * i;
+    return kStyle == kInterleaved ? 2 * i : i;
   }
   static __device__ __forceinline__ constexpr int b(int i) {
-    return kStyle == kRopeHalves ? i + kPairs : 2 * i + 1;
+    return kStyle == kInterleaved ? 2 * i + 1 : i + kPairs;
   }
-  __device__ __forceinline__ uint4 load(const T *row) const { return ld8x2(row + lo, row + hi); }
-  __device__ __forceinline__ void store(T *row, uint4 v) const { st8x2(row + lo, row + hi, v); }
+  // element of the row that a[i] (second: b[i]) holds
+  __device__ __forceinline__ int element(int i, bool second) const {
+    return kStyle == kInterleaved ? lo + 2 * i + second : lo + i + (second ? apart : 0);
+  }
+  static __device__ __forceinline__ void unpack(uint4 v, uint64_t (&a)[kTwos],
+                                                uint64_t (&b)[kTwos]) {
+    float x[kN];
+    Vec<T>::unpack(v, x);
+#pragma unroll
+    for (int i = 0; i < kTwos; ++i) {
+      constexpr bool kSide = kStyle == kInterleaved;
+      a[i] = kSide ? f2_pack(x[4 * i], x[4 * i + 2]) : f2_pack(x[2 * i], x[2 * i + 1]);
+      b[i] = kSide ? f2_pack(x[4 * i + 1], x[4 * i + 3])
+                   : f2_pack(x[kPairs + 2 * i], x[kPairs + 2 * i + 1]);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const uint64_t (&a)[kTwos],
+                                               const uint64_t (&b)[kTwos]) {
+    float x[kN];
+#pragma unroll
+    for (int i = 0; i < kTwos; ++i) {
+      constexpr bool kSide = kStyle == kInterleaved;
+      f2_unpack(a[i], x[kSide ? 4 * i : 2 * i], x[kSide ? 4 * i + 2 : 2 * i + 1]);
+      f2_unpack(b[i], x[kSide ? 4 * i + 1 : kPairs + 2 * i],
+                x[kSide ? 4 * i + 3 : kPairs + 2 * i + 1]);
+    }
+    return Vec<T>::pack(x);
+  }
 };
 
 template <int kLanes>
@@ -137,147 +212,137 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-struct TokenInfo {
-  long long cell;  // appending: cache row of head 0, or -1
-  int pos;
-  int live;
+// cos and sin of a lane's pairs.  A warp's kGroups row groups need the same angles:
+// each forms its share, and they pass them around.
+template <typename T, int D>
+struct Angles {
+  static constexpr int kN = Vec<T>::kN, kPairs = kN / 2, kLanes = D / kN, kGroups = 32 / kLanes;
+  static constexpr int kOwn = kPairs / kGroups;
+  static_assert(kOwn >= 1, "a lane forms at least one angle");
+  unsigned long long turns[kOwn];
+  uint64_t c[kPairs / 2], s[kPairs / 2];
+  // lanes outside the rotation keep angle 0
+  __device__ __forceinline__ void frequencies(const float *inv_freq, int first, bool on, int group) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      turns[i] = on ? turn_fraction(inv_freq[first + group * kOwn + i]) : 0ull;
+  }
+  __device__ __forceinline__ void at(int pos, int col) {
+    float2 own[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) own[i] = angle_cos_sin(pos, turns[i]);
+    float x[kPairs], y[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      x[i] = __shfl_sync(0xffffffffu, own[i % kOwn].x, (i / kOwn) * kLanes + col);
+      y[i] = __shfl_sync(0xffffffffu, own[i % kOwn].y, (i / kOwn) * kLanes + col);
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs / 2; ++i) {
+      c[i] = f2_pack(x[2 * i], x[2 * i + 1]);
+      s[i] = f2_pack(y[2 * i], y[2 * i + 1]);
+    }
+  }
 };
 
-template <typename T, int D, int kStyle, bool kAppend>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a, int tb) {
-  using P = Place<T, kStyle>;
-  constexpr int kN = Vec<T>::kN, kPairs = kN / 2, kLanes = D / kN, kSlots = kThreads / kLanes;
-  constexpr int kAhead = 4;
-  __shared__ float2 cs[kMaxTokens][D / 2];
-  __shared__ unsigned long long turns[D / 2];
-  __shared__ TokenInfo info[kMaxTokens];
-  griddep_launch_dependents();
-  const int col = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
-  const int tok = slot % tb, h0 = slot / tb, hstep = kSlots / tb;
-  const int t0 = blockIdx.x * tb, t = t0 + tok;
-  const P place(col, a.rotary);
-  const int rounds_q = (a.H + hstep - 1) / hstep, rounds_k = (a.Hkv + hstep - 1) / hstep;
-  const int rows = rounds_q + (kAppend ? 2 : 1) * rounds_k;
-  const int layout = kAppend ? kLayoutBSHD : a.layout;
-  const Rows rq = rows_of(layout, t, a.H, a.L, D), rk = rows_of(layout, t, a.Hkv, a.L, D);
-  // element offsets of a slot's first row and between its rows
-  const long long q0 = rq.base + h0 * rq.step, dq = hstep * rq.step;
-  const long long k0 = rk.base + h0 * rk.step, dk = hstep * rk.step;
-  // where the next row to load lies
-  const T *src = static_cast<const T *>(a.q) + q0;
-  int lj = 0, lh = h0;
-  auto load = [&]() {
-    if (lj == rounds_q || (kAppend && lj == rounds_q + rounds_k)) {
-      src = static_cast<const T *>(lj == rounds_q ? a.k : a.v) + k0;
-      lh = h0;
-    }
-    const bool q = lj < rounds_q;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (lj < rows && t < a.tokens && lh < (q ? a.H : a.Hkv)) v = place.load(src);
-    src += q ? dq : dk;
-    lh += hstep;
-    ++lj;
-    return v;
-  };
-  griddep_wait();
-  uint4 raw[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) raw[i] = load();
-  const int half = a.rotary >> 1;
-  if (threadIdx.x >= kThreads - half) {
-    const int f = threadIdx.x - (kThreads - half);
-    turns[f] = turn_fraction(a.inv_freq[f]);
+// Sequence of row t (whole warp): the last one that starts at or before it, -1 when
+// the row belongs to none.  32 offsets are looked at a time; q_starts[lo] <= t <
+// q_starts[hi] holds throughout, whatever the numbers.
+__device__ __forceinline__ int seq_of_row(const PagedBatch &p, int t, int lane) {
+  int lo = 0, hi = p.B;
+  if (t < p.q_starts[0] || t >= p.q_starts[p.B]) return -1;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const unsigned below = __ballot_sync(0xffffffffu, at < hi && p.q_starts[min(at, hi)] <= t);
+    const int last = 31 - __clz(below | 1u);
+    lo += last * step;
+    hi = min(lo + step, hi);
   }
-  if (threadIdx.x < tb) {
-    const int u = t0 + threadIdx.x;
-    TokenInfo ti{-1, 0, 0};
-    if (u < a.tokens) {
-      if (kAppend) {
-        const int b = paged_seq_of_row(a.batch, u);
-        if (b >= 0) {
-          // tokens up to the sequence's end count back from its length
-          const int end = min(a.batch.q_starts[b + 1], a.tokens);
-          ti.live = 1;
-          ti.pos = max(a.batch.kv_lengths[b], 0) - (end - u);
-          ti.cell = paged_cell(a.batch, b, ti.pos, 0, a.Hkv);
-        }
-      } else {
-        ti.live = 1;
-        ti.pos = a.positions != nullptr ? a.positions[u] : u % a.L;
-      }
-    }
-    info[threadIdx.x] = ti;
+  return lo;
+}
+
+// A warp's work.  A token's rows come in rounds of kGroups heads: q's rounds, then
+// k's, then, when appending, v's.  The warps take equal stretches of all tokens'
+// rounds, so that a token count that does not fill the last pass over the SMs costs
+// nothing; a warp forms the angles of each token that its stretch touches.
+struct Stretch {
+  long long at, end;
+  __device__ __forceinline__ Stretch(long long total, int warp, int warps) {
+    const long long each = total / warps, over = total % warps;
+    at = each * warp + over * warp / warps;
+    end = each * (warp + 1) + over * (warp + 1) / warps;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < tb * half; i += kThreads) {
-    const int k = i / half, f = i - k * half;
-    cs[k][f] = angle_cos_sin(info[k].pos, turns[f]);
+  // the next token and its rounds [lo, hi) of `rounds`; false at the end
+  __device__ __forceinline__ bool next(int rounds, int &token, int &lo, int &hi) {
+    if (at >= end) return false;
+    const long long t = at <= 0x7fffffff ? static_cast<int>(at) / rounds : at / rounds;
+    token = static_cast<int>(t);
+    lo = static_cast<int>(at - t * rounds);
+    hi = static_cast<int>(min(static_cast<long long>(rounds), lo + (end - at)));
+    at += hi - lo;
+    return true;
   }
-  __syncthreads();
-  const bool live = info[tok].live != 0;
-  const long long cell = info[tok].cell;
-  float c[kPairs], s[kPairs];
-#pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    const float2 v = place.on ? cs[tok][place.freq + i] : make_float2(1.f, 0.f);
-    c[i] = v.x;
-    s[i] = v.y;
-  }
-  // where the row goes, and this tensor's factors: y_a = r (a ca - b sb),
-  // y_b = r (a sa + b cb), with the weight in them
-  T *dst = static_cast<T *>(a.q_out) + q0;
-  long long step = dq;
-  int h = h0, heads = a.H;
-  bool writes = live, normed = false, copies = false;
+};
+
+// Norms and rotates (or, kCopy, copies) rounds [from, to) of one tensor.  Row h lies
+// at src + h * in and goes to dst + h * out.
+template <typename T, int D, int kStyle, bool kCopy>
+__device__ __forceinline__ void fwd_rows(const T *src, long long in, T *dst, long long out,
+                                         int heads, int from, int to, int group, bool live,
+                                         const Place<T, D, kStyle> &place, const T *weight, float eps,
+                                         const Angles<T, D> &ang) {
+  using P = Place<T, D, kStyle>;
+  using A = Angles<T, D>;
+  constexpr int kN = P::kN, kPairs = P::kPairs, kBatch = 4;
+  if (from >= to) return;
+  // y_a = r (a ca - b sb), y_b = r (a sa + b cb), the weight in the factors
   float ca[kPairs], sb[kPairs], sa[kPairs], cb[kPairs];
-  for (int j0 = 0; j0 < rows; j0 += kAhead) {
+  const bool normed = !kCopy && weight != nullptr;
+  int h = from * A::kGroups + group;
+  src += h * in;
+  dst += h * out;
+  in *= A::kGroups;
+  out *= A::kGroups;
+  uint4 raw[kBatch];
+  auto load = [&](int j) {
+    const T *row = src;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i;
-      if (j >= rows) break;
-      uint4 v = raw[i];
-      raw[i] = load();
-      if (j == 0 || j == rounds_q || (kAppend && j == rounds_q + rounds_k)) {
-        const bool q = j < rounds_q;
-        copies = kAppend && j == rounds_q + rounds_k;
-        if (!q) {
-          h = h0;
-          heads = a.Hkv;
-          dst = static_cast<T *>(copies ? a.v_out : a.k_out);
-          if (kAppend) {
-            const long long per = a.batch.layout == kLayoutBHSD
-                                      ? static_cast<long long>(a.batch.page_size) * D
-                                      : D;
-            writes = live && cell >= 0;
-            dst += cell * D + h0 * per;
-            step = hstep * per;
-          } else {
-            dst += k0;
-            step = dk;
-          }
-        }
-        const T *weight = static_cast<const T *>(q ? a.q_weight : a.k_weight);
-        normed = weight != nullptr && !copies;
-        float w[kN];
-        if (normed) Vec<T>::unpack(place.load(weight), w);
+    for (int i = 0; i < kBatch; ++i) {
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (live && j + i < to && h + i * A::kGroups < heads) raw[i] = place.load(row);
+      row += in;
+    }
+    src = row;
+  };
+  load(from);
+  if (!kCopy) {
+    float w[kN];
+    if (normed) Vec<T>::unpack(place.load(weight), w);
 #pragma unroll
-        for (int e = 0; e < kPairs; ++e) {
-          const float wa = normed ? w[P::a(e)] : 1.f, wb = normed ? w[P::b(e)] : 1.f;
-          ca[e] = c[e] * wa;
-          sb[e] = s[e] * wb;
-          sa[e] = s[e] * wa;
-          cb[e] = c[e] * wb;
-        }
-      }
-      if (!kAppend || !copies) {
+    for (int e = 0; e < kPairs; ++e) {
+      float c0, c1, s0, s1;
+      f2_unpack(ang.c[e / 2], c0, c1);
+      f2_unpack(ang.s[e / 2], s0, s1);
+      const float c = e % 2 == 0 ? c0 : c1, s = e % 2 == 0 ? s0 : s1;
+      const float wa = normed ? w[P::a(e)] : 1.f, wb = normed ? w[P::b(e)] : 1.f;
+      ca[e] = c * wa;
+      sb[e] = s * wb;
+      sa[e] = s * wa;
+      cb[e] = c * wb;
+    }
+  }
+  for (int j = from; j < to; j += kBatch) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (!kCopy) {
         float y[kN];
-        Vec<T>::unpack(v, y);
+        Vec<T>::unpack(raw[i], y);
         float r = 1.f;
         if (normed) {
           float sq = 0.f;
 #pragma unroll
           for (int e = 0; e < kN; ++e) sq = fmaf(y[e], y[e], sq);
-          r = rsqrtf(row_sum<kLanes>(sq) * (1.f / D) + a.eps);
+          r = rsqrtf(row_sum<A::kLanes>(sq) * (1.f / D) + eps);
         }
 #pragma unroll
         for (int e = 0; e < kPairs; ++e) {
@@ -290,152 +355,206 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a, in
           y[P::a(e)] = oa * r;
           y[P::b(e)] = ob * r;
         }
-        v = Vec<T>::pack(y);
+        raw[i] = Vec<T>::pack(y);
       }
-      if (writes && h < heads) place.store(dst, v);
-      dst += step;
-      h += hstep;
+      if (live && j + i < to && h + i * A::kGroups < heads) place.store(dst, raw[i]);
+      dst += out;
     }
+    h += kBatch * A::kGroups;
+    if (j + kBatch < to) load(j + kBatch);
+  }
+}
+
+template <typename T, int D, int kStyle, bool kAppend>
+__global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const RopeArgs a, int warps) {
+  using A = Angles<T, D>;
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = lane % A::kLanes, group = lane / A::kLanes;
+  const Place<T, D, kStyle> place(col, a.rotary);
+  const int rq = (a.H + A::kGroups - 1) / A::kGroups, rk = (a.Hkv + A::kGroups - 1) / A::kGroups;
+  const int rounds = rq + (kAppend ? 2 : 1) * rk;
+  const int w = blockIdx.x * kWarps + warp;
+  griddep_wait();
+  if (w >= warps) return;
+  A ang;
+  ang.frequencies(a.inv_freq, place.freq, place.on, group);
+  Stretch stretch(static_cast<long long>(a.tokens) * rounds, w, warps);
+  int t, lo, hi;
+  while (stretch.next(rounds, t, lo, hi)) {
+    int pos = 0, seq = 0;
+    bool live = true;
+    if (kAppend) {
+      seq = seq_of_row(a.batch, t, lane);
+      live = seq >= 0;
+      // tokens up to the sequence's end count back from its length
+      if (live)
+        pos = max(a.batch.kv_lengths[seq], 0) - (min(a.batch.q_starts[seq + 1], a.tokens) - t);
+    } else {
+      pos = a.positions != nullptr ? a.positions[t] : t % a.L;
+    }
+    ang.at(pos, col);
+    const int layout = kAppend ? kLayoutBSHD : a.layout;
+    const Rows q = rows_of(layout, t, a.H, a.L, D), k = rows_of(layout, t, a.Hkv, a.L, D);
+    fwd_rows<T, D, kStyle, false>(static_cast<const T *>(a.q) + q.base, q.step,
+                                  static_cast<T *>(a.q_out) + q.base, q.step, a.H, lo,
+                                  min(hi, rq), group, live, place,
+                                  static_cast<const T *>(a.q_weight), a.eps, ang);
+    Rows to = k;
+    if (kAppend) {
+      const long long cell = live ? paged_cell(a.batch, seq, pos, 0, a.Hkv) : -1;
+      live = cell >= 0;
+      to.base = cell * D;
+      to.step = a.batch.layout == kLayoutBHSD ? static_cast<long long>(a.batch.page_size) * D : D;
+    }
+    fwd_rows<T, D, kStyle, false>(static_cast<const T *>(a.k) + k.base, k.step,
+                                  static_cast<T *>(a.k_out) + to.base, to.step, a.Hkv,
+                                  max(lo - rq, 0), min(hi - rq, rk), group, live, place,
+                                  static_cast<const T *>(a.k_weight), a.eps, ang);
+    if (kAppend)
+      fwd_rows<T, D, kStyle, true>(static_cast<const T *>(a.v) + k.base, k.step,
+                                   static_cast<T *>(a.v_out) + to.base, to.step, a.Hkv,
+                                   max(lo - rq - rk, 0), hi - rq - rk, group, live, place,
+                                   nullptr, 0.f, ang);
+  }
+}
+
+// Gradients of rounds [from, to) of one tensor; this lane's share of the weight's
+// gradient is added to dw.
+template <typename T, int D, int kStyle>
+__device__ __forceinline__ void bwd_rows(const T *x_in, const T *dy, T *dx, long long step,
+                                         int heads, int from, int to, int group,
+                                         const Place<T, D, kStyle> &place, const T *weight, float eps,
+                                         const Angles<T, D> &ang,
+                                         uint64_t (&da)[Place<T, D, kStyle>::kTwos],
+                                         uint64_t (&db)[Place<T, D, kStyle>::kTwos]) {
+  using P = Place<T, D, kStyle>;
+  using A = Angles<T, D>;
+  constexpr int kTwos = P::kTwos, kBatch = 2;
+  if (from >= to) return;
+  const bool normed = weight != nullptr;
+  uint64_t wa[kTwos], wb[kTwos];
+  if (normed) P::unpack(place.load(weight), wa, wb);
+  int h = from * A::kGroups + group;
+  x_in += h * step;
+  dy += h * step;
+  dx += h * step;
+  step *= A::kGroups;
+  uint4 raw_x[kBatch], raw_g[kBatch];
+  auto load = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      raw_x[i] = raw_g[i] = make_uint4(0, 0, 0, 0);
+      if (j + i < to && h + i * A::kGroups < heads) {
+        raw_g[i] = place.load(dy);
+        if (normed) raw_x[i] = place.load(x_in);
+      }
+      dy += step;
+      x_in += step;
+    }
+  };
+  load(from);
+  for (int j = from; j < to; j += kBatch) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const bool is = j + i < to && h + i * A::kGroups < heads;
+      uint64_t ga[kTwos], gb[kTwos];
+      P::unpack(raw_g[i], ga, gb);
+      if (place.on) {
+#pragma unroll
+        for (int e = 0; e < kTwos; ++e) {
+          const uint64_t a = ga[e], b = gb[e];
+          ga[e] = fma2(b, ang.s[e], mul2(a, ang.c[e]));
+          gb[e] = fma2(mul2(a, both(-1.f)), ang.s[e], mul2(b, ang.c[e]));
+        }
+      }
+      if (normed) {
+        uint64_t xa[kTwos], xb[kTwos], va[kTwos], vb[kTwos];
+        P::unpack(raw_x[i], xa, xb);
+        uint64_t sq2 = 0ull, dot2 = 0ull;
+#pragma unroll
+        for (int e = 0; e < kTwos; ++e) {
+          va[e] = mul2(ga[e], wa[e]);
+          vb[e] = mul2(gb[e], wb[e]);
+          sq2 = fma2(xb[e], xb[e], fma2(xa[e], xa[e], sq2));
+          dot2 = fma2(vb[e], xb[e], fma2(va[e], xa[e], dot2));
+        }
+        const float sq = row_sum<A::kLanes>(sum2(sq2)), dot = row_sum<A::kLanes>(sum2(dot2));
+        const float inv = rsqrtf(sq * (1.f / D) + eps);
+        // minus inv^2 times the mean of (w g) x
+        const uint64_t m = both(-(dot * (1.f / D)) * inv * inv), i2 = both(inv);
+        const uint64_t add = both(is ? inv : 0.f);  // an absent row adds nothing (its inv may be infinite)
+#pragma unroll
+        for (int e = 0; e < kTwos; ++e) {
+          da[e] = fma2(ga[e], mul2(xa[e], add), da[e]);
+          db[e] = fma2(gb[e], mul2(xb[e], add), db[e]);
+          ga[e] = mul2(i2, fma2(xa[e], m, va[e]));
+          gb[e] = mul2(i2, fma2(xb[e], m, vb[e]));
+        }
+      }
+      if (is) place.store(dx, P::pack(ga, gb));
+      dx += step;
+    }
+    h += kBatch * A::kGroups;
+    if (j + kBatch < to) load(j + kBatch);
   }
 }
 
 template <typename T, int D, int kStyle>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeArgs a, int tb) {
-  using P = Place<T, kStyle>;
-  constexpr int kN = Vec<T>::kN, kPairs = kN / 2, kLanes = D / kN, kSlots = kThreads / kLanes;
-  constexpr int kAhead = 2;
-  __shared__ float2 cs[kMaxTokens][D / 2];
-  __shared__ unsigned long long turns[D / 2];
-  __shared__ float sums[kSlots][D];
+__global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const RopeArgs a, int warps) {
+  using A = Angles<T, D>;
+  using P = Place<T, D, kStyle>;
+  __shared__ float sums[kWarps * A::kGroups][D];
   griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = lane % A::kLanes, group = lane / A::kLanes;
+  const Place<T, D, kStyle> place(col, a.rotary);
+  const int rq = (a.H + A::kGroups - 1) / A::kGroups, rk = (a.Hkv + A::kGroups - 1) / A::kGroups;
+  const int w = blockIdx.x * kWarps + warp;
+  uint64_t qa[P::kTwos], qb[P::kTwos], ka[P::kTwos], kb[P::kTwos];  // the weights' gradients
+#pragma unroll
+  for (int e = 0; e < P::kTwos; ++e) qa[e] = qb[e] = ka[e] = kb[e] = 0ull;
   griddep_wait();
-  const int col = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
-  const int tok = slot % tb, h0 = slot / tb, hstep = kSlots / tb;
-  const int half = a.rotary >> 1;
-  const P place(col, a.rotary);
-  const int rounds_q = (a.H + hstep - 1) / hstep;
-  const int rows = rounds_q + (a.Hkv + hstep - 1) / hstep;
-  // this lane's share of the weights' gradients: of the tensor at hand, and of the other
-  float dw[kN], other[kN];
-#pragma unroll
-  for (int e = 0; e < kN; ++e) dw[e] = other[e] = 0.f;
-  if (threadIdx.x < half) turns[threadIdx.x] = turn_fraction(a.inv_freq[threadIdx.x]);
-  const int tiles = (a.tokens + tb - 1) / tb;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int t0 = tile * tb, t = t0 + tok;
-    const Rows rq = rows_of(a.layout, t, a.H, a.L, D), rk = rows_of(a.layout, t, a.Hkv, a.L, D);
-    long long from = rq.base + h0 * rq.step, to = from;  // next row to load, to store
-    int lj = 0, lh = h0, h = h0;
-    uint4 raw_x[kAhead], raw_g[kAhead];
-    auto load = [&](int i) {
-      if (lj == rounds_q) {
-        from = rk.base + h0 * rk.step;
-        lh = h0;
-      }
-      const bool q = lj < rounds_q;
-      raw_x[i] = raw_g[i] = make_uint4(0, 0, 0, 0);
-      if (lj < rows && t < a.tokens && lh < (q ? a.H : a.Hkv)) {
-        raw_g[i] = place.load(static_cast<const T *>(q ? a.dq_out : a.dk_out) + from);
-        if ((q ? a.q_weight : a.k_weight) != nullptr)
-          raw_x[i] = place.load(static_cast<const T *>(q ? a.q : a.k) + from);
-      }
-      from += hstep * (q ? rq.step : rk.step);
-      lh += hstep;
-      ++lj;
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(i);
-    __syncthreads();  // the tile before has read cs; turns are written
-    for (int i = threadIdx.x; i < tb * half; i += kThreads) {
-      const int k = i / half, f = i - k * half;
-      const int u = min(t0 + k, a.tokens - 1);
-      const int pos = a.positions != nullptr ? a.positions[u] : u % a.L;
-      cs[k][f] = angle_cos_sin(pos, turns[f]);
-    }
-    __syncthreads();
-    float c[kPairs], s[kPairs], w[kN];
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const float2 v = place.on ? cs[tok][place.freq + i] : make_float2(1.f, 0.f);
-      c[i] = v.x;
-      s[i] = v.y;
-    }
-    bool normed = false;
-    auto turn = [&]() {
-#pragma unroll
-      for (int e = 0; e < kN; ++e) {
-        const float v = dw[e];
-        dw[e] = other[e];
-        other[e] = v;
-      }
-    };
-    for (int j0 = 0; j0 < rows; j0 += kAhead) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int j = j0 + i;
-        if (j >= rows) break;
-        const bool q = j < rounds_q;
-        if (j == rounds_q) {
-          to = rk.base + h0 * rk.step;
-          h = h0;
-          turn();
-        }
-        if (j == 0 || j == rounds_q) {
-          const T *weight = static_cast<const T *>(q ? a.q_weight : a.k_weight);
-          normed = weight != nullptr;
-          if (normed) Vec<T>::unpack(place.load(weight), w);
-        }
-        float g[kN], x[kN];
-        Vec<T>::unpack(raw_g[i], g);
-        Vec<T>::unpack(raw_x[i], x);
-        load(i);
-        const bool is = t < a.tokens && h < (q ? a.H : a.Hkv);
-        if (place.on) {
-#pragma unroll
-          for (int e = 0; e < kPairs; ++e) {
-            const float ga = g[P::a(e)], gb = g[P::b(e)];
-            g[P::a(e)] = fmaf(gb, s[e], ga * c[e]);
-            g[P::b(e)] = fmaf(-ga, s[e], gb * c[e]);
-          }
-        }
-        if (normed) {
-          float sq = 0.f, dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < kN; ++e) {
-            sq = fmaf(x[e], x[e], sq);
-            dot = fmaf(g[e] * w[e], x[e], dot);
-          }
-          sq = row_sum<kLanes>(sq);
-          dot = row_sum<kLanes>(dot);
-          const float inv = rsqrtf(sq * (1.f / D) + a.eps);
-          const float mean = dot * inv * (1.f / D);  // mean of (w g) (x inv)
-          const float add = is ? inv : 0.f;  // an absent row adds nothing (its inv may be infinite)
-#pragma unroll
-          for (int e = 0; e < kN; ++e) {
-            dw[e] = fmaf(g[e], x[e] * add, dw[e]);
-            g[e] = inv * (g[e] * w[e] - x[e] * inv * mean);
-          }
-        }
-        if (is) place.store(static_cast<T *>(q ? a.q_out : a.k_out) + to, Vec<T>::pack(g));
-        to += hstep * (q ? rq.step : rk.step);
-        h += hstep;
-      }
-    }
-    if (rounds_q < rows) turn();  // q's again
+  A ang;
+  ang.frequencies(a.inv_freq, place.freq, place.on, group);
+  // (a warp past the last has an empty stretch: it still joins the sums)
+  Stretch stretch(static_cast<long long>(a.tokens) * (rq + rk), min(w, warps - 1), warps);
+  if (w >= warps) stretch.at = stretch.end;
+  int t, lo, hi;
+  while (stretch.next(rq + rk, t, lo, hi)) {
+    ang.at(a.positions != nullptr ? a.positions[t] : t % a.L, col);
+    const Rows q = rows_of(a.layout, t, a.H, a.L, D), k = rows_of(a.layout, t, a.Hkv, a.L, D);
+    bwd_rows<T, D, kStyle>(static_cast<const T *>(a.q) + q.base,
+                           static_cast<const T *>(a.dq_out) + q.base,
+                           static_cast<T *>(a.q_out) + q.base, q.step, a.H, lo, min(hi, rq),
+                           group, place, static_cast<const T *>(a.q_weight), a.eps, ang, qa, qb);
+    bwd_rows<T, D, kStyle>(static_cast<const T *>(a.k) + k.base,
+                           static_cast<const T *>(a.dk_out) + k.base,
+                           static_cast<T *>(a.k_out) + k.base, k.step, a.Hkv, max(lo - rq, 0),
+                           hi - rq, group, place, static_cast<const T *>(a.k_weight), a.eps,
+                           ang, ka, kb);
   }
-  // this CTA's sums over its row slots, in a fixed order
+  // this CTA's sums over its row groups, in a fixed order
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if ((which == 0 ? a.q_weight : a.k_weight) == nullptr) continue;
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < kN; ++e)
-      sums[slot][(e < kPairs ? place.lo : place.hi) + e % kPairs] = which == 0 ? dw[e] : other[e];
+    for (int e = 0; e < P::kTwos; ++e) {
+      float *row = sums[warp * A::kGroups + group];
+      float x, y;
+      f2_unpack(which == 0 ? qa[e] : ka[e], x, y);
+      row[place.element(2 * e, false)] = x;
+      row[place.element(2 * e + 1, false)] = y;
+      f2_unpack(which == 0 ? qb[e] : kb[e], x, y);
+      row[place.element(2 * e, true)] = x;
+      row[place.element(2 * e + 1, true)] = y;
+    }
     __syncthreads();
     if (threadIdx.x < D) {
       float v = 0.f;
 #pragma unroll
-      for (int k = 0; k < kSlots; ++k) v += sums[k][threadIdx.x];
+      for (int k = 0; k < kWarps * A::kGroups; ++k) v += sums[k][threadIdx.x];
       a.partial[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + threadIdx.x] = v;
     }
   }
@@ -482,48 +601,54 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Tokens per CTA: more share a CTA, and its angles' latency, while a row slot has
-// fewer than 8 rows and the SMs keep several CTAs each.
-int tokens_per_cta(int tokens, int heads, int slots, int num_sms) {
-  int tb = 1;
-  while (tb < std::min(kMaxTokens, slots) && tb * heads < 8 * slots &&
-         tokens / (2 * tb) >= 4 * num_sms)
-    tb *= 2;
-  return tb;
+template <typename T, int D>
+int rounds(int heads) {
+  constexpr int g = Angles<T, D>::kGroups;
+  return (heads + g - 1) / g;
 }
 
-template <typename T, int D>
-constexpr int slots() {
-  return kThreads / (D / Vec<T>::kN);
+// Warps for a number of rounds: the `resident` ones, but no more than leave each two.
+int warps_of(long long total, int resident) {
+  return static_cast<int>(std::max(std::min<long long>((total + 1) / 2, resident), 1LL));
 }
 
 template <typename T, int D, int kStyle>
 cudaError_t fwd(const RopeArgs &a, bool append, int num_sms, cudaStream_t stream) {
-  const int tb = tokens_per_cta(a.tokens, a.H + (append ? 2 : 1) * a.Hkv, slots<T, D>(), num_sms);
-  const dim3 grid((a.tokens + tb - 1) / tb);
-  return append ? launch(rope_fwd_kernel<T, D, kStyle, true>, grid, kThreads, stream, a, tb)
-                : launch(rope_fwd_kernel<T, D, kStyle, false>, grid, kThreads, stream, a, tb);
+  const long long total =
+      static_cast<long long>(a.tokens) *
+      (rounds<T, D>(a.H) + (append ? 2 : 1) * rounds<T, D>(a.Hkv));
+  const int warps = warps_of(total, kFwdCtas * kWarps * num_sms);
+  const dim3 grid((warps + kWarps - 1) / kWarps);
+  return append ? launch(rope_fwd_kernel<T, D, kStyle, true>, grid, kThreads, stream, a, warps)
+                : launch(rope_fwd_kernel<T, D, kStyle, false>, grid, kThreads, stream, a, warps);
 }
 
 template <typename T, int D, int kStyle>
 cudaError_t bwd(const RopeArgs &a, int num_sms, cudaStream_t stream) {
-  const int tb = tokens_per_cta(a.tokens, a.H + a.Hkv, slots<T, D>(), num_sms);
-  const int grid = std::min({(a.tokens + tb - 1) / tb, 4 * num_sms, kRopeBwdMaxCtas});
+  const long long total =
+      static_cast<long long>(a.tokens) * (rounds<T, D>(a.H) + rounds<T, D>(a.Hkv));
+  const int warps =
+      warps_of(total, std::min(kBwdCtas * num_sms, kRopeBwdMaxCtas) * kWarps);
+  const int grid = total > 0 ? (warps + kWarps - 1) / kWarps : 0;
   cudaError_t e = cudaSuccess;
-  if (grid > 0) e = launch(rope_bwd_kernel<T, D, kStyle>, dim3(grid), kThreads, stream, a, tb);
+  if (grid > 0) e = launch(rope_bwd_kernel<T, D, kStyle>, dim3(grid), kThreads, stream, a, warps);
   if (e == cudaSuccess && (a.dq_weight != nullptr || a.dk_weight != nullptr))
     e = launch(rope_dweight_kernel, dim3(D / 32, 2), kSumWarps * 32, stream,
                static_cast<const float *>(a.partial), grid, D, a.dq_weight, a.dk_weight);
   return e;
 }
 
+template <typename T, int D, int kStyle>
+cudaError_t rope_style(const RopeArgs &a, int mode, int num_sms, cudaStream_t stream) {
+  return mode < 2 ? fwd<T, D, kStyle>(a, mode == 1, num_sms, stream)
+                  : bwd<T, D, kStyle>(a, num_sms, stream);
+}
+
 template <typename T, int D>
 cudaError_t rope(const RopeArgs &a, int mode, int num_sms, cudaStream_t stream) {
-  if (a.style == kRopeHalves)
-    return mode < 2 ? fwd<T, D, kRopeHalves>(a, mode == 1, num_sms, stream)
-                    : bwd<T, D, kRopeHalves>(a, num_sms, stream);
-  return mode < 2 ? fwd<T, D, kRopeInterleaved>(a, mode == 1, num_sms, stream)
-                  : bwd<T, D, kRopeInterleaved>(a, num_sms, stream);
+  if (a.style == kRopeInterleaved) return rope_style<T, D, kInterleaved>(a, mode, num_sms, stream);
+  return a.rotary == D ? rope_style<T, D, kWholeHalves>(a, mode, num_sms, stream)
+                       : rope_style<T, D, kHalves>(a, mode, num_sms, stream);
 }
 
 // mode: 0 forward, 1 append, 2 backward
