@@ -22,7 +22,7 @@ PagedProblem problem(const int32_t *starts, const int32_t *lens, const int32_t *
   p.tb = tb;
   p.causal = causal;
   p.rows = hpu * tb;
-  p.min_stretch = 4;
+  p.split = PagedSplit{kTileCost * 3 / 2, 2, 4};
   return p;
 }
 }  // namespace
@@ -36,7 +36,7 @@ static PagedSpan span_of(const PagedProblem &p, int cta, int grid) {
       one += paged_unit_cost(p, s, paged_blocks(p, s), u);
   }
   const int hbs = p.Hkv * p.hblocks;
-  PagedSpan sp = paged_stretch(one * hbs, units * hbs, cta, grid, p.min_stretch);
+  PagedSpan sp = paged_stretch(one * hbs, units * hbs, cta, grid, p.split.min_stretch);
   long long s = 0;
   for (int hb = 0; hb < hbs; ++hb)
     for (int b = 0; b < p.batch.B; ++b) {
@@ -109,7 +109,7 @@ extern "C" int unit_sums(const int32_t *starts, const int32_t *lens, int T, int 
   for (int u = 0; u < blocks; ++u) {
     const long long cost = paged_unit_cost(p, s, blocks, u);
     if (paged_cost_before(p, s, blocks, u) != sum) return 1 + u;
-    if (cost < kUnitCost) return -1;
+    if (cost < p.split.unit_cost) return -1;
     if (paged_unit_at(p, s, blocks, sum) != u || paged_unit_at(p, s, blocks, sum + cost - 1) != u)
       return -2 - u;
     sum += cost;

@@ -55,6 +55,16 @@ constexpr int kPagedTile = 128;     // keys per tile: the unit that work is spli
 constexpr int kPagedMaxCtas = 608;      // CTAs that may hold partial sums, at most 16 rows per unit
 constexpr int kPagedManyMaxCtas = 192;  // ... 256 rows per unit
 
+constexpr int kTileCost = 256;  // 2^8: shifts below
+static_assert(kTileCost == 1 << 8, "tile cost");
+
+// How a kernel's work is split, in key tiles.
+struct PagedSplit {
+  int unit_cost;    // a unit's own work (queries, first and last tile, output), in 1/256 tile
+  int min_part;     // tiles of a part at least
+  int min_stretch;  // tiles of work below which a CTA is not worth having
+};
+
 // A unit of attention work: `tb` consecutive new tokens of one sequence times
 // `hpu` query heads of one key/value head's group.  Row r of a unit is head
 // r / tb of its heads, token r % tb of its tokens.
@@ -64,7 +74,7 @@ struct PagedProblem {
   int hpu, hblocks;   // query heads per unit; units that cover a group's heads
   int tb;             // tokens per unit
   int causal;
-  int min_stretch;   // tiles of work below which a CTA is not worth having
+  PagedSplit split;
   float scale_log2;  // scale * log2(e)
   const void *q, *k, *v;
   void *out;
@@ -117,7 +127,7 @@ MHA_HD int paged_kv_end(const PagedSeq &s, int i1, int causal) {
 // head block by head block, for each all sequences, for each its token blocks.
 // CTA c of G takes the stretch [c X / G, (c + 1) X / G) of the line, X its length;
 // a unit's keys are cut where a stretch ends inside it, unless that leaves a part
-// of under kMinPart tiles.  G is at most the grid, and no larger than leaves every
+// of under `min_part` tiles.  G is at most the grid, and no larger than leaves every
 // CTA `min_stretch` tiles or, if that is more, one unit each.
 //
 // Heads come first because every head's piece of the line is alike: with G a
@@ -125,17 +135,12 @@ MHA_HD int paged_kv_end(const PagedSeq &s, int i1, int causal) {
 // at about the same time, and in the [page, position, head, d] layout those lie
 // side by side in memory (66 -> 58 us on 256 sequences of 128 to 1024 keys, 8
 // heads, d 64).
-constexpr int kTileCost = 256;
-// a unit's own work -- queries, sums, output -- costs about 1.5 tiles
-constexpr int kUnitCost = kTileCost * 3 / 2;
-constexpr int kMinPart = 2;
-
 // tiles of a unit before offset x (> 0) of its piece of the line
-MHA_HD int paged_cut(long long x, int nt) {
+MHA_HD int paged_cut(const PagedSplit &sp, long long x, int nt) {
   if (x <= 0) return 0;
-  const long long t = (x - kUnitCost + kTileCost / 2) / kTileCost;
-  if (t < kMinPart) return 0;
-  if (t > nt - kMinPart) return nt;
+  const long long t = (x - sp.unit_cost + kTileCost / 2) >> 8;
+  if (t < sp.min_part) return 0;
+  if (t > nt - sp.min_part) return nt;
   return static_cast<int>(t);
 }
 
@@ -153,13 +158,15 @@ struct PagedSpan {
 MHA_HD PagedSpan paged_stretch(long long total, long long units, int cta, int grid,
                                int min_stretch) {
   PagedSpan sp;
-  const long long by_work = total / (static_cast<long long>(min_stretch) * kTileCost);
+  const long long by_work = static_cast<int>(total >> 8 > 0x7fffffff ? 0x7fffffff : total >> 8) / min_stretch;  // kTileCost is 2^8
   const long long most = by_work > units ? by_work : units;
   sp.ctas = static_cast<int>(most < 1 ? 1 : (most < grid ? most : grid));
-  // total * cta / ctas without the product of the two
-  const long long each = total / sp.ctas, over = total % sp.ctas;
-  sp.lo = cta < sp.ctas ? each * cta + over * cta / sp.ctas : total;
-  sp.hi = cta < sp.ctas ? each * (cta + 1) + over * (cta + 1) / sp.ctas : total;
+  // equal stretches, a little short (the last CTA takes what is left, some millionths):
+  // an approximate quotient, for a 64-bit division is a hundred instructions
+  const long long each = static_cast<long long>(static_cast<float>(total) /
+                                                static_cast<float>(sp.ctas) * 0.999999f);
+  sp.lo = cta < sp.ctas ? each * cta : total;
+  sp.hi = cta + 1 < sp.ctas ? each * (cta + 1) : total;
   sp.s = total;
   sp.hb = sp.b = sp.u = 0;
   return sp;
@@ -176,23 +183,30 @@ MHA_HD int paged_blocks_end(const PagedProblem &p, const PagedSeq &s, int u) {
 }
 MHA_HD long long paged_unit_cost(const PagedProblem &p, const PagedSeq &s, int blocks, int u) {
   const long long keys = paged_kv_end(s, paged_blocks_end(p, s, u), p.causal);
-  if (blocks == 1) return kUnitCost + (keys + kPagedTile - 1) / kPagedTile * kTileCost;
-  return kUnitCost + kTileCost / 2 + keys * (kTileCost / kPagedTile);
+  if (blocks == 1) return p.split.unit_cost + (keys + kPagedTile - 1) / kPagedTile * kTileCost;
+  return p.split.unit_cost + kTileCost / 2 + keys * (kTileCost / kPagedTile);
 }
 // Length of the units before u (0 <= u <= blocks) of a sequence.
 MHA_HD long long paged_cost_before(const PagedProblem &p, const PagedSeq &s, int blocks, int u) {
   if (blocks <= 1) return u > 0 ? paged_unit_cost(p, s, blocks, 0) : 0;
-  const long long fixed = kUnitCost + kTileCost / 2, per_key = kTileCost / kPagedTile;
+  const long long fixed = p.split.unit_cost + kTileCost / 2, per_key = kTileCost / kPagedTile;
   if (!p.causal) return u * (fixed + per_key * s.len);
   // units before the last see base + (v + 1) tb keys, held to [0, len]
-  const long long full = u < blocks ? u : blocks - 1;
-  const long long tb = p.tb, base = s.base, len = s.len;
-  long long lo = base < 0 ? -base / tb : 0;  // units that see nothing
-  if (lo > full) lo = full;
-  long long hi = len - base > 0 ? (len - base - 1) / tb : 0;  // ... and from here on, all of len
-  if (hi > full) hi = full;
+  const int full = u < blocks ? u : blocks - 1;
+  const unsigned tb = static_cast<unsigned>(p.tb);
+  int lo = s.base < 0 ? static_cast<int>((0u - static_cast<unsigned>(s.base)) / tb) : 0;
+  if (lo > full) lo = full;  // units that see nothing
+  // ... and from `hi` on, all of len
+  const unsigned room = s.len > s.base
+                            ? static_cast<unsigned>(s.len) - static_cast<unsigned>(s.base) - 1u
+                            : 0u;
+  int hi = s.len > s.base && room / tb < static_cast<unsigned>(full) ? static_cast<int>(room / tb)
+           : s.len > s.base                                          ? full
+                                                                     : 0;
   if (hi < lo) hi = lo;
-  long long keys = (hi - lo) * base + tb * ((hi - lo) * (hi + lo + 1) / 2) + (full - hi) * len;
+  const long long some = hi - lo;
+  long long keys = some * s.base + ((some * (hi + lo + 1)) >> 1) * p.tb +
+                   static_cast<long long>(full - hi) * s.len;
   if (u == blocks) keys += paged_kv_end(s, s.n, 1);
   return u * fixed + per_key * keys;
 }
@@ -245,9 +259,14 @@ __device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long l
     all_units += scratch[16 + w];
   }
   const int hbs = p.Hkv * p.hblocks;
-  PagedSpan sp = paged_stretch(one * hbs, all_units * hbs, cta, grid, p.min_stretch);
+  PagedSpan sp = paged_stretch(one * hbs, all_units * hbs, cta, grid, p.split.min_stretch);
   const bool any = sp.lo < one * hbs;
-  const int hb = any ? static_cast<int>(sp.lo / one) : hbs;
+  int hb = hbs;
+  if (any) {  // sp.lo / one, from an approximate quotient
+    hb = static_cast<int>(static_cast<float>(sp.lo) / static_cast<float>(one));
+    while (hb > 0 && hb * one > sp.lo) --hb;
+    while ((hb + 1) * one <= sp.lo) ++hb;
+  }
   const long long at = any ? sp.lo - hb * one : 0, first = before + inc - mine;
   if (any && at >= first && at < first + mine) {  // one thread of the block
     long long s = first;
@@ -334,8 +353,8 @@ struct PagedWalk {
       const long long from = at;
       at += paged_unit_cost(p, seq, blocks, u);
       ++u;
-      part.t0 = paged_cut(sp.lo - from, part.nt);
-      part.t1 = sp.hi < at ? paged_cut(sp.hi - from, part.nt) : part.nt;
+      part.t0 = paged_cut(p.split, sp.lo - from, part.nt);
+      part.t1 = sp.hi < at ? paged_cut(p.split, sp.hi - from, part.nt) : part.nt;
       if (part.nt == 0) {  // nothing to attend to: zeros, by the CTA that holds its beginning
         if (from >= sp.lo) return true;
         continue;

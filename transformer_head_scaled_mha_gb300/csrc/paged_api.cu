@@ -117,6 +117,7 @@ enum PagedPath { kNone = 0, kSimt = 1, kFew = 2, kMany = 3 };
 // Units of work of a kernel (PagedProblem): heads, tokens, and its CTAs at most.
 struct Units {
   int hpu, hblocks, tb, rows, ctas;
+  PagedSplit split;
 };
 
 int paged_path(int B, int T, int H, int H_kv, int d, int max_q, int dtype) {
@@ -140,6 +141,7 @@ Units units_of(int path, int group, int max_q) {
   u.tb = path == kMany ? 2 * (rows / u.hpu) : std::min(rows / u.hpu, max_q);
   u.rows = u.hpu * u.tb;
   u.ctas = path == kMany ? kPagedManyMaxCtas : kPagedMaxCtas;
+  u.split = path == kMany ? PagedSplit{kTileCost * 4, 3, 6} : PagedSplit{kTileCost * 3 / 2, 2, 4};
   return u;
 }
 
@@ -412,7 +414,7 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   p.status = dev.status;
   p.wait_ns = wait_limit_ns();
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  p.min_stretch = 4;
+  p.split = u.split;
   int grid = u.ctas;
   cudaError_t err = cudaSuccess;
   if (path == kSimt) {
@@ -436,10 +438,10 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
       err = launch_paged_few(qm, km, vm, p, d, grid, dev.sms, stream);
     }
   }
-  // a unit is cut only when both parts have kMinPart tiles: not where the block
+  // a unit is cut only when both parts have min_part tiles: not where the block
   // table has no room for them
   const long long most = static_cast<long long>(max_pages) * page_size;
-  if (err == cudaSuccess && most > (2 * kMinPart - 1) * kPagedTile)
+  if (err == cudaSuccess && most > (2 * u.split.min_part - 1) * kPagedTile)
     err = launch_paged_merge(p, d, dtype, grid, stream);
   return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }

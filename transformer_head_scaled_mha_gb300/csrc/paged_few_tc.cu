@@ -168,7 +168,8 @@ __device__ __forceinline__ bool take_desc(Shared<RP> *sh, int n, Desc &d, uint64
 
 template <int D, int RP>
 __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
-    paged_few_tc_kernel(const __grid_constant__ FewMaps maps, const PagedProblem p) {
+    paged_few_tc_kernel(const __grid_constant__ FewMaps maps,
+                        const __grid_constant__ PagedProblem p) {
   using C = Cfg<D, RP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(

@@ -50,9 +50,9 @@ constexpr int kBN = kPagedTile;
 constexpr int kThreads = 384;
 constexpr int kWgThreads = 128;
 // Register split: 384 threads launched at 168 each; the control warpgroup drops
-// to 88 and the softmax warpgroups rise to 208: 2 x 128 x 208 + 128 x 88 = 384 x 168.
-constexpr uint32_t kRegsSoftmax = 208;
-constexpr uint32_t kRegsControl = 88;
+// to 72 and the softmax warpgroups rise to 216: 2 x 128 x 216 + 128 x 72 = 384 x 168.
+constexpr uint32_t kRegsSoftmax = 216;
+constexpr uint32_t kRegsControl = 72;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsControl <= kThreads * 168, "register split");
 constexpr uint32_t kTmemCols = 512;        // S_w at 128 w, O_w at 256 + 128 w
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -165,29 +165,6 @@ __device__ __noinline__ void rescale_p16(uint32_t taddr, float f) {
   tmem_st16(taddr, r);
 }
 
-// N lanes with N 16-byte pieces of a row each: lane l ends with piece l of all N
-// rows (v[k]: of lane k's), so that N lanes store N x 16 bytes side by side.  Storing
-// each lane's own row instead touches 32 lines per instruction.
-template <int N>
-__device__ __forceinline__ void swap_rows(uint4 (&v)[N], int lane) {
-#pragma unroll
-  for (int s = N / 2; s > 0; s >>= 1) {
-    const bool up = (lane & s) != 0;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      if (k & s) continue;
-      const uint4 give = up ? v[k] : v[k + s];
-      uint4 got;
-      got.x = __shfl_xor_sync(0xffffffffu, give.x, s);
-      got.y = __shfl_xor_sync(0xffffffffu, give.y, s);
-      got.z = __shfl_xor_sync(0xffffffffu, give.z, s);
-      got.w = __shfl_xor_sync(0xffffffffu, give.w, s);
-      if (up) v[k] = got;
-      else v[k + s] = got;
-    }
-  }
-}
-
 // Stores the warp's 32 rows of O (TMEM o0 times a0, plus TMEM o1 times a1): as fp32
 // to rows `mine` of a slot of sums, or as bf16 to rows `mine` of out (-1: no row of
 // ours).  kNoTmem stands for zeros; `none`: this lane's row is zeros whatever TMEM
@@ -195,7 +172,7 @@ __device__ __forceinline__ void swap_rows(uint4 (&v)[N], int lane) {
 constexpr uint32_t kNoTmem = 0xffffffffu;
 template <int D>
 __device__ __forceinline__ void store_rows(uint32_t o0, uint32_t o1, float a0, float a1, bool none,
-                                           int mine, float *slot, uint16_t *out, int lane) {
+                                           int mine, float *slot, uint16_t *out) {
 #pragma unroll 1
   for (int c0 = 0; c0 < D; c0 += 32) {
     uint32_t o[32];
@@ -220,36 +197,20 @@ __device__ __forceinline__ void store_rows(uint32_t o0, uint32_t o1, float a0, f
         }
       }
     }
-    if (slot != nullptr) {
-      uint4 f[8];
+    if (mine >= 0 && slot != nullptr) {
+      float *to = slot + static_cast<size_t>(mine) * D + c0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        f[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-      swap_rows(f, lane);
-      slot += (lane & 7) * 4 + c0;
+      for (int e = 0; e < 32; e += 4)
+        st_global_v4(to + e, make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+    } else if (mine >= 0) {
+      uint16_t *to = out + static_cast<size_t>(mine) * D + c0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int to = __shfl_sync(0xffffffffu, mine, (lane & 24) + k);
-        if (to >= 0) st_global_v4(slot + static_cast<size_t>(to) * D, f[k]);
-      }
-      slot -= (lane & 7) * 4 + c0;
-    } else {
-      uint4 q[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int e = 0; e < 32; e += 8) {
         uint32_t v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[e] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * e]),
-                             __uint_as_float(o[8 * k + 2 * e + 1]));
-        q[k] = make_uint4(v[0], v[1], v[2], v[3]);
-      }
-      swap_rows(q, lane);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int to = __shfl_sync(0xffffffffu, mine, (lane & 28) + k);
-        if (to >= 0)
-          st_global_v4(out + static_cast<size_t>(to) * D + c0 + (lane & 3) * 8, q[k]);
+        for (int k = 0; k < 4; ++k)
+          v[k] = pack_bf16x2(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
+        st_global_v4(to + e, make_uint4(v[0], v[1], v[2], v[3]));
       }
     }
   }
@@ -257,7 +218,8 @@ __device__ __forceinline__ void store_rows(uint32_t o0, uint32_t o1, float a0, f
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_many_tc_kernel(const __grid_constant__ ManyMaps maps, const PagedProblem p) {
+    paged_many_tc_kernel(const __grid_constant__ ManyMaps maps,
+                         const __grid_constant__ PagedProblem p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -325,112 +287,143 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slab = loads ? lane / pieces : 0;
       const int dst0 = slab * C::kBlkBytes + piece * box * 128;
       const uint32_t whole = (1u << pieces) - 1;
-      PagedWalk walk;
-      walk.begin(p, span);
-      PagedPart part;
+      // Lane 0 walks, one part ahead of the loads, so that the other roles find the
+      // next part's description when they get there.  The walk and the two parts live
+      // in shared memory (where the span was found), out of this warpgroup's few
+      // registers.
+      PagedWalk &walk = *reinterpret_cast<PagedWalk *>(&sh->scratch[0]);
+      PagedPart *const two = reinterpret_cast<PagedPart *>(&sh->scratch[14]);
+      static_assert(sizeof(PagedWalk) <= 14 * 8 && 14 * 8 + 2 * sizeof(PagedPart) <= 32 * 8,
+                    "where they live");
+      if (lane == 0) walk.begin(p, span);
       int n = 0, flags = 0, mseq = 0, mtok = 0, mhead = 0;
-      bool ok = true;
-      for (;;) {
-        const bool more = walk.next(p, part);
+      bool ok = true, more = false;
+      // the next part, into two[n & 1], and its description
+      auto advance = [&]() {
+        PagedPart &part = two[n & 1];
+        bool got = lane == 0 && walk.next(p, part);
+        got = __any_sync(0xffffffffu, got);
         ok = mbar_wait_warp(&sh->desc_empty[n % kDescs], ((n / kDescs) & 1) ^ 1, abort_flag,
                             p.wait_ns);
-        if (!ok) break;
-        const bool split = more && paged_split(part);
-        const int tokens = part.i1 - part.i0;
-        const bool both = tokens <= tbw;
+        if (!ok) return;
         if (lane == 0) {
+          const bool split = got && paged_split(part);
           Desc d;
-          d.go = more;
+          d.go = got;
           d.tiles = part.t1 - part.t0;
           const int end0 = paged_kv_end(part.seq, min(part.i0 + tbw, part.i1), p.causal);
           d.tiles0 = max(min((end0 + kBN - 1) / kBN, part.t1) - part.t0, 0);
-          d.both = both;
+          d.both = part.i1 - part.i0 <= tbw;
           d.key0 = part.t0 * kBN;
           d.kv_end = part.kv_end;
           d.lim0 = p.causal ? part.seq.base + part.i0 + 1 : part.seq.len;
           d.lim_step = p.causal;
           d.row0 = part.seq.q0 + part.i0;
-          d.tokens = tokens;
+          d.tokens = part.i1 - part.i0;
           d.heads = part.heads;
           d.h0 = part.h0;
           d.slot = split ? paged_slot(part) : -1;
           sh->desc[n % kDescs] = d;
           mbar_arrive(&sh->desc_full[n % kDescs]);
+          if (split) {
+            if (part.t0 > 0) {
+              flags |= kPartContinues | (part.t1 == part.nt ? kPartEnds : 0);
+              mseq = part.b;
+              mtok = part.i0;
+              mhead = part.h0;
+            } else {
+              flags |= kPartBegins;
+            }
+          }
         }
         __syncwarp();
+        more = got;
         ++n;
-        if (!more) break;
-        if (split) {
-          if (part.t0 > 0) {
-            flags |= kPartContinues | (part.t1 == part.nt ? kPartEnds : 0);
-            mseq = part.b;
-            mtok = part.i0;
-            mhead = part.h0;
-          } else {
-            flags |= kPartBegins;
-          }
-        }
-        if (part.nt == 0) continue;
-        ok = mbar_wait_warp(&sh->q_empty, (q_issued & 1) ^ 1, abort_flag, p.wait_ns);
-        if (!ok) break;
-        if (lane == 0) {
-          const int halves = both ? 1 : 2;
-          mbar_arrive_expect_tx(&sh->q_full,
-                                static_cast<uint32_t>(halves * C::kSlabs * tbw * p.hpu * 128));
-          for (int w = 0; w < halves; ++w)
-            for (int blk = 0; blk < C::kSlabs; ++blk)
-              tma_load_4d(q_smem + w * C::kTileBytes + blk * C::kBlkBytes, &maps.q, &sh->q_full,
-                          blk * 64, part.seq.q0 + part.i0 + w * tbw, part.h0, 0);
-        }
-        ++q_issued;
-        const int32_t *table = pb.block_table + static_cast<size_t>(part.b) * pb.max_pages;
-        // page of this lane's copies of tile j; -1 when it holds no key or is not there
-        auto page_of = [&](int j) -> int {
-          const int key = j * kBN + piece * box;
-          if (!loads || j >= part.t1 || key >= part.kv_end) return -1;
-          const int id = table[key >> pb.page_shift];
-          return static_cast<unsigned>(id) < static_cast<unsigned>(pb.num_pages) ? id : -1;
-        };
-        int id = page_of(part.t0);
-        for (int j = part.t0; j < part.t1 && ok; ++j) {
-          const int id_next = page_of(j + 1);
-          const uint32_t there = __ballot_sync(0xffffffffu, id >= 0) & whole;
-          const uint32_t bytes = static_cast<uint32_t>(__popc(there) * box * 128 * C::kSlabs);
-          const int rows = min(part.kv_end - j * kBN, kBN);
-          const int row_in_page = (j * kBN + piece * box) & (pb.page_size - 1);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {  // K, then V
-            const int slot = issued % C::kSlots, round = issued / C::kSlots;
-            ok = mbar_wait_warp(&sh->kv_empty[slot], (round & 1) ^ 1, abort_flag, p.wait_ns);
+      };
+      // the part whose tiles are being loaded: tiles [j, t1) are left
+      int j = 0, t1 = 0, kv_end = 0, head = 0, id = -1;
+      const int32_t *table = nullptr;
+      // page of this lane's copies of tile j; -1 when it holds no key or is not there
+      auto page_of = [&](int tile) -> int {
+        const int key = tile * kBN + piece * box;
+        if (!loads || tile >= t1 || key >= kv_end) return -1;
+        const int at = table[key >> pb.page_shift];
+        return static_cast<unsigned>(at) < static_cast<unsigned>(pb.num_pages) ? at : -1;
+      };
+      while (ok) {
+        advance();
+        // the rest of the part at hand, then the first tile of the next one (this loop
+        // has one copy of the code that issues a tile: it competes with the softmax for
+        // the instruction cache)
+#pragma unroll 1
+        for (int phase = 0; phase < 2 && ok; ++phase) {
+          int stop = t1;
+          if (phase == 1) {
+            if (!more) break;
+            const PagedPart &part = two[(n - 1) & 1];
+            j = stop = t1 = 0;
+            if (part.nt == 0) break;
+            j = part.t0;
+            t1 = part.t1;
+            stop = j + 1;
+            kv_end = part.kv_end;
+            head = part.kv;
+            table = pb.block_table + static_cast<size_t>(part.b) * pb.max_pages;
+            id = page_of(j);
+            ok = mbar_wait_warp(&sh->q_empty, (q_issued & 1) ^ 1, abort_flag, p.wait_ns);
             if (!ok) break;
-            uint64_t *bar = &sh->kv_full[slot];
-            if (kv == 1 && (there != whole || rows < kBN)) {
-              // the zeroing warp announces this tile once its rows are finished
-              bar = &sh->v_landed;
-              ok = mbar_wait_warp(&sh->zero_empty, (zeroed & 1) ^ 1, abort_flag, p.wait_ns);
-              if (!ok) break;
-            }
             if (lane == 0) {
-              if (kv == 0) {
-                sh->present[(issued >> 1) % kPresent] = there;
-              } else if (bar == &sh->v_landed) {
-                sh->zero_slot = slot;
-                sh->zero_rows = rows;
-                sh->zero_present = there;
-                mbar_arrive(&sh->zero_full);
-              }
-              mbar_arrive_expect_tx(bar, bytes);
+              const int halves = part.i1 - part.i0 <= tbw ? 1 : 2;
+              mbar_arrive_expect_tx(&sh->q_full,
+                                    static_cast<uint32_t>(halves * C::kSlabs * tbw * p.hpu * 128));
+              for (int w = 0; w < halves; ++w)
+                for (int blk = 0; blk < C::kSlabs; ++blk)
+                  tma_load_4d(q_smem + w * C::kTileBytes + blk * C::kBlkBytes, &maps.q,
+                              &sh->q_full, blk * 64, part.seq.q0 + part.i0 + w * tbw, part.h0, 0);
             }
-            if (bar == &sh->v_landed) ++zeroed;
-            __syncwarp();
-            if (id >= 0)
-              tma_load_4d(kv_smem + slot * C::kTileBytes + dst0, kv == 0 ? &maps.k : &maps.v, bar,
-                          slab * 64, row_in_page, part.kv, id);
-            ++issued;
+            ++q_issued;
           }
-          id = id_next;
+          for (; j < stop && ok; ++j) {
+            const int id_next = page_of(j + 1);
+            const uint32_t there = __ballot_sync(0xffffffffu, id >= 0) & whole;
+            const uint32_t bytes = static_cast<uint32_t>(__popc(there) * box * 128 * C::kSlabs);
+            const int rows = min(kv_end - j * kBN, kBN);
+            const int row_in_page = (j * kBN + piece * box) & (pb.page_size - 1);
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {  // K, then V
+              const int slot = issued % C::kSlots, round = issued / C::kSlots;
+              ok = mbar_wait_warp(&sh->kv_empty[slot], (round & 1) ^ 1, abort_flag, p.wait_ns);
+              if (!ok) break;
+              uint64_t *bar = &sh->kv_full[slot];
+              const bool partial = kv == 1 && (there != whole || rows < kBN);
+              if (partial) {
+                // the zeroing warp announces this tile once its rows are finished
+                bar = &sh->v_landed;
+                ok = mbar_wait_warp(&sh->zero_empty, (zeroed & 1) ^ 1, abort_flag, p.wait_ns);
+                if (!ok) break;
+                ++zeroed;
+              }
+              if (lane == 0) {
+                if (kv == 0) {
+                  sh->present[(issued >> 1) % kPresent] = there;
+                } else if (partial) {
+                  sh->zero_slot = slot;
+                  sh->zero_rows = rows;
+                  sh->zero_present = there;
+                  mbar_arrive(&sh->zero_full);
+                }
+                mbar_arrive_expect_tx(bar, bytes);
+              }
+              __syncwarp();
+              if (id >= 0)
+                tma_load_4d(kv_smem + slot * C::kTileBytes + dst0, kv == 0 ? &maps.k : &maps.v,
+                            bar, slab * 64, row_in_page, head, id);
+              ++issued;
+            }
+            id = id_next;
+          }
         }
-        if (!ok) break;
+        if (!more) break;
       }
       if (ok && mbar_wait_warp(&sh->zero_empty, (zeroed & 1) ^ 1, abort_flag, p.wait_ns) &&
           lane == 0) {
@@ -485,7 +478,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             vr[w] = (at + 1) / C::kSlots;
           }
           const int stride = both ? 4 : 2;
+          // the first key step of O's product overwrites O when `first`
+          auto pv = [&](int slot, int w, bool first) {
+            uint32_t lo = v_lo + slot * kTileLo;
+            asm volatile("" : "+r"(lo));
+#pragma unroll
+            for (int kk = 0; kk < kBN / 16; ++kk)
+              tc_mma_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8,
+                        desc_join(lo + ((kk * 16 * 128) >> 4), hi), idesc_o, !first || kk > 0);
+          };
+          auto score = [&](int slot, int w, int q_tile) {
+            // opaque, or the compiler keeps every step's descriptor in registers and spills
+            uint32_t lo = k_lo + slot * kTileLo, ql = q_lo + q_tile * kTileLo;
+            asm volatile("" : "+r"(lo), "+r"(ql));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * C::kBlkBytes + (kk & 3) * 32) >> 4;
+              tc_mma_ss(tmem + w * 128, desc_join(ql + off, hi), desc_join(lo + off, hi), idesc_s,
+                        kk > 0);
+            }
+            tc_commit(&sh->s_full[w]);
+          };
+          auto step = [&](int &slot, int &round) {
+            slot += stride;
+            if (slot >= C::kSlots) {
+              slot -= C::kSlots;
+              ++round;
+            }
+          };
+          mma_issued = true;
           for (int i = 0; ok && i <= steps; ++i) {
+            if (!both && i >= 2 && i < cnt[0]) {
+              // an inner step of rows of their own: nothing but the products and their
+              // waits (this thread sets the kernel's pace)
+              if (!(ok = mbar_wait_spin(&sh->kv_full[ks[0]], kr[0] & 1, abort_flag, p.wait_ns) &&
+                         mbar_wait_spin(&sh->kv_full[vs[0]], vr[0] & 1, abort_flag, p.wait_ns)))
+                break;
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                if (!(ok = mbar_wait_spin(&sh->p_full[w], (tw[w] + i - 1) & 1, abort_flag,
+                                          p.wait_ns)))
+                  break;
+                tc_fence_after();
+                pv(vs[0], w, false);
+                score(ks[0], w, w);
+              }
+              if (!ok) break;
+              if (i == steps - 1) tc_commit(&sh->q_empty);
+              step(vs[0], vr[0]);
+              step(ks[0], kr[0]);
+              vs[1] = vs[0];
+              vr[1] = vr[0];
+              ks[1] = ks[0];
+              kr[1] = kr[0];
+              continue;
+            }
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const bool do_pv = i >= 1 && i - 1 < cnt[w];
@@ -509,36 +556,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tc_fence_after();
               if (do_pv) {
-                const uint32_t lo = v_lo + vs[w] * kTileLo;
-#pragma unroll
-                for (int kk = 0; kk < kBN / 16; ++kk)
-                  tc_mma_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8,
-                            desc_join(lo + ((kk * 16 * 128) >> 4), hi), idesc_o,
-                            i > 1 || kk > 0);
+                pv(vs[w], w, i == 1);
                 if (i == cnt[w]) tc_commit(&sh->pv_done[w]);
-                mma_issued = true;
-                vs[w] += stride;
-                if (vs[w] >= C::kSlots) {
-                  vs[w] -= C::kSlots;
-                  ++vr[w];
-                }
+                step(vs[w], vr[w]);
               }
               if (do_s) {
-                const uint32_t lo = k_lo + ks[w] * kTileLo;
-                const uint32_t ql = q_lo + (both ? 0 : w) * kTileLo;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t off = ((kk >> 2) * C::kBlkBytes + (kk & 3) * 32) >> 4;
-                  tc_mma_ss(tmem + w * 128, desc_join(ql + off, hi), desc_join(lo + off, hi),
-                            idesc_s, kk > 0);
-                }
-                tc_commit(&sh->s_full[w]);
-                mma_issued = true;
-                ks[w] += stride;
-                if (ks[w] >= C::kSlots) {
-                  ks[w] -= C::kSlots;
-                  ++kr[w];
-                }
+                score(ks[w], w, both ? 0 : w);
+                step(ks[w], kr[w]);
               }
             }
             if (ok && i == steps - 1) tc_commit(&sh->q_empty);  // every S of the part is issued
@@ -629,6 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh->p_full[w]);
           continue;
         }
+        uint32_t sr[4][32];  // the loads go out first, what the tile needs is worked out meanwhile
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_tmem + ch * 32, sr[ch]);
         const int key = d.key0 + jj * kBN;
         const int lim = min(max(jmax - key, 0), kBN);
         const uint32_t there = sh->present[(tile0 + jj) % kPresent];
@@ -637,20 +664,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             whole & ~there & ((2u << ((min(d.kv_end - key, kBN) - 1) >> box_shift)) - 1);
         const bool need_mask = holes != 0 || __any_sync(0xffffffffu, lim < kBN);
         float alpha = 1.f;
+        tmem_wait_ld();
         if (pos && !need_mask && __all_sync(0xffffffffu, m_use != -INFINITY || !row)) {
           // Unmasked tile, every row of the warp has a running max: 32-column
           // chunks, exponents against the running max.  A chunk whose max exceeds
           // it by more than 2^8 moves it first (and rescales the P of the chunks
           // already stored).  P of chunk ch goes to columns [16 ch, 16 ch + 16),
           // whose scores are already read.
-          uint32_t vall[4][32];
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_tmem + ch * 32, vall[ch]);
-          tmem_wait_ld();
           float tsum = 0.f;
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) {
-            uint32_t(&cur)[32] = vall[ch];
+            uint32_t(&cur)[32] = sr[ch];
             const float cm = chunk_max32(cur) * p.scale_log2;
             const bool climb = cm > m_use + kRescaleThreshold;
             if (__any_sync(0xffffffffu, climb)) {
@@ -667,33 +691,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l_run = l_run * alpha + tsum;
         } else {
-          uint32_t sr[4][32];
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_tmem + ch * 32, sr[ch]);
-          tmem_wait_ld();
-          // raw scores of a positive scale (one FMA each later), else scaled ones:
-          // the max of scale * s is not scale * max s, and a hole's -inf must not
-          // meet a scale of 0
+          // raw scores of a positive scale; else, or with holes, scaled ones (the max of
+          // scale * s is not scale * max s, and a hole's -inf must not meet a scale of 0)
           const bool raw = pos && holes == 0;
-          if (holes != 0) {
+          float mt;
+          if (raw) {
+            mt = mask_max128(sr, need_mask, 0, lim) * p.scale_log2;
+          } else {
+            mt = scale_mask_max128(sr, p.scale_log2, need_mask, 0, lim);
+            if (holes != 0) {  // pages have at least 16 rows
 #pragma unroll
-            for (int c = 0; c < kBN; ++c) {
-              const float x = __uint_as_float(sr[c >> 5][c & 31]) * p.scale_log2;
-              const bool gone = c >= lim || ((holes >> (c >> box_shift)) & 1);
-              sr[c >> 5][c & 31] = __float_as_uint(gone ? -INFINITY : x);
+              for (int g = 0; g < 8; ++g)
+                if ((holes >> ((g * 16) >> box_shift)) & 1) {
+#pragma unroll
+                  for (int c = g * 16; c < g * 16 + 16; ++c)
+                    sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+                }
+              mt = fmaxf(fmaxf(chunk_max32(sr[0]), chunk_max32(sr[1])),
+                         fmaxf(chunk_max32(sr[2]), chunk_max32(sr[3])));
             }
           }
-          const float mt = raw ? mask_max128(sr, need_mask, 0, lim) * p.scale_log2
-                               : (holes != 0 ? mask_max128(sr, false, 0, kBN)
-                                             : scale_mask_max128(sr, p.scale_log2, need_mask, 0, lim));
           const float m_new = fmaxf(m_use, mt);
           if (m_new > m_use + kRescaleThreshold) {
             if (m_use != -INFINITY) alpha = ex2_approx(m_use - m_new);
             m_use = m_new;
           }
           const bool live = m_use != -INFINITY;
-          l_run = l_run * alpha + (raw ? exp2_fma_sum128(sr, p.scale_log2, m_use, live)
-                                       : exp2_sum128(sr, m_use, live));
+          l_run = l_run * alpha + exp2_fma_sum128(sr, raw ? p.scale_log2 : 1.f, m_use, live);
           // P_w as bf16 pairs over the first 64 columns of S_w
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -774,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int mine = row ? (slot != nullptr ? unit_row : static_cast<int>(out_row)) : -1;
       if (live_warp)
         store_rows<D>(cnt > 0 ? o_tmem : kNoTmem, join ? o_tmem + 128 : kNoTmem,
-                      none ? 0.f : f0 * inv, none ? 0.f : f1 * inv, none, mine, slot, out, lane);
+                      none ? 0.f : f0 * inv, none ? 0.f : f1 * inv, none, mine, slot, out);
       tc_fence_before();
       if (cnt > 0) mbar_arrive(&sh->o_free[w]);
       if (join) mbar_arrive(&sh->o_free[1]);  // warpgroup 1's, with its statistics

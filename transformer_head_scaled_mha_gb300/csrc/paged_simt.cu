@@ -64,7 +64,7 @@ struct Smem {
 };
 
 template <int D, int RP>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedProblem p) {
+__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_constant__ PagedProblem p) {
   constexpr int kC = D / 32;  // output columns of a lane
   static_assert(kRows <= kKeys, "a warp's sums fit where its values were");
   extern __shared__ __align__(16) uint8_t smem_raw[];
