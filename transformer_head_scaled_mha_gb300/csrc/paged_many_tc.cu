@@ -483,19 +483,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t lo = v_lo + slot * kTileLo;
             asm volatile("" : "+r"(lo));
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
-              tc_mma_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8,
-                        desc_join(lo + ((kk * 16 * 128) >> 4), hi), idesc_o, !first || kk > 0);
+            for (int kk = 0; kk < kBN / 16; ++kk) {
+              tc_mma_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, desc_join(lo, hi), idesc_o,
+                        !first || kk > 0);
+              lo += (16 * 128) >> 4;
+            }
           };
           auto score = [&](int slot, int w, int q_tile) {
-            // opaque, or the compiler keeps every step's descriptor in registers and spills
             uint32_t lo = k_lo + slot * kTileLo, ql = q_lo + q_tile * kTileLo;
             asm volatile("" : "+r"(lo), "+r"(ql));
+#pragma unroll 1
+            for (int blk = 0; blk < C::kSlabs; ++blk) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * C::kBlkBytes + (kk & 3) * 32) >> 4;
-              tc_mma_ss(tmem + w * 128, desc_join(ql + off, hi), desc_join(lo + off, hi), idesc_s,
-                        kk > 0);
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_ss(tmem + w * 128, desc_join(ql + kk * 2, hi), desc_join(lo + kk * 2, hi),
+                          idesc_s, blk > 0 || kk > 0);
+              ql += C::kBlkBytes >> 4;
+              lo += C::kBlkBytes >> 4;
             }
             tc_commit(&sh->s_full[w]);
           };
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o_tmem = tmem + lane_base + 256 + w * 128;
     const int box_shift = min(p.batch.page_shift, 7);
     const uint32_t whole = (1u << (kBN >> box_shift)) - 1;
-    const bool pos = p.scale_log2 > 0.f;
+    const bool pos = p.scale_log2 > 0.f;  // the max over scaled scores is the scaled max
     uint16_t *out = static_cast<uint16_t *>(p.out);
     int ts = 0;        // tiles of this warpgroup so far
     int parts[2] = {0, 0};  // parts with tiles of each warpgroup so far
@@ -653,9 +657,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh->p_full[w]);
           continue;
         }
-        uint32_t sr[4][32];  // the loads go out first, what the tile needs is worked out meanwhile
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_tmem + ch * 32, sr[ch]);
         const int key = d.key0 + jj * kBN;
         const int lim = min(max(jmax - key, 0), kBN);
         const uint32_t there = sh->present[(tile0 + jj) % kPresent];
@@ -663,74 +664,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t holes =
             whole & ~there & ((2u << ((min(d.kv_end - key, kBN) - 1) >> box_shift)) - 1);
         const bool need_mask = holes != 0 || __any_sync(0xffffffffu, lim < kBN);
-        float alpha = 1.f;
-        tmem_wait_ld();
-        if (pos && !need_mask && __all_sync(0xffffffffu, m_use != -INFINITY || !row)) {
-          // Unmasked tile, every row of the warp has a running max: 32-column
-          // chunks, exponents against the running max.  A chunk whose max exceeds
-          // it by more than 2^8 moves it first (and rescales the P of the chunks
-          // already stored).  P of chunk ch goes to columns [16 ch, 16 ch + 16),
-          // whose scores are already read.
-          float tsum = 0.f;
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t(&cur)[32] = sr[ch];
-            const float cm = chunk_max32(cur) * p.scale_log2;
-            const bool climb = cm > m_use + kRescaleThreshold;
-            if (__any_sync(0xffffffffu, climb)) {
-              const float f = climb ? ex2_approx(m_use - cm) : 1.f;
-              if (climb) m_use = cm;
-              alpha *= f;
-              tsum *= f;
+        // 32-column chunks, exponents against the running max.  A chunk whose max exceeds
+        // it by more than 2^8 moves it first (and rescales the P of the chunks already
+        // stored).  P of chunk ch goes to columns [16 ch, 16 ch + 16), whose scores are
+        // already read.  Loops, not straight code: the roles' loops together have to
+        // stay in the instruction cache (305 -> 243 us on 4 x 4096 tokens, 16 heads,
+        // d 64, with the products' loops from 183 to 94 KB).
+        float alpha = 1.f, tsum = 0.f;
+        // P of chunk ch of scores v times sl, whose row maximum (scaled) is cm
+        auto chunk = [&](const uint32_t(&v)[32], float sl, float cm, int ch, bool masked) {
+          const bool climb = cm > m_use + kRescaleThreshold;
+          if (__any_sync(0xffffffffu, climb)) {
+            const float f = climb ? ex2_approx(m_use - cm) : 1.f;
+            if (climb) m_use = cm;
+            alpha *= f;
+            tsum *= f;
 #pragma unroll 1
-              for (int c = 0; c < ch; ++c) rescale_p16(s_tmem + c * 16, f);
-            }
-            uint32_t pk[16];
-            tsum += chunk_exp_pack32(cur, p.scale_log2, m_use, pk);
-            tmem_st16(s_tmem + ch * 16, pk);
+            for (int c = 0; c < ch; ++c) rescale_p16(s_tmem + c * 16, f);
           }
-          l_run = l_run * alpha + tsum;
+          uint32_t pk[16];
+          // no key so far: weights of 0, not of -inf less -inf
+          tsum += chunk_exp_pack32(v, sl, masked && m_use == -INFINITY ? 0.f : m_use, pk);
+          tmem_st16(s_tmem + ch * 16, pk);
+        };
+        if (pos && !need_mask) {
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ch += 2) {
+            uint32_t v[2][32];
+            tmem_ld32(s_tmem + ch * 32, v[0]);
+            tmem_ld32(s_tmem + ch * 32 + 32, v[1]);
+            tmem_wait_ld();
+            chunk(v[0], p.scale_log2, chunk_max32(v[0]) * p.scale_log2, ch, false);
+            chunk(v[1], p.scale_log2, chunk_max32(v[1]) * p.scale_log2, ch + 1, false);
+          }
         } else {
-          // raw scores of a positive scale; else, or with holes, scaled ones (the max of
-          // scale * s is not scale * max s, and a hole's -inf must not meet a scale of 0)
-          const bool raw = pos && holes == 0;
-          float mt;
-          if (raw) {
-            mt = mask_max128(sr, need_mask, 0, lim) * p.scale_log2;
-          } else {
-            mt = scale_mask_max128(sr, p.scale_log2, need_mask, 0, lim);
-            if (holes != 0) {  // pages have at least 16 rows
+          // masks, holes, a scale that is not positive: scores scaled (the max of
+          // scale * s is not scale * max s) and masked first
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t v[32];
+            tmem_ld32(s_tmem + ch * 32, v);
+            // columns of the chunk's two halves that count: below the limit, and not of
+            // a page that is not there (pages have at least 16 rows)
+            const int upto = lim - ch * 32;
+            const int upto0 = (holes >> ((ch * 32) >> box_shift)) & 1 ? 0 : upto;
+            const int upto1 = (holes >> ((ch * 32 + 16) >> box_shift)) & 1 ? 0 : upto;
+            tmem_wait_ld();
 #pragma unroll
-              for (int g = 0; g < 8; ++g)
-                if ((holes >> ((g * 16) >> box_shift)) & 1) {
-#pragma unroll
-                  for (int c = g * 16; c < g * 16 + 16; ++c)
-                    sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-                }
-              mt = fmaxf(fmaxf(chunk_max32(sr[0]), chunk_max32(sr[1])),
-                         fmaxf(chunk_max32(sr[2]), chunk_max32(sr[3])));
-            }
-          }
-          const float m_new = fmaxf(m_use, mt);
-          if (m_new > m_use + kRescaleThreshold) {
-            if (m_use != -INFINITY) alpha = ex2_approx(m_use - m_new);
-            m_use = m_new;
-          }
-          const bool live = m_use != -INFINITY;
-          l_run = l_run * alpha + exp2_fma_sum128(sr, raw ? p.scale_log2 : 1.f, m_use, live);
-          // P_w as bf16 pairs over the first 64 columns of S_w
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int t = 0; t < 32; ++t) {
-              const int c = h * 64 + 2 * t;
-              pk[t] = pack_bf16x2(__uint_as_float(sr[c >> 5][c & 31]),
-                                  __uint_as_float(sr[c >> 5][(c + 1) & 31]));
-            }
-            tmem_st32(s_tmem + h * 32, pk);
+            for (int e = 0; e < 32; ++e)
+              v[e] = __float_as_uint(e < (e < 16 ? upto0 : upto1)
+                                         ? __uint_as_float(v[e]) * p.scale_log2
+                                         : -INFINITY);
+            chunk(v, 1.f, chunk_max32(v), ch, true);
           }
         }
+        l_run = l_run * alpha + tsum;
         // the running max moved: rescale this row of O (rare, warp-wide)
         if (it > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
