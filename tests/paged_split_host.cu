@@ -9,7 +9,8 @@ using namespace mha;
 namespace {
 PagedProblem problem(const int32_t *starts, const int32_t *lens, const int32_t *table, int B, int T,
                      int H, int Hkv, int hpu, int tb, int causal, int pages, int page_shift,
-                     int max_pages, int layout) {
+                     int max_pages, int layout, int which = 1) {
+  const PagedSplit splits[3] = {kSplitSimt, kSplitFew, kSplitMany};
   PagedProblem p;
   std::memset(&p, 0, sizeof p);
   p.batch = PagedBatch{starts, lens, table, B, T, pages, 1 << page_shift, page_shift, max_pages,
@@ -22,7 +23,7 @@ PagedProblem problem(const int32_t *starts, const int32_t *lens, const int32_t *
   p.tb = tb;
   p.causal = causal;
   p.rows = hpu * tb;
-  p.split = PagedSplit{kTileCost * 3 / 2, 2, 4};
+  p.split = splits[which];
   return p;
 }
 }  // namespace
@@ -60,9 +61,9 @@ static PagedSpan span_of(const PagedProblem &p, int cta, int grid) {
 // Rows of (cta, b, i0, i1, h0, heads, kv, nt, t0, t1, slot or -1); returns their number.
 extern "C" int parts(const int32_t *starts, const int32_t *lens, int B, int T, int H, int Hkv,
                      int hpu, int tb, int causal, int page_shift, int max_pages, int grid,
-                     int32_t *out, int most) {
+                     int which, int32_t *out, int most) {
   const PagedProblem p =
-      problem(starts, lens, nullptr, B, T, H, Hkv, hpu, tb, causal, 0, page_shift, max_pages, 0);
+      problem(starts, lens, nullptr, B, T, H, Hkv, hpu, tb, causal, 0, page_shift, max_pages, 0, which);
   int n = 0;
   for (int c = 0; c < grid; ++c) {
     PagedWalk w;
@@ -115,4 +116,8 @@ extern "C" int unit_sums(const int32_t *starts, const int32_t *lens, int T, int 
     sum += cost;
   }
   return paged_cost_before(p, s, blocks, blocks) == sum ? 0 : -100;
+}
+
+extern "C" long long slot_floats(int rows, int d) {
+  return static_cast<long long>(paged_slot_floats(rows, d));
 }

@@ -321,19 +321,24 @@ def test_paged_bindings(recorded):
 # ---------------------------------------------------------------------------
 # the split of attention work
 # ---------------------------------------------------------------------------
-def all_parts(host, starts, lens, H, Hkv, hpu, tb, causal, page_shift, max_pages, grid, T=None):
+SIMT, FEW, MANY = range(3)  # the kernels' ways to split
+
+
+def all_parts(host, starts, lens, H, Hkv, hpu, tb, causal, page_shift, max_pages, grid, which=FEW):
     (s, sp), (ln, lp) = i32(starts), i32(lens)
     out = np.zeros((400000, 11), dtype=np.int32)
-    n = host.parts(sp, lp, len(lens), int(s[-1]) if T is None else T, H, Hkv, hpu, tb, causal,
-                   page_shift, max_pages, grid, out.ctypes.data_as(ctypes.c_void_p), len(out))
+    n = host.parts(sp, lp, len(lens), int(s[-1]), H, Hkv, hpu, tb, causal,
+                   page_shift, max_pages, grid, which, out.ctypes.data_as(ctypes.c_void_p), len(out))
     assert n >= 0
     return out[:n]
 
 
-def check_split(host, starts, lens, H, Hkv, hpu, tb, causal, page_shift, max_pages, grid):
+def check_split(host, starts, lens, H, Hkv, hpu, tb, causal, page_shift, max_pages, grid,
+                which=FEW):
     """Every key tile of every unit is taken once, in order, by neighbouring CTAs;
     no CTA needs more than its two slots; every row of every sequence has a unit."""
-    rows = all_parts(host, starts, lens, H, Hkv, hpu, tb, causal, page_shift, max_pages, grid)
+    rows = all_parts(host, starts, lens, H, Hkv, hpu, tb, causal, page_shift, max_pages, grid,
+                     which)
     units = {}
     slots = set()
     load = np.zeros(grid, dtype=np.int64)
@@ -341,7 +346,7 @@ def check_split(host, starts, lens, H, Hkv, hpu, tb, causal, page_shift, max_pag
         assert 0 <= t0 <= t1 <= nt and heads >= 1 and h0 // (H // Hkv) == kv
         assert (h0 + heads - 1) // (H // Hkv) == kv
         units.setdefault((b, i0, h0), []).append((c, i1, heads, nt, t0, t1, slot))
-        load[c] += 3 + 2 * (t1 - t0)
+        load[c] += (8 if which == MANY else 3) + 2 * (t1 - t0)
         if slot >= 0:
             assert (c, slot) not in slots
             slots.add((c, slot))
@@ -369,8 +374,9 @@ def check_split(host, starts, lens, H, Hkv, hpu, tb, causal, page_shift, max_pag
 
 
 @pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("which", [SIMT, FEW, MANY])
 @pytest.mark.parametrize("seed", range(12))
-def test_every_tile_is_taken_once(host, seed, causal):
+def test_every_tile_is_taken_once(host, seed, which, causal):
     rng = np.random.default_rng(seed)
     for _ in range(12):
         B = int(rng.integers(1, 40))
@@ -382,12 +388,24 @@ def test_every_tile_is_taken_once(host, seed, causal):
         Hkv = int(rng.choice([1, 2, 8]))
         group = int(rng.choice([1, 3, 4, 20]))
         hpu = min(group, 16)
-        tb = int(rng.integers(1, 16 // hpu + 1))
+        tb = int(rng.integers(1, (256 if which == MANY else 16) // hpu + 1))
         shift = int(rng.choice([4, 6, 9]))
         max_pages = max(1, -(-int(lens.max()) >> shift) - int(rng.integers(0, 2)))
         grid = int(rng.choice([1, 2, 7, 152, 456]))
         check_split(host, starts.tolist(), lens.tolist(), group * Hkv, Hkv, hpu, tb, causal, shift,
-                    max_pages, grid)
+                    max_pages, grid, which)
+
+
+@pytest.mark.parametrize("which", [SIMT, FEW, MANY])
+def test_a_unit_over_many_ctas(host, which):
+    # one unit as long as the grid and longer, alone and among empty ones
+    for tiles in (1, 2, 3, 4, 5, 7, 100, 151, 152, 153, 157, 300, 304, 305, 700, 2000):
+        for grid in (2, 152, 304, 608):
+            for off in (0, 1, 127):
+                ln = tiles * 128 - off
+                check_split(host, [0, 1], [ln], 2, 1, 2, 1, 1, 4, -(-ln // 16), grid, which)
+                check_split(host, list(range(43)), [0] * 20 + [ln] + [0] * 20 + [ln // 3], 2, 1, 2,
+                            1, 1, 4, -(-ln // 16), grid, which)
 
 
 def test_split_balances_long_and_short_sequences(host):
@@ -401,6 +419,15 @@ def test_split_balances_long_and_short_sequences(host):
     # one short sequence: a CTA per head, nothing split
     load = check_split(host, [0, 1], [300], 8, 8, 1, 1, 1, 4, 20, 152)
     assert (load > 0).sum() == 8
+
+
+def test_slots_of_sums_are_aligned(host):
+    # 16-byte accesses at row and column multiples of 4 floats
+    host.slot_floats.restype = ctypes.c_longlong
+    for rows in range(1, 257):
+        for d in (64, 128):
+            n = host.slot_floats(rows, d)
+            assert n % 4 == 0 and rows * (d + 2) <= n < rows * (d + 2) + 4
 
 
 def test_empty_units_are_taken_once(host):
@@ -425,9 +452,10 @@ def test_unit_lengths_have_their_closed_form(host):
 @pytest.mark.parametrize("causal", [0, 1])
 def test_chunks_are_split_evenly(host, causal):
     # units of 256 rows: a long prompt from its beginning, and chunks behind caches
-    load = check_split(host, [0, 8192], [8192], 16, 16, 1, 256, causal, 7, 64, 152)
+    load = check_split(host, [0, 8192], [8192], 16, 16, 1, 256, causal, 7, 64, 152, MANY)
     assert load.max() <= 1.25 * load.sum() / 152
-    load = check_split(host, [0, 512, 600, 601], [4096, 3000, 2500], 32, 8, 4, 64, causal, 6, 64, 152)
+    load = check_split(host, [0, 512, 600, 601], [4096, 3000, 2500], 32, 8, 4, 64, causal, 6, 64, 152,
+                       MANY)
     assert load.max() <= 1.4 * load.sum() / 152
 
 

@@ -103,6 +103,10 @@ CASES = [
     ([(2, 300), (5, 5), (3, 129), (5, 1000)], 6, 2, 64, 16, "bhsd"),     # drafted tokens
     ([(4, 400), (1, 90), (4, 4)], 4, 4, 128, 16, "bshd"),
     ([(16, 513), (7, 300)], 4, 4, 64, 64, "bshd"),
+    ([(8, 300), (3, 129), (1, 700), (0, 40)], 8, 2, 64, 16, "bhsd"),     # up to 32 rows
+    ([(7, 1000), (7, 7), (2, 5000)], 4, 1, 128, 64, "bshd"),
+    ([(1, 333), (1, 129)], 32, 1, 128, 32, "bshd"),
+    ([(3, 200), (1, 1)], 18, 2, 64, 128, "bhsd"),
     ([(17, 17), (40, 400), (1, 77), (130, 131)], 4, 2, 64, 16, "bshd"),  # chunks
     ([(200, 900), (0, 300), (1, 1000), (64, 64)], 8, 2, 128, 64, "bhsd"),
     ([(300, 300)], 3, 1, 128, 128, "bhsd"),
@@ -184,7 +188,7 @@ def test_scales(dt, scale, n):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("n", [1, 12, 20])
 @pytest.mark.parametrize("d", [64, 128])
 def test_climbing_scores(dt, n, d):
     # the running maximum moves tile after tile; then falls from the first key on

@@ -64,6 +64,13 @@ struct PagedSplit {
   int min_part;     // tiles of a part at least
   int min_stretch;  // tiles of work below which a CTA is not worth having
 };
+// The many-query kernel's units cost it the time of 4 tile pairs besides their keys,
+// and a cut the sums of 256 rows; the others' 1 and 1.5 tiles.  A tile of the fp32
+// kernel takes about 2 us, so there every tile may have a CTA of its own (44 -> 23 us
+// on 8 sequences of 90 to 700 keys, 5 tokens of 8 heads).
+constexpr PagedSplit kSplitSimt{kTileCost, 1, 1};
+constexpr PagedSplit kSplitFew{kTileCost * 3 / 2, 2, 3};
+constexpr PagedSplit kSplitMany{kTileCost * 4, 3, 6};
 
 // A unit of attention work: `tb` consecutive new tokens of one sequence times
 // `hpu` query heads of one key/value head's group.  Row r of a unit is head
@@ -159,7 +166,11 @@ MHA_HD PagedSpan paged_stretch(long long total, long long units, int cta, int gr
                                int min_stretch) {
   PagedSpan sp;
   const long long by_work = static_cast<int>(total >> 8 > 0x7fffffff ? 0x7fffffff : total >> 8) / min_stretch;  // kTileCost is 2^8
-  const long long most = by_work > units ? by_work : units;
+  long long most = by_work > units ? by_work : units;
+  // a stretch is longer than a tile, so that no CTA between a unit's first and last
+  // part is without one (paged_merge_kernel takes them as neighbours)
+  const long long cap = (total >> 8) * 31 / 32;
+  if (most > cap) most = cap;
   sp.ctas = static_cast<int>(most < 1 ? 1 : (most < grid ? most : grid));
   // equal stretches, a little short (the last CTA takes what is left, some millionths):
   // an approximate quotient, for a 64-bit division is a hundred instructions
@@ -370,9 +381,10 @@ MHA_HD bool paged_split(const PagedPart &part) {
 // slot of a split part
 MHA_HD int paged_slot(const PagedPart &part) { return part.t0 > 0 ? 0 : 1; }
 
-// one slot: rows x d sums, then rows x (max, sum)
+// One slot: rows x d sums, then rows x (max, sum); whole 16-byte pieces, because the
+// sums are read and written 16 bytes at a time.
 MHA_HD size_t paged_slot_floats(int rows, int d) {
-  return static_cast<size_t>(rows) * (d + 2);
+  return (static_cast<size_t>(rows) * (d + 2) + 3) / 4 * 4;
 }
 MHA_HD float *paged_slot_ptr(const PagedProblem &p, int d, int cta, int slot) {
   return p.part + (static_cast<size_t>(cta) * 2 + slot) * paged_slot_floats(p.rows, d);

@@ -112,6 +112,12 @@ bool current_device(Device *d) {
 }
 
 // ---- attention over the cache -------------------------------------------------
+// Expected query rows per key/value head up to which the few-query kernel is taken.
+// Measured, few / many: 16 rows, 32 sequences of 500-2000 keys, d 128: 47 / 59 us, 16
+// sequences of 1000-8000: 40 / 53 us; 32 rows (a few-query kernel of that size), 64
+// sequences of 1000-4000: 101 / 88 us, 128 of 300-900: 160 / 97 us.
+constexpr int kFewRows = 16;
+
 enum PagedPath { kNone = 0, kSimt = 1, kFew = 2, kMany = 3 };
 
 // Units of work of a kernel (PagedProblem): heads, tokens, and its CTAs at most.
@@ -130,7 +136,7 @@ int paged_path(int B, int T, int H, int H_kv, int d, int max_q, int dtype) {
     return -MHA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0 || H == 0) return kNone;
   if (dtype == MHA_DTYPE_F32) return kSimt;
-  return static_cast<long long>(H / H_kv) * max_q <= 16 ? kFew : kMany;
+  return static_cast<long long>(H / H_kv) * max_q <= kFewRows ? kFew : kMany;
 }
 
 Units units_of(int path, int group, int max_q) {
@@ -141,7 +147,7 @@ Units units_of(int path, int group, int max_q) {
   u.tb = path == kMany ? 2 * (rows / u.hpu) : std::min(rows / u.hpu, max_q);
   u.rows = u.hpu * u.tb;
   u.ctas = path == kMany ? kPagedManyMaxCtas : kPagedMaxCtas;
-  u.split = path == kMany ? PagedSplit{kTileCost * 4, 3, 6} : PagedSplit{kTileCost * 3 / 2, 2, 4};
+  u.split = path == kMany ? kSplitMany : (path == kFew ? kSplitFew : kSplitSimt);
   return u;
 }
 

@@ -15,11 +15,11 @@
 //                        maximum moves only when it grows by more than 2^8
 //                        (numerator and denominator share it), and O is rescaled
 //                        in TMEM when it does; partial row sums per thread
-//   P -> smem (bf16)     up to 8 rows as a sum of two bf16; 9 to 16 rows rounded to
-//                        one (2^-8 relative)
+//   P -> smem (bf16)     up to 8 rows as a sum of two bf16; more rows rounded to one
+//                        (2^-8 relative)
 //   O^T += V_j^T P^T     A = the V tile read MN-major.  d = 64: both 64-key halves
 //                        of the tile in one product, M rows 0..63 the first
-//                        half's values and 64..127 the second's, N = 32 the first
+//                        half's values and 64..127 the second's, B the first
 //                        half's P rows then the second's; the two diagonal blocks
 //                        of D are partial outputs, summed at the end
 //
@@ -50,7 +50,7 @@ namespace {
 constexpr int kThreads = 224;
 constexpr int kSoftmaxThreads = 128;
 constexpr int kBN = kPagedTile;
-constexpr int kN = 16;               // query rows per score product
+constexpr int kN = 16;  // query rows per score product
 constexpr uint32_t kTmemCols = 128;  // S0 S1 (kN each), O0 O1 (kOCols each)
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kMaxSlots = 3;
@@ -67,22 +67,23 @@ struct Cfg {
   static constexpr int kTileBytes = kSlabs * kBlkBytes;  // a K or V tile
   static constexpr int kSlotBytes = 2 * kTileBytes;      // ring slot: K tile, V tile
   static constexpr int kSlots = 3;
-  static constexpr int kQBlk = kN * 128;  // [16 rows x 64] of Q
+  static constexpr int kQBlk = kN * 128;  // [kN rows x 64] of Q
   static constexpr int kQBytes = kSlabs * kQBlk;
   // Up to 8 rows the weights go in as two bf16, the rounded weight and what the
   // rounding left (2^-17 relative together), in rows of the product that would
   // otherwise be padding: row r and row r + kLo.
   static constexpr bool kTwo = RP <= 8;
   static constexpr int kLo = D == 64 && RP <= 4 ? 4 : 8;
-  static constexpr int kPRows = D == 64 && RP <= 4 ? 8 : 16;  // rows of P per 64-key half
+  static constexpr int kPRows = D == 64 && RP <= 4 ? 8 : kN;  // rows of P per 64-key half
   static constexpr int kPHalf = kPRows * 128;
   static constexpr int kPBytes = 2 * kPHalf;
-  static constexpr int kPvN = D == 64 ? 2 * kPRows : 16;
+  static constexpr int kPvN = D == 64 ? 2 * kPRows : kN;
   static constexpr int kPvSteps = D == 64 ? 4 : 8;
   // A's second M block: d = 64, the tile's keys 64..127 (64 rows down);
   // d = 128, value dims 64..127 (the next swizzle block)
   static constexpr uint32_t kVLbo = D == 64 ? 64 * 128 : kBlkBytes;
   static constexpr int kOCols = kPvN;
+  static_assert(2 * kN + 2 * kOCols <= static_cast<int>(kTmemCols), "tensor memory");
 };
 
 // A part as the other roles need it.
@@ -100,9 +101,11 @@ struct Desc {
 
 template <int RP>
 struct __align__(16) Shared {
-  float4 red[2][RP];    // tile maxima of the four warps, double-buffered by tile
+  union {
+    float4 red[2][RP];      // tile maxima of the four warps, double-buffered by tile
+    long long scratch[40];  // before: where the span is found
+  };
   float lsum[4][RP];    // per-warp row sums
-  long long scratch[40];
   Desc desc[kDescs];
   uint32_t present[kMaxSlots];  // pages of the slot's tile that were loaded
   uint64_t desc_full[kDescs], desc_empty[kDescs];

@@ -515,8 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!both && i >= 2 && i < cnt[0]) {
               // an inner step of rows of their own: nothing but the products and their
               // waits (this thread sets the kernel's pace)
-              if (!(ok = mbar_wait_spin(&sh->kv_full[ks[0]], kr[0] & 1, abort_flag, p.wait_ns) &&
-                         mbar_wait_spin(&sh->kv_full[vs[0]], vr[0] & 1, abort_flag, p.wait_ns)))
+              if (!(ok = mbar_wait_spin(&sh->kv_full[vs[0]], vr[0] & 1, abort_flag, p.wait_ns)))
                 break;
 #pragma unroll
               for (int w = 0; w < 2; ++w) {
@@ -525,6 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   break;
                 tc_fence_after();
                 pv(vs[0], w, false);
+                if (w == 0 && !(ok = mbar_wait_spin(&sh->kv_full[ks[0]], kr[0] & 1, abort_flag,
+                                                    p.wait_ns)))
+                  break;
                 score(ks[0], w, w);
               }
               if (!ok) break;
@@ -543,9 +545,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               const bool do_s = i < cnt[w];
               // a tile that the other warpgroup waited for is there
               const bool waits = both || w == 0;
-              if (do_s && (waits || i >= cnt[0]) &&
-                  !(ok = mbar_wait_spin(&sh->kv_full[ks[w]], kr[w] & 1, abort_flag, p.wait_ns)))
-                break;
               if (do_pv) {
                 if ((waits || i - 1 >= cnt[0]) &&
                     !(ok = mbar_wait_spin(&sh->kv_full[vs[w]], vr[w] & 1, abort_flag, p.wait_ns)))
@@ -557,13 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i == 1 &&
                     !(ok = mbar_wait_spin(&sh->o_free[w], (pw[w] & 1) ^ 1, abort_flag, p.wait_ns)))
                   break;
-              }
-              tc_fence_after();
-              if (do_pv) {
+                tc_fence_after();
                 pv(vs[w], w, i == 1);
                 if (i == cnt[w]) tc_commit(&sh->pv_done[w]);
                 step(vs[w], vr[w]);
               }
+              if (do_s && (waits || i >= cnt[0]) &&
+                  !(ok = mbar_wait_spin(&sh->kv_full[ks[w]], kr[w] & 1, abort_flag, p.wait_ns)))
+                break;
               if (do_s) {
                 score(ks[w], w, both ? 0 : w);
                 step(ks[w], kr[w]);

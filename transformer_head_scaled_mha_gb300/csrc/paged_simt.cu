@@ -38,8 +38,31 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
+// a lane's 2 or 4 columns of a row of sums, and of a row of output
+__device__ __forceinline__ void ld_cols(const float *p, float (&x)[2]) {
+  const float2 v = *reinterpret_cast<const float2 *>(p);
+  x[0] = v.x;
+  x[1] = v.y;
+}
+__device__ __forceinline__ void ld_cols(const float *p, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4 *>(p);
+  x[0] = v.x;
+  x[1] = v.y;
+  x[2] = v.z;
+  x[3] = v.w;
+}
+__device__ __forceinline__ void st_cols(float *p, const float (&x)[2]) {
+  *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+}
+__device__ __forceinline__ void st_cols(float *p, const float (&x)[4]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void st_cols(__nv_bfloat16 *p, const float (&x)[2]) {
+  *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(x[0], x[1]);
+}
+__device__ __forceinline__ void st_cols(__nv_bfloat16 *p, const float (&x)[4]) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+}
 
 // 16 bytes global -> shared, or zeros
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t saddr, const void *gptr, bool there) {
@@ -294,28 +317,31 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       for (int k = c - 1 + share; k <= last; k += kSplit) {
         const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
         const float f = ex2_approx(slot[ml] - use);
+        float part[kC];  // this lane's kC columns
+        ld_cols(slot + static_cast<size_t>(r) * D + lane * kC, part);
 #pragma unroll
-        for (int e = 0; e < kC; ++e)
-          o[e] = fmaf(slot[static_cast<size_t>(r) * D + e * 32 + lane], f, o[e]);
+        for (int e = 0; e < kC; ++e) o[e] = fmaf(part[e], f, o[e]);
       }
     }
     if (kSplit > 1) {
 #pragma unroll
-      for (int e = 0; e < kC; ++e) sums[warp][e * 32 + lane] = o[e];
+      for (int e = 0; e < kC; ++e) sums[warp][lane * kC + e] = o[e];
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < kC; ++e) {
         o[e] = 0.f;
 #pragma unroll
-        for (int g = 0; g < kSplit; ++g) o[e] += sums[warp - share + g][e * 32 + lane];
+        for (int g = 0; g < kSplit; ++g) o[e] += sums[warp - share + g][lane * kC + e];
       }
       __syncthreads();
     }
     if (row && share == 0) {
       T *to = static_cast<T *>(p.out) +
-              (static_cast<long long>(seq.q0 + i) * p.H + h0 + h) * D + lane;
+              (static_cast<long long>(seq.q0 + i) * p.H + h0 + h) * D + lane * kC;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-      for (int e = 0; e < kC; ++e) store_as(to + e * 32, l > 0.f ? o[e] / l : 0.f);
+      for (int e = 0; e < kC; ++e) o[e] = l > 0.f ? o[e] * inv : 0.f;
+      st_cols(to, o);
     }
   }
 }
