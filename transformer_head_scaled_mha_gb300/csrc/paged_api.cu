@@ -99,16 +99,10 @@ int check_batch(const int32_t *q_starts, const int32_t *kv_lengths, const int32_
   return MHA_OK;
 }
 
-struct Device {
-  int sms;
-  int *status;
-};
-bool current_device(Device *d) {
+// SMs of the current device; 0 on failure
+int current_sms() {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  d->sms = sm_count(dev);
-  d->status = status_ptr();
-  return d->sms > 0 && d->status != nullptr;
+  return cudaGetDevice(&dev) == cudaSuccess ? sm_count(dev) : 0;
 }
 
 // ---- attention over the cache -------------------------------------------------
@@ -188,8 +182,8 @@ extern "C" int mha_qk_norm_rope_fwd(const void *q, const void *k, void *q_out, v
                          {positions, positions != nullptr ? tokens * sizeof(int32_t) : 0, 4},
                          {inv_freq, rotary_dim / 2 * sizeof(float), 4}};
   if (!present(outs) || !present(ins) || clash(outs, ins, {0, 1})) return MHA_ERR_INVALID_ARGUMENT;
-  Device dev;
-  if (!current_device(&dev)) return MHA_ERR_CUDA;
+  const int sms = current_sms();
+  if (sms <= 0) return MHA_ERR_CUDA;
   RopeArgs a{};
   a.q = q;
   a.k = k;
@@ -208,7 +202,7 @@ extern "C" int mha_qk_norm_rope_fwd(const void *q, const void *k, void *q_out, v
   a.layout = layout;
   a.style = style;
   a.eps = eps;
-  return launch_rope_fwd(a, d, dtype, false, dev.sms, static_cast<cudaStream_t>(stream)) ==
+  return launch_rope_fwd(a, d, dtype, false, sms, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? MHA_OK
              : MHA_ERR_CUDA;
@@ -259,8 +253,8 @@ extern "C" int mha_qk_norm_rope_bwd(const void *q, const void *k, const void *dq
   if (!present(outs) || !present(ins) || clash(outs, ins, {0, 1, -1, -1, -1}))
     return MHA_ERR_INVALID_ARGUMENT;
   if (nq + nk == 0 && !weights) return MHA_OK;
-  Device dev;
-  if (!current_device(&dev)) return MHA_ERR_CUDA;
+  const int sms = current_sms();
+  if (sms <= 0) return MHA_ERR_CUDA;
   RopeArgs a{};
   a.q = q;
   a.k = k;
@@ -284,7 +278,7 @@ extern "C" int mha_qk_norm_rope_bwd(const void *q, const void *k, const void *dq
   a.layout = layout;
   a.style = style;
   a.eps = eps;
-  return launch_rope_bwd(a, d, dtype, dev.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_rope_bwd(a, d, dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MHA_OK
              : MHA_ERR_CUDA;
 }
@@ -326,8 +320,8 @@ extern "C" int mha_paged_append(const void *q, const void *k, const void *v, voi
       {block_table, sizeof(int32_t) * static_cast<size_t>(B) * max_pages, 4}};
   if (!present(outs) || !present(ins) || clash(outs, ins, {0, -1, -1}))
     return MHA_ERR_INVALID_ARGUMENT;
-  Device dev;
-  if (!current_device(&dev)) return MHA_ERR_CUDA;
+  const int sms = current_sms();
+  if (sms <= 0) return MHA_ERR_CUDA;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -345,7 +339,7 @@ extern "C" int mha_paged_append(const void *q, const void *k, const void *v, voi
   a.layout = kLayoutBSHD;
   a.style = style;
   a.eps = eps;
-  return launch_rope_fwd(a, d, dtype, true, dev.sms, static_cast<cudaStream_t>(stream)) ==
+  return launch_rope_fwd(a, d, dtype, true, sms, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? MHA_OK
              : MHA_ERR_CUDA;
@@ -400,8 +394,8 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
                          {block_table, sizeof(int32_t) * static_cast<size_t>(B) * max_pages, 4}};
   if (!present(outs) || !present(ins) || clash(outs, ins, {-1, -1}))
     return MHA_ERR_INVALID_ARGUMENT;
-  Device dev;
-  if (!current_device(&dev)) return MHA_ERR_CUDA;
+  const int sms = current_sms();
+  if (sms <= 0) return MHA_ERR_CUDA;
   p.H = H;
   p.Hkv = H_kv;
   p.group = H / H_kv;
@@ -417,14 +411,15 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   p.out = out;
   p.meta = static_cast<int32_t *>(workspace);
   p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + meta_bytes(u));
-  p.status = dev.status;
+  p.status = status_ptr();
+  if (p.status == nullptr) return MHA_ERR_CUDA;
   p.wait_ns = wait_limit_ns();
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   p.split = u.split;
   int grid = u.ctas;
   cudaError_t err = cudaSuccess;
   if (path == kSimt) {
-    grid = std::min(u.ctas, (d == 64 ? 2 : 1) * dev.sms);  // CTAs that run at a time
+    grid = std::min(u.ctas, (d == 64 ? 2 : 1) * sms);  // CTAs that run at a time
     err = launch_paged_simt(p, d, grid, stream);
   } else {
     CUtensorMap qm, km, vm;
@@ -438,10 +433,10 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
         !make_map(&vm, vb, d, page_size, H_kv, pages, layout, box, 1))
       return MHA_ERR_CUDA;
     if (path == kMany) {
-      grid = std::min(grid, dev.sms);
+      grid = std::min(grid, sms);
       err = launch_paged_many(qm, km, vm, p, d, grid, stream);
     } else {
-      err = launch_paged_few(qm, km, vm, p, d, grid, dev.sms, stream);
+      err = launch_paged_few(qm, km, vm, p, d, grid, sms, stream);
     }
   }
   // a unit is cut only when both parts have min_part tiles: not where the block

@@ -49,8 +49,21 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, device="cuda"):
     return (float(base) ** (-2.0 * i / rotary_dim)).float().to(device)
 
 
+_modules = {}
+
+
+def _torch():
+    """torch, imported at the first call that needs it (an import statement in every
+    call costs a third of a microsecond each)."""
+    torch = _modules.get("torch")
+    if torch is None:
+        import torch
+        _modules["torch"] = torch
+    return torch
+
+
 def _dtype_of(t) -> int:
-    import torch
+    torch = _torch()
     if t.dtype == torch.bfloat16:
         return MHA_DTYPE_BF16
     if t.dtype == torch.float32:
@@ -66,67 +79,57 @@ def _layout_of(layout: str) -> int:
     raise ValueError("layout must be 'bhsd' or 'bshd'")
 
 
-# These checks run on every call of a generation step, where they weigh as much as
-# the kernels: plain attribute reads, the device by its number (-1: not CUDA).
-def _like(name, t, ref, shape):
-    """Address of a tensor of the call: contiguous, on ref's device, of ref's dtype
-    and ``shape``."""
+def _device_of(t) -> int:
+    """Number of a CUDA tensor's device."""
     dev = t.get_device()
-    if t.shape != shape or t.dtype != ref.dtype or dev < 0 or dev != ref.get_device() or \
-            not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s CUDA tensor of shape %s on %s"
-                         % (name, ref.dtype, tuple(shape), ref.device))
-    return t.data_ptr()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    return dev
 
 
-def _array(name, t, ref, dtype, shape):
-    """Address of an int32 or float32 array of the call, or None."""
+def _at(name, t, shape, dtype, dev):
+    """Address of a tensor or array of the call (None: none): contiguous, of that
+    shape, dtype and device.  Every tensor of every call of a generation step passes
+    here: plain attribute reads, the device by its number."""
     if t is None:
         return None
-    dev = t.get_device()
-    if t.shape != shape or t.dtype != dtype or dev < 0 or dev != ref.get_device() or \
-            not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s CUDA tensor of shape %s on %s"
-                         % (name, dtype, tuple(shape), ref.device))
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d, not %s of shape "
+                         "%s on %s" % (name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape),
+                                       t.device))
     return t.data_ptr()
 
 
-def _scratch(t, ref):
+def _scratch(t, dev):
     """(address, bytes) of a workspace, or (None, 0)."""
     if t is None:
         return None, 0
-    if t.get_device() < 0 or t.get_device() != ref.get_device() or not t.is_contiguous():
+    if t.get_device() != dev or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _weight(name, t, ref):
-    return None if t is None else _like(name, t, ref, ref.shape[-1:])
-
-
-def _rotary(inv_freq, ref):
+def _rotary(inv_freq, dev):
     """(address, rotary_dim) of the frequencies; (None, 0) without."""
-    import torch
     if inv_freq is None:
         return None, 0
-    return _array("inv_freq", inv_freq, ref, torch.float32, (inv_freq.numel(),)), \
-        2 * inv_freq.numel()
+    n = inv_freq.numel()
+    return _at("inv_freq", inv_freq, (n,), _torch().float32, dev), 2 * n
 
 
 def _on(stream, device):
     """Context in which this call's own tensors are allocated: its stream, so that
     the memory is not handed to other work while the call's kernels use it."""
-    import torch
     if stream is None:
         return contextlib.nullcontext()
+    torch = _torch()
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
 
 
-def _call(name, ref, stream, args):
-    import torch
-    dev = ref.get_device()
+def _call(name, dev, stream, args):
+    torch = _torch()
     if stream is None:
         handle = _current_stream(dev)
     else:
@@ -142,7 +145,7 @@ def _call(name, ref, stream, args):
 
 def _current_stream(dev: int) -> int:
     """Handle of torch's current stream on device ``dev``."""
-    import torch
+    torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public call's time
     return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
@@ -176,23 +179,22 @@ def mha_qk_norm_rope_fwd(q, k, q_out=None, k_out=None, *, q_weight=None, k_weigh
     ``k_out`` may be q and k themselves.  Enqueued on ``stream`` (default: torch's
     current stream).
     """
-    import torch
+    torch = _torch()
     lay = _layout_of(layout)
     B, H, Hkv, L, d, qs, ks = _head_rows(q, k, lay)
     ref = q if q is not None else k
-    dtype = _dtype_of(ref)
+    dtype, dt, dev = _dtype_of(ref), ref.dtype, _device_of(ref)
     if q_out is None or k_out is None:
         with _on(stream, ref.device):
             q_out = torch.empty_like(q) if q_out is None and q is not None else q_out
             k_out = torch.empty_like(k) if k_out is None and k is not None else k_out
-    addr = lambda name, t, shape: None if t is None else _like(name, t, ref, shape)  # noqa: E731
-    freq, rotary = _rotary(inv_freq, ref)
-    args = (addr("q", q, qs), addr("k", k, ks), addr("q_out", q_out, qs),
-            addr("k_out", k_out, ks), _weight("q_weight", q_weight, ref),
-            _weight("k_weight", k_weight, ref),
-            _array("positions", positions, ref, torch.int32, (B, L)), freq, B, H, Hkv, L, d,
-            rotary, lay, int(bool(interleaved)), float(eps), dtype)
-    _call("mha_qk_norm_rope_fwd", ref, stream, args)
+    freq, rotary = _rotary(inv_freq, dev)
+    args = (_at("q", q, qs, dt, dev), _at("k", k, ks, dt, dev), _at("q_out", q_out, qs, dt, dev),
+            _at("k_out", k_out, ks, dt, dev), _at("q_weight", q_weight, (d,), dt, dev),
+            _at("k_weight", k_weight, (d,), dt, dev),
+            _at("positions", positions, (B, L), torch.int32, dev), freq, B, H, Hkv, L, d, rotary,
+            lay, 1 if interleaved else 0, eps, dtype)
+    _call("mha_qk_norm_rope_fwd", dev, stream, args)
     return q_out, k_out
 
 
@@ -211,11 +213,11 @@ def mha_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq=None, dk=None, dq_weight=None,
     themselves.  ``workspace``: uint8 CUDA tensor of at least
     mha_qk_norm_rope_bwd_workspace_size(d) bytes (allocated here when None and
     needed)."""
-    import torch
+    torch = _torch()
     lay = _layout_of(layout)
     B, H, Hkv, L, d, qs, ks = _head_rows(dq_out, dk_out, lay)
     ref = dq_out if dq_out is not None else dk_out
-    dtype = _dtype_of(ref)
+    dtype, dt, dev = _dtype_of(ref), ref.dtype, _device_of(ref)
     weights = q_weight is not None or k_weight is not None
     if q_weight is None and dq_weight is not None or k_weight is None and dk_weight is not None:
         raise ValueError("dq_weight and dk_weight go with q_weight and k_weight")
@@ -229,42 +231,43 @@ def mha_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq=None, dk=None, dq_weight=None,
             if workspace is None and weights:
                 workspace = torch.empty(max(mha_qk_norm_rope_bwd_workspace_size(d), 1),
                                         dtype=torch.uint8, device=ref.device)
-    addr = lambda name, t, shape: None if t is None else _like(name, t, ref, shape)  # noqa: E731
     for name, x, w, shape in (("q", q, q_weight, qs), ("k", k, k_weight, ks)):
         if x is None and w is not None and 0 not in shape:
             raise ValueError("%s is needed with %s_weight" % (name, name))
-    freq, rotary = _rotary(inv_freq, ref)
-    args = (addr("q", q, qs), addr("k", k, ks), addr("dq_out", dq_out, qs),
-            addr("dk_out", dk_out, ks), addr("dq", dq, qs), addr("dk", dk, ks),
-            _array("dq_weight", dq_weight, ref, torch.float32, (d,)),
-            _array("dk_weight", dk_weight, ref, torch.float32, (d,)),
-            _weight("q_weight", q_weight, ref), _weight("k_weight", k_weight, ref),
-            _array("positions", positions, ref, torch.int32, (B, L)), freq, B, H, Hkv, L, d,
-            rotary, lay, int(bool(interleaved)), float(eps), dtype,
-            *_scratch(workspace, ref))
-    _call("mha_qk_norm_rope_bwd", ref, stream, args)
+    freq, rotary = _rotary(inv_freq, dev)
+    args = (_at("q", q, qs, dt, dev), _at("k", k, ks, dt, dev), _at("dq_out", dq_out, qs, dt, dev),
+            _at("dk_out", dk_out, ks, dt, dev), _at("dq", dq, qs, dt, dev),
+            _at("dk", dk, ks, dt, dev), _at("dq_weight", dq_weight, (d,), torch.float32, dev),
+            _at("dk_weight", dk_weight, (d,), torch.float32, dev),
+            _at("q_weight", q_weight, (d,), dt, dev), _at("k_weight", k_weight, (d,), dt, dev),
+            _at("positions", positions, (B, L), torch.int32, dev), freq, B, H, Hkv, L, d, rotary,
+            lay, 1 if interleaved else 0, eps, dtype, *_scratch(workspace, dev))
+    _call("mha_qk_norm_rope_bwd", dev, stream, args)
     return dq, dk, dq_weight, dk_weight
 
 
-def _cache(k_cache, v_cache, ref, Hkv, layout):
+def _cache(k_cache, v_cache, d, Hkv, layout, dt, dev):
     """(k address, v address, num_pages, page_size) of a paged cache."""
     if k_cache.dim() != 4:
         raise ValueError("the caches must have 4 dimensions")
-    pages, page = k_cache.shape[0], k_cache.shape[1 if layout == MHA_LAYOUT_BSHD else 2]
-    d = ref.shape[-1]
-    shape = (pages, page, Hkv, d) if layout == MHA_LAYOUT_BSHD else (pages, Hkv, page, d)
-    return _like("k_cache", k_cache, ref, shape), _like("v_cache", v_cache, ref, shape), pages, page
+    pages, a, b, _ = shape = k_cache.shape
+    page = a if layout == MHA_LAYOUT_BSHD else b
+    if (b if layout == MHA_LAYOUT_BSHD else a) != Hkv or shape[3] != d:
+        raise ValueError("the caches must have %d heads of %d, not shape %s"
+                         % (Hkv, d, tuple(shape)))
+    return (_at("k_cache", k_cache, shape, dt, dev), _at("v_cache", v_cache, shape, dt, dev), pages,
+            page)
 
 
-def _batch(q_starts, kv_lengths, block_table, ref):
+def _batch(q_starts, kv_lengths, block_table, dev):
     """(addresses of the three arrays, B, max_pages) of a ragged batch."""
-    import torch
+    i32 = _torch().int32
     if block_table.dim() != 2:
         raise ValueError("block_table must have 2 dimensions")
-    B, max_pages = block_table.shape
-    return (_array("q_starts", q_starts, ref, torch.int32, (B + 1,)),
-            _array("kv_lengths", kv_lengths, ref, torch.int32, (B,)),
-            _array("block_table", block_table, ref, torch.int32, (B, max_pages))), B, max_pages
+    B, max_pages = table = block_table.shape
+    return (_at("q_starts", q_starts, (B + 1,), i32, dev),
+            _at("kv_lengths", kv_lengths, (B,), i32, dev),
+            _at("block_table", block_table, table, i32, dev)), B, max_pages
 
 
 def mha_paged_append(q, k, v, k_cache, v_cache, q_out=None, *, q_starts, kv_lengths, block_table,
@@ -281,33 +284,33 @@ def mha_paged_append(q, k, v, k_cache, v_cache, q_out=None, *, q_starts, kv_leng
     [pages,page_size,H_kv,d].  Rows of no sequence keep what ``q_out`` held (zeros
     when it is allocated here); ``q_out`` may be q itself.
     """
-    import torch
     lay = _layout_of(layout)
     if k.dim() != 3:
         raise ValueError("q, k and v must have 3 dimensions")
-    dtype = _dtype_of(k)
-    T, Hkv, d = k.shape
+    dtype, dt, dev = _dtype_of(k), k.dtype, _device_of(k)
+    T, Hkv, d = ks = k.shape
     H = 0 if q is None else q.shape[1]
-    if q is not None and q_out is None:
+    if q is None:
+        q_out = None
+    elif q_out is None:
         with _on(stream, k.device):
-            q_out = torch.zeros_like(q)
-    kc, vc, pages, page = _cache(k_cache, v_cache, k, Hkv, lay)
-    arrays, B, max_pages = _batch(q_starts, kv_lengths, block_table, k)
-    freq, rotary = _rotary(inv_freq, k)
-    args = (None if q is None else _like("q", q, k, (T, H, d)), _like("k", k, k, (T, Hkv, d)),
-            _like("v", v, k, (T, Hkv, d)),
-            None if q is None else _like("q_out", q_out, k, (T, H, d)), kc, vc,
-            _weight("q_weight", q_weight, k), _weight("k_weight", k_weight, k), freq, *arrays, B, T,
-            H, Hkv, d, pages, page, max_pages, rotary, lay, int(bool(interleaved)), float(eps),
-            dtype)
-    _call("mha_paged_append", k, stream, args)
+            q_out = _torch().zeros_like(q)
+    kc, vc, pages, page = _cache(k_cache, v_cache, d, Hkv, lay, dt, dev)
+    arrays, B, max_pages = _batch(q_starts, kv_lengths, block_table, dev)
+    freq, rotary = _rotary(inv_freq, dev)
+    args = (_at("q", q, (T, H, d), dt, dev), _at("k", k, ks, dt, dev), _at("v", v, ks, dt, dev),
+            _at("q_out", q_out, (T, H, d), dt, dev), kc, vc,
+            _at("q_weight", q_weight, (d,), dt, dev), _at("k_weight", k_weight, (d,), dt, dev), freq,
+            *arrays, B, T, H, Hkv, d, pages, page, max_pages, rotary, lay, 1 if interleaved else 0,
+            eps, dtype)
+    _call("mha_paged_append", dev, stream, args)
     return q_out
 
 
 def mha_paged_workspace_size(B, T, H, H_kv, d, max_q, dtype) -> int:
     """Bytes of workspace of mha_paged_fwd; ``dtype``: a torch dtype or MHA_DTYPE_*."""
     if not isinstance(dtype, int):
-        import torch
+        torch = _torch()
         dtype = {torch.bfloat16: MHA_DTYPE_BF16, torch.float32: MHA_DTYPE_F32}[dtype]
     return int(lib.mha_paged_workspace_size(B, T, H, H_kv, d, max_q, dtype))
 
@@ -328,25 +331,23 @@ def mha_paged_fwd(q, k_cache, v_cache, out=None, *, q_starts, kv_lengths, block_
     1/sqrt(d).  ``workspace``: uint8 CUDA tensor of at least
     mha_paged_workspace_size(B, T, H, H_kv, d, max_q, q.dtype) bytes (allocated here
     when None)."""
-    import torch
     lay = _layout_of(layout)
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must have 3 dimensions and the caches 4")
-    dtype = _dtype_of(q)
-    T, H, d = q.shape
+    dtype, dt, dev = _dtype_of(q), q.dtype, _device_of(q)
+    T, H, d = qs = q.shape
     Hkv = k_cache.shape[2 if lay == MHA_LAYOUT_BSHD else 1]
-    kc, vc, pages, page = _cache(k_cache, v_cache, q, Hkv, lay)
-    arrays, B, max_pages = _batch(q_starts, kv_lengths, block_table, q)
+    kc, vc, pages, page = _cache(k_cache, v_cache, d, Hkv, lay, dt, dev)
+    arrays, B, max_pages = _batch(q_starts, kv_lengths, block_table, dev)
     if out is None or workspace is None:
+        torch = _torch()
         with _on(stream, q.device):
             out = torch.zeros_like(q) if out is None else out
             if workspace is None:
                 n = mha_paged_workspace_size(B, T, H, Hkv, d, max_q, dtype)
                 workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
-    if scale is None:
-        scale = float(d) ** -0.5
-    args = (_like("q", q, q, (T, H, d)), kc, vc, _like("out", out, q, (T, H, d)), *arrays, B, T, H,
-            Hkv, d, max_q, pages, page, max_pages, lay, int(mask_kind), float(scale), dtype,
-            *_scratch(workspace, q))
-    _call("mha_paged_fwd", q, stream, args)
+    args = (_at("q", q, qs, dt, dev), kc, vc, _at("out", out, qs, dt, dev), *arrays, B, T, H, Hkv, d,
+            max_q, pages, page, max_pages, lay, mask_kind, d ** -0.5 if scale is None else scale,
+            dtype, *_scratch(workspace, dev))
+    _call("mha_paged_fwd", dev, stream, args)
     return out
