@@ -35,6 +35,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kFwdCtas = 3, kBwdCtas = 2;  // per SM
+constexpr int kSlots = 4;                  // rounds of the backward in shared memory, per warp
+constexpr int kSlotBytes = 1024;           // of a round: 16 of dy and 16 of x per lane
 
 // 16 bytes of a row, as a lane holds them: two pieces of 8 bytes.
 template <typename T>
@@ -102,6 +104,19 @@ __device__ __forceinline__ uint4 ld8x2(const void *lo, const void *hi) {
 __device__ __forceinline__ void st8x2(void *lo, void *hi, uint4 v) {
   asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(lo), "r"(v.x), "r"(v.y) : "memory");
   asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(hi), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// 8 bytes to shared memory, without waiting; zeros unless `is`
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool is) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(is ? 8 : 0)
+               : "memory");
+}
+// a lane's two pieces of 8 bytes, 256 apart
+__device__ __forceinline__ uint4 lds8x2(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.z), "=r"(v.w) : "r"(at + 256) : "memory");
+  return v;
 }
 
 // frac(f / 2 pi) 2^64 for f = m 2^e: m times 2^66 / 2 pi (rounded to 64 bits), shifted
@@ -419,84 +434,160 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const Rope
   }
 }
 
+// Where a token's rows lie in q and k, from token to token without a division.
+struct Token {
+  long long q, k, step;  // element offsets of heads 0, step per head
+  int l;
+  __device__ __forceinline__ Token(const RopeArgs &a, int t, int d) {
+    const Rows rq = rows_of(a.layout, t, a.H, a.L, d), rk = rows_of(a.layout, t, a.Hkv, a.L, d);
+    q = rq.base;
+    k = rk.base;
+    step = rq.step;
+    l = a.layout == kLayoutBSHD ? 0 : t % a.L;
+  }
+  __device__ __forceinline__ void next(const RopeArgs &a, int d) {
+    if (a.layout == kLayoutBSHD) {
+      q += a.H * d;
+      k += a.Hkv * d;
+    } else {
+      q += d;
+      k += d;
+      if (++l == a.L) {  // past the other heads' rows, to the next sequence's first
+        l = 0;
+        q += (a.H - 1) * step;
+        k += (a.Hkv - 1) * step;
+      }
+    }
+  }
+};
+
+// The backward's rows on their way in.  A warp copies the rounds of its stretch
+// kSlots - 1 rounds before it works on them, into its own slots of shared memory: every
+// lane reads back what it copied itself, so nothing is waited for but the copies, and
+// they go on across heads and tokens.  A copy goes to the slot whose round was worked
+// on last, never to the one being read.
+template <typename T, int D, int kStyle>
+struct Ahead {
+  static constexpr int G = Angles<T, D>::kGroups;
+  const RopeArgs &a;
+  const Place<T, D, kStyle> &place;
+  Token token;
+  const T *g, *x;       // this lane's row of the next round: dy, x (null: not needed)
+  int left;             // rounds still to be copied
+  int group, h, heads;  // its head, of how many
+  int more;             // rounds of this token's tensor still to be copied
+  bool of_q;
+  int slot;
+  uint32_t at;  // this lane's 32 bytes of slot 0: dy's two pieces, x's two pieces
+  __device__ __forceinline__ Ahead(const RopeArgs &args, const Place<T, D, kStyle> &pl, int t, int r,
+                                   int rounds, int rq, int rk, int grp, uint32_t base)
+      : a(args), place(pl), token(args, t, D), left(rounds), group(grp), slot(0), at(base) {
+    of_q = r < rq;
+    if (left > 0) tensor(of_q ? r : r - rq, of_q ? rq : rk);
+  }
+  // round `from` of `rounds` comes next
+  __device__ __forceinline__ void tensor(int from, int rounds) {
+    h = from * G + group;
+    heads = of_q ? a.H : a.Hkv;
+    more = rounds - from;
+    const long long first = (of_q ? token.q : token.k) + h * token.step + place.lo;
+    g = static_cast<const T *>(of_q ? a.dq_out : a.dk_out) + first;
+    const void *rows = of_q ? a.q : a.k;
+    x = (of_q ? a.q_weight : a.k_weight) != nullptr ? static_cast<const T *>(rows) + first : nullptr;
+  }
+  // starts the next round's copies (an absent row's places are zeroed)
+  __device__ __forceinline__ void start(int rq, int rk) {
+    if (left > 0) {
+      const bool is = h < heads;
+      const uint32_t dst = at + slot * kSlotBytes;
+      copy8(dst, g, is);
+      copy8(dst + 256, g + place.apart, is);
+      if (x != nullptr) {
+        copy8(dst + 512, x, is);
+        copy8(dst + 768, x + place.apart, is);
+        x += G * token.step;
+      }
+      g += G * token.step;
+      h += G;
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
+      if (--left > 0 && --more == 0) {
+        of_q = !of_q;
+        if (of_q ? rq == 0 : rk == 0) {  // one tensor alone
+          of_q = !of_q;
+          token.next(a, D);
+        } else if (of_q) {
+          token.next(a, D);
+        }
+        tensor(0, of_q ? rq : rk);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
+
 // Gradients of rounds [from, to) of one tensor; this lane's share of the weight's
 // gradient is added to dw.
 template <typename T, int D, int kStyle>
-__device__ __forceinline__ void bwd_rows(const T *x_in, const T *dy, T *dx, long long step,
-                                         int heads, int from, int to, int group,
-                                         const Place<T, D, kStyle> &place, const T *weight, float eps,
-                                         const Angles<T, D> &ang,
+__device__ __forceinline__ void bwd_rows(Ahead<T, D, kStyle> &ahead, int rq, int rk, int &slot, T *dx,
+                                         long long step, int heads, int from, int to,
+                                         const Place<T, D, kStyle> &place, bool normed, uint4 weight,
+                                         float eps, const Angles<T, D> &ang,
                                          uint64_t (&da)[Place<T, D, kStyle>::kTwos],
                                          uint64_t (&db)[Place<T, D, kStyle>::kTwos]) {
   using P = Place<T, D, kStyle>;
   using A = Angles<T, D>;
-  constexpr int kTwos = P::kTwos, kBatch = 2;
+  constexpr int kTwos = P::kTwos;
   if (from >= to) return;
-  const bool normed = weight != nullptr;
   uint64_t wa[kTwos], wb[kTwos];
-  if (normed) P::unpack(place.load(weight), wa, wb);
-  int h = from * A::kGroups + group;
-  x_in += h * step;
-  dy += h * step;
+  P::unpack(weight, wa, wb);
+  int h = from * A::kGroups + ahead.group;
   dx += h * step;
   step *= A::kGroups;
-  uint4 raw_x[kBatch], raw_g[kBatch];
-  auto load = [&](int j) {
+#pragma unroll 1
+  for (int j = from; j < to; ++j) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
+    const uint32_t src = ahead.at + slot * kSlotBytes;
+    const uint4 raw_g = lds8x2(src), raw_x = normed ? lds8x2(src + 512) : make_uint4(0, 0, 0, 0);
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
+    ahead.start(rq, rk);
+    const bool is = h < heads;
+    uint64_t ga[kTwos], gb[kTwos];
+    P::unpack(raw_g, ga, gb);
+    if (place.on) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      raw_x[i] = raw_g[i] = make_uint4(0, 0, 0, 0);
-      if (j + i < to && h + i * A::kGroups < heads) {
-        raw_g[i] = place.load(dy);
-        if (normed) raw_x[i] = place.load(x_in);
+      for (int e = 0; e < kTwos; ++e) {
+        const uint64_t a = ga[e], b = gb[e];
+        ga[e] = fma2(b, ang.s[e], mul2(a, ang.c[e]));
+        gb[e] = fma2(mul2(a, both(-1.f)), ang.s[e], mul2(b, ang.c[e]));
       }
-      dy += step;
-      x_in += step;
     }
-  };
-  load(from);
-  for (int j = from; j < to; j += kBatch) {
+    if (normed) {
+      uint64_t xa[kTwos], xb[kTwos], va[kTwos], vb[kTwos];
+      P::unpack(raw_x, xa, xb);
+      uint64_t sq2 = 0ull, dot2 = 0ull;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const bool is = j + i < to && h + i * A::kGroups < heads;
-      uint64_t ga[kTwos], gb[kTwos];
-      P::unpack(raw_g[i], ga, gb);
-      if (place.on) {
-#pragma unroll
-        for (int e = 0; e < kTwos; ++e) {
-          const uint64_t a = ga[e], b = gb[e];
-          ga[e] = fma2(b, ang.s[e], mul2(a, ang.c[e]));
-          gb[e] = fma2(mul2(a, both(-1.f)), ang.s[e], mul2(b, ang.c[e]));
-        }
+      for (int e = 0; e < kTwos; ++e) {
+        va[e] = mul2(ga[e], wa[e]);
+        vb[e] = mul2(gb[e], wb[e]);
+        sq2 = fma2(xb[e], xb[e], fma2(xa[e], xa[e], sq2));
+        dot2 = fma2(vb[e], xb[e], fma2(va[e], xa[e], dot2));
       }
-      if (normed) {
-        uint64_t xa[kTwos], xb[kTwos], va[kTwos], vb[kTwos];
-        P::unpack(raw_x[i], xa, xb);
-        uint64_t sq2 = 0ull, dot2 = 0ull;
+      const float sq = row_sum<A::kLanes>(sum2(sq2)), dot = row_sum<A::kLanes>(sum2(dot2));
+      const float inv = rsqrtf(sq * (1.f / D) + eps);
+      // minus inv^2 times the mean of (w g) x
+      const uint64_t m = both(-(dot * (1.f / D)) * inv * inv), i2 = both(inv);
+      const uint64_t add = both(is ? inv : 0.f);  // an absent row adds nothing (its inv may be infinite)
 #pragma unroll
-        for (int e = 0; e < kTwos; ++e) {
-          va[e] = mul2(ga[e], wa[e]);
-          vb[e] = mul2(gb[e], wb[e]);
-          sq2 = fma2(xb[e], xb[e], fma2(xa[e], xa[e], sq2));
-          dot2 = fma2(vb[e], xb[e], fma2(va[e], xa[e], dot2));
-        }
-        const float sq = row_sum<A::kLanes>(sum2(sq2)), dot = row_sum<A::kLanes>(sum2(dot2));
-        const float inv = rsqrtf(sq * (1.f / D) + eps);
-        // minus inv^2 times the mean of (w g) x
-        const uint64_t m = both(-(dot * (1.f / D)) * inv * inv), i2 = both(inv);
-        const uint64_t add = both(is ? inv : 0.f);  // an absent row adds nothing (its inv may be infinite)
-#pragma unroll
-        for (int e = 0; e < kTwos; ++e) {
-          da[e] = fma2(ga[e], mul2(xa[e], add), da[e]);
-          db[e] = fma2(gb[e], mul2(xb[e], add), db[e]);
-          ga[e] = mul2(i2, fma2(xa[e], m, va[e]));
-          gb[e] = mul2(i2, fma2(xb[e], m, vb[e]));
-        }
+      for (int e = 0; e < kTwos; ++e) {
+        da[e] = fma2(ga[e], mul2(xa[e], add), da[e]);
+        db[e] = fma2(gb[e], mul2(xb[e], add), db[e]);
+        ga[e] = mul2(i2, fma2(xa[e], m, va[e]));
+        gb[e] = mul2(i2, fma2(xb[e], m, vb[e]));
       }
-      if (is) place.store(dx, P::pack(ga, gb));
-      dx += step;
     }
-    h += kBatch * A::kGroups;
-    if (j + kBatch < to) load(j + kBatch);
+    if (is) place.store(dx, P::pack(ga, gb));
+    dx += step;
+    h += A::kGroups;
   }
 }
 
@@ -504,7 +595,9 @@ template <typename T, int D, int kStyle>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const RopeArgs a, int warps) {
   using A = Angles<T, D>;
   using P = Place<T, D, kStyle>;
-  __shared__ float sums[kWarps * A::kGroups][D];
+  __shared__ __align__(16) unsigned char ring[kWarps * kSlots * kSlotBytes];
+  float (*sums)[D] = reinterpret_cast<float (*)[D]>(ring);  // when the rows are done
+  static_assert(sizeof(float) * kWarps * A::kGroups * D <= sizeof(ring), "the sums fit");
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = lane % A::kLanes, group = lane / A::kLanes;
@@ -514,26 +607,38 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const Rope
   uint64_t qa[P::kTwos], qb[P::kTwos], ka[P::kTwos], kb[P::kTwos];  // the weights' gradients
 #pragma unroll
   for (int e = 0; e < P::kTwos; ++e) qa[e] = qb[e] = ka[e] = kb[e] = 0ull;
-  griddep_wait();
-  A ang;
-  ang.frequencies(a.inv_freq, place.freq, place.on, group);
   // (a warp past the last has an empty stretch: it still joins the sums)
   Stretch stretch(static_cast<long long>(a.tokens) * (rq + rk), min(w, warps - 1), warps);
   if (w >= warps) stretch.at = stretch.end;
-  int t, lo, hi;
+  griddep_wait();
+  const long long first = stretch.at / (rq + rk);
+  Token token(a, static_cast<int>(first), D);
+  Ahead<T, D, kStyle> ahead(a, place, static_cast<int>(first),
+                            static_cast<int>(stretch.at - first * (rq + rk)),
+                            static_cast<int>(stretch.end - stretch.at), rq, rk, group,
+                            smem_addr(ring) + warp * (kSlots * kSlotBytes) + lane * 8);
+#pragma unroll 1
+  for (int i = 0; i < kSlots - 1; ++i) ahead.start(rq, rk);
+  auto position = [&](int t) { return a.positions != nullptr ? a.positions[t] : t % a.L; };
+  int pos = stretch.at < stretch.end ? position(static_cast<int>(first)) : 0;
+  const bool q_normed = a.q_weight != nullptr, k_normed = a.k_weight != nullptr;
+  uint4 qw = make_uint4(0, 0, 0, 0), kw = qw;
+  if (q_normed) qw = place.load(static_cast<const T *>(a.q_weight));
+  if (k_normed) kw = place.load(static_cast<const T *>(a.k_weight));
+  A ang;
+  ang.frequencies(a.inv_freq, place.freq, place.on, group);
+  int t, lo, hi, slot = 0;
   while (stretch.next(rq + rk, t, lo, hi)) {
-    ang.at(a.positions != nullptr ? a.positions[t] : t % a.L, col);
-    const Rows q = rows_of(a.layout, t, a.H, a.L, D), k = rows_of(a.layout, t, a.Hkv, a.L, D);
-    bwd_rows<T, D, kStyle>(static_cast<const T *>(a.q) + q.base,
-                           static_cast<const T *>(a.dq_out) + q.base,
-                           static_cast<T *>(a.q_out) + q.base, q.step, a.H, lo, min(hi, rq),
-                           group, place, static_cast<const T *>(a.q_weight), a.eps, ang, qa, qb);
-    bwd_rows<T, D, kStyle>(static_cast<const T *>(a.k) + k.base,
-                           static_cast<const T *>(a.dk_out) + k.base,
-                           static_cast<T *>(a.k_out) + k.base, k.step, a.Hkv, max(lo - rq, 0),
-                           hi - rq, group, place, static_cast<const T *>(a.k_weight), a.eps,
-                           ang, ka, kb);
+    const int now = pos;
+    if (stretch.at < stretch.end) pos = position(t + 1);
+    ang.at(now, col);
+    bwd_rows<T, D, kStyle>(ahead, rq, rk, slot, static_cast<T *>(a.q_out) + token.q, token.step, a.H,
+                           lo, min(hi, rq), place, q_normed, qw, a.eps, ang, qa, qb);
+    bwd_rows<T, D, kStyle>(ahead, rq, rk, slot, static_cast<T *>(a.k_out) + token.k, token.step,
+                           a.Hkv, max(lo - rq, 0), hi - rq, place, k_normed, kw, a.eps, ang, ka, kb);
+    token.next(a, D);
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   // this CTA's sums over its row groups, in a fixed order
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
