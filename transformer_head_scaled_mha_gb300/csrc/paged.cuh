@@ -161,16 +161,21 @@ struct PagedSpan {
   int ctas;          // G
 };
 
+// CTAs that a line of length `total` with `units` units has work for.
+MHA_HD long long paged_ctas(long long total, long long units, int min_stretch) {
+  const long long by_work = static_cast<int>(total >> 8 > 0x7fffffff ? 0x7fffffff : total >> 8) / min_stretch;  // kTileCost is 2^8
+  const long long most = by_work > units ? by_work : units;
+  // a stretch is longer than a tile, so that no CTA between a unit's first and last
+  // part is without one (paged_merge_kernel takes them as neighbours)
+  const long long cap = (total >> 8) * 31 / 32;
+  return most < cap ? most : cap;
+}
+
 // The stretch of CTA `cta` of `grid` on a line of length `total` with `units` units.
 MHA_HD PagedSpan paged_stretch(long long total, long long units, int cta, int grid,
                                int min_stretch) {
   PagedSpan sp;
-  const long long by_work = static_cast<int>(total >> 8 > 0x7fffffff ? 0x7fffffff : total >> 8) / min_stretch;  // kTileCost is 2^8
-  long long most = by_work > units ? by_work : units;
-  // a stretch is longer than a tile, so that no CTA between a unit's first and last
-  // part is without one (paged_merge_kernel takes them as neighbours)
-  const long long cap = (total >> 8) * 31 / 32;
-  if (most > cap) most = cap;
+  const long long most = paged_ctas(total, units, min_stretch);
   sp.ctas = static_cast<int>(most < 1 ? 1 : (most < grid ? most : grid));
   // equal stretches, a little short (the last CTA takes what is left, some millionths):
   // an approximate quotient, for a 64-bit division is a hundred instructions

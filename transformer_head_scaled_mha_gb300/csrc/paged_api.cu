@@ -360,6 +360,19 @@ extern "C" size_t mha_paged_workspace_size(int B, int T, int H, int H_kv, int d,
   return workspace_bytes_of(units_of(path, H / H_kv, max_q), d);
 }
 
+// The CTAs that a call's shapes have work for, at most `grid`: what no sequence can
+// need is not launched (one token over 300 keys of 8 heads: 24 CTAs, not 304).
+static int launched_ctas(const PagedProblem &p, int grid) {
+  const long long blocks = std::min<long long>(p.batch.T, p.batch.B + p.batch.T / p.tb);
+  const long long units = blocks * p.Hkv * p.hblocks;
+  if (units >= grid) return grid;
+  const long long keys = static_cast<long long>(p.batch.max_pages) << p.batch.page_shift;
+  const long long tiles = (keys + kPagedTile - 1) / kPagedTile;
+  const long long total = units * (p.split.unit_cost + kTileCost / 2 + tiles * kTileCost);
+  return static_cast<int>(
+      std::max(1LL, std::min<long long>(grid, paged_ctas(total, units, p.split.min_stretch))));
+}
+
 extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_cache, void *out,
                              const int32_t *q_starts, const int32_t *kv_lengths,
                              const int32_t *block_table, int B, int T, int H, int H_kv, int d,
@@ -416,10 +429,10 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   p.wait_ns = wait_limit_ns();
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   p.split = u.split;
-  int grid = u.ctas;
+  int grid = launched_ctas(p, u.ctas);
   cudaError_t err = cudaSuccess;
   if (path == kSimt) {
-    grid = std::min(u.ctas, (d == 64 ? 2 : 1) * sms);  // CTAs that run at a time
+    grid = std::min(grid, (d == 64 ? 2 : 1) * sms);  // CTAs that run at a time
     err = launch_paged_simt(p, d, grid, stream);
   } else {
     CUtensorMap qm, km, vm;

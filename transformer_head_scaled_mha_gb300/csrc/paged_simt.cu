@@ -3,13 +3,18 @@
 //
 // A CTA of four warps walks its parts (paged.cuh): R <= 16 query rows of one
 // key/value head against tiles of 128 keys.  Warp w takes keys 32 w .. 32 w + 31
-// of each tile, a key per lane: scores of all R rows against the lane's key
-// (keys staged in shared memory, rows padded by 16 bytes so that lanes read
-// without conflicts; queries broadcast), an online softmax per warp, then the
-// value rows, each lane owning d / 32 output columns.  Keys and values are copied
-// to shared memory without registers (cp.async): the next tile's keys while this
-// one's softmax and values are worked on, its values while the next scores are, so
-// a warp always has a tile in flight.  The warps' sums are joined once per part.
+// of each tile: scores with a key per lane (keys staged in shared memory, rows padded
+// by 16 bytes so that lanes read without conflicts; queries broadcast), an online
+// softmax with a row per lane, or 32 / R lanes to a row, through a small square of
+// shared memory, then the value rows, each lane owning d / 32 output columns.  Keys and
+// values are copied to shared memory without registers (cp.async): the next tile's keys
+// while this one's softmax and values are worked on, its values while the next scores
+// are, so a warp always has a tile in flight.  The warps' sums are joined once per part.
+//
+// Bound: few parts per CTA, so the time from launch to the first score and the code's
+// own way into the instruction caches; hence one copy loop for both ends of a tile
+// (the walk starts one tile early, with nothing to work on) and rows' places and
+// limits in shared memory, found once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -80,15 +85,20 @@ template <int D>
 struct Smem {
   float q[kRows][D];
   float k[kWarps][kKeys][D + 4];
-  float v[kWarps][kKeys][D];  // at a part's end the warps' sums
-  float p[kWarps][kKeys][kRows];
+  float v[kWarps][kKeys][D];          // at a part's end the warps' sums
+  float p[kWarps][kKeys][kRows + 4];  // scores, then their powers
+  float alpha[kWarps][kRows];         // what the older sums shrink to
   float m[kWarps][kRows], l[kWarps][kRows];
+  float f[kWarps][kRows], total[kRows];  // the warps' weights when joined, and the sum
+  long long row[kRows];                  // where a row's query and output begin (-1: no row)
+  int lim[kRows];                        // keys below this are allowed
   long long scratch[40];
 };
 
 template <int D, int RP>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_constant__ PagedProblem p) {
+__global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_constant__ PagedProblem p) {
   constexpr int kC = D / 32;  // output columns of a lane
+  constexpr int kPer = 32 / RP;  // lanes to a row in the softmax
   static_assert(kRows <= kKeys, "a warp's sums fit where its values were");
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
@@ -103,142 +113,175 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
   const float *q = static_cast<const float *>(p.q);
   const float *kc = static_cast<const float *>(p.k), *vc = static_cast<const float *>(p.v);
   float *out = static_cast<float *>(p.out);
+  float *kw = &sm.k[warp][0][0], *vw = &sm.v[warp][0][0];
+  // copies a warp's 32 cache rows, one per lane's cell, zeros where there is none; 16
+  // bytes per lane
+  auto copy = [&](const float *cache, float *to, int stride, long long cell) {
+    constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;  // lanes per row, rows at once
+    const int c = (lane % kLanes) * 4;
+#pragma unroll 4
+    for (int j = 0; j < kKeys; j += kAtOnce) {
+      const int row = j + lane / kLanes;
+      const long long at = __shfl_sync(0xffffffffu, cell, row);
+      cp_async16_or_zero(smem_addr(to + row * stride + c), cache + (at < 0 ? 0 : at) * D + c,
+                         at >= 0);
+    }
+    cp_async_commit();
+  };
   while (walk.next(p, part)) {
     __syncthreads();  // the part before has read q and the warps' sums
-    for (int e = threadIdx.x; e < RP * D; e += kThreads) {
-      const int r = e / D, c = e - r * D;
-      const int h = r / p.tb, i = part.i0 + r % p.tb;
-      float x = 0.f;
-      if (h < part.heads && i < part.i1)
-        x = q[(static_cast<long long>(part.seq.q0 + i) * p.H + part.h0 + h) * D + c];
-      sm.q[r][c] = x;
+    if (threadIdx.x < RP) {
+      const int r = threadIdx.x, h = r / p.tb, i = part.i0 + r - h * p.tb;
+      sm.row[r] = h < part.heads && i < part.i1
+                      ? (static_cast<long long>(part.seq.q0 + i) * p.H + part.h0 + h) * D
+                      : -1;
+      sm.lim[r] = paged_kv_end(part.seq, i + 1, p.causal);
     }
     __syncthreads();
-    float m[RP], l[RP], acc[RP][kC];
-    int lim[RP];  // keys below this are allowed
+    for (int e = threadIdx.x * 4; e < RP * D; e += kThreads * 4) {
+      const long long row = sm.row[e / D];
+      *reinterpret_cast<float4 *>(&sm.q[0][e]) =
+          row >= 0 ? *reinterpret_cast<const float4 *>(q + row + e % D) : make_float4(0, 0, 0, 0);
+    }
+    const int mine = lane % RP, lim = sm.lim[mine];  // this lane's row in the softmax
+    float m = -INFINITY, l = 0.f;                    // ... its maximum, and its share of the sum
+    float acc[RP][kC];
 #pragma unroll
-    for (int r = 0; r < RP; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
+    for (int r = 0; r < RP; ++r)
 #pragma unroll
       for (int c = 0; c < kC; ++c) acc[r][c] = 0.f;
-      const int i = part.i0 + r % p.tb;
-      lim[r] = paged_kv_end(part.seq, i + 1, p.causal);
-    }
-    // a warp's keys of tile t: the cache rows, one per lane (-1: none)
-    auto cell_of = [&](int t) -> long long {
-      const int key = t * kPagedTile + warp * kKeys + lane;
-      return t < part.t1 && key < part.kv_end ? paged_cell(p.batch, part.b, key, part.kv, p.Hkv)
-                                              : -1;
-    };
-    // copies those rows, zeros where there is none; 16 bytes per lane
-    auto copy = [&](const float *cache, float *to, int stride, long long cell) {
-      constexpr int kPer = D / 4, kAtOnce = 32 / kPer;  // lanes per row, rows at once
-      const int c = (lane % kPer) * 4;
-#pragma unroll 8
-      for (int j = 0; j < kKeys; j += kAtOnce) {
-        const int row = j + lane / kPer;
-        const long long at = __shfl_sync(0xffffffffu, cell, row);
-        cp_async16_or_zero(smem_addr(to + row * stride + c), cache + (at < 0 ? 0 : at) * D + c,
-                           at >= 0);
-      }
-      cp_async_commit();
-    };
-    float *kw = &sm.k[warp][0][0], *vw = &sm.v[warp][0][0];
-    long long cell = cell_of(part.t0);
-    copy(kc, kw, D + 4, cell);
-    copy(vc, vw, D, cell);
-    for (int t = part.t0; t < part.t1; ++t) {
-      const int key = t * kPagedTile + warp * kKeys + lane;
-      const long long next = cell_of(t + 1);
-      cp_async_wait<1>();  // this tile's keys (its values may be on their way)
-      __syncwarp();
-      float s[RP];
+    __syncthreads();
+    long long cell = -1;
+#pragma unroll 1
+    for (int t = part.t0 - 1; t < part.t1; ++t) {
+      const bool work = t >= part.t0;
+      const int first = t * kPagedTile + warp * kKeys;  // this warp's keys
+      // the next tile's cache row, one per lane (-1: none)
+      const int ahead = first + kPagedTile + lane;
+      const long long next = t + 1 < part.t1 && ahead < part.kv_end
+                                 ? paged_cell(p.batch, part.b, ahead, part.kv, p.Hkv)
+                                 : -1;
+      if (work) {
+        cp_async_wait<1>();  // this tile's keys (its values may be on their way)
+        __syncwarp();
+        float s[RP];
 #pragma unroll
-      for (int r = 0; r < RP; ++r) s[r] = 0.f;
-#pragma unroll 4
-      for (int c = 0; c < D; c += 4) {
-        const float4 kv = *reinterpret_cast<const float4 *>(&sm.k[warp][lane][c]);
+        for (int r = 0; r < RP; ++r) s[r] = 0.f;
+#pragma unroll 2
+        for (int c = 0; c < D; c += 4) {
+          const float4 kv = *reinterpret_cast<const float4 *>(&sm.k[warp][lane][c]);
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[r][c]);
-          s[r] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[r]))));
+          for (int r = 0; r < RP; ++r) {
+            const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[r][c]);
+            s[r] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[r]))));
+          }
         }
+#pragma unroll
+        for (int r = 0; r < RP; ++r)
+          sm.p[warp][lane][r] = cell >= 0 ? s[r] * p.scale_log2 : -INFINITY;
+        __syncwarp();
       }
-      __syncwarp();
       copy(kc, kw, D + 4, next);
+      if (work) {
+        // row `mine`, keys lane / RP, + kPer, ...
+        float x[RP], top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        const float x = cell >= 0 && key < lim[r] ? s[r] * p.scale_log2 : -INFINITY;
-        const float mn = fmaxf(m[r], warp_max(x));
-        const float use = mn == -INFINITY ? 0.f : mn;
-        const float pr = ex2_approx(x - use);
-        const float alpha = ex2_approx(m[r] - use);
-        l[r] = l[r] * alpha + pr;
-        m[r] = mn;
+        for (int i = 0; i < RP; ++i) {
+          const int j = i * kPer + lane / RP;
+          x[i] = first + j < lim ? sm.p[warp][j][mine] : -INFINITY;
+          top = fmaxf(top, x[i]);
+        }
 #pragma unroll
-        for (int c = 0; c < kC; ++c) acc[r][c] *= alpha;
-        sm.p[warp][lane][r] = pr;
-      }
-      cp_async_wait<1>();  // this tile's values
-      __syncwarp();
-#pragma unroll 4
-      for (int j = 0; j < kKeys; ++j) {
-        float v[kC];
+        for (int o = RP; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float mn = fmaxf(m, top), use = mn == -INFINITY ? 0.f : mn;
+        const float alpha = ex2_approx(m - use);
 #pragma unroll
-        for (int c = 0; c < kC; ++c) v[c] = sm.v[warp][j][c * 32 + lane];
+        for (int i = 0; i < RP; ++i) {
+          const float pr = ex2_approx(x[i] - use);
+          sum += pr;
+          sm.p[warp][i * kPer + lane / RP][mine] = pr;
+        }
+        l = fmaf(l, alpha, sum);
+        m = mn;
+        if (lane < RP) sm.alpha[warp][lane] = alpha;
+        cp_async_wait<1>();  // this tile's values
+        __syncwarp();
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-          const float pr = sm.p[warp][j][r];
+          const float shrink = sm.alpha[warp][r];
 #pragma unroll
-          for (int c = 0; c < kC; ++c) acc[r][c] = fmaf(pr, v[c], acc[r][c]);
+          for (int c = 0; c < kC; ++c) acc[r][c] *= shrink;
         }
+#pragma unroll 4
+        for (int j = 0; j < kKeys; ++j) {
+          float v[kC];
+#pragma unroll
+          for (int c = 0; c < kC; ++c) v[c] = sm.v[warp][j][c * 32 + lane];
+#pragma unroll
+          for (int r = 0; r < RP; ++r) {
+            const float pr = sm.p[warp][j][r];
+#pragma unroll
+            for (int c = 0; c < kC; ++c) acc[r][c] = fmaf(pr, v[c], acc[r][c]);
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
       copy(vc, vw, D, next);
       cell = next;
     }
     cp_async_wait<0>();
     // join the warps: each leaves its sums where its values were
     __syncwarp();
-    float *mine = vw;
 #pragma unroll
-    for (int r = 0; r < RP; ++r) {
-      const float lw = warp_sum(l[r]);
-      if (lane == 0) {
-        sm.m[warp][r] = m[r];
-        sm.l[warp][r] = lw;
-      }
-#pragma unroll
-      for (int c = 0; c < kC; ++c) mine[r * D + c * 32 + lane] = acc[r][c];
+    for (int o = RP; o < 32; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane < RP) {
+      sm.m[warp][lane] = m;
+      sm.l[warp][lane] = l;
     }
+#pragma unroll
+    for (int r = 0; r < RP; ++r)
+#pragma unroll
+      for (int c = 0; c < kC; ++c) vw[r * D + c * 32 + lane] = acc[r][c];
     __syncthreads();
     const bool split = paged_split(part);
     float *slot = split ? paged_slot_ptr(p, D, blockIdx.x, paged_slot(part)) : nullptr;
-    for (int e = threadIdx.x; e < RP * D; e += kThreads) {
-      const int r = e / D, c = e - r * D;
-      const int h = r / p.tb, i = part.i0 + r % p.tb;
-      if (h >= part.heads || i >= part.i1) continue;
-      float mt = -INFINITY;
+    if (threadIdx.x < RP) {
+      const int r = threadIdx.x;
+      float mt = -INFINITY, lt = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, sm.m[w][r]);
       const float use = mt == -INFINITY ? 0.f : mt;
-      float lt = 0.f, o = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2_approx(sm.m[w][r] - use);
         lt = fmaf(sm.l[w][r], f, lt);
-        o = fmaf(sm.v[w][0][r * D + c], f, o);
+        sm.f[w][r] = f;
+      }
+      sm.total[r] = lt;
+      if (split && sm.row[r] >= 0) {
+        slot[p.rows * D + 2 * r] = mt;
+        slot[p.rows * D + 2 * r + 1] = lt;
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x * 4; e < RP * D; e += kThreads * 4) {
+      const int r = e / D;
+      const long long row = sm.row[r];
+      if (row < 0) continue;
+      float o[4] = {0.f, 0.f, 0.f, 0.f}, v[4];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        ld_cols(&sm.v[w][0][e], v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = fmaf(v[c], sm.f[w][r], o[c]);
       }
       if (split) {
-        slot[r * D + c] = o;
-        if (c == 0) {
-          slot[p.rows * D + 2 * r] = mt;
-          slot[p.rows * D + 2 * r + 1] = lt;
-        }
+        st_cols(slot + e, o);
       } else {
-        out[(static_cast<long long>(part.seq.q0 + i) * p.H + part.h0 + h) * D + c] =
-            lt > 0.f ? o / lt : 0.f;
+        const float lt = sm.total[r];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = lt > 0.f ? o[c] / lt : 0.f;
+        st_cols(out + row + e % D, o);
       }
     }
     if (split) {
