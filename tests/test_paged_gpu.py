@@ -181,6 +181,31 @@ def test_offsets_and_lengths_out_of_range(dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 12, 90])
+def test_output_at_any_16_bytes(dt, n):
+    # the rows' stores may be wider than that: the same numbers whatever the address
+    import torch
+    import transformer_head_scaled_mha_gb300 as mha
+    rng = np.random.default_rng(3)
+    H, d, page = 4, 64, 32
+    b = batch(rng, [(n, 300), (0, 40), (2 * n, 5 * n + 7)], page, behind=2)
+    kc, vc = (dev(x, dt) for x in cache_of(rng, b, 2, page, d, dt, "bshd"))
+    q = dev(rnd(rng, (b["T"], H, d), dt), dt)
+    outs = []
+    for offset in (0, 16 // q.element_size(), 32 // q.element_size()):
+        buf = torch.full((q.numel() + 64,), 3.0, dtype=q.dtype, device="cuda")
+        out = buf[offset:offset + q.numel()].view(q.shape)
+        mha.mha_paged_fwd(q, kc, vc, out, q_starts=dev(b["starts"]), kv_lengths=dev(b["lens"]),
+                          block_table=dev(b["table"]), max_q=2 * n, layout="bshd", mask_kind=8,
+                          scale=0.1)
+        torch.cuda.synchronize()
+        assert (buf[:offset] == 3).all() and (buf[offset + q.numel():] == 3).all()
+        assert (out[-2:] == 3).all()
+        outs.append(out.clone())
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0])
 @pytest.mark.parametrize("n", [1, 33])
 def test_scales(dt, scale, n):

@@ -386,8 +386,9 @@ MHA_HD bool paged_split(const PagedPart &part) {
 // slot of a split part
 MHA_HD int paged_slot(const PagedPart &part) { return part.t0 > 0 ? 0 : 1; }
 
-// One slot: rows x d sums, then rows x (max, sum); whole 16-byte pieces, because the
-// sums are read and written 16 bytes at a time.
+// One slot: rows x d sums (of the many-query kernel [d / 4][rows][4]), then rows x
+// (max, sum); whole 16-byte pieces, because the sums are read and written 16 bytes at a
+// time.
 MHA_HD size_t paged_slot_floats(int rows, int d) {
   return (static_cast<size_t>(rows) * (d + 2) + 3) / 4 * 4;
 }
@@ -422,8 +423,8 @@ cudaError_t launch_paged_many(const CUtensorMap &q, const CUtensorMap &k, const 
                               const PagedProblem &p, int d, int grid, cudaStream_t stream);
 // fp32, at most 16 rows per unit
 cudaError_t launch_paged_simt(const PagedProblem &p, int d, int grid, cudaStream_t stream);
-// joins the parts of split units
-cudaError_t launch_paged_merge(const PagedProblem &p, int d, int dtype, int grid,
+// joins the parts of split units; `many`: of launch_paged_many
+cudaError_t launch_paged_merge(const PagedProblem &p, int d, int dtype, bool many, int grid,
                                cudaStream_t stream);
 
 }  // namespace mha

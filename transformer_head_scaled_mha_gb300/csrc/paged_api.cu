@@ -456,6 +456,6 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   // table has no room for them
   const long long most = static_cast<long long>(max_pages) * page_size;
   if (err == cudaSuccess && most > (2 * u.split.min_part - 1) * kPagedTile)
-    err = launch_paged_merge(p, d, dtype, grid, stream);
+    err = launch_paged_merge(p, d, dtype, path == kMany, grid, stream);
   return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }

@@ -165,14 +165,23 @@ __device__ __noinline__ void rescale_p16(uint32_t taddr, float f) {
   tmem_st16(taddr, r);
 }
 
+__device__ __forceinline__ void st_global_v8(void *to, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // Stores the warp's 32 rows of O (TMEM o0 times a0, plus TMEM o1 times a1): as fp32
 // to rows `mine` of a slot of sums, or as bf16 to rows `mine` of out (-1: no row of
-// ours).  kNoTmem stands for zeros; `none`: this lane's row is zeros whatever TMEM
-// holds.
+// ours).  A store's time is that of the 128-byte lines it touches: a slot holds its
+// rows' columns four by four ([d / 4][rows][4]; a warp's store is 512 bytes in a
+// stretch), and out is written 32 bytes a lane where it is aligned to that.
+// kNoTmem stands for zeros; `none`: this lane's row is zeros whatever TMEM holds.
 constexpr uint32_t kNoTmem = 0xffffffffu;
 template <int D>
 __device__ __forceinline__ void store_rows(uint32_t o0, uint32_t o1, float a0, float a1, bool none,
-                                           int mine, float *slot, uint16_t *out) {
+                                           int mine, float *slot, int rows, uint16_t *out) {
+  const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
 #pragma unroll 1
   for (int c0 = 0; c0 < D; c0 += 32) {
     uint32_t o[32];
@@ -198,19 +207,24 @@ __device__ __forceinline__ void store_rows(uint32_t o0, uint32_t o1, float a0, f
       }
     }
     if (mine >= 0 && slot != nullptr) {
-      float *to = slot + static_cast<size_t>(mine) * D + c0;
+      float *to = slot + (static_cast<size_t>(c0 / 4) * rows + mine) * 4;
 #pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        st_global_v4(to + e, make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+      for (int e = 0; e < 32; e += 4, to += static_cast<size_t>(rows) * 4)
+        st_global_v4(to, make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
     } else if (mine >= 0) {
       uint16_t *to = out + static_cast<size_t>(mine) * D + c0;
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint32_t v[4];
+      for (int e = 0; e < 32; e += 16) {
+        uint32_t v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
           v[k] = pack_bf16x2(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
-        st_global_v4(to + e, make_uint4(v[0], v[1], v[2], v[3]));
+        if (wide) {
+          st_global_v8(to + e, v);
+        } else {
+          st_global_v4(to + e, make_uint4(v[0], v[1], v[2], v[3]));
+          st_global_v4(to + e + 8, make_uint4(v[4], v[5], v[6], v[7]));
+        }
       }
     }
   }
@@ -786,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int mine = row ? (slot != nullptr ? unit_row : static_cast<int>(out_row)) : -1;
       if (live_warp)
         store_rows<D>(cnt > 0 ? o_tmem : kNoTmem, join ? o_tmem + 128 : kNoTmem,
-                      none ? 0.f : f0 * inv, none ? 0.f : f1 * inv, none, mine, slot, out);
+                      none ? 0.f : f0 * inv, none ? 0.f : f1 * inv, none, mine, slot, p.rows, out);
       tc_fence_before();
       if (cnt > 0) mbar_arrive(&sh->o_free[w]);
       if (join) mbar_arrive(&sh->o_free[1]);  // warpgroup 1's, with its statistics

@@ -304,18 +304,28 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
   }
 }
 
+// Last CTA whose slot 0 continues the unit that CTA c holds a part of (whole warp).
+__device__ __forceinline__ int last_part(const PagedProblem &p, int c, int ctas, int lane) {
+  for (int at = c; at < ctas; at += 32) {
+    const int k = min(at + lane, ctas - 1);
+    const unsigned ends = __ballot_sync(
+        0xffffffffu, (p.meta[static_cast<size_t>(k) * kPagedMeta + kMetaFlags] & kPartEnds) != 0);
+    if (ends != 0) return min(at + __ffs(ends) - 1, ctas - 1);
+  }
+  return c;
+}
+
 // CTA (c, y): if CTA c + 1 of the attention kernel holds the second part of a unit,
-// that unit's rows are joined from its parts, in the order of their keys.  kSplit of
-// the eight warps share a row: each takes every kSplit-th part, its lanes d / 32
-// columns each.  With few rows a unit may have as many parts as there are CTAs, and
-// a warp that went through them alone would wait for memory over and over (13 of the
-// 22 us of one token over 8192 keys, d 128); with 256 rows there are few parts.
+// that unit's rows are joined from its parts (slot 1 of CTA c, slot 0 of those behind
+// it), in the order of their keys.  The eight warps share a row, row y of the unit:
+// each takes every eighth part, its lanes d / 32 columns each.  A unit may have as many
+// parts as there are CTAs, and a warp that went through them alone would wait for
+// memory over and over (13 of the 22 us of one token over 8192 keys, d 128).
 constexpr int kMergeWarps = 8;
-template <typename T, int D, int kSplit>
+template <typename T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     paged_merge_kernel(const PagedProblem p, int ctas) {
   constexpr int kC = D / 32;
-  constexpr int kRowsAtOnce = kMergeWarps / kSplit;
   __shared__ float sums[kMergeWarps][D];
   griddep_launch_dependents();
   griddep_wait();
@@ -323,69 +333,107 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int32_t *meta = p.meta + static_cast<size_t>(c) * kPagedMeta;
   if (!(meta[kMetaFlags] & kPartContinues) || !(meta[kMetaFlags - kPagedMeta] & kPartBegins)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int share = warp % kSplit;
-  int last = c;  // the parts are slot 1 of CTA c - 1 and slot 0 of CTAs c .. last
-  for (int at = c; at < ctas; at += 32) {
-    const int k = min(at + lane, ctas - 1);
-    const unsigned ends = __ballot_sync(
-        0xffffffffu, (p.meta[static_cast<size_t>(k) * kPagedMeta + kMetaFlags] & kPartEnds) != 0);
-    if (ends != 0) {
-      last = min(at + __ffs(ends) - 1, ctas - 1);
-      break;
-    }
-  }
+  const int last = last_part(p, c, ctas, lane);
   const PagedSeq seq = paged_seq(p.batch, meta[kMetaSeq]);
   const int i0 = meta[kMetaTok], h0 = meta[kMetaHead];
   const int heads = min(p.hpu, p.group - h0 % p.group);
-  for (int r0 = blockIdx.y * kRowsAtOnce; r0 < p.rows; r0 += gridDim.y * kRowsAtOnce) {
-    const int r = r0 + warp / kSplit;
-    const int h = r / p.tb, i = i0 + r % p.tb;
-    const bool row = r < p.rows && h < heads && i < seq.n;
-    float o[kC], m = -INFINITY, l = 0.f, use = 0.f;
+  const int r = blockIdx.y, h = r / p.tb, i = i0 + r % p.tb;
+  if (h >= heads || i >= seq.n) return;
+  float o[kC], m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int e = 0; e < kC; ++e) o[e] = 0.f;
-    if (row) {
-      const size_t ml = static_cast<size_t>(p.rows) * D + 2 * r;  // (max, sum) in a slot
-      for (int k = c - 1 + lane; k <= last; k += 32) {
-        const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
-        const float mk = slot[ml], lk = slot[ml + 1];
-        const float mn = fmaxf(m, mk), u = mn == -INFINITY ? 0.f : mn;
-        l = l * ex2_approx(m - u) + lk * ex2_approx(mk - u);
-        m = mn;
-      }
-      const float top = warp_max(m);
-      use = top == -INFINITY ? 0.f : top;
-      l = warp_sum(l * ex2_approx(m - use));
+  for (int e = 0; e < kC; ++e) o[e] = 0.f;
+  const size_t ml = static_cast<size_t>(p.rows) * D + 2 * r;  // (max, sum) in a slot
+  for (int k = c - 1 + lane; k <= last; k += 32) {
+    const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
+    const float mk = slot[ml], lk = slot[ml + 1];
+    const float mn = fmaxf(m, mk), u = mn == -INFINITY ? 0.f : mn;
+    l = l * ex2_approx(m - u) + lk * ex2_approx(mk - u);
+    m = mn;
+  }
+  const float top = warp_max(m), use = top == -INFINITY ? 0.f : top;
+  l = warp_sum(l * ex2_approx(m - use));
 #pragma unroll 4
-      for (int k = c - 1 + share; k <= last; k += kSplit) {
-        const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
-        const float f = ex2_approx(slot[ml] - use);
-        float part[kC];  // this lane's kC columns
-        ld_cols(slot + static_cast<size_t>(r) * D + lane * kC, part);
+  for (int k = c - 1 + warp; k <= last; k += kMergeWarps) {
+    const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
+    const float f = ex2_approx(slot[ml] - use);
+    float part[kC];  // this lane's kC columns
+    ld_cols(slot + static_cast<size_t>(r) * D + lane * kC, part);
 #pragma unroll
-        for (int e = 0; e < kC; ++e) o[e] = fmaf(part[e], f, o[e]);
-      }
+    for (int e = 0; e < kC; ++e) o[e] = fmaf(part[e], f, o[e]);
+  }
+  st_cols(&sums[warp][lane * kC], o);
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int e = 0; e < kC; ++e) o[e] = 0.f;
+#pragma unroll
+  for (int g = 0; g < kMergeWarps; ++g) {
+    float part[kC];
+    ld_cols(&sums[g][lane * kC], part);
+#pragma unroll
+    for (int e = 0; e < kC; ++e) o[e] += part[e];
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < kC; ++e) o[e] = l > 0.f ? o[e] * inv : 0.f;
+  st_cols(static_cast<T *>(p.out) + (static_cast<long long>(seq.q0 + i) * p.H + h0 + h) * D +
+              lane * kC,
+          o);
+}
+
+// The same for the slots of paged_many_tc_kernel, [d / 4][rows][4] of up to 256 rows and
+// few parts: CTA (c, y) takes rows 32 y + lane, warp w an eighth of the columns, so that
+// a warp reads 512 bytes in a stretch.
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    paged_merge_rows_kernel(const PagedProblem p, int ctas) {
+  constexpr int kC4 = D / 4 / kMergeWarps;  // fours of columns of a thread
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = blockIdx.x + 1;
+  const int32_t *meta = p.meta + static_cast<size_t>(c) * kPagedMeta;
+  if (!(meta[kMetaFlags] & kPartContinues) || !(meta[kMetaFlags - kPagedMeta] & kPartBegins)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int last = last_part(p, c, ctas, lane);
+  const PagedSeq seq = paged_seq(p.batch, meta[kMetaSeq]);
+  const int i0 = meta[kMetaTok], h0 = meta[kMetaHead];
+  const int heads = min(p.hpu, p.group - h0 % p.group);
+  const int r = blockIdx.y * 32 + lane, h = r / p.tb, i = i0 + r % p.tb;
+  if (r >= p.rows || h >= heads || i >= seq.n) return;
+  float o[kC4][4], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kC4; ++e)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[e][x] = 0.f;
+#pragma unroll 2
+  for (int k = c - 1; k <= last; ++k) {
+    const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
+    float part[kC4][4];
+#pragma unroll
+    for (int e = 0; e < kC4; ++e)
+      ld_cols(slot + (static_cast<size_t>(warp * kC4 + e) * p.rows + r) * 4, part[e]);
+    const float2 ml = *reinterpret_cast<const float2 *>(slot + static_cast<size_t>(p.rows) * D + 2 * r);
+    const float mn = fmaxf(m, ml.x), use = mn == -INFINITY ? 0.f : mn;
+    const float older = ex2_approx(m - use), f = ex2_approx(ml.x - use);
+    m = mn;
+    l = fmaf(l, older, ml.y * f);
+#pragma unroll
+    for (int e = 0; e < kC4; ++e)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[e][x] = fmaf(o[e][x], older, part[e][x] * f);
+  }
+  __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.out) +
+                      (static_cast<long long>(seq.q0 + i) * p.H + h0 + h) * D + warp * kC4 * 4;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < kC4; e += 2) {
+    uint32_t v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float a = o[e + x / 2][2 * (x % 2)], b = o[e + x / 2][2 * (x % 2) + 1];
+      v[x] = l > 0.f ? pack_bf16x2(a * inv, b * inv) : 0u;
     }
-    if (kSplit > 1) {
-#pragma unroll
-      for (int e = 0; e < kC; ++e) sums[warp][lane * kC + e] = o[e];
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < kC; ++e) {
-        o[e] = 0.f;
-#pragma unroll
-        for (int g = 0; g < kSplit; ++g) o[e] += sums[warp - share + g][lane * kC + e];
-      }
-      __syncthreads();
-    }
-    if (row && share == 0) {
-      T *to = static_cast<T *>(p.out) +
-              (static_cast<long long>(seq.q0 + i) * p.H + h0 + h) * D + lane * kC;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-      for (int e = 0; e < kC; ++e) o[e] = l > 0.f ? o[e] * inv : 0.f;
-      st_cols(to, o);
-    }
+    st_global_v4(to + e * 4, make_uint4(v[0], v[1], v[2], v[3]));
   }
 }
 
@@ -432,18 +480,22 @@ namespace {
 
 template <typename T, int D>
 cudaError_t merge(const PagedProblem &p, int grid, cudaStream_t stream) {
-  if (p.rows <= 16)
-    return launch(paged_merge_kernel<T, D, kMergeWarps>, dim3(grid - 1, p.rows), kMergeWarps * 32,
-                  0, stream, p, grid);
-  return launch(paged_merge_kernel<T, D, 1>, dim3(grid - 1, 8), kMergeWarps * 32, 0, stream, p,
+  return launch(paged_merge_kernel<T, D>, dim3(grid - 1, p.rows), kMergeWarps * 32, 0, stream, p,
                 grid);
+}
+
+template <int D>
+cudaError_t merge_rows(const PagedProblem &p, int grid, cudaStream_t stream) {
+  return launch(paged_merge_rows_kernel<D>, dim3(grid - 1, (p.rows + 31) / 32), kMergeWarps * 32, 0,
+                stream, p, grid);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_merge(const PagedProblem &p, int d, int dtype, int grid,
+cudaError_t launch_paged_merge(const PagedProblem &p, int d, int dtype, bool many, int grid,
                                cudaStream_t stream) {
   if (grid < 2) return cudaSuccess;
+  if (many) return d == 64 ? merge_rows<64>(p, grid, stream) : merge_rows<128>(p, grid, stream);
   if (dtype == 0)
     return d == 64 ? merge<float, 64>(p, grid, stream) : merge<float, 128>(p, grid, stream);
   return d == 64 ? merge<__nv_bfloat16, 64>(p, grid, stream)
