@@ -37,16 +37,16 @@ static PagedSpan span_of(const PagedProblem &p, int cta, int grid) {
       one += paged_unit_cost(p, s, paged_blocks(p, s), u);
   }
   const int hbs = p.Hkv * p.hblocks;
-  PagedSpan sp = paged_stretch(one * hbs, units * hbs, cta, grid, p.split.min_stretch);
+  PagedSpan sp = paged_stretch(one * hbs, units * hbs, cta, grid, p.split.stretches);
   long long s = 0;
   for (int hb = 0; hb < hbs; ++hb)
     for (int b = 0; b < p.batch.B; ++b) {
       const PagedSeq q = paged_seq(p.batch, b);
       const int blocks = paged_blocks(p, q);
-      sp.s = s;
       for (int u = 0; u < blocks; ++u) {
         const long long cost = paged_unit_cost(p, q, blocks, u);
         if (sp.lo >= s && sp.lo < s + cost) {
+          sp.at = s;
           sp.hb = hb;
           sp.b = b;
           sp.u = u;
@@ -101,9 +101,9 @@ extern "C" void seq(const int32_t *starts, const int32_t *lens, int T, int page_
 // Units of a sequence: their lengths' prefix sums by the closed form, and the unit
 // at each boundary; returns 0 when they agree with sums and a plain search.
 extern "C" int unit_sums(const int32_t *starts, const int32_t *lens, int T, int tb, int causal,
-                         int page_shift, int max_pages) {
+                         int page_shift, int max_pages, int which) {
   const PagedProblem p =
-      problem(starts, lens, nullptr, 1, T, 1, 1, 1, tb, causal, 0, page_shift, max_pages, 0);
+      problem(starts, lens, nullptr, 1, T, 1, 1, 1, tb, causal, 0, page_shift, max_pages, 0, which);
   const PagedSeq s = paged_seq(p.batch, 0);
   const int blocks = paged_blocks(p, s);
   long long sum = 0;
@@ -111,7 +111,9 @@ extern "C" int unit_sums(const int32_t *starts, const int32_t *lens, int T, int 
     const long long cost = paged_unit_cost(p, s, blocks, u);
     if (paged_cost_before(p, s, blocks, u) != sum) return 1 + u;
     if (cost < p.split.unit_cost) return -1;
-    if (paged_unit_at(p, s, blocks, sum) != u || paged_unit_at(p, s, blocks, sum + cost - 1) != u)
+    long long first = -1, last = -1;
+    if (paged_unit_at(p, s, blocks, sum, first) != u ||
+        paged_unit_at(p, s, blocks, sum + cost - 1, last) != u || first != sum || last != sum)
       return -2 - u;
     sum += cost;
   }

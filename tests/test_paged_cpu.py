@@ -446,7 +446,9 @@ def test_unit_lengths_have_their_closed_form(host):
         max_pages = int(rng.choice([0, 3, 400]))
         (a, ap), (l, lp) = i32([0, n]), i32([ln])
         for causal in (0, 1):
-            assert host.unit_sums(ap, lp, n, int(rng.integers(1, 300)), causal, 4, max_pages) == 0
+            for split in (SIMT, FEW, MANY):
+                assert host.unit_sums(ap, lp, n, int(rng.integers(1, 300)), causal, 4, max_pages,
+                                      split) == 0
 
 
 @pytest.mark.parametrize("causal", [0, 1])

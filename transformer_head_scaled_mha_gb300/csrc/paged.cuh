@@ -62,15 +62,18 @@ static_assert(kTileCost == 1 << 8, "tile cost");
 struct PagedSplit {
   int unit_cost;    // a unit's own work (queries, first and last tile, output), in 1/256 tile
   int min_part;     // tiles of a part at least
-  int min_stretch;  // tiles of work below which a CTA is not worth having
+  int stretches;    // CTAs that 2^16 tiles of work are worth: fewer tiles, no CTA of their own
+  int half_tile;    // a tile of a unit that has at most half its tokens, in 1/256 tile
+  int half_per;     // 2^16 / half_tile
 };
-// The many-query kernel's units cost it the time of 4 tile pairs besides their keys,
-// and a cut the sums of 256 rows; the others' 1 and 1.5 tiles.  A tile of the fp32
-// kernel takes about 2 us, so there every tile may have a CTA of its own (44 -> 23 us
-// on 8 sequences of 90 to 700 keys, 5 tokens of 8 heads).
-constexpr PagedSplit kSplitSimt{kTileCost, 1, 1};
-constexpr PagedSplit kSplitFew{kTileCost * 3 / 2, 2, 3};
-constexpr PagedSplit kSplitMany{kTileCost * 4, 3, 6};
+// The many-query kernel's units cost it the time of 3 tile pairs besides their keys,
+// and a cut the sums of 256 rows; the others' 1 and 1.5 tiles.  Its units with tokens
+// for one warpgroup only take 0.8 of the time per tile.  A tile of the fp32 kernel takes
+// about 2 us, so there every tile may have a CTA of its own (44 -> 23 us on 8 sequences
+// of 90 to 700 keys, 5 tokens of 8 heads).
+constexpr PagedSplit kSplitSimt{kTileCost, 1, 65536, kTileCost, 256};
+constexpr PagedSplit kSplitFew{kTileCost * 3 / 2, 2, 65536 / 3, kTileCost, 256};
+constexpr PagedSplit kSplitMany{kTileCost * 3 / 2, 2, 65536 / 3, 215, 305};
 
 // A unit of attention work: `tb` consecutive new tokens of one sequence times
 // `hpu` query heads of one key/value head's group.  Row r of a unit is head
@@ -135,17 +138,18 @@ MHA_HD int paged_kv_end(const PagedSeq &s, int i1, int causal) {
 // CTA c of G takes the stretch [c X / G, (c + 1) X / G) of the line, X its length;
 // a unit's keys are cut where a stretch ends inside it, unless that leaves a part
 // of under `min_part` tiles.  G is at most the grid, and no larger than leaves every
-// CTA `min_stretch` tiles or, if that is more, one unit each.
+// CTA 2^16 / `stretches` tiles or, if that is more, one unit each.
 //
 // Heads come first because every head's piece of the line is alike: with G a
 // multiple of the head blocks, the CTAs of different heads read the same positions
 // at about the same time, and in the [page, position, head, d] layout those lie
 // side by side in memory (66 -> 58 us on 256 sequences of 128 to 1024 keys, 8
 // heads, d 64).
-// tiles of a unit before offset x (> 0) of its piece of the line
-MHA_HD int paged_cut(const PagedSplit &sp, long long x, int nt) {
+// tiles of a unit (of at most half its tokens: `half`) before offset x (> 0) of its
+// piece of the line
+MHA_HD int paged_cut(const PagedSplit &sp, bool half, long long x, int nt) {
   if (x <= 0) return 0;
-  const long long t = (x - sp.unit_cost + kTileCost / 2) >> 8;
+  const long long t = ((x - sp.unit_cost) * (half ? sp.half_per : 256) + 32768) >> 16;
   if (t < sp.min_part) return 0;
   if (t > nt - sp.min_part) return nt;
   return static_cast<int>(t);
@@ -154,16 +158,25 @@ MHA_HD int paged_cut(const PagedSplit &sp, long long x, int nt) {
 // A CTA's place on the line: where its stretch begins and ends, and its first unit.
 struct PagedSpan {
   long long lo, hi;  // the stretch
-  long long s;       // where this head block's units of the first unit's sequence begin
+  long long at;      // where the first unit begins
   int hb;            // head block of the first unit
   int b;             // its sequence
   int u;             // its token block
   int ctas;          // G
 };
 
+// A quotient for a place to start from: a division that rounds is a call.
+MHA_HD float paged_about(float a, float b) {
+#ifdef __CUDA_ARCH__
+  return __fdividef(a, b);
+#else
+  return a / b;
+#endif
+}
+
 // CTAs that a line of length `total` with `units` units has work for.
-MHA_HD long long paged_ctas(long long total, long long units, int min_stretch) {
-  const long long by_work = static_cast<int>(total >> 8 > 0x7fffffff ? 0x7fffffff : total >> 8) / min_stretch;  // kTileCost is 2^8
+MHA_HD long long paged_ctas(long long total, long long units, int stretches) {
+  const long long by_work = (total >> 8) * stretches >> 16;  // kTileCost is 2^8
   const long long most = by_work > units ? by_work : units;
   // a stretch is longer than a tile, so that no CTA between a unit's first and last
   // part is without one (paged_merge_kernel takes them as neighbours)
@@ -173,17 +186,17 @@ MHA_HD long long paged_ctas(long long total, long long units, int min_stretch) {
 
 // The stretch of CTA `cta` of `grid` on a line of length `total` with `units` units.
 MHA_HD PagedSpan paged_stretch(long long total, long long units, int cta, int grid,
-                               int min_stretch) {
+                               int stretches) {
   PagedSpan sp;
-  const long long most = paged_ctas(total, units, min_stretch);
+  const long long most = paged_ctas(total, units, stretches);
   sp.ctas = static_cast<int>(most < 1 ? 1 : (most < grid ? most : grid));
   // equal stretches, a little short (the last CTA takes what is left, some millionths):
   // an approximate quotient, for a 64-bit division is a hundred instructions
-  const long long each = static_cast<long long>(static_cast<float>(total) /
-                                                static_cast<float>(sp.ctas) * 0.999999f);
+  const long long each = static_cast<long long>(
+      paged_about(static_cast<float>(total), static_cast<float>(sp.ctas)) * 0.999999f);
   sp.lo = cta < sp.ctas ? each * cta : total;
   sp.hi = cta + 1 < sp.ctas ? each * (cta + 1) : total;
-  sp.s = total;
+  sp.at = total;
   sp.hb = sp.b = sp.u = 0;
   return sp;
 }
@@ -197,18 +210,24 @@ MHA_HD int paged_blocks_end(const PagedProblem &p, const PagedSeq &s, int u) {
   const long long i1 = static_cast<long long>(u + 1) * p.tb;
   return i1 < s.n ? static_cast<int>(i1) : s.n;
 }
+MHA_HD bool paged_half(const PagedProblem &p, const PagedSeq &s, int u) {
+  return 2 * (paged_blocks_end(p, s, u) - u * p.tb) <= p.tb;
+}
 MHA_HD long long paged_unit_cost(const PagedProblem &p, const PagedSeq &s, int blocks, int u) {
   const long long keys = paged_kv_end(s, paged_blocks_end(p, s, u), p.causal);
-  if (blocks == 1) return p.split.unit_cost + (keys + kPagedTile - 1) / kPagedTile * kTileCost;
-  return p.split.unit_cost + kTileCost / 2 + keys * (kTileCost / kPagedTile);
+  const int tile = paged_half(p, s, u) ? p.split.half_tile : kTileCost;
+  if (blocks == 1) return p.split.unit_cost + (keys + kPagedTile - 1) / kPagedTile * tile;
+  return p.split.unit_cost + kTileCost / 2 + keys * tile / kPagedTile;
 }
 // Length of the units before u (0 <= u <= blocks) of a sequence.
 MHA_HD long long paged_cost_before(const PagedProblem &p, const PagedSeq &s, int blocks, int u) {
-  if (blocks <= 1) return u > 0 ? paged_unit_cost(p, s, blocks, 0) : 0;
+  if (u <= 0) return 0;
+  const long long last = u == blocks ? paged_unit_cost(p, s, blocks, blocks - 1) : 0;
+  const int full = u == blocks ? blocks - 1 : u;  // units before the last
+  if (full == 0) return last;
   const long long fixed = p.split.unit_cost + kTileCost / 2, per_key = kTileCost / kPagedTile;
-  if (!p.causal) return u * (fixed + per_key * s.len);
+  if (!p.causal) return full * (fixed + per_key * s.len) + last;
   // units before the last see base + (v + 1) tb keys, held to [0, len]
-  const int full = u < blocks ? u : blocks - 1;
   const unsigned tb = static_cast<unsigned>(p.tb);
   int lo = s.base < 0 ? static_cast<int>((0u - static_cast<unsigned>(s.base)) / tb) : 0;
   if (lo > full) lo = full;  // units that see nothing
@@ -221,19 +240,25 @@ MHA_HD long long paged_cost_before(const PagedProblem &p, const PagedSeq &s, int
                                                                      : 0;
   if (hi < lo) hi = lo;
   const long long some = hi - lo;
-  long long keys = some * s.base + ((some * (hi + lo + 1)) >> 1) * p.tb +
-                   static_cast<long long>(full - hi) * s.len;
-  if (u == blocks) keys += paged_kv_end(s, s.n, 1);
-  return u * fixed + per_key * keys;
+  const long long keys = some * s.base + ((some * (hi + lo + 1)) >> 1) * p.tb +
+                         static_cast<long long>(full - hi) * s.len;
+  return full * fixed + per_key * keys + last;
 }
 
-// The unit of a sequence whose piece of the line holds offset x.
-MHA_HD int paged_unit_at(const PagedProblem &p, const PagedSeq &s, int blocks, long long x) {
+// The unit of a sequence whose piece of the line holds offset x, and the length before it.
+MHA_HD int paged_unit_at(const PagedProblem &p, const PagedSeq &s, int blocks, long long x,
+                         long long &before) {
   int lo = 0, hi = blocks;
+  before = 0;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (paged_cost_before(p, s, blocks, mid) <= x) lo = mid;
-    else hi = mid;
+    const long long c = paged_cost_before(p, s, blocks, mid);
+    if (c <= x) {
+      lo = mid;
+      before = c;
+    } else {
+      hi = mid;
+    }
   }
   return lo;
 }
@@ -275,11 +300,11 @@ __device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long l
     all_units += scratch[16 + w];
   }
   const int hbs = p.Hkv * p.hblocks;
-  PagedSpan sp = paged_stretch(one * hbs, all_units * hbs, cta, grid, p.split.min_stretch);
+  PagedSpan sp = paged_stretch(one * hbs, all_units * hbs, cta, grid, p.split.stretches);
   const bool any = sp.lo < one * hbs;
   int hb = hbs;
   if (any) {  // sp.lo / one, from an approximate quotient
-    hb = static_cast<int>(static_cast<float>(sp.lo) / static_cast<float>(one));
+    hb = static_cast<int>(paged_about(static_cast<float>(sp.lo), static_cast<float>(one)));
     while (hb > 0 && hb * one > sp.lo) --hb;
     while ((hb + 1) * one <= sp.lo) ++hb;
   }
@@ -291,9 +316,10 @@ __device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long l
       const int nu = paged_blocks(p, q);
       const long long whole = paged_cost_before(p, q, nu, nu);
       if (at < s + whole || b + 1 >= b1) {
-        scratch[32] = s;
+        long long before_u;
+        scratch[34] = paged_unit_at(p, q, nu, at - s, before_u);
+        scratch[32] = s + before_u;
         scratch[33] = b;
-        scratch[34] = paged_unit_at(p, q, nu, at - s);
         break;
       }
       s += whole;
@@ -302,7 +328,7 @@ __device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long l
   __syncthreads();
   sp.hb = hb;
   if (any) {
-    sp.s = hb * one + scratch[32];
+    sp.at = hb * one + scratch[32];
     sp.b = static_cast<int>(scratch[33]);
     sp.u = static_cast<int>(scratch[34]);
   }
@@ -341,7 +367,7 @@ struct PagedWalk {
     at = sp.hi;
     if (sp.lo < sp.hi) {
       take(p, paged_seq(p.batch, b));
-      at = sp.s + paged_cost_before(p, seq, blocks, u);
+      at = sp.at;
     }
   }
   // The next part; false when the span is done.
@@ -369,8 +395,9 @@ struct PagedWalk {
       const long long from = at;
       at += paged_unit_cost(p, seq, blocks, u);
       ++u;
-      part.t0 = paged_cut(p.split, sp.lo - from, part.nt);
-      part.t1 = sp.hi < at ? paged_cut(p.split, sp.hi - from, part.nt) : part.nt;
+      const bool half = 2 * (part.i1 - part.i0) <= p.tb;
+      part.t0 = paged_cut(p.split, half, sp.lo - from, part.nt);
+      part.t1 = sp.hi < at ? paged_cut(p.split, half, sp.hi - from, part.nt) : part.nt;
       if (part.nt == 0) {  // nothing to attend to: zeros, by the CTA that holds its beginning
         if (from >= sp.lo) return true;
         continue;

@@ -370,7 +370,7 @@ static int launched_ctas(const PagedProblem &p, int grid) {
   const long long tiles = (keys + kPagedTile - 1) / kPagedTile;
   const long long total = units * (p.split.unit_cost + kTileCost / 2 + tiles * kTileCost);
   return static_cast<int>(
-      std::max(1LL, std::min<long long>(grid, paged_ctas(total, units, p.split.min_stretch))));
+      std::max(1LL, std::min<long long>(grid, paged_ctas(total, units, p.split.stretches))));
 }
 
 extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_cache, void *out,

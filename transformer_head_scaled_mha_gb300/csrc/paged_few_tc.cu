@@ -243,6 +243,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
     bool ok = true;
     for (;;) {
       const bool more = walk.next(p, part);
+      const int32_t *table = pb.block_table + static_cast<size_t>(more ? part.b : 0) * pb.max_pages;
+      // page of this lane's copy of tile j; -1 when it holds no key or is not there
+      auto page_of = [&](int j) -> int {
+        const int key = j * kBN + piece * box;
+        if (!loads || j >= part.t1 || key >= part.kv_end) return -1;
+        const int id = table[key >> pb.page_shift];
+        return static_cast<unsigned>(id) < static_cast<unsigned>(pb.num_pages) ? id : -1;
+      };
+      int id = more ? page_of(part.t0) : -1;
       ok = mbar_wait_warp(&sh->desc_empty[n % kDescs], ((n / kDescs) & 1) ^ 1, abort_flag,
                           p.wait_ns);
       if (!ok) break;
@@ -287,15 +296,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
                       part.seq.q0 + part.i0, part.h0, 0);
       }
       ++q_issued;
-      const int32_t *table = pb.block_table + static_cast<size_t>(part.b) * pb.max_pages;
-      // page of this lane's copy of tile j; -1 when it holds no key or is not there
-      auto page_of = [&](int j) -> int {
-        const int key = j * kBN + piece * box;
-        if (!loads || j >= part.t1 || key >= part.kv_end) return -1;
-        const int id = table[key >> pb.page_shift];
-        return static_cast<unsigned>(id) < static_cast<unsigned>(pb.num_pages) ? id : -1;
-      };
-      int id = page_of(part.t0);
       for (int j = part.t0; j < part.t1; ++j) {
         const int id_next = page_of(j + 1);
         const int slot = issued % C::kSlots, round = issued / C::kSlots;

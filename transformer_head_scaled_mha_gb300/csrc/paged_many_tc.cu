@@ -312,11 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) walk.begin(p, span);
       int n = 0, flags = 0, mseq = 0, mtok = 0, mhead = 0;
       bool ok = true, more = false;
-      // the next part, into two[n & 1], and its description
-      auto advance = [&]() {
-        PagedPart &part = two[n & 1];
-        bool got = lane == 0 && walk.next(p, part);
-        got = __any_sync(0xffffffffu, got);
+      // the description of the part in two[n & 1], or of the end
+      auto describe = [&]() {
+        const PagedPart &part = two[n & 1];
+        const bool got = more;
         ok = mbar_wait_warp(&sh->desc_empty[n % kDescs], ((n / kDescs) & 1) ^ 1, abort_flag,
                             p.wait_ns);
         if (!ok) return;
@@ -351,7 +350,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        more = got;
         ++n;
       };
       // the part whose tiles are being loaded: tiles [j, t1) are left
@@ -365,7 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return static_cast<unsigned>(at) < static_cast<unsigned>(pb.num_pages) ? at : -1;
       };
       while (ok) {
-        advance();
+        // the next part, into two[n & 1] (the one at hand is two[(n - 1) & 1])
+        more = __any_sync(0xffffffffu, lane == 0 && walk.next(p, two[n & 1]));
+        __syncwarp();
         // the rest of the part at hand, then the first tile of the next one (this loop
         // has one copy of the code that issues a tile: it competes with the softmax for
         // the instruction cache)
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int stop = t1;
           if (phase == 1) {
             if (!more) break;
-            const PagedPart &part = two[(n - 1) & 1];
+            const PagedPart &part = two[n & 1];
             j = stop = t1 = 0;
             if (part.nt == 0) break;
             j = part.t0;
@@ -437,6 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             id = id_next;
           }
         }
+        // (after its first loads are on their way)
+        if (ok) describe();
         if (!more) break;
       }
       if (ok && mbar_wait_warp(&sh->zero_empty, (zeroed & 1) ^ 1, abort_flag, p.wait_ns) &&
