@@ -132,6 +132,28 @@ def test_in_place_and_one_tensor_alone(dt, layout):
         check(w.double().cpu().numpy(), want, tol, "weight")
 
 
+@pytest.mark.parametrize("layout", ["bshd", "bhsd"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_many_rows_of_one_tensor_alone(dt, layout):
+    # enough rows that a warp goes through many, across tokens and sequences
+    import torch
+    import transformer_head_scaled_mha_gb300 as mha
+    s = make(7, 9, 5, 801, 64, dt, layout, 64, 12, far=5000)
+    g = on_gpu(s, dt)
+    kw = dict(positions=g["pos"], inv_freq=g["freq"], layout=layout)
+    full = mha.mha_qk_norm_rope_bwd(g["q"], g["k"], g["gq"], g["gk"], q_weight=g["qw"],
+                                    k_weight=g["kw"], **kw)
+    q = mha.mha_qk_norm_rope_bwd(g["q"], None, g["gq"], None, q_weight=g["qw"], **kw)
+    k = mha.mha_qk_norm_rope_bwd(None, g["k"], None, g["gk"], k_weight=g["kw"], **kw)
+    assert torch.equal(q[0], full[0]) and torch.equal(k[1], full[1])
+    pos = np.expand_dims(s["pos"], s["axis"])
+    for x, w, gy, dx, dw in (("q", "qw", "gq", full[0], full[2]), ("k", "kw", "gk", full[1], full[3])):
+        args = (f64(s[x], dt), f64(s[w], dt), f64(s[gy], dt), pos, s["freq"], False, 1e-6)
+        (wx, ww), (tx, tw) = ref.norm_rope_bwd(*args), ref.norm_rope_bwd_tol(*args, dt, chain=464)
+        check(f64(from_device(dx), dt), wx, tx, "d" + x)
+        check(dw.double().cpu().numpy(), ww, tw, "d" + x + " weight")
+
+
 def test_positions():
     import torch
     import transformer_head_scaled_mha_gb300 as mha

@@ -66,11 +66,12 @@ struct PagedSplit {
   int half_tile;    // a tile of a unit that has at most half its tokens, in 1/256 tile
   int half_per;     // 2^16 / half_tile
 };
-// The many-query kernel's units cost it the time of 3 tile pairs besides their keys,
-// and a cut the sums of 256 rows; the others' 1 and 1.5 tiles.  Its units with tokens
-// for one warpgroup only take 0.8 of the time per tile.  A tile of the fp32 kernel takes
-// about 2 us, so there every tile may have a CTA of its own (44 -> 23 us on 8 sequences
-// of 90 to 700 keys, 5 tokens of 8 heads).
+// Units cost the tensor-core kernels the time of 1.5 tiles besides their keys (the
+// many-query one, with 3 and cuts from 3 tiles on: chunks 84 us, not 80), the fp32
+// kernel's one.  The many-query kernel's units with tokens for one warpgroup only take
+// 0.8 of the time per tile.  A tile of the fp32 kernel takes about 2 us, so there every
+// tile may have a CTA of its own (44 -> 26 us on 8 sequences of 90 to 700 keys, 5 tokens
+// of 8 heads).
 constexpr PagedSplit kSplitSimt{kTileCost, 1, 65536, kTileCost, 256};
 constexpr PagedSplit kSplitFew{kTileCost * 3 / 2, 2, 65536 / 3, kTileCost, 256};
 constexpr PagedSplit kSplitMany{kTileCost * 3 / 2, 2, 65536 / 3, 215, 305};
@@ -145,6 +146,7 @@ MHA_HD int paged_kv_end(const PagedSeq &s, int i1, int causal) {
 // at about the same time, and in the [page, position, head, d] layout those lie
 // side by side in memory (66 -> 58 us on 256 sequences of 128 to 1024 keys, 8
 // heads, d 64).
+
 // tiles of a unit (of at most half its tokens: `half`) before offset x (> 0) of its
 // piece of the line
 MHA_HD int paged_cut(const PagedSplit &sp, bool half, long long x, int nt) {

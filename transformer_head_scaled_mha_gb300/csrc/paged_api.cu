@@ -107,9 +107,10 @@ int current_sms() {
 
 // ---- attention over the cache -------------------------------------------------
 // Expected query rows per key/value head up to which the few-query kernel is taken.
-// Measured, few / many: 16 rows, 32 sequences of 500-2000 keys, d 128: 47 / 59 us, 16
-// sequences of 1000-8000: 40 / 53 us; 32 rows (a few-query kernel of that size), 64
-// sequences of 1000-4000: 101 / 88 us, 128 of 300-900: 160 / 97 us.
+// Measured, few / many: 16 rows, 8 sequences of 1000-8000 keys, d 128: 27 / 39 us; 12
+// rows, 64 of 500-2000, d 64: 91 / 105; the other way at worst 256 of 200-600, 16 rows,
+// d 128: 81 / 75.  32 rows (a few-query kernel of that size), 64 sequences of 1000-4000:
+// 101 / 84 us, 128 of 300-900: 160 / 87 us.
 constexpr int kFewRows = 16;
 
 enum PagedPath { kNone = 0, kSimt = 1, kFew = 2, kMany = 3 };
