@@ -174,6 +174,7 @@ size_t mha_paged_workspace_size(int B, int T, int H, int H_kv, int d, int max_q,
  *            is right whatever it is; a good value is the largest
  *            q_starts[b + 1] - q_starts[b].
  * scale      finite
+ * max_pages * page_size  at most 2^31 - 1024
  * workspace  device memory of at least mha_paged_workspace_size(...) bytes,
  *            256-byte aligned, overlapping nothing; scratch afterwards
  *

@@ -162,9 +162,12 @@ def test_paged_fwd_rejects_before_launch(mha):
                dict(lens=P[5] + 1)):
         assert paged(mha, **kw) == E_ARG, kw
     for kw in (dict(page=4), dict(d=80), dict(T=1 << 30), dict(B=1 << 30),
-               dict(pages=(1 << 31) - 1, page=1 << 30)):
+               dict(pages=(1 << 31) - 1, page=1 << 30),
+               # positions, rounded up to whole tiles of keys, stay below 2^31
+               dict(page=1 << 20, max_pages=1 << 11), dict(page=16, max_pages=(1 << 27) - 63)):
         assert paged(mha, **kw) == E_UNS, kw
-    for kw in (dict(T=0), dict(B=0), dict(H=0, Hkv=0), dict(H=0)):
+    for kw in (dict(T=0), dict(B=0), dict(H=0, Hkv=0), dict(H=0),
+               dict(T=0, page=16, max_pages=(1 << 27) - 64)):
         assert paged(mha, q=None, out=None, ws=None, ws_n=0, **kw) == mha.MHA_OK, kw
 
 

@@ -392,6 +392,9 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
     return MHA_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(scale)) return MHA_ERR_INVALID_ARGUMENT;
   if (!fits({num_pages, page_size, H_kv, d}) || !fits({B, max_pages})) return MHA_ERR_UNSUPPORTED;
+  // the kernels count keys, and a few tiles past them, in 32 bits
+  if ((static_cast<long long>(max_pages) << p.batch.page_shift) > (1LL << 31) - 1024)
+    return MHA_ERR_UNSUPPORTED;
   if (path == kNone) return MHA_OK;
   const Units u = units_of(path, H / H_kv, max_q);
   const size_t e = elem_size(dtype);
