@@ -178,7 +178,9 @@ size_t mha_paged_workspace_size(int B, int T, int H, int H_kv, int d, int max_q,
  * workspace  device memory of at least mha_paged_workspace_size(...) bytes,
  *            256-byte aligned, overlapping nothing; scratch afterwards
  *
- * Tokens with nothing to attend to are written as +0.0.  Sums and softmax
+ * A position that a token does not see adds nothing to it whatever its key holds;
+ * its value must be finite where a later token of the same call sees it (a weight
+ * of 0 times infinity is NaN).  Tokens with nothing to attend to are written as +0.0.  Sums and softmax
  * statistics are fp32; with BF16 the softmax weights are rounded to bfloat16
  * for the product with the values.
  */

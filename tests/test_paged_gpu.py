@@ -169,6 +169,17 @@ def test_pages_that_are_not_there(dt, n, causal):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 6, 40])
+def test_pages_shared_by_sequences(dt, n):
+    def share(b):
+        b["table"][1, :8] = b["table"][0, :8]    # one prefix
+        b["table"][2, :4] = b["table"][2, 0]     # one page again and again
+        b["table"][3] = b["table"][0]            # a whole table
+    check_paged([(n, 500), (n, 300), (n, 400), (n, 450)], 4, 2, 64, dt, 16, "bshd", change=share,
+                seed=21)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_offsets_and_lengths_out_of_range(dt):
     def change(b):
         b["starts"][0], b["starts"][-1] = -4, b["T"] + 1000
