@@ -235,11 +235,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
     // ---- producer: walks the parts; per part Q, then (K_j, V_j) ------------
     const PagedBatch &pb = p.batch;
     const int box = min(pb.page_size, kBN);        // rows of a copy
-    const int pieces = kBN / box;                  // copies per 64 columns of a tile
+    const int pieces_shift = 7 - min(pb.page_shift, 7);
+    const int pieces = 1 << pieces_shift;          // copies per 64 columns of a tile
     const bool loads = lane < 2 * C::kSlabs * pieces;
-    const int piece = lane & (pieces - 1);         // pieces is a power of two
-    const int slab = loads ? (lane / pieces) % C::kSlabs : 0;
-    const int kv = loads ? lane / (pieces * C::kSlabs) : 0;  // 0: K, 1: V
+    const int piece = lane & (pieces - 1);
+    const int slab = loads ? (lane >> pieces_shift) % C::kSlabs : 0;
+    const int kv = loads ? (lane >> pieces_shift) / C::kSlabs : 0;  // 0: K, 1: V
     const CUtensorMap *map = kv == 0 ? &maps.k : &maps.v;
     const int dst0 = kv * C::kTileBytes + slab * C::kBlkBytes + piece * box * 128;
     PagedWalk walk;

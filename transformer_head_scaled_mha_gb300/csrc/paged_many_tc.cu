@@ -304,10 +304,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- producer: walks the parts; per part Q, then K_j V_j K_j+1 ... ----
       const PagedBatch &pb = p.batch;
       const int box = min(pb.page_size, kBN);  // rows of a copy
-      const int pieces = kBN / box;            // copies per 64 columns of a tile
+      const int pieces_shift = 7 - min(pb.page_shift, 7);
+      const int pieces = 1 << pieces_shift;    // copies per 64 columns of a tile
       const bool loads = lane < C::kSlabs * pieces;
-      const int piece = lane & (pieces - 1);   // pieces is a power of two
-      const int slab = loads ? lane / pieces : 0;
+      const int piece = lane & (pieces - 1);
+      const int slab = loads ? lane >> pieces_shift : 0;
       const int dst0 = slab * C::kBlkBytes + piece * box * 128;
       const uint32_t whole = (1u << pieces) - 1;
       // Lane 0 walks, one part ahead of the loads, so that the other roles find the
