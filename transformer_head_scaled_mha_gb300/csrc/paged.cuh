@@ -103,8 +103,8 @@ struct PagedProblem {
 // unit that the CTAs behind it continue.
 constexpr int kPagedMeta = 8;
 constexpr int kMetaFlags = 0;  // kPart* bits
-constexpr int kMetaSeq = 1, kMetaTok = 2, kMetaHead = 3;  // unit of slot 0: sequence, first token
-                                                          // in it, first query head
+// unit of slot 0: first row of out, its tokens, first query head, query heads
+constexpr int kMetaRow = 1, kMetaTokens = 2, kMetaHead = 3, kMetaHeads = 4;
 constexpr int kPartContinues = 1;  // slot 0 is used
 constexpr int kPartEnds = 2;       // ... and holds the unit's last keys
 constexpr int kPartBegins = 4;     // slot 1 is used

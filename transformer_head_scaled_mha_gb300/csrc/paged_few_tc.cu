@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
     PagedWalk walk;
     walk.begin(p, span);
     PagedPart part;
-    int n = 0, flags = 0, mseq = 0, mtok = 0, mhead = 0;
+    int n = 0, flags = 0, mrow = 0, mtokens = 0, mhead = 0, mheads = 0;
     bool ok = true;
     for (;;) {
       const bool more = walk.next(p, part);
@@ -285,9 +285,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
       if (split) {
         if (part.t0 > 0) {
           flags |= kPartContinues | (part.t1 == part.nt ? kPartEnds : 0);
-          mseq = part.b;
-          mtok = part.i0;
+          mrow = part.seq.q0 + part.i0;
+          mtokens = part.i1 - part.i0;
           mhead = part.h0;
+          mheads = part.heads;
         } else {
           flags |= kPartBegins;
         }
@@ -326,9 +327,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
     if (lane == 0) {
       int32_t *meta = p.meta + static_cast<size_t>(blockIdx.x) * kPagedMeta;
       meta[kMetaFlags] = flags;
-      meta[kMetaSeq] = mseq;
-      meta[kMetaTok] = mtok;
+      meta[kMetaRow] = mrow;
+      meta[kMetaTokens] = mtokens;
       meta[kMetaHead] = mhead;
+      meta[kMetaHeads] = mheads;
     }
   } else if (warp == 5) {
     // ---- score products S_t = K_t Q^T (lane 0 issues; the warp waits) -----

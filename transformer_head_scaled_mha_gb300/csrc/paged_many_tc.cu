@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       static_assert(sizeof(PagedWalk) <= 14 * 8 && 14 * 8 + 2 * sizeof(PagedPart) <= 32 * 8,
                     "where they live");
       if (lane == 0) walk.begin(p, span);
-      int n = 0, flags = 0, mseq = 0, mtok = 0, mhead = 0;
+      int n = 0, flags = 0, mrow = 0, mtokens = 0, mhead = 0, mheads = 0;
       bool ok = true, more = false;
       // the description of the part in two[n & 1], or of the end
       auto describe = [&]() {
@@ -351,9 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (split) {
             if (part.t0 > 0) {
               flags |= kPartContinues | (part.t1 == part.nt ? kPartEnds : 0);
-              mseq = part.b;
-              mtok = part.i0;
+              mrow = part.seq.q0 + part.i0;
+              mtokens = part.i1 - part.i0;
               mhead = part.h0;
+              mheads = part.heads;
             } else {
               flags |= kPartBegins;
             }
@@ -459,9 +460,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         int32_t *meta = p.meta + static_cast<size_t>(blockIdx.x) * kPagedMeta;
         meta[kMetaFlags] = flags;
-        meta[kMetaSeq] = mseq;
-        meta[kMetaTok] = mtok;
+        meta[kMetaRow] = mrow;
+        meta[kMetaTokens] = mtokens;
         meta[kMetaHead] = mhead;
+        meta[kMetaHeads] = mheads;
       }
       __syncwarp();
     } else if (warp == 9) {

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
   PagedWalk walk;
   walk.begin(p, span);
   PagedPart part;
-  int flags = 0, mseq = 0, mtok = 0, mhead = 0;
+  int flags = 0, mrow = 0, mtokens = 0, mhead = 0, mheads = 0;
   const float *q = static_cast<const float *>(p.q);
   const float *kc = static_cast<const float *>(p.k), *vc = static_cast<const float *>(p.v);
   float *out = static_cast<float *>(p.out);
@@ -290,9 +290,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
     if (split) {
       if (part.t0 > 0) {
         flags |= kPartContinues | (part.t1 == part.nt ? kPartEnds : 0);
-        mseq = part.b;
-        mtok = part.i0;
+        mrow = part.seq.q0 + part.i0;
+        mtokens = part.i1 - part.i0;
         mhead = part.h0;
+        mheads = part.heads;
       } else {
         flags |= kPartBegins;
       }
@@ -301,22 +302,43 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
   if (threadIdx.x == 0) {
     int32_t *meta = p.meta + static_cast<size_t>(blockIdx.x) * kPagedMeta;
     meta[kMetaFlags] = flags;
-    meta[kMetaSeq] = mseq;
-    meta[kMetaTok] = mtok;
+    meta[kMetaRow] = mrow;
+    meta[kMetaTokens] = mtokens;
     meta[kMetaHead] = mhead;
+    meta[kMetaHeads] = mheads;
   }
 }
 
-// Last CTA whose slot 0 continues the unit that CTA c holds a part of (whole warp).
-__device__ __forceinline__ int last_part(const PagedProblem &p, int c, int ctas, int lane) {
-  for (int at = c; at < ctas; at += 32) {
-    const int k = min(at + lane, ctas - 1);
-    const unsigned ends = __ballot_sync(
-        0xffffffffu, (p.meta[static_cast<size_t>(k) * kPagedMeta + kMetaFlags] & kPartEnds) != 0);
-    if (ends != 0) return min(at + __ffs(ends) - 1, ctas - 1);
+// A unit to join, as its second part's CTA c describes it.
+struct Joined {
+  int row0, tokens, h0, heads;
+  int last;  // CTA of its last part
+  // false: CTA c holds no unit's second part.  (Whole warp; the words are loaded at
+  // once, for the merge is a chain of loads.)
+  __device__ __forceinline__ bool find(const PagedProblem &p, int c, int ctas, int lane) {
+    const int32_t *meta = p.meta + static_cast<size_t>(c) * kPagedMeta;
+    const int4 own = *reinterpret_cast<const int4 *>(meta);
+    const int before = meta[kMetaFlags - kPagedMeta];
+    int flags = p.meta[static_cast<size_t>(min(c + lane, ctas - 1)) * kPagedMeta + kMetaFlags];
+    heads = meta[kMetaHeads];
+    static_assert(kMetaFlags == 0 && kMetaRow == 1 && kMetaTokens == 2 && kMetaHead == 3, "int4");
+    row0 = own.y;
+    tokens = own.z;
+    h0 = own.w;
+    if (!(own.x & kPartContinues) || !(before & kPartBegins)) return false;
+    last = c;
+    for (int at = c;;) {
+      const unsigned ends = __ballot_sync(0xffffffffu, (flags & kPartEnds) != 0);
+      if (ends != 0) {
+        last = min(at + __ffs(ends) - 1, ctas - 1);
+        break;
+      }
+      if ((at += 32) >= ctas) break;
+      flags = p.meta[static_cast<size_t>(min(at + lane, ctas - 1)) * kPagedMeta + kMetaFlags];
+    }
+    return true;
   }
-  return c;
-}
+};
 
 // CTA (c, y): if CTA c + 1 of the attention kernel holds the second part of a unit,
 // that unit's rows are joined from its parts (slot 1 of CTA c, slot 0 of those behind
@@ -333,30 +355,26 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   griddep_launch_dependents();
   griddep_wait();
   const int c = blockIdx.x + 1;
-  const int32_t *meta = p.meta + static_cast<size_t>(c) * kPagedMeta;
-  if (!(meta[kMetaFlags] & kPartContinues) || !(meta[kMetaFlags - kPagedMeta] & kPartBegins)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int last = last_part(p, c, ctas, lane);
-  const PagedSeq seq = paged_seq(p.batch, meta[kMetaSeq]);
-  const int i0 = meta[kMetaTok], h0 = meta[kMetaHead];
-  const int heads = min(p.hpu, p.group - h0 % p.group);
-  const int r = blockIdx.y, h = r / p.tb, i = i0 + r % p.tb;
-  if (h >= heads || i >= seq.n) return;
+  Joined u;
+  if (!u.find(p, c, ctas, lane)) return;
+  const int r = blockIdx.y, h = r / p.tb, i = r - h * p.tb;
+  if (h >= u.heads || i >= u.tokens) return;
   float o[kC], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int e = 0; e < kC; ++e) o[e] = 0.f;
   const size_t ml = static_cast<size_t>(p.rows) * D + 2 * r;  // (max, sum) in a slot
-  for (int k = c - 1 + lane; k <= last; k += 32) {
+  for (int k = c - 1 + lane; k <= u.last; k += 32) {
     const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
     const float mk = slot[ml], lk = slot[ml + 1];
-    const float mn = fmaxf(m, mk), u = mn == -INFINITY ? 0.f : mn;
-    l = l * ex2_approx(m - u) + lk * ex2_approx(mk - u);
+    const float mn = fmaxf(m, mk), to = mn == -INFINITY ? 0.f : mn;
+    l = l * ex2_approx(m - to) + lk * ex2_approx(mk - to);
     m = mn;
   }
   const float top = warp_max(m), use = top == -INFINITY ? 0.f : top;
   l = warp_sum(l * ex2_approx(m - use));
 #pragma unroll 4
-  for (int k = c - 1 + warp; k <= last; k += kMergeWarps) {
+  for (int k = c - 1 + warp; k <= u.last; k += kMergeWarps) {
     const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
     const float f = ex2_approx(slot[ml] - use);
     float part[kC];  // this lane's kC columns
@@ -379,7 +397,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int e = 0; e < kC; ++e) o[e] = l > 0.f ? o[e] * inv : 0.f;
-  st_cols(static_cast<T *>(p.out) + (static_cast<long long>(seq.q0 + i) * p.H + h0 + h) * D +
+  st_cols(static_cast<T *>(p.out) + (static_cast<long long>(u.row0 + i) * p.H + u.h0 + h) * D +
               lane * kC,
           o);
 }
@@ -394,22 +412,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   griddep_launch_dependents();
   griddep_wait();
   const int c = blockIdx.x + 1;
-  const int32_t *meta = p.meta + static_cast<size_t>(c) * kPagedMeta;
-  if (!(meta[kMetaFlags] & kPartContinues) || !(meta[kMetaFlags - kPagedMeta] & kPartBegins)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int last = last_part(p, c, ctas, lane);
-  const PagedSeq seq = paged_seq(p.batch, meta[kMetaSeq]);
-  const int i0 = meta[kMetaTok], h0 = meta[kMetaHead];
-  const int heads = min(p.hpu, p.group - h0 % p.group);
-  const int r = blockIdx.y * 32 + lane, h = r / p.tb, i = i0 + r % p.tb;
-  if (r >= p.rows || h >= heads || i >= seq.n) return;
+  Joined u;
+  if (!u.find(p, c, ctas, lane)) return;
+  const int r = blockIdx.y * 32 + lane, h = r / p.tb, i = r - h * p.tb;
+  if (r >= p.rows || h >= u.heads || i >= u.tokens) return;
   float o[kC4][4], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int e = 0; e < kC4; ++e)
 #pragma unroll
     for (int x = 0; x < 4; ++x) o[e][x] = 0.f;
 #pragma unroll 2
-  for (int k = c - 1; k <= last; ++k) {
+  for (int k = c - 1; k <= u.last; ++k) {
     const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
     float part[kC4][4];
 #pragma unroll
@@ -426,7 +440,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       for (int x = 0; x < 4; ++x) o[e][x] = fmaf(o[e][x], older, part[e][x] * f);
   }
   __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.out) +
-                      (static_cast<long long>(seq.q0 + i) * p.H + h0 + h) * D + warp * kC4 * 4;
+                      (static_cast<long long>(u.row0 + i) * p.H + u.h0 + h) * D + warp * kC4 * 4;
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int e = 0; e < kC4; e += 2) {
