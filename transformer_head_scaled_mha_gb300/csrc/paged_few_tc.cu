@@ -8,9 +8,9 @@
 // paged_merge_kernel joins the cut ones.
 //
 // Measured, with the merge: one token, 64 sequences of 4096-8192 keys, 32 heads over 8,
-// d 128: 235 us, 6.9 TB/s (1.01 of a copy's rate); 256 sequences of 128-1024 keys, 8
-// heads, d 64: 60 us, 5.0 TB/s (0.74; its 2048 short units and the way to a CTA's first
-// tile, about 6 us); one sequence of 300 keys: 8.6 us, a chain of latencies.
+// d 128: 230-235 us, 6.9 TB/s (1.02 of a copy's rate); 256 sequences of 128-1024 keys, 8
+// heads, d 64: 59 us, 5.1 TB/s (0.76; its 2048 short units and the way to a CTA's first
+// tile, 7 us); one sequence of 300 keys: 8.2 us, a chain of latencies.
 //
 // Scores are computed transposed, keys on the 128 TMEM lanes, so that a thread
 // owns a key and the few rows cost a few exponentials per thread:
