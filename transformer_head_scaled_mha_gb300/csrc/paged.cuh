@@ -32,7 +32,7 @@ struct RopeArgs {
   const void *q_weight, *k_weight;  // nullptr: that tensor is not normed
   const float *inv_freq;
   const int32_t *positions;  // [B, L] or nullptr (not appending)
-  int B, H, Hkv, L;          // not appending: token t = (t / L, t % L)
+  int H, Hkv, L;             // not appending: token t = (t / L, t % L)
   int tokens;                // B * L, or the batch's T
   int rotary, layout, style;
   float eps;

@@ -194,7 +194,6 @@ extern "C" int mha_qk_norm_rope_fwd(const void *q, const void *k, void *q_out, v
   a.k_weight = k_weight;
   a.positions = positions;
   a.inv_freq = inv_freq;
-  a.B = B;
   a.H = H;
   a.Hkv = H_kv;
   a.L = L;
@@ -270,7 +269,6 @@ extern "C" int mha_qk_norm_rope_bwd(const void *q, const void *k, const void *dq
   a.partial = static_cast<float *>(workspace);
   a.positions = positions;
   a.inv_freq = inv_freq;
-  a.B = B;
   a.H = H;
   a.Hkv = H_kv;
   a.L = L;

@@ -21,7 +21,7 @@
 // Measured: forward, 4 x 8192 tokens of 16 + 16 heads, d 128: 90 us, 5.95 TB/s (0.88 of a
 // copy's rate); appended prompts of 32 + 8 + 8 heads, d 128: 41 us (0.79); backward, 2 x
 // 4096 tokens of 32 + 8 heads, d 128: 47 us (0.79), 128 x 127 tokens of 8 + 8, d 64: 28
-// us (0.53: 330 instructions for a warp's four rows, and 5 us before the first row and
+// us (0.53: about 290 instructions for a warp's four rows, and 5 us before the first row and
 // for the weights' last sums).
 //
 // Angles: with the frequency in turns as a 64-bit binary fraction F =
