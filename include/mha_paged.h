@@ -178,11 +178,15 @@ size_t mha_paged_workspace_size(int B, int T, int H, int H_kv, int d, int max_q,
  * workspace  device memory of at least mha_paged_workspace_size(...) bytes,
  *            256-byte aligned, overlapping nothing; scratch afterwards
  *
- * A position that a token does not see adds nothing to it whatever its key holds;
- * its value must be finite where a later token of the same call sees it (a weight
- * of 0 times infinity is NaN).  Tokens with nothing to attend to are written as
- * +0.0.  Sums and softmax statistics are fp32; with BF16 the softmax weights are
- * rounded to bfloat16 for the product with the values.
+ * A position that a token does not see adds nothing to it whatever its key
+ * holds; its value must be finite where a later token of the same call sees it
+ * (a weight of 0 times infinity is NaN). Tokens with nothing to attend to are
+ * written as +0.0, whatever their query holds. What a token does see counts as
+ * the formula says: a NaN in its query or in such a key, a score past the range
+ * of fp32, or scores all of which are -infinity make its row NaN; a score of
+ * -infinity beside others weighs nothing. Sums and softmax statistics are fp32;
+ * with BF16 the softmax weights are rounded to bfloat16 for the product with
+ * the values.
  */
 int mha_paged_fwd(const void *q, const void *k_cache, const void *v_cache, void *out,
                   const int32_t *q_starts, const int32_t *kv_lengths, const int32_t *block_table,

@@ -55,6 +55,12 @@ constexpr int kPagedTile = 128;     // keys per tile: the unit that work is spli
 constexpr int kPagedMaxCtas = 608;      // CTAs that may hold partial sums, at most 16 rows per unit
 constexpr int kPagedManyMaxCtas = 192;  // ... 256 rows per unit
 
+// What a visible score counts as at least.  A score that is not seen is -infinity, and a
+// visible one of -infinity this, so that a row with nothing to attend to (maximum
+// -infinity, written as +0.0) is told from one all of whose scores are -infinity (maximum
+// kLowestScore: 0 / 0, NaN); next to any other score both weigh 0.
+constexpr float kLowestScore = -3.402823466e38f;
+
 constexpr int kTileCost = 256;  // 2^8: shifts below
 static_assert(kTileCost == 1 << 8, "tile cost");
 

@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
           tmem_wait_ld();
 #pragma unroll
           for (int r = 0; r < RP; ++r) {
-            x[r] = __uint_as_float(s[r]) * p.scale_log2;
+            x[r] = max_nan(__uint_as_float(s[r]) * p.scale_log2, kLowestScore);
             if (RP > 1 && r >= R) x[r] = -INFINITY;  // padding rows of the product
           }
           // a tile that crosses some row's limit, or has keys that are not there
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
           if (r < R && h < d.heads && i < d.tokens) {
-            const float lt = (sh->lsum[0][r] + sh->lsum[1][r]) + (sh->lsum[2][r] + sh->lsum[3][r]);
+            float lt = (sh->lsum[0][r] + sh->lsum[1][r]) + (sh->lsum[2][r] + sh->lsum[3][r]);
             float acc = __uint_as_float(o[r]);
             if (D == 64) acc += xo[r * 64 + vdim];
             if (sums != nullptr) {
@@ -612,7 +612,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
                 sums[p.rows * D + 2 * r + 1] = lt;
               }
             } else {  // a row with no allowed key is stored as +0.0
-              out[row_at(h, i) * D + vdim] = bf16_bits(lt > 0.f ? acc * (1.f / lt) : 0.f);
+              if (m[r] == kLowestScore) lt = NAN;
+              out[row_at(h, i) * D + vdim] = bf16_bits(lt == 0.f ? 0.f : acc * (1.f / lt));
             }
           }
           if (++i == p.tb) {

@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
             cm = fmax3(cm, chunk_max32(v[0]), chunk_max32(v[1]));
           }
-          cm *= p.scale_log2;
+          cm = fmaxf(cm * p.scale_log2, kLowestScore);
           const bool climb = cm > m_use + kRescaleThreshold;
           if (__any_sync(0xffffffffu, climb) && climb) {
             alpha = ex2_approx(m_use - cm);
@@ -753,7 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[e] = __float_as_uint(e < (e < 16 ? upto0 : upto1)
                                          ? __uint_as_float(v[e]) * p.scale_log2
                                          : -INFINITY);
-            const float cm = chunk_max32(v);
+            float cm = chunk_max32(v);
+            if (upto0 > 0 || upto1 > 16) cm = fmaxf(cm, kLowestScore);  // a key is seen
             const bool climb = cm > m_use + kRescaleThreshold;
             if (__any_sync(0xffffffffu, climb)) {
               const float f = climb ? ex2_approx(m_use - cm) : 1.f;
@@ -832,6 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ml[0] = m_use;
         ml[1] = l_run;
       }
+      if (slot == nullptr && m_use == kLowestScore) l_run = NAN;
       const bool none = l_run == 0.f;  // nothing attended to: +0.0
       const float inv = slot != nullptr ? 1.f : (none ? 0.f : 1.f / l_run);
       const int mine = row ? (slot != nullptr ? unit_row : static_cast<int>(out_row)) : -1;

@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
         }
 #pragma unroll
         for (int r = 0; r < RP; ++r)
-          sm.p[warp][lane][r] = cell >= 0 ? s[r] * p.scale_log2 : -INFINITY;
+          sm.p[warp][lane][r] =
+              cell >= 0 ? max_nan(s[r] * p.scale_log2, kLowestScore) : -INFINITY;
         __syncwarp();
       }
       copy(kc, kw, D + 4, next);
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
         lt = fmaf(sm.l[w][r], f, lt);
         sm.f[w][r] = f;
       }
-      sm.total[r] = lt;
+      sm.total[r] = mt == kLowestScore ? NAN : lt;
       if (split && sm.row[r] >= 0) {
         slot[p.rows * D + 2 * r] = mt;
         slot[p.rows * D + 2 * r + 1] = lt;
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
       } else {
         const float lt = sm.total[r];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = lt > 0.f ? o[c] / lt : 0.f;
+        for (int c = 0; c < 4; ++c) o[c] = lt == 0.f ? 0.f : o[c] / lt;
         st_cols(out + row + e % D, o);
       }
     }
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
   const float top = warp_max(m), use = top == -INFINITY ? 0.f : top;
   l = warp_sum(l * ex2_approx(m - use));
+  if (top == kLowestScore) l = NAN;
 #pragma unroll 4
   for (int k = c - 1 + warp; k <= u.last; k += kMergeWarps) {
     const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
@@ -394,9 +396,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 #pragma unroll
     for (int e = 0; e < kC; ++e) o[e] += part[e];
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = 1.f / l;
 #pragma unroll
-  for (int e = 0; e < kC; ++e) o[e] = l > 0.f ? o[e] * inv : 0.f;
+  for (int e = 0; e < kC; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
   st_cols(static_cast<T *>(p.out) + (static_cast<long long>(u.row0 + i) * p.H + u.h0 + h) * D +
               lane * kC,
           o);
@@ -441,14 +443,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
   __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.out) +
                       (static_cast<long long>(u.row0 + i) * p.H + u.h0 + h) * D + warp * kC4 * 4;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (m == kLowestScore) l = NAN;
+  const float inv = 1.f / l;
 #pragma unroll
   for (int e = 0; e < kC4; e += 2) {
     uint32_t v[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const float a = o[e + x / 2][2 * (x % 2)], b = o[e + x / 2][2 * (x % 2) + 1];
-      v[x] = l > 0.f ? pack_bf16x2(a * inv, b * inv) : 0u;
+      v[x] = l == 0.f ? 0u : pack_bf16x2(a * inv, b * inv);
     }
     st_global_v4(to + e * 4, make_uint4(v[0], v[1], v[2], v[3]));
   }
