@@ -144,3 +144,29 @@ def test_scores_past_the_range_of_fp32_are_nan(dt, H, Hkv, n, d):
                             block_table=dev(b["table"]), max_q=n, layout="bshd")
     bad = torch.isnan(out).all(-1).cpu().numpy()
     assert bad[row, H - 1] and bad.sum() == 1 and not torch.isnan(out[row + 1:]).any()
+
+
+@pytest.mark.parametrize("cut", [False, True], ids=["whole", "cut"])
+@pytest.mark.parametrize("dt,H,Hkv,n,d", FORMS)
+@pytest.mark.filterwarnings("ignore::RuntimeWarning")
+def test_infinite_values_are_infinite_outputs(dt, H, Hkv, n, d, cut):
+    import transformer_head_scaled_mha_gb300 as mha
+    page, ln, scale = 16, 2000 if cut else max(n, 100), d ** -0.5
+    rng = np.random.default_rng(2)
+    b = batch(rng, [(n, ln)] * 6, page)
+    q = f64(rnd(rng, (b["T"], H, d), dt), dt)
+    kc, vc = (f64(rnd(rng, (b["pool"], page, Hkv, d), dt), dt) for _ in range(2))
+    for s, (pos, value) in enumerate(((0, INF), (0, -INF), (ln - n, INF), (ln - n, -INF))):
+        vc[b["table"][s][pos // page], pos % page, s % Hkv, 5 + s] = value  # every token sees it
+    vc[b["table"][4][0], 0, 0, d - 1] = INF
+    vc[b["table"][4][0], min(1, ln - n), 0, d - 1] = -INF  # (a chunk from the start: one value)
+    qs, ks, vs = (store(x, dt) for x in (q, kc, vc))
+    want, tol = defined(f64(qs, dt), f64(ks, dt), f64(vs, dt), b, "bshd", scale, dt)
+    out = mha.mha_paged_fwd(dev(qs, dt), dev(ks, dt), dev(vs, dt), q_starts=dev(b["starts"]),
+                            kv_lengths=dev(b["lens"]), block_table=dev(b["table"]), max_q=n,
+                            layout="bshd", scale=scale)
+    got = f64(from_device(out), dt)
+    fin = np.isfinite(want)
+    assert np.isinf(want).any() and (n == ln or np.isnan(want).any())
+    np.testing.assert_array_equal(np.where(fin, 0.0, got), np.where(fin, 0.0, want))
+    assert np.all(np.abs(got - want)[fin] <= tol[fin])

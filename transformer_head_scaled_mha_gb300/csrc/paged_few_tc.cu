@@ -581,8 +581,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
           tmem_ld_cols(ta + C::kLo, lo);
           tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < RP; ++r)
-            o[r] = __float_as_uint(__uint_as_float(o[r]) + __uint_as_float(lo[r]));
+          for (int r = 0; r < RP; ++r) {
+            // (an infinite value: what the rounding left, of either sign, times infinity)
+            const float a = __uint_as_float(o[r]), b = __uint_as_float(lo[r]);
+            o[r] = __float_as_uint(fabsf(a) == INFINITY ? a : a + b);
+          }
         } else {
           tmem_wait_ld();
         }
