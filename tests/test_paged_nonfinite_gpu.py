@@ -170,3 +170,35 @@ def test_infinite_values_are_infinite_outputs(dt, H, Hkv, n, d, cut):
     assert np.isinf(want).any() and (n == ln or np.isnan(want).any())
     np.testing.assert_array_equal(np.where(fin, 0.0, got), np.where(fin, 0.0, want))
     assert np.all(np.abs(got - want)[fin] <= tol[fin])
+
+
+@pytest.mark.parametrize("far", [25, 60, 120])
+@pytest.mark.parametrize("dt,H,Hkv,n,d", FORMS)
+def test_far_scores(dt, H, Hkv, n, d, far):
+    # scores of one sign, 2^far and more: the largest one's value (the others are 2^far / 8
+    # and more below it), whatever tile it is in
+    import torch
+    import transformer_head_scaled_mha_gb300 as mha
+    page, ln = 16, max(n + 200, 500)
+    rng = np.random.default_rng(3)
+    b = batch(rng, [(n, ln)] * 3, page)
+    sign = np.array([1.0, -1.0, 1.0])
+    q, kc = np.zeros((b["T"], H, d)), np.zeros((b["pool"], page, Hkv, d))
+    vc = f64(rnd(rng, (b["pool"], page, Hkv, d), dt), dt)
+    best = []
+    for s in range(3):
+        q[b["starts"][s]:b["starts"][s + 1], :, 3] = sign[s]
+        top = [ln - n, 3, 130][s]  # seen by every token
+        best.append(top)
+        for pos in range(ln):
+            size = 1.0 if (pos == top) == (sign[s] < 0) else 2.0
+            kc[b["table"][s][pos // page], pos % page, :, 3] = size * 2.0 ** far * d ** 0.5
+    out = mha.mha_paged_fwd(dev(store(q, dt), dt), dev(store(kc, dt), dt), dev(store(vc, dt), dt),
+                            q_starts=dev(b["starts"]), kv_lengths=dev(b["lens"]),
+                            block_table=dev(b["table"]), max_q=n, layout="bshd", scale=d ** -0.5)
+    got = f64(from_device(out), dt)
+    for s, top in enumerate(best):
+        v = vc[b["table"][s][top // page], top % page]  # [Hkv, d], stored exactly
+        want = np.repeat(v, H // Hkv, axis=0)
+        assert np.array_equal(got[b["starts"][s]:b["starts"][s + 1]],
+                              np.broadcast_to(want, (n, H, d)))

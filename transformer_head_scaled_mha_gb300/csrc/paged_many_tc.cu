@@ -65,6 +65,7 @@ constexpr uint32_t kRegsControl = 72;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsControl <= kThreads * 168, "register split");
 constexpr uint32_t kTmemCols = 512;        // S_w at 128 w, O_w at 256 + 128 w
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr float kFarScore = 16777216.f;    // 2^24
 constexpr int kMaxSlots = 8;
 constexpr int kDescs = 4;     // part descriptions in flight
 constexpr int kPresent = 16;  // tiles whose pages' presence is kept (more than are in flight)
@@ -702,10 +703,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // us on 4 x 4096 tokens, 16 heads, d 64, with the products' loops from 183 to 94
         // KB).
         float alpha = 1.f, tsum = 0.f;
-        if (pos && !need_mask) {
+        bool plain = pos && !need_mask;
+        uint32_t v[2][32];
+        float cm = -INFINITY;
+        if (plain) {
           // (the first 64 columns last: the second pass begins with them)
-          uint32_t v[2][32];
-          float cm = -INFINITY;
 #pragma unroll 1
           for (int ch = 2; ch >= 0; ch -= 2) {
             tmem_ld32(s_tmem + ch * 32, v[0]);
@@ -714,11 +716,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             cm = fmax3(cm, chunk_max32(v[0]), chunk_max32(v[1]));
           }
           cm = fmaxf(cm * p.scale_log2, kLowestScore);
-          const bool climb = cm > m_use + kRescaleThreshold;
-          if (__any_sync(0xffffffffu, climb) && climb) {
-            alpha = ex2_approx(m_use - cm);
-            m_use = cm;
+          // The weights' exponents come from one fused product and difference, which the
+          // rounding of the maximum shifts by up to 2^-24 of it: the same for a row's weights
+          // and their sum, but past 2^31 enough to leave the range of fp32.  Such scores take
+          // the other way.
+          const bool climb = cm > m_use + kRescaleThreshold, far = fabsf(cm) > kFarScore;
+          if (__any_sync(0xffffffffu, climb || far)) {
+            plain = !__any_sync(0xffffffffu, far);
+            if (plain && climb) {
+              alpha = ex2_approx(m_use - cm);
+              m_use = cm;
+            }
           }
+        }
+        if (plain) {
 #pragma unroll 1
           for (int ch = 0; ch < 4; ch += 2) {
             if (ch > 0) {
@@ -734,14 +745,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          // masks, holes, a scale that is not positive: scores scaled (the max of
+          // masks, holes, far scores, a scale that is not positive: scores scaled (the max of
           // scale * s is not scale * max s) and masked first; in one pass, for these tiles
           // are few.  A chunk whose max exceeds the running one rescales the P of the
           // chunks already stored.
 #pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
-            uint32_t v[32];
-            tmem_ld32(s_tmem + ch * 32, v);
+            uint32_t(&v0)[32] = v[0];
+            tmem_ld32(s_tmem + ch * 32, v0);
             // columns of the chunk's two halves that count: below the limit, and not of
             // a page that is not there (pages have at least 16 rows)
             const int upto = lim - ch * 32;
@@ -750,10 +761,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              v[e] = __float_as_uint(e < (e < 16 ? upto0 : upto1)
-                                         ? __uint_as_float(v[e]) * p.scale_log2
-                                         : -INFINITY);
-            float cm = chunk_max32(v);
+              v0[e] = __float_as_uint(e < (e < 16 ? upto0 : upto1)
+                                          ? __uint_as_float(v0[e]) * p.scale_log2
+                                          : -INFINITY);
+            cm = chunk_max32(v0);
             if (upto0 > 0 || upto1 > 16) cm = fmaxf(cm, kLowestScore);  // a key is seen
             const bool climb = cm > m_use + kRescaleThreshold;
             if (__any_sync(0xffffffffu, climb)) {
@@ -766,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             uint32_t pk[16];
             // no key so far: weights of 0, not of -inf less -inf
-            tsum += chunk_exp_pack32(v, 1.f, m_use == -INFINITY ? 0.f : m_use, pk);
+            tsum += chunk_exp_pack32(v0, 1.f, m_use == -INFINITY ? 0.f : m_use, pk);
             tmem_st16(s_tmem + ch * 16, pk);
           }
         }
