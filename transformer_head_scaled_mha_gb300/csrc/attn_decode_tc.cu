@@ -568,9 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float lt = (sh->lsum[0][r] + sh->lsum[1][r]) + (sh->lsum[2][r] + sh->lsum[3][r]);
             float acc = __uint_as_float(o[r]);
             if (D == 64) acc += sh->xo[r][vdim];
-            // a row with no allowed key is stored as +0.0
-            *out_at(r) = bf16_bits(lt > 0.f ? acc * (1.f / lt) : 0.f);
-            if (p.lse != nullptr && k == 0) *lse_at(r) = lt > 0.f ? m[r] + __log2f(lt) : INFINITY;
+            // a row with no allowed key is stored as +0.0 (a NaN stays one)
+            *out_at(r) = bf16_bits(lt == 0.f ? 0.f : acc * (1.f / lt));
+            if (p.lse != nullptr && k == 0) *lse_at(r) = lt == 0.f ? INFINITY : m[r] + __log2f(lt);
           }
       }
       // lsum and xo are rewritten only after the next pair's first tile
