@@ -16,6 +16,7 @@ int *status_ptr();
 
 // Wait limit of the kernels' bounded waits (mha_debug_set_wait).
 uint64_t wait_limit_ns();
+int wait_stall();  // ... and its stall bits
 
 // 4-D view (d, L, heads, B) of a contiguous bf16 tensor in either layout,
 // 128-byte swizzle; box (64, box_rows, box_heads, 1)

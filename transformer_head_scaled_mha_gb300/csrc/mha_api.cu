@@ -141,6 +141,7 @@ void *symbol_ptr(const void *symbol) {
 int *status_ptr() { return static_cast<int *>(symbol_ptr(reinterpret_cast<const void *>(&g_status))); }
 
 uint64_t wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
+int wait_stall() { return g_stall.load(std::memory_order_relaxed); }
 
 cudaError_t set_smem_once(const void *kernel, int bytes) {
   const unsigned long long ctx = current_ctx_id();
@@ -825,7 +826,7 @@ extern "C" int mha_debug_status(void *stream_) {
 }
 
 extern "C" int mha_debug_set_wait(unsigned long long limit_ns, int stall) {
-  if (stall & ~(kStallShortMma | kStallLongMma)) return MHA_ERR_INVALID_ARGUMENT;
+  if (stall & ~kStallBits) return MHA_ERR_INVALID_ARGUMENT;
   g_wait_ns.store(limit_ns == 0 ? kWaitLimitNs : limit_ns, std::memory_order_relaxed);
   g_stall.store(stall, std::memory_order_relaxed);
   return MHA_OK;

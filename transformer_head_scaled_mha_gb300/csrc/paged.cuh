@@ -102,6 +102,7 @@ struct PagedProblem {
   int rows;       // rows of a slot
   int *status;
   uint64_t wait_ns;
+  int stall;  // test hook: kStall* bits (common.cuh)
 };
 
 // meta words of a CTA: which parts of split units it holds.  Slot 0 holds a part

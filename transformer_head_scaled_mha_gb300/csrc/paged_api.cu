@@ -429,6 +429,7 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   p.status = status_ptr();
   if (p.status == nullptr) return MHA_ERR_CUDA;
   p.wait_ns = wait_limit_ns();
+  p.stall = wait_stall();
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   p.split = u.split;
   int grid = launched_ctas(p, u.ctas);

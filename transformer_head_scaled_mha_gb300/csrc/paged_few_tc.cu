@@ -121,6 +121,7 @@ struct __align__(16) Shared {
   uint64_t p_full[2];   // P_t in smem, S_t read (softmax threads)
   uint64_t pv_done[2];  // PV_t done, by tile parity
   uint64_t o_free[2];   // the epilogue has read O of a part
+  uint64_t never;       // nothing signals it (test hook)
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
       mbar_init(&sh->kv_full[s], 1);
       mbar_init(&sh->kv_empty[s], 1);
     }
+    mbar_init(&sh->never, 1);
     sh->abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.q);
@@ -376,7 +378,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
   } else if (warp == 6) {
     // ---- PV products O (+)= P_t V_t (lane 0 issues; the warp waits) --------
     const uint32_t idesc_o = idesc_bf16_f32_amn(128, C::kPvN, 0);
-    bool ok = true;
+    // test hook: a wait on a barrier that nothing signals, with copies and score products
+    // in flight
+    bool ok = (p.stall & kStallPagedFewMma) == 0 ||
+              mbar_wait_warp(&sh->never, 0, abort_flag, p.wait_ns);
     int t = 0, oi = 0, slot = 0, round = 0;
     Desc d;
     for (int n = 0; ok && take_desc(sh, n, d, p.wait_ns, ok); ++n) {
@@ -455,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
         m[r] = -INFINITY;
         l[r] = 0.f;
       }
-      for (int j = 0; j < d.tiles; ++j) {
+      int j = 0;
+      for (; j < d.tiles; ++j) {
         const bool okw =
             mbar_wait_warp(&sh->kv_full[slot], round & 1, abort_flag, p.wait_ns) &&
             mbar_wait_warp(&sh->s_full[t & 1], (t >> 1) & 1, abort_flag, p.wait_ns);
@@ -559,7 +565,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
           ++round;
         }
       }
-      if (!ok) break;
+      // All four gave up at a tile's barrier.  (A warp alone may have in its waits behind the
+      // last one: it meets the others at the barrier below, where all learn of it.)
+      if (j < d.tiles) break;
       // ---- l = sum over the key slots; O = O^T / l, or both as they are -----
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
@@ -567,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
         if (lane == 0) sh->lsum[warp][r] = v;
       }
       const int u = t - 1;
-      const bool oke = mbar_wait_warp(&sh->pv_done[u & 1], (u >> 1) & 1, abort_flag, p.wait_ns);
+      const bool oke =
+          ok && mbar_wait_warp(&sh->pv_done[u & 1], (u >> 1) & 1, abort_flag, p.wait_ns);
       // d = 64: the second key half's output goes through the P buffer of the last
       // tile, which its product has read
       float *xo = reinterpret_cast<float *>(pbuf + (u & 1) * C::kPBytes);
@@ -597,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
       tc_fence_before();
       mbar_arrive(&sh->o_free[oi & 1]);
       ++oi;
-      ok = named_barrier_and(kBarSoftmax, kSoftmaxThreads, ok && oke);
+      ok = named_barrier_and(kBarSoftmax, kSoftmaxThreads, oke);
       if (!ok) break;
       if (stores) {
         float *sums = d.slot >= 0 ? paged_slot_ptr(p, D, blockIdx.x, d.slot) : nullptr;
