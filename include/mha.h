@@ -366,9 +366,10 @@ int mha_debug_status(void *stream);
  *      product;
  *   2  long-sequence kernel: the MMA issuer stalls before its third key
  *      tile, with products and copies in flight;
- *  16  few-query paged kernel (mha_paged_fwd): the issuer of the products with
- *      the values stalls before its first one, with copies and score products
- *      in flight.
+ *   8  few-query kernel of decoding steps: the issuer of the products with the
+ *      values stalls before its first one, with copies and score products in
+ *      flight;
+ *  16  few-query paged kernel (mha_paged_fwd): the same.
  * The output of a stalled call is undefined.  Process-wide setting; not for
  * use while other threads enqueue work.  Returns MHA_ERR_INVALID_ARGUMENT for
  * unknown stall bits.

@@ -5,12 +5,14 @@ tells MHA_ERR_TIMEOUT, and the next normal call is right."""
 import numpy as np
 import pytest
 
+import gen
+from helpers import check_case, run_gpu, spec
 from test_paged_gpu import batch, cache_of, check_paged
 from test_qk_rope_gpu import rnd
 
 pytestmark = pytest.mark.gpu
 
-STALL_FEW = 16
+STALL_DECODE, STALL_FEW = 8, 16
 
 
 def stalled(stall, call):
@@ -52,3 +54,14 @@ def test_few_query_paged_kernel(tiles, H, Hkv, n, d):
     stalled_paged(STALL_FEW, seqs, H, Hkv, d)
     stalled_paged(STALL_FEW, [(n, 20000 + 128 * tiles)] * 2, H, Hkv, d)
     check_paged(seqs[:40] + [(n, 3000)], H, Hkv, d, "bf16", 64, "bshd")
+
+
+@pytest.mark.parametrize("tiles", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("H,Hkv,Lq,d", [(2, 2, 1, 64), (4, 1, 1, 128), (4, 1, 4, 64)])
+def test_decoding_kernel(tiles, H, Hkv, Lq, d):
+    # a pair's last tile is the one whose wait runs out (three tiles), and others
+    case = spec(200, H, Lq, 128 * tiles + 1, d, mask=gen.MASK_KEY_PADDING, Hkv=Hkv,
+                len_range=(128 * tiles, 128 * tiles))
+    q, k, v, lens = gen.make_inputs(case, seed=3)
+    stalled(STALL_DECODE, lambda: run_gpu(q, k, v, lens, case))
+    check_case(spec(3, H, Lq, 128 * tiles + 1, d, Hkv=Hkv), seed=3)

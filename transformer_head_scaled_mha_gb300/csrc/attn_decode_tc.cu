@@ -101,6 +101,7 @@ struct __align__(16) Shared {
   uint64_t p_full[2];   // P_t in smem, S_t read (softmax threads)
   uint64_t pv_done[2];  // PV_t done, by tile parity
   uint64_t o_free[2];   // the epilogue has read O of a pair
+  uint64_t never;       // nothing signals it (test hook)
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->kv_full[s], 1);
       mbar_init(&sh->kv_empty[s], 1);
     }
+    mbar_init(&sh->never, 1);
     sh->abort_flag = 0;
     fence_barrier_init();
   }
@@ -354,7 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
     int lo, hi;
     pair_range(p, lane, lo, hi);
-    bool ok = true;
+    // test hook: a wait on a barrier that nothing signals, with copies and score products
+    // in flight
+    bool ok = (p.stall & kStallDecodeMma) == 0 ||
+              mbar_wait_warp(&sh->never, 0, abort_flag, p.wait_ns);
     int t = 0, oi = 0, slot = 0, round = 0;
     int lens = 0;
     for (int pair = lo; pair < hi && ok; ++pair) {
@@ -452,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         m[r] = -INFINITY;
         l[r] = 0.f;
       }
-      for (int j = 0; j < nt; ++j) {
+      int j = 0;
+      for (; j < nt; ++j) {
         const bool okw =
             __all_sync(0xffffffffu, mbar_wait(&sh->s_full[t & 1], (t >> 1) & 1, abort_flag));
         float x[RP];
@@ -536,7 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sh->p_full[t & 1]);
         ++t;
       }
-      if (!ok) break;
+      // All four gave up at a tile's barrier.  (A warp alone may have in its waits behind the
+      // last one: it meets the others at the barrier below, where all learn of it.)
+      if (j < nt) break;
       // ---- epilogue: l = sum over the key slots, O = O^T / l -------------
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
@@ -544,8 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) sh->lsum[warp][r] = v;
       }
       const int u = t - 1;
-      const bool oke =
-          __all_sync(0xffffffffu, mbar_wait(&sh->pv_done[u & 1], (u >> 1) & 1, abort_flag));
+      const bool oke = ok && __all_sync(0xffffffffu, mbar_wait(&sh->pv_done[u & 1], (u >> 1) & 1,
+                                                               abort_flag));
       uint32_t o[RP];
       if (oke) {
         tc_fence_after();
@@ -559,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(&sh->o_free[oi & 1]);
       ++oi;
-      ok = named_barrier_and(kBarSoftmax, kSoftmaxThreads, ok && oke);
+      ok = named_barrier_and(kBarSoftmax, kSoftmaxThreads, oke);
       if (!ok) break;
       if (stores) {
 #pragma unroll

@@ -43,8 +43,9 @@ struct Problem {
 // Test hooks for the give-up path of the bounded waits (Problem::stall).
 constexpr int kStallShortMma = 1;  // short kernel: the MMA issuer waits before its first product
 constexpr int kStallLongMma = 2;   // long kernel: the MMA issuer waits before its third iteration
+constexpr int kStallDecodeMma = 8;  // decoding kernel: the PV issuer, before its first product
 constexpr int kStallPagedFewMma = 16;  // few-query paged kernel: the PV issuer, before its first product
-constexpr int kStallBits = kStallShortMma | kStallLongMma | kStallPagedFewMma;
+constexpr int kStallBits = kStallShortMma | kStallLongMma | kStallDecodeMma | kStallPagedFewMma;
 
 // Sets the dynamic shared-memory limit of a kernel once per device context
 // (a driver call per launch costs host time on every call).
