@@ -65,3 +65,35 @@ def test_decoding_kernel(tiles, H, Hkv, Lq, d):
     q, k, v, lens = gen.make_inputs(case, seed=3)
     stalled(STALL_DECODE, lambda: run_gpu(q, k, v, lens, case))
     check_case(spec(3, H, Lq, 128 * tiles + 1, d, Hkv=Hkv), seed=3)
+
+
+@pytest.mark.parametrize("H,Hkv,n,d,page", [(16, 16, 8192, 128, 128), (16, 16, 8192, 64, 64)])
+def test_a_limit_shorter_than_the_kernel(H, Hkv, n, d, page):
+    """A prompt of whole tiles takes longer than the limit (about 220 us against 100): no
+    wait is for work that others have in hand as long, so nothing gives up."""
+    import torch
+    import transformer_head_scaled_mha_gb300 as mha
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q, kc, vc = (torch.randn(s, generator=g, device="cuda").bfloat16()
+                 for s in ((n, H, d), (n // page, page, Hkv, d), (n // page, page, Hkv, d)))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kw = dict(q_starts=torch.tensor([0, n], **i32), kv_lengths=torch.tensor([n], **i32),
+              block_table=torch.randperm(n // page, generator=g, device="cuda").int()[None],
+              max_q=n, layout="bshd")
+    want = mha.mha_paged_fwd(q, kc, vc, **kw)
+    torch.cuda.synchronize()
+    ws = torch.empty(mha.mha_paged_workspace_size(1, n, H, Hkv, d, n, q.dtype),
+                     dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(q) for _ in range(5)]
+    torch.cuda.synchronize()
+    assert mha.mha_debug_status() == mha.MHA_OK
+    assert mha.mha_debug_set_wait(100_000, 0) == mha.MHA_OK
+    try:
+        for o in outs:
+            mha.mha_paged_fwd(q, kc, vc, o, workspace=ws, **kw)
+        torch.cuda.synchronize()
+    finally:
+        assert mha.mha_debug_set_wait(0, 0) == mha.MHA_OK
+    assert mha.mha_debug_status() == mha.MHA_OK
+    for o in outs:
+        assert torch.equal(o, want)

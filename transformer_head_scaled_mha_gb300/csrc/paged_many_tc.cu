@@ -100,6 +100,7 @@ struct __align__(16) Shared {
   uint32_t present[kPresent];  // pages of a tile that were loaded
   int zero_slot, zero_rows;    // for the zeroing warp: V slot (-1: done), rows below are whole
   uint32_t zero_present;       // ... pages that were loaded
+  int steps;                   // loads that the producer has come to
   uint64_t desc_full[kDescs], desc_empty[kDescs];
   uint64_t q_full, q_empty;
   uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
@@ -279,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sh->join, kWgThreads);
     mbar_init(&sh->drain, 1);
+    sh->steps = 0;
     sh->abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.q);
@@ -431,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (lane == 0) {
                 if (kv == 0) {
+                  *const_cast<volatile int *>(&sh->steps) = issued;
                   sh->present[(issued >> 1) % kPresent] = there;
                 } else if (partial) {
                   sh->zero_slot = slot;
@@ -613,7 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- finishes V tiles whose last rows, or some pages, were not loaded ----
       const int box_shift = min(p.batch.page_shift, 7);
       for (int n = 0;; ++n) {
-        if (!mbar_wait_warp(&sh->zero_full, n & 1, abort_flag, p.wait_ns)) break;
+        // (tiles that need finishing may be few: a chunk of whole tiles has none)
+        if (!mbar_wait_idle(&sh->zero_full, n & 1, abort_flag, p.wait_ns, &sh->steps)) break;
         const int slot = sh->zero_slot, rows = sh->zero_rows;
         const uint32_t there = sh->zero_present;
         if (slot < 0) break;

@@ -119,6 +119,28 @@ __device__ __forceinline__ bool mbar_wait_spin(uint64_t *bar, uint32_t parity,
   }
 }
 
+// mbar_wait for work that there may not be for as long as the kernel runs: gives up when
+// `steps` stands still for the limit, a count that the warp that would hand the work over
+// moves on with its own (whose waits are bounded).  Warp-uniform.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t *bar, uint32_t parity,
+                                               volatile int *abort_flag, uint64_t limit_ns,
+                                               const volatile int *steps) {
+  bool ok = true;
+  int seen = *steps;
+  uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 0; ok && !mbar_test(bar, parity); ++it) {
+    if ((it & 63u) != 63u) continue;
+    if (global_timer_ns() - t0 > limit_ns) {
+      const int now = *steps;
+      if (now == seen) *abort_flag = 1;
+      seen = now;
+      t0 = global_timer_ns();
+    }
+    ok = !*abort_flag;
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Warp-uniform bounded wait: every lane gets the same answer, so a warp
 // never reaches a later collective instruction (tcgen05.ld/st, shuffles,
 // barriers) with only part of its lanes.
