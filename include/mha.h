@@ -369,7 +369,9 @@ int mha_debug_status(void *stream);
  *   8  few-query kernel of decoding steps: the issuer of the products with the
  *      values stalls before its first one, with copies and score products in
  *      flight;
- *  16  few-query paged kernel (mha_paged_fwd): the same.
+ *  16  few-query paged kernel (mha_paged_fwd): the same;
+ *  32  many-query paged kernel: the MMA issuer stalls before its first product, or
+ *      before those of its second part of work.
  * The output of a stalled call is undefined.  Process-wide setting; not for
  * use while other threads enqueue work.  Returns MHA_ERR_INVALID_ARGUMENT for
  * unknown stall bits.

@@ -12,7 +12,7 @@ from test_qk_rope_gpu import rnd
 
 pytestmark = pytest.mark.gpu
 
-STALL_DECODE, STALL_FEW = 8, 16
+STALL_DECODE, STALL_FEW, STALL_MANY = 8, 16, 32
 
 
 def stalled(stall, call):
@@ -65,6 +65,17 @@ def test_decoding_kernel(tiles, H, Hkv, Lq, d):
     q, k, v, lens = gen.make_inputs(case, seed=3)
     stalled(STALL_DECODE, lambda: run_gpu(q, k, v, lens, case))
     check_case(spec(3, H, Lq, 128 * tiles + 1, d, Hkv=Hkv), seed=3)
+
+
+@pytest.mark.parametrize("seqs,H,Hkv,d", [
+    ([(512, 1024)] * 40, 2, 2, 128),              # whole tiles, several parts to a CTA
+    ([(300, 1000 + 7 * i) for i in range(60)], 4, 2, 64),   # ragged ones
+    ([(40, 700)] * 100 + [(60, 33)] * 100, 4, 2, 128),     # rows for one tile: both share them
+    ([(100, 20001)], 2, 1, 64),                   # one unit cut over the CTAs
+])
+def test_many_query_paged_kernel(seqs, H, Hkv, d):
+    stalled_paged(STALL_MANY, seqs, H, Hkv, d)
+    check_paged(seqs[:3], H, Hkv, d, "bf16", 64, "bshd")
 
 
 @pytest.mark.parametrize("H,Hkv,n,d,page", [(16, 16, 8192, 128, 128), (16, 16, 8192, 64, 64)])

@@ -45,7 +45,9 @@ constexpr int kStallShortMma = 1;  // short kernel: the MMA issuer waits before 
 constexpr int kStallLongMma = 2;   // long kernel: the MMA issuer waits before its third iteration
 constexpr int kStallDecodeMma = 8;  // decoding kernel: the PV issuer, before its first product
 constexpr int kStallPagedFewMma = 16;  // few-query paged kernel: the PV issuer, before its first product
-constexpr int kStallBits = kStallShortMma | kStallLongMma | kStallDecodeMma | kStallPagedFewMma;
+constexpr int kStallPagedManyMma = 32;  // many-query paged kernel: the issuer, before a part's first product
+constexpr int kStallBits = kStallShortMma | kStallLongMma | kStallDecodeMma | kStallPagedFewMma |
+                           kStallPagedManyMma;
 
 // Sets the dynamic shared-memory limit of a kernel once per device context
 // (a driver call per launch costs host time on every call).

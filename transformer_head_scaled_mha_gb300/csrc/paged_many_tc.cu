@@ -496,6 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++n;
           if (!go) break;
           if (tiles == 0) continue;
+          // test hook: a wait on a barrier that nothing signals before the teardown; in every
+          // other CTA before its first product, in the others with a part's behind it
+          if ((p.stall & kStallPagedManyMma) != 0 && nq == static_cast<int>(blockIdx.x & 1) &&
+              !(ok = mbar_wait_spin(&sh->drain, 0, abort_flag, p.wait_ns)))
+            break;
           ok = mbar_wait_spin(&sh->q_full, nq & 1, abort_flag, p.wait_ns);
           const int cnt[2] = {both ? (tiles + 1) >> 1 : tiles0, both ? tiles >> 1 : tiles};
           const int steps = max(cnt[0], cnt[1]);
