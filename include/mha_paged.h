@@ -63,7 +63,8 @@ enum {
  * inv_freq      fp32 [rotary_dim / 2], 4-byte aligned, finite, |f| < 2^20
  *               (ignored when rotary_dim is 0)
  * B, H, H_kv, L >= 0; a tensor without elements is ignored (its pointers may be
- *               NULL), e.g. H_kv = 0 for queries alone; H_kv need not divide H
+ *               NULL), e.g. H_kv = 0 for queries alone; H_kv need not divide H.
+ *               B * L and H + 2 H_kv are at most 2^31 - 2^20 - 1
  * rotary_dim    0 .. d, a multiple of 16
  * style         MHA_ROPE_HALVES or MHA_ROPE_INTERLEAVED
  * eps           finite, >= 0
@@ -129,6 +130,9 @@ int mha_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, const
  *             [num_pages, page_size, H_kv, d] (MHA_LAYOUT_BSHD).  Cells that
  *             hold no position of a sequence may contain anything.  Sequences
  *             may share pages that they only read.
+ *
+ * T * H and B * H are at most 2^31 - 1 (mha_paged_fwd); T and H + 2 H_kv at most
+ * 2^31 - 2^20 - 1 (mha_paged_append).  More is MHA_ERR_UNSUPPORTED.
  *
  * These three arrays are 4-byte aligned.  page_size is a power of two >= 16;
  * d is 64 or 128; H_kv divides H; dtype F32 or BF16 for every tensor.

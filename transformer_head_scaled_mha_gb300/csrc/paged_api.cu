@@ -58,8 +58,12 @@ bool fits(std::initializer_list<long long> counts) {
   return true;
 }
 
-// tokens of the row operators: their warps step through 32-bit numbers
+// tokens of the row operators, and a token's rows: their warps step through 32-bit numbers
 constexpr long long kMaxTokens = 0x7fffffffLL - (1 << 20);
+bool rows_fit(long long tokens, int H, int H_kv, int d) {
+  return tokens <= kMaxTokens && H + 2LL * H_kv <= kMaxTokens && fits({tokens, H, d}) &&
+         fits({tokens, H_kv, d});
+}
 
 size_t elem_size(int dtype) { return dtype == MHA_DTYPE_F32 ? 4 : 2; }
 
@@ -169,8 +173,7 @@ extern "C" int mha_qk_norm_rope_fwd(const void *q, const void *k, void *q_out, v
   if (st == MHA_OK) st = check_rope(d, rotary_dim, style, eps);
   if (st != MHA_OK) return st;
   const long long tokens = static_cast<long long>(B) * L;
-  if (tokens > kMaxTokens || !fits({tokens, H, d}) || !fits({tokens, H_kv, d}))
-    return MHA_ERR_UNSUPPORTED;
+  if (!rows_fit(tokens, H, H_kv, d)) return MHA_ERR_UNSUPPORTED;
   if (tokens == 0 || (H == 0 && H_kv == 0)) return MHA_OK;
   const size_t e = elem_size(dtype);
   const size_t nq = static_cast<size_t>(tokens) * H * d * e;
@@ -225,8 +228,7 @@ extern "C" int mha_qk_norm_rope_bwd(const void *q, const void *k, const void *dq
   if (st == MHA_OK) st = check_rope(d, rotary_dim, style, eps);
   if (st != MHA_OK) return st;
   const long long tokens = static_cast<long long>(B) * L;
-  if (tokens > kMaxTokens || !fits({tokens, H, d}) || !fits({tokens, H_kv, d}))
-    return MHA_ERR_UNSUPPORTED;
+  if (!rows_fit(tokens, H, H_kv, d)) return MHA_ERR_UNSUPPORTED;
   if ((q_weight == nullptr) != (dq_weight == nullptr) ||
       (k_weight == nullptr) != (dk_weight == nullptr))
     return MHA_ERR_INVALID_ARGUMENT;
@@ -298,7 +300,7 @@ extern "C" int mha_paged_append(const void *q, const void *k, const void *v, voi
     st = check_batch(q_starts, kv_lengths, block_table, B, T, num_pages, page_size, max_pages,
                      layout, &a.batch);
   if (st != MHA_OK) return st;
-  if (T > kMaxTokens || !fits({T, H, d}) || !fits({num_pages, page_size, H_kv, d}) ||
+  if (!rows_fit(T, H, H_kv, d) || !fits({num_pages, page_size, H_kv, d}) ||
       !fits({B, max_pages}))
     return MHA_ERR_UNSUPPORTED;
   if (T == 0 || B == 0 || H_kv == 0) return MHA_OK;

@@ -456,8 +456,8 @@ struct Token {
   }
   __device__ __forceinline__ void next(const RopeArgs &a, int d) {
     if (a.layout == kLayoutBSHD) {
-      q += a.H * d;
-      k += a.Hkv * d;
+      q += static_cast<long long>(a.H) * d;
+      k += static_cast<long long>(a.Hkv) * d;
     } else {
       q += d;
       k += d;
