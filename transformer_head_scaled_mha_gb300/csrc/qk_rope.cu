@@ -26,8 +26,9 @@
 //
 // Angles: with the frequency in turns as a 64-bit binary fraction F =
 // frac(f / 2 pi) 2^64, the position times F modulo 2^64 is the angle's fraction of
-// a turn for any 32-bit position, because whole turns fall off the top; only the
-// last step to fp32 rounds (to 2^-25 of a turn).
+// a turn for any 32-bit position, because whole turns fall off the top.  F is short of
+// the fraction by less than 2^-64, the angle of the farthest position by 2^-33 of a turn;
+// the step to fp32 drops less than 2^-32 and rounds to 2^-26 of a turn.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -128,19 +129,20 @@ __device__ __forceinline__ uint4 lds8x2(uint32_t at) {
   return v;
 }
 
-// frac(f / 2 pi) 2^64 for f = m 2^e: m times 2^66 / 2 pi (rounded to 64 bits), shifted
+// frac(f / 2 pi) 2^64, the fraction rounded down, for f = m 2^e, |f| < 2^20: m times
+// 2^130 / (2 pi) in two words, shifted.  The second word carries the fraction's last bits
+// for f > 2^-4: without it a position of 2^31 at f = 2^20 is off by up to 2^-18 of a turn.
 __device__ __forceinline__ unsigned long long turn_fraction(float f) {
-  constexpr unsigned long long k = 11743562013128004906ull;  // 2^66 / (2 pi)
+  constexpr unsigned long long k0 = 11743562013128004905ull, k1 = 18169587780923219392ull;
   const uint32_t bits = __float_as_uint(f);
   const int exp = (bits >> 23) & 255;
   const unsigned long long m = (bits & 0x7fffffu) | (exp != 0 ? 0x800000u : 0u);
-  const int right = 2 - ((exp != 0 ? exp : 1) - 150);  // bits to drop of the 88-bit product
-  const unsigned long long lo = m * k, hi = __umul64hi(m, k);
-  unsigned long long v;
-  if (right >= 128) v = 0;
-  else if (right >= 64) v = hi >> (right - 64);
+  const int right = 2 - ((exp != 0 ? exp : 1) - 150);  // bits to drop of the 88 above k1's
+  const unsigned long long carry = __umul64hi(m, k1), lo = m * k0 + carry;
+  const unsigned long long hi = __umul64hi(m, k0) + (lo < carry ? 1 : 0);
+  unsigned long long v = 0;  // (|f| from 2^28 on, infinities and NaN: no rotation)
+  if (right >= 64) v = right < 128 ? hi >> (right - 64) : 0;
   else if (right > 0) v = (hi << (64 - right)) | (lo >> right);
-  else v = right > -64 ? lo << -right : 0;
   return (bits >> 31) != 0 ? 0 - v : v;
 }
 
