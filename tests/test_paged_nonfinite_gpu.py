@@ -202,3 +202,29 @@ def test_far_scores(dt, H, Hkv, n, d, far):
         want = np.repeat(v, H // Hkv, axis=0)
         assert np.array_equal(got[b["starts"][s]:b["starts"][s + 1]],
                               np.broadcast_to(want, (n, H, d)))
+
+
+@pytest.mark.parametrize("mask_kind", [8, 0], ids=["causal", "all"])
+@pytest.mark.parametrize("dt,H,Hkv,n,d", FORMS)
+def test_rows_without_keys_are_plus_zero_bit_for_bit(dt, H, Hkv, n, d, mask_kind):
+    import torch
+    import transformer_head_scaled_mha_gb300 as mha
+    page = 16
+    rng = np.random.default_rng(7)
+    b = batch(rng, [(n, 0), (n, 300), (n, n // 2), (n, 2000)], page)
+    b["table"][1] = -1                     # no pages: nothing is there
+    qs = rnd(rng, (b["T"], H, d), dt)
+    ks, vs = (store(-np.abs(f64(rnd(rng, (b["pool"], page, Hkv, d), dt), dt)), dt)
+              for _ in range(2))           # negative values: a sum of none of them times 0 is -0
+    qd = dev(qs, dt)
+    out = mha.mha_paged_fwd(qd, dev(ks, dt), dev(vs, dt), torch.full_like(qd, -3.0),
+                            q_starts=dev(b["starts"]), kv_lengths=dev(b["lens"]),
+                            block_table=dev(b["table"]), max_q=n, layout="bshd",
+                            mask_kind=mask_kind)
+    bits = np.ascontiguousarray(from_device(out)).view(np.uint16 if dt == "bf16" else np.uint32)
+    none = np.zeros(b["T"], dtype=bool)
+    none[:2 * n] = True
+    # tokens before the first position (without a mask they see what there is)
+    none[2 * n:2 * n + (n - n // 2 if mask_kind == 8 else n if n // 2 == 0 else 0)] = True
+    assert np.all(bits[none] == 0)
+    assert np.all((bits[~none] != 0).any(-1))
