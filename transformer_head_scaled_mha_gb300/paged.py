@@ -15,6 +15,8 @@ from .mha import (MHA_DTYPE_BF16, MHA_DTYPE_F32, MHA_LAYOUT_BHSD, MHA_LAYOUT_BSH
 MHA_ROPE_HALVES, MHA_ROPE_INTERLEAVED = 0, 1
 PAGED_PATH_NAMES = {0: "none", 1: "paged_simt", 2: "paged_few_tc", 3: "paged_many_tc"}
 
+_INT_MAX = 0x7fffffff
+
 EXPORTED = ("mha_qk_norm_rope_fwd", "mha_qk_norm_rope_bwd_workspace_size", "mha_qk_norm_rope_bwd",
             "mha_paged_append", "mha_paged_workspace_size", "mha_paged_fwd", "mha_paged_path")
 
@@ -265,6 +267,8 @@ def _batch(q_starts, kv_lengths, block_table, dev):
     if block_table.dim() != 2:
         raise ValueError("block_table must have 2 dimensions")
     B, max_pages = table = block_table.shape
+    if B > _INT_MAX or max_pages > _INT_MAX:  # ctypes would keep the low 32 bits
+        raise ValueError("block_table has more than 2^31 - 1 rows or columns")
     return (_at("q_starts", q_starts, (B + 1,), i32, dev),
             _at("kv_lengths", kv_lengths, (B,), i32, dev),
             _at("block_table", block_table, table, i32, dev)), B, max_pages
