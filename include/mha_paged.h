@@ -176,7 +176,8 @@ size_t mha_paged_workspace_size(int B, int T, int H, int H_kv, int d, int max_q,
  * max_q      the most new tokens of a sequence that the caller expects, >= 1 (1
  *            for a step of single tokens).  It chooses the kernel, and the result
  *            is right whatever it is; a good value is the largest
- *            q_starts[b + 1] - q_starts[b].
+ *            q_starts[b + 1] - q_starts[b].  (BF16: up to (H / H_kv) max_q = 8 the
+ *            softmax weights are kept to 2^-17, past that to 2^-8.)
  * scale      finite
  * max_pages * page_size  at most 2^31 - 1024
  * workspace  device memory of at least mha_paged_workspace_size(...) bytes,

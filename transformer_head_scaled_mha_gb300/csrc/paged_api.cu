@@ -111,10 +111,13 @@ int current_sms() {
 
 // ---- attention over the cache -------------------------------------------------
 // Expected query rows per key/value head up to which the few-query kernel is taken.
-// Measured, few / many: 16 rows, 8 sequences of 1000-8000 keys, d 128: 27 / 39 us; 12
-// rows, 64 of 500-2000, d 64: 91 / 105; the other way at worst 256 of 200-600, 16 rows,
-// d 128: 81 / 75.  32 rows (a few-query kernel of that size), 64 sequences of 1000-4000:
-// 101 / 84 us, 128 of 300-900: 160 / 87 us.
+// Measured at 16 rows, few / many: one token of 16 heads over 1, 8 sequences of 1000-8000
+// keys, d 128: 17 / 32 us; of 64 over 4, 16 such sequences: 38 / 49; 4 tokens of 32 heads
+// over 8, 32 sequences of 500-2000, d 128: 44 / 50.  Units short beside their number go the
+// other way: the same 32 sequences at d 64: 41 / 36; 256 of 200-600, d 128: 144 / 129 (12
+// rows: 141 / 129).  8 rows, 16 x 2 tokens of 32 heads over 8, 4000 keys, d 128: 52 / 66.
+// A few-query kernel of 32 rows, 64 sequences of 1000-4000: 101 / 84 us, 128 of 300-900:
+// 160 / 87.
 constexpr int kFewRows = 16;
 
 enum PagedPath { kNone = 0, kSimt = 1, kFew = 2, kMany = 3 };

@@ -29,14 +29,17 @@
 // there, are zeroed in shared memory by a warp of their own before the product
 // reads them.
 //
-// Measured, with the merge: a prompt of 8192 tokens, 16 heads, d 128: 221-228 us, 1.2
-// PFLOP/s of allowed products (0.63 of a library product's rate); 8 chunks of up to 512
-// tokens behind 1000-4096 keys, 32 heads over 8: 79 us, 0.72 PFLOP/s.  A pair of tiles
-// takes 1.75 us: a warpgroup's softmax (0.85) and its two products (0.9 with the waits)
-// follow one another, because P_w lies in S_w's columns; d = 64 has columns for P of its
-// own, but scores formed before the products then cost more in waits than they gain (215
-// -> 227 us on 4 x 4096 tokens, 16 heads).  The way to the first tile is 8 us, a part's
-// beginning and end 3, the merge 8.
+// Measured, with the merge: a prompt of 8192 tokens, 16 heads, d 128: 223 us, 1.23
+// PFLOP/s of allowed products (0.65 of a library product's rate); 8 chunks of up to 512
+// tokens behind 1000-4096 keys, 32 heads over 8: 78 us, 0.73 PFLOP/s; 4 x 4096 tokens, 16
+// heads, d 64: 215 us, 0.64 PFLOP/s.  A pair of tiles takes about 1.75 us at d 128 and
+// 1.55 at d 64, whose products are half as long, so the chain of a row sets the pace: one
+// thread's two passes over 128 columns (0.85 us), then its two products, which have to
+// wait because P_w lies in S_w's columns.  d = 64 has columns for P of its own, but scores
+// formed before the products then cost more in waits than they gain (215 -> 227 us).  The
+// way to the first tile is 8 us, a part's beginning and end 3, the merge 8.  Up to 32 rows
+// (drafts of grouped heads) lie in one warp of a warpgroup, and the others wait for its
+// exponentials: 16 x 8 tokens over 4000 keys, 32 heads over 8, d 128: 65 us, 0.60 of HBM.
 //
 // Warp roles (384 threads): warps 0-3 and 4-7 softmax, warp 8 producer (walks the
 // parts and hands their descriptions to the others), warp 9 TMEM owner and product

@@ -17,7 +17,11 @@
 // limits in shared memory, found once.  Measured, with the merge: 8 sequences of 90-700
 // keys, 5 tokens of 8 heads over 2, d 64: 17.5 us (44 with two tiles to a CTA and rows in
 // registers); one token, 16 sequences of 1000-4000 keys, 32 heads over 8, d 128: 69 us,
-// 4.8 TB/s.
+// 4.8 TB/s; 4 tokens, 8 such sequences: 69 us, 2.4 TB/s.  Chunks and prompts take it as
+// well, 16 rows at a time, each of which reads the keys again: 4 x 2048 tokens of 16 heads,
+// d 64: 1391 us, 25 TFLOP/s; d 128: 3075 us, 22 TFLOP/s (0.3 of the CUDA cores' nominal
+// 80), bound by the loads from shared memory (20 wavefronts to 64 FFMA in the score loop)
+// and, at d 128, by one CTA of four warps to an SM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -18,11 +18,14 @@
 // The backward reads two rows for each it writes and sums for the weights between
 // them: its rows are copied ahead into shared memory (Ahead).
 //
-// Measured: forward, 4 x 8192 tokens of 16 + 16 heads, d 128: 90 us, 5.95 TB/s (0.88 of a
-// copy's rate); appended prompts of 32 + 8 + 8 heads, d 128: 41 us (0.79); backward, 2 x
-// 4096 tokens of 32 + 8 heads, d 128: 47 us (0.79), 128 x 127 tokens of 8 + 8, d 64: 28
-// us (0.53: about 290 instructions for a warp's four rows, and 5 us before the first row and
-// for the weights' last sums).
+// Measured: forward, 4 x 8192 tokens of 16 + 16 heads, d 128: 90 us, 5.96 TB/s (0.88 of a
+// copy's rate); appended prompts of 32 + 8 + 8 heads, d 128: 40.4 us (0.79); backward, 2 x
+// 4096 tokens of 32 + 8 heads, d 128: 47 us (0.79).  fp32: forward, 2 x 8192 tokens of 16 +
+// 16, d 128: 87 us (0.91); those prompts 73 us (0.88); that backward 82 us (0.90).  Few short
+// rows to a token are bound by latency, with neither the issue slots (54%) nor DRAM (31%)
+// full: 128 x 127 tokens of 8 + 8 heads, d 64, backward 28 us (0.53: a round at a time, its
+// sums six shuffles behind one another, and 5 us before the first row and for the weights'
+// last sums), forward 26 (0.38: two rounds of loads to a token's tensor).
 //
 // Angles: with the frequency in turns as a 64-bit binary fraction F =
 // frac(f / 2 pi) 2^64, the position times F modulo 2^64 is the angle's fraction of
