@@ -294,9 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&sh->tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  tc_fence_before();
+  // The next launch may begin only when this CTA has its tensor memory: a CTA of it that
+  // allocated first could hold what this one waits for, and itself wait for this launch.
+  __syncthreads();
   griddep_launch_dependents();
   griddep_wait();  // lengths, queries and cache come from earlier work
-  tc_fence_before();
   const PagedSpan span = paged_span<kThreads>(p, blockIdx.x, gridDim.x, sh->scratch);
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
