@@ -359,9 +359,10 @@ int mha_debug_status(void *stream);
  * wall time (default 2 s) the waiting warp gives up, the CTA lets the copies
  * and products it has in flight finish, frees its tensor memory and records
  * MHA_ERR_TIMEOUT in the status word that mha_debug_status() reads.  This call
- * sets that limit for the calls enqueued after it (0 restores the default)
- * and, for tests, `stall` bits that make a kernel wait on a barrier nothing
- * signals, so the give-up path runs without any fault:
+ * sets that limit for the calls enqueued after it (0 restores the default; the
+ * decoding, backward and projection kernels keep the default but where they
+ * are stalled) and, for tests, `stall` bits that make a kernel wait on a
+ * barrier nothing signals, so the give-up path runs without any fault:
  *   1  packed short-sequence kernel: the MMA issuer stalls before its first
  *      product;
  *   2  long-sequence kernel: the MMA issuer stalls before its third key
@@ -370,8 +371,8 @@ int mha_debug_status(void *stream);
  *      values stalls before its first one, with copies and score products in
  *      flight;
  *  16  few-query paged kernel (mha_paged_fwd): the same;
- *  32  many-query paged kernel: the MMA issuer stalls before its first product, or
- *      before those of its second part of work.
+ *  32  many-query paged kernel: the MMA issuer stalls before its first product,
+ *      or before those of its second part of work.
  * The output of a stalled call is undefined.  Process-wide setting; not for
  * use while other threads enqueue work.  Returns MHA_ERR_INVALID_ARGUMENT for
  * unknown stall bits.
