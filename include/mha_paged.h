@@ -8,9 +8,12 @@
  *   mha_paged_append       the same for new tokens of ragged sequences, the
  *                          keys and values going into the pages of a cache
  *   mha_paged_fwd          attention of the new tokens over the paged cache
+ *   mha_paged_append_at    mha_paged_append with given positions: drafted trees
+ *   mha_paged_tree_fwd     attention of trees of drafted tokens
  *
  * A generation step is mha_linear_fwd (the projections), mha_paged_append,
- * mha_paged_fwd, mha_linear_fwd.  The pages that mha.h cites describe a decoder
+ * mha_paged_fwd, mha_linear_fwd; one that verifies drafted trees takes
+ * mha_paged_append_at and mha_paged_tree_fwd instead.  The pages that mha.h cites describe a decoder
  * that attends to every earlier position (alexdo.xyz, "How predictions are
  * generated"); paging, rotation and head norms are how present decoders carry
  * that out, and have no counterpart on the pages.
@@ -158,6 +161,23 @@ int mha_paged_append(const void *q, const void *k, const void *v, void *q_out, v
                      int num_pages, int page_size, int max_pages, int rotary_dim, int layout,
                      int style, float eps, int dtype, void *stream);
 
+/*
+ * mha_paged_append_at -- mha_paged_append whose rotation angles are those of given
+ * positions: a token of a drafted tree is rotated at the position it would have
+ * (the cached length plus its depth), and written to the cell of its place among
+ * the new tokens.
+ *
+ * positions  int32 [T]: row t is rotated by positions[t] f_i; any value, not read
+ *            for rows of no sequence.  Everything else as above: cells are those
+ *            of p = kv_lengths[b] - n + i.
+ */
+int mha_paged_append_at(const void *q, const void *k, const void *v, void *q_out, void *k_cache,
+                        void *v_cache, const void *q_weight, const void *k_weight,
+                        const float *inv_freq, const int32_t *positions, const int32_t *q_starts,
+                        const int32_t *kv_lengths, const int32_t *block_table, int B, int T, int H,
+                        int H_kv, int d, int num_pages, int page_size, int max_pages,
+                        int rotary_dim, int layout, int style, float eps, int dtype, void *stream);
+
 /* Bytes of device workspace mha_paged_fwd needs for these arguments, whatever
    the lengths (sums of sequences whose keys are split over the GPU); 0 for
    arguments it would reject or an empty problem. */
@@ -198,6 +218,29 @@ int mha_paged_fwd(const void *q, const void *k_cache, const void *v_cache, void 
                   int B, int T, int H, int H_kv, int d, int max_q, int num_pages, int page_size,
                   int max_pages, int layout, int mask_kind, float scale, int dtype,
                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * mha_paged_tree_fwd -- mha_paged_fwd for drafted tokens that form trees: token i of
+ * a sequence's n new ones sees every position before the first new token, and of
+ * the new ones those that the mask names (its ancestors, and itself).
+ *
+ * tree_mask  int32 [T, tree_words], 4-byte aligned: bit m % 32 of word m / 32 of
+ *            row t says whether token t sees new token m of its sequence (position
+ *            kv_lengths[b] - n + m).  Bits from n on mean nothing; new tokens from
+ *            32 tree_words on are seen by none.  Any bits are allowed, none too:
+ *            what a row sees need not be a path, and a row that sees nothing (and
+ *            has nothing cached before the new tokens) is written as +0.0.
+ * tree_words >= 1
+ * The workspace is that of mha_paged_fwd, and mha_paged_path tells the kernel;
+ * everything else as there (a new token's value must be finite where any other
+ * token of its sequence is in the call).
+ */
+int mha_paged_tree_fwd(const void *q, const void *k_cache, const void *v_cache, void *out,
+                       const int32_t *tree_mask, const int32_t *q_starts,
+                       const int32_t *kv_lengths, const int32_t *block_table, int B, int T, int H,
+                       int H_kv, int d, int max_q, int num_pages, int page_size, int max_pages,
+                       int tree_words, int layout, float scale, int dtype, void *workspace,
+                       size_t workspace_bytes, void *stream);
 
 /* Which kernel mha_paged_fwd would launch: 0 = none (empty problem), 1 = fp32
    CUDA-core kernel, 2 = few-query tensor-core kernel (at most 16 expected query

@@ -31,7 +31,7 @@ struct RopeArgs {
   void *q_out, *k_out, *v_out;  // appending: k_out, v_out are the caches
   const void *q_weight, *k_weight;  // nullptr: that tensor is not normed
   const float *inv_freq;
-  const int32_t *positions;  // [B, L] or nullptr (not appending)
+  const int32_t *positions;  // [B, L], or when appending [tokens]; nullptr: from the place
   int H, Hkv, L;             // not appending: token t = (t / L, t % L)
   int tokens;                // B * L, or the batch's T
   int rotary, layout, style;
@@ -103,6 +103,11 @@ struct PagedProblem {
   int *status;
   uint64_t wait_ns;
   int stall;  // test hook: kStall* bits (common.cuh)
+  // Trees of drafted tokens (nullptr: none; then `causal` says what a token sees): bit m
+  // of row t's `tree_words` words is set when token t sees new token m of its sequence.
+  // What lies before the new tokens every one of them sees.
+  const uint32_t *tree;
+  int tree_words;
 };
 
 // meta words of a CTA: which parts of split units it holds.  Slot 0 holds a part
@@ -138,6 +143,24 @@ MHA_HD PagedSeq paged_seq(const PagedBatch &p, int b) {
 MHA_HD int paged_kv_end(const PagedSeq &s, int i1, int causal) {
   if (!causal) return s.len;
   return max(min(s.base + i1, s.len), 0);
+}
+
+// ---- trees of drafted tokens -----------------------------------------------
+// Word i of a token's row; 0 outside it.
+MHA_HD uint32_t tree_word(const uint32_t *row, int words, int i) {
+  return static_cast<unsigned>(i) < static_cast<unsigned>(words) ? row[i] : 0u;
+}
+// Which of 32 positions a token sees, the first `from` positions behind its sequence's
+// first new token (negative: before it): lo and hi are words from >> 5 and the one behind.
+MHA_HD uint32_t tree_window(uint32_t lo, uint32_t hi, int from) {
+  const int s = from & 31;
+#ifdef __CUDA_ARCH__
+  uint32_t see = __funnelshift_r(lo, hi, s);
+#else
+  uint32_t see = s == 0 ? lo : (lo >> s) | (hi << (32 - s));
+#endif
+  if (from < 0) see |= from <= -32 ? 0xffffffffu : (1u << -from) - 1u;
+  return see;
 }
 
 // ---- the split of the units' keys over CTAs --------------------------------

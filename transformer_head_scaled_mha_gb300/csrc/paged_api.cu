@@ -287,13 +287,14 @@ extern "C" int mha_qk_norm_rope_bwd(const void *q, const void *k, const void *dq
              : MHA_ERR_CUDA;
 }
 
-extern "C" int mha_paged_append(const void *q, const void *k, const void *v, void *q_out,
-                                void *k_cache, void *v_cache, const void *q_weight,
-                                const void *k_weight, const float *inv_freq,
-                                const int32_t *q_starts, const int32_t *kv_lengths,
-                                const int32_t *block_table, int B, int T, int H, int H_kv, int d,
-                                int num_pages, int page_size, int max_pages, int rotary_dim,
-                                int layout, int style, float eps, int dtype, void *stream) {
+// mha_paged_append and mha_paged_append_at: `at` says whether the angles' positions are
+// given.
+static int append(const void *q, const void *k, const void *v, void *q_out, void *k_cache,
+                  void *v_cache, const void *q_weight, const void *k_weight, const float *inv_freq,
+                  bool at, const int32_t *positions, const int32_t *q_starts,
+                  const int32_t *kv_lengths, const int32_t *block_table, int B, int T, int H,
+                  int H_kv, int d, int num_pages, int page_size, int max_pages, int rotary_dim,
+                  int layout, int style, float eps, int dtype, void *stream) {
   if (H < 0 || H_kv < 0) return MHA_ERR_INVALID_ARGUMENT;
   if (H_kv == 0 ? H > 0 : H % H_kv != 0) return MHA_ERR_INVALID_ARGUMENT;
   int st = check_common(d, layout, dtype);
@@ -312,13 +313,14 @@ extern "C" int mha_paged_append(const void *q, const void *k, const void *v, voi
   const size_t nk = static_cast<size_t>(T) * H_kv * d * e;
   const size_t nc = static_cast<size_t>(num_pages) * page_size * H_kv * d * e;
   const Buffer outs[3] = {{q_out, nq, 16}, {k_cache, nc, 16}, {v_cache, nc, 16}};
-  const Buffer ins[9] = {
+  const Buffer ins[10] = {
       {q, nq, 16},
       {k, nk, 16},
       {v, nk, 16},
       {q_weight, q_weight != nullptr && nq > 0 ? d * e : 0, 16},
       {k_weight, k_weight != nullptr ? d * e : 0, 16},
       {inv_freq, rotary_dim / 2 * sizeof(float), 4},
+      {positions, at ? sizeof(int32_t) * static_cast<size_t>(T) : 0, 4},
       {q_starts, sizeof(int32_t) * (static_cast<size_t>(B) + 1), 4},
       {kv_lengths, sizeof(int32_t) * static_cast<size_t>(B), 4},
       {block_table, sizeof(int32_t) * static_cast<size_t>(B) * max_pages, 4}};
@@ -335,6 +337,7 @@ extern "C" int mha_paged_append(const void *q, const void *k, const void *v, voi
   a.q_weight = q_weight;
   a.k_weight = k_weight;
   a.inv_freq = inv_freq;
+  a.positions = at ? positions : nullptr;
   a.H = H;
   a.Hkv = H_kv;
   a.L = T;
@@ -347,6 +350,31 @@ extern "C" int mha_paged_append(const void *q, const void *k, const void *v, voi
                  cudaSuccess
              ? MHA_OK
              : MHA_ERR_CUDA;
+}
+
+extern "C" int mha_paged_append(const void *q, const void *k, const void *v, void *q_out,
+                                void *k_cache, void *v_cache, const void *q_weight,
+                                const void *k_weight, const float *inv_freq,
+                                const int32_t *q_starts, const int32_t *kv_lengths,
+                                const int32_t *block_table, int B, int T, int H, int H_kv, int d,
+                                int num_pages, int page_size, int max_pages, int rotary_dim,
+                                int layout, int style, float eps, int dtype, void *stream) {
+  return append(q, k, v, q_out, k_cache, v_cache, q_weight, k_weight, inv_freq, false, nullptr,
+                q_starts, kv_lengths, block_table, B, T, H, H_kv, d, num_pages, page_size,
+                max_pages, rotary_dim, layout, style, eps, dtype, stream);
+}
+
+extern "C" int mha_paged_append_at(const void *q, const void *k, const void *v, void *q_out,
+                                   void *k_cache, void *v_cache, const void *q_weight,
+                                   const void *k_weight, const float *inv_freq,
+                                   const int32_t *positions, const int32_t *q_starts,
+                                   const int32_t *kv_lengths, const int32_t *block_table, int B,
+                                   int T, int H, int H_kv, int d, int num_pages, int page_size,
+                                   int max_pages, int rotary_dim, int layout, int style, float eps,
+                                   int dtype, void *stream) {
+  return append(q, k, v, q_out, k_cache, v_cache, q_weight, k_weight, inv_freq, true, positions,
+                q_starts, kv_lengths, block_table, B, T, H, H_kv, d, num_pages, page_size,
+                max_pages, rotary_dim, layout, style, eps, dtype, stream);
 }
 
 extern "C" int mha_paged_path(int B, int T, int H, int H_kv, int d, int max_q, int page_size,
@@ -377,12 +405,14 @@ static int launched_ctas(const PagedProblem &p, int grid) {
       std::max(1LL, std::min<long long>(grid, paged_ctas(total, units, p.split.stretches))));
 }
 
-extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_cache, void *out,
-                             const int32_t *q_starts, const int32_t *kv_lengths,
-                             const int32_t *block_table, int B, int T, int H, int H_kv, int d,
-                             int max_q, int num_pages, int page_size, int max_pages, int layout,
-                             int mask_kind, float scale, int dtype, void *workspace,
-                             size_t workspace_bytes, void *stream_) {
+// mha_paged_fwd and mha_paged_tree_fwd: `of_tree` says whether tokens see one another as
+// the tree says.
+static int attend(const void *q, const void *k_cache, const void *v_cache, void *out, bool of_tree,
+                  const uint32_t *tree, int tree_words, const int32_t *q_starts,
+                  const int32_t *kv_lengths, const int32_t *block_table, int B, int T, int H,
+                  int H_kv, int d, int max_q, int num_pages, int page_size, int max_pages,
+                  int layout, int mask_kind, float scale, int dtype, void *workspace,
+                  size_t workspace_bytes, void *stream_) {
   int st = check_common(d, layout, dtype);
   PagedProblem p{};
   if (st == MHA_OK)
@@ -393,8 +423,9 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   if (path < 0) return -path;
   if (mask_kind != MHA_MASK_NONE && mask_kind != MHA_MASK_CAUSAL_TAIL)
     return MHA_ERR_INVALID_ARGUMENT;
-  if (!std::isfinite(scale)) return MHA_ERR_INVALID_ARGUMENT;
-  if (!fits({num_pages, page_size, H_kv, d}) || !fits({B, max_pages})) return MHA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || (of_tree && tree_words < 1)) return MHA_ERR_INVALID_ARGUMENT;
+  if (!fits({num_pages, page_size, H_kv, d}) || !fits({B, max_pages}) || !fits({T, tree_words}))
+    return MHA_ERR_UNSUPPORTED;
   // the kernels count keys, and a few tiles past them, in 32 bits
   if ((static_cast<long long>(max_pages) << p.batch.page_shift) > (1LL << 31) - 1024)
     return MHA_ERR_UNSUPPORTED;
@@ -406,9 +437,11 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   const size_t nw = workspace_bytes_of(u, d);
   if (workspace_bytes < nw) return MHA_ERR_INVALID_ARGUMENT;
   const Buffer outs[2] = {{out, nq, 16}, {workspace, nw, kAlign}};
-  const Buffer ins[6] = {{q, nq, 16},
+  const size_t nt = of_tree ? sizeof(uint32_t) * static_cast<size_t>(T) * tree_words : 0;
+  const Buffer ins[7] = {{q, nq, 16},
                          {k_cache, nc, 16},
                          {v_cache, nc, 16},
+                         {tree, nt, 4},
                          {q_starts, sizeof(int32_t) * (static_cast<size_t>(B) + 1), 4},
                          {kv_lengths, sizeof(int32_t) * static_cast<size_t>(B), 4},
                          {block_table, sizeof(int32_t) * static_cast<size_t>(B) * max_pages, 4}};
@@ -435,6 +468,10 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   if (p.status == nullptr) return MHA_ERR_CUDA;
   p.wait_ns = wait_limit_ns();
   p.stall = wait_stall();
+  if (of_tree) {
+    p.tree = tree;
+    p.tree_words = tree_words;
+  }
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   p.split = u.split;
   int grid = launched_ctas(p, u.ctas);
@@ -466,4 +503,28 @@ extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_c
   if (err == cudaSuccess && most > (2 * u.split.min_part - 1) * kPagedTile)
     err = launch_paged_merge(p, d, dtype, path == kMany, grid, stream);
   return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+}
+
+extern "C" int mha_paged_fwd(const void *q, const void *k_cache, const void *v_cache, void *out,
+                             const int32_t *q_starts, const int32_t *kv_lengths,
+                             const int32_t *block_table, int B, int T, int H, int H_kv, int d,
+                             int max_q, int num_pages, int page_size, int max_pages, int layout,
+                             int mask_kind, float scale, int dtype, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+  return attend(q, k_cache, v_cache, out, false, nullptr, 0, q_starts, kv_lengths, block_table, B,
+                T, H, H_kv, d, max_q, num_pages, page_size, max_pages, layout, mask_kind, scale,
+                dtype, workspace, workspace_bytes, stream);
+}
+
+extern "C" int mha_paged_tree_fwd(const void *q, const void *k_cache, const void *v_cache,
+                                  void *out, const int32_t *tree_mask, const int32_t *q_starts,
+                                  const int32_t *kv_lengths, const int32_t *block_table, int B,
+                                  int T, int H, int H_kv, int d, int max_q, int num_pages,
+                                  int page_size, int max_pages, int tree_words, int layout,
+                                  float scale, int dtype, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+  return attend(q, k_cache, v_cache, out, true, reinterpret_cast<const uint32_t *>(tree_mask),
+                tree_words, q_starts, kv_lengths, block_table, B, T, H, H_kv, d, max_q, num_pages,
+                page_size, max_pages, layout, MHA_MASK_NONE, scale, dtype, workspace,
+                workspace_bytes, stream);
 }

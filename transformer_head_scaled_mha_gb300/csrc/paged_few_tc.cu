@@ -182,7 +182,7 @@ __device__ __forceinline__ bool take_desc(Shared<RP> *sh, int n, Desc &d, uint64
   return d.go != 0;
 }
 
-template <int D, int RP>
+template <int D, int RP, bool kTree>
 __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
     paged_few_tc_kernel(const __grid_constant__ FewMaps maps,
                         const __grid_constant__ PagedProblem p) {
@@ -280,7 +280,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
         d.tiles = part.t1 - part.t0;
         d.key0 = part.t0 * kBN;
         d.kv_end = part.kv_end;
-        d.lim0 = p.causal ? part.seq.base + part.i0 + 1 : part.seq.len;
+        // of a tree: where its tokens begin
+        d.lim0 = kTree ? part.seq.base : (p.causal ? part.seq.base + part.i0 + 1 : part.seq.len);
         d.lim_step = p.causal;
         d.row0 = part.seq.q0 + part.i0;
         d.tokens = part.i1 - part.i0;
@@ -471,6 +472,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
       }
       int j = 0;
       for (; j < d.tiles; ++j) {
+        // Of a tree: tokens that see this thread's key, bit by token.  Their words are
+        // loaded before the waits; only a sequence's last tiles need any.
+        uint32_t seen = 0xffffffffu;
+        if (kTree && d.key0 + j * kBN + kBN > d.lim0) {
+          const int m = d.key0 + j * kBN + k - d.lim0;
+          if (m >= 0) {
+            seen = 0;
+            const uint32_t *tree = p.tree + static_cast<size_t>(d.row0) * p.tree_words;
+#pragma unroll 4
+            for (int tok = 0; tok < d.tokens; ++tok, tree += p.tree_words)
+              seen |= ((tree_word(tree, p.tree_words, m >> 5) >> (m & 31)) & 1u) << tok;
+          }
+        }
         const bool okw =
             mbar_wait_warp(&sh->kv_full[slot], round & 1, abort_flag, p.wait_ns) &&
             mbar_wait_warp(&sh->s_full[t & 1], (t >> 1) & 1, abort_flag, p.wait_ns);
@@ -493,7 +507,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
             int tok = 0;
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
-              if (!there || key >= d.lim0 + tok * d.lim_step) x[r] = -INFINITY;
+              const bool sees = kTree ? (seen >> tok) & 1u : key < d.lim0 + tok * d.lim_step;
+              if (!there || !sees) x[r] = -INFINITY;
               if (++tok == p.tb) tok = 0;
             }
             if (!there) {  // this key's value row: zeros (chunk order avoids bank conflicts)
@@ -664,8 +679,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
   if (warp == 5) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, int RP>
-cudaError_t launch_impl(const FewMaps &maps, const PagedProblem &p, int &grid, int num_sms,
+template <int D, int RP, bool kTree>
+cudaError_t launch_as(const FewMaps &maps, const PagedProblem &p, int &grid, int num_sms,
                         cudaStream_t stream) {
   using C = Cfg<D, RP>;
   constexpr size_t kSmem = smem_bytes<D, RP>();
@@ -675,7 +690,7 @@ cudaError_t launch_impl(const FewMaps &maps, const PagedProblem &p, int &grid, i
   static_assert(C::kSlots <= kMaxSlots, "ring size");
   grid = std::min(grid, C::kCtas * num_sms);
   const cudaError_t e = set_smem_once(
-      reinterpret_cast<const void *>(paged_few_tc_kernel<D, RP>), static_cast<int>(kSmem));
+      reinterpret_cast<const void *>(paged_few_tc_kernel<D, RP, kTree>), static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -687,7 +702,14 @@ cudaError_t launch_impl(const FewMaps &maps, const PagedProblem &p, int &grid, i
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_few_tc_kernel<D, RP>, maps, p);
+  return cudaLaunchKernelEx(&cfg, paged_few_tc_kernel<D, RP, kTree>, maps, p);
+}
+
+template <int D, int RP>
+cudaError_t launch_impl(const FewMaps &maps, const PagedProblem &p, int &grid, int num_sms,
+                        cudaStream_t stream) {
+  return p.tree != nullptr ? launch_as<D, RP, true>(maps, p, grid, num_sms, stream)
+                           : launch_as<D, RP, false>(maps, p, grid, num_sms, stream);
 }
 
 template <int D>

@@ -244,7 +244,7 @@ __device__ __forceinline__ void store_rows(uint32_t o0, uint32_t o1, float a0, f
   }
 }
 
-template <int D>
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_many_tc_kernel(const __grid_constant__ ManyMaps maps,
                          const __grid_constant__ PagedProblem p) {
@@ -348,7 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           d.both = part.i1 - part.i0 <= tbw;
           d.key0 = part.t0 * kBN;
           d.kv_end = part.kv_end;
-          d.lim0 = p.causal ? part.seq.base + part.i0 + 1 : part.seq.len;
+          // of a tree: where its tokens begin
+          d.lim0 =
+              kTree ? part.seq.base : (p.causal ? part.seq.base + part.i0 + 1 : part.seq.len);
           d.lim_step = p.causal;
           d.row0 = part.seq.q0 + part.i0;
           d.tokens = part.i1 - part.i0;
@@ -687,6 +689,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l_run = 0.f;
       for (int it = 0; it < cnt; ++it) {
         const int jj = d.both ? 2 * it + w : it;  // tile of the part
+        // Of a tree: the row's words that this tile needs, loaded before the wait; only a
+        // sequence's last tiles need any.
+        uint32_t words[5] = {0u, 0u, 0u, 0u, 0u};
+        const int from = d.key0 + jj * kBN - d.lim0;
+        if (kTree && row && from > -kBN) {
+          const uint32_t *tree = p.tree + static_cast<size_t>(d.row0 + i) * p.tree_words;
+#pragma unroll
+          for (int x = 0; x < 5; ++x) words[x] = tree_word(tree, p.tree_words, (from >> 5) + x);
+        }
         // S_w is ready, and so is every product issued before it (same commit)
         if (!(ok = mbar_wait_warp(&sh->s_full[w], ts & 1, abort_flag, p.wait_ns))) break;
         tc_fence_after();
@@ -770,17 +781,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(s_tmem + ch * 32, v0);
             // columns of the chunk's two halves that count: below the limit, and not of
             // a page that is not there (pages have at least 16 rows)
-            const int upto = lim - ch * 32;
+            const int upto = (kTree ? min(d.kv_end - key, kBN) : lim) - ch * 32;
             const int upto0 = (holes >> ((ch * 32) >> box_shift)) & 1 ? 0 : upto;
             const int upto1 = (holes >> ((ch * 32 + 16) >> box_shift)) & 1 ? 0 : upto;
+            uint32_t see = 0xffffffffu;
+            if (kTree) {
+              see = tree_window(words[0], words[1], from + ch * 32);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) words[x] = words[x + 1];
+              see &= (upto0 >= 16 ? 0xffffu : (1u << max(upto0, 0)) - 1u) |
+                     ((upto1 >= 32 ? 0xffffu : (1u << max(upto1 - 16, 0)) - 1u) << 16);
+            }
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              v0[e] = __float_as_uint(e < (e < 16 ? upto0 : upto1)
+              v0[e] = __float_as_uint((kTree ? (see >> e) & 1u : e < (e < 16 ? upto0 : upto1))
                                           ? __uint_as_float(v0[e]) * p.scale_log2
                                           : -INFINITY);
             cm = chunk_max32(v0);
-            if (upto0 > 0 || upto1 > 16) cm = fmaxf(cm, kLowestScore);  // a key is seen
+            // a key is seen
+            if (kTree ? see != 0 : upto0 > 0 || upto1 > 16) cm = fmaxf(cm, kLowestScore);
             const bool climb = cm > m_use + kRescaleThreshold;
             if (__any_sync(0xffffffffu, climb)) {
               const float f = climb ? ex2_approx(m_use - cm) : 1.f;
@@ -892,8 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D>
-cudaError_t launch_impl(const ManyMaps &maps, const PagedProblem &p, int grid,
+template <int D, bool kTree>
+cudaError_t launch_as(const ManyMaps &maps, const PagedProblem &p, int grid,
                         cudaStream_t stream) {
   constexpr size_t kSmem = smem_bytes<D>();
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -904,7 +924,7 @@ cudaError_t launch_impl(const ManyMaps &maps, const PagedProblem &p, int grid,
   static std::atomic<int> regs_ok{0};  // 0 unknown, 1 enough, 2 too few
   if (regs_ok.load(std::memory_order_acquire) == 0) {
     cudaFuncAttributes fa;
-    const cudaError_t e = cudaFuncGetAttributes(&fa, paged_many_tc_kernel<D>);
+    const cudaError_t e = cudaFuncGetAttributes(&fa, paged_many_tc_kernel<D, kTree>);
     if (e != cudaSuccess) return e;
     regs_ok.store(static_cast<long long>(fa.numRegs) * kThreads >=
                           2LL * 128 * kRegsSoftmax + 128LL * kRegsControl
@@ -913,8 +933,9 @@ cudaError_t launch_impl(const ManyMaps &maps, const PagedProblem &p, int grid,
                   std::memory_order_release);
   }
   if (regs_ok.load(std::memory_order_acquire) != 1) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(paged_many_tc_kernel<D>),
-                                      static_cast<int>(kSmem));
+  const cudaError_t e =
+      set_smem_once(reinterpret_cast<const void *>(paged_many_tc_kernel<D, kTree>),
+                    static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -926,7 +947,14 @@ cudaError_t launch_impl(const ManyMaps &maps, const PagedProblem &p, int grid,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_many_tc_kernel<D>, maps, p);
+  return cudaLaunchKernelEx(&cfg, paged_many_tc_kernel<D, kTree>, maps, p);
+}
+
+template <int D>
+cudaError_t launch_impl(const ManyMaps &maps, const PagedProblem &p, int grid,
+                        cudaStream_t stream) {
+  return p.tree != nullptr ? launch_as<D, true>(maps, p, grid, stream)
+                           : launch_as<D, false>(maps, p, grid, stream);
 }
 
 }  // namespace

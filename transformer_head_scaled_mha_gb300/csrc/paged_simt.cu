@@ -98,11 +98,12 @@ struct Smem {
   float m[kWarps][kRows], l[kWarps][kRows];
   float f[kWarps][kRows], total[kRows];  // the warps' weights when joined, and the sum
   long long row[kRows];                  // where a row's query and output begin (-1: no row)
-  int lim[kRows];                        // keys below this are allowed
+  int lim[kRows];                        // keys below this are allowed (of a tree: the row's
+                                         // token, -1: no row)
   long long scratch[40];
 };
 
-template <int D, int RP>
+template <int D, int RP, bool kTree>
 __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_constant__ PagedProblem p) {
   constexpr int kC = D / 32;  // output columns of a lane
   constexpr int kPer = 32 / RP;  // lanes to a row in the softmax
@@ -142,7 +143,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
       sm.row[r] = h < part.heads && i < part.i1
                       ? (static_cast<long long>(part.seq.q0 + i) * p.H + part.h0 + h) * D
                       : -1;
-      sm.lim[r] = paged_kv_end(part.seq, i + 1, p.causal);
+      // of a tree: the row's token
+      sm.lim[r] = kTree ? (h < part.heads && i < part.i1 ? part.seq.q0 + i : -1)
+                        : paged_kv_end(part.seq, i + 1, p.causal);
     }
     __syncthreads();
     for (int e = threadIdx.x * 4; e < RP * D; e += kThreads * 4) {
@@ -151,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
           row >= 0 ? *reinterpret_cast<const float4 *>(q + row + e % D) : make_float4(0, 0, 0, 0);
     }
     const int mine = lane % RP, lim = sm.lim[mine];  // this lane's row in the softmax
+    const uint32_t *tree = kTree && lim >= 0 ? p.tree + static_cast<size_t>(lim) * p.tree_words : nullptr;
     float m = -INFINITY, l = 0.f;                    // ... its maximum, and its share of the sum
     float acc[RP][kC];
 #pragma unroll
@@ -191,12 +195,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
       }
       copy(kc, kw, D + 4, next);
       if (work) {
+        // keys of this warp that row `mine` sees, one bit each
+        uint32_t see = 0xffffffffu;
+        if (kTree) {
+          const int from = first - part.seq.base;
+          uint32_t lo = 0, hi = 0;
+          if (tree != nullptr && from > -kKeys) {
+            lo = tree_word(tree, p.tree_words, from >> 5);
+            hi = tree_word(tree, p.tree_words, (from >> 5) + 1);
+          }
+          see = tree_window(lo, hi, from);
+        }
         // row `mine`, keys lane / RP, + kPer, ...
         float x[RP], top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int i = 0; i < RP; ++i) {
           const int j = i * kPer + lane / RP;
-          x[i] = first + j < lim ? sm.p[warp][j][mine] : -INFINITY;
+          x[i] = (kTree ? (see >> j) & 1u : first + j < lim) ? sm.p[warp][j][mine] : -INFINITY;
           top = fmaxf(top, x[i]);
         }
 #pragma unroll
@@ -477,12 +492,18 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, int smem, cu
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+template <int D, int RP, bool kTree>
+cudaError_t simt_as(const PagedProblem &p, int grid, cudaStream_t stream) {
+  const cudaError_t e =
+      set_smem_once(reinterpret_cast<const void *>(paged_simt_kernel<D, RP, kTree>), sizeof(Smem<D>));
+  if (e != cudaSuccess) return e;
+  return launch(paged_simt_kernel<D, RP, kTree>, dim3(grid), kThreads, sizeof(Smem<D>), stream, p);
+}
+
 template <int D, int RP>
 cudaError_t simt(const PagedProblem &p, int grid, cudaStream_t stream) {
-  const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(paged_simt_kernel<D, RP>),
-                                      sizeof(Smem<D>));
-  if (e != cudaSuccess) return e;
-  return launch(paged_simt_kernel<D, RP>, dim3(grid), kThreads, sizeof(Smem<D>), stream, p);
+  return p.tree != nullptr ? simt_as<D, RP, true>(p, grid, stream)
+                           : simt_as<D, RP, false>(p, grid, stream);
 }
 
 template <int D>

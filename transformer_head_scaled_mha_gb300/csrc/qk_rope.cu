@@ -419,10 +419,12 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const Rope
       // tokens up to the sequence's end count back from its length
       if (live)
         pos = max(a.batch.kv_lengths[seq], 0) - (min(a.batch.q_starts[seq + 1], a.tokens) - t);
+      // (drafted trees: the angle's position is not the cell's)
+      ang.at(a.positions != nullptr ? a.positions[t] : pos, col);
     } else {
       pos = a.positions != nullptr ? a.positions[t] : t % a.L;
+      ang.at(pos, col);
     }
-    ang.at(pos, col);
     const int layout = kAppend ? kLayoutBSHD : a.layout;
     const Rows q = rows_of(layout, t, a.H, a.L, D), k = rows_of(layout, t, a.Hkv, a.L, D);
     fwd_rows<T, D, kStyle, false>(static_cast<const T *>(a.q) + q.base, q.step,

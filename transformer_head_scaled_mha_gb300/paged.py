@@ -1,7 +1,8 @@
 """Python binding of the C ABI in include/mha_paged.h (ctypes; argument marshalling only).
 
 The per-head norm and position rotation of queries and keys with its gradients,
-the paged key/value cache and the attention over it.  Same library, same errors
+the paged key/value cache and the attention over it, for trees of drafted tokens
+too.  Same library, same errors
 and same conventions as ``mha.py``: torch CUDA tensors in, nothing computed here.
 """
 from __future__ import annotations
@@ -18,7 +19,8 @@ PAGED_PATH_NAMES = {0: "none", 1: "paged_simt", 2: "paged_few_tc", 3: "paged_man
 _INT_MAX = 0x7fffffff
 
 EXPORTED = ("mha_qk_norm_rope_fwd", "mha_qk_norm_rope_bwd_workspace_size", "mha_qk_norm_rope_bwd",
-            "mha_paged_append", "mha_paged_workspace_size", "mha_paged_fwd", "mha_paged_path")
+            "mha_paged_append", "mha_paged_append_at", "mha_paged_workspace_size", "mha_paged_fwd",
+            "mha_paged_tree_fwd", "mha_paged_path")
 
 
 def _declare() -> None:
@@ -32,10 +34,14 @@ def _declare() -> None:
     lib.mha_qk_norm_rope_bwd.argtypes = [vp] * 12 + numbers + [vp, sz, vp]
     lib.mha_paged_append.restype = i32
     lib.mha_paged_append.argtypes = [vp] * 12 + [i32] * 11 + [f32, i32, vp]
+    lib.mha_paged_append_at.restype = i32
+    lib.mha_paged_append_at.argtypes = [vp] * 13 + [i32] * 11 + [f32, i32, vp]
     lib.mha_paged_workspace_size.restype = sz
     lib.mha_paged_workspace_size.argtypes = [i32] * 7
     lib.mha_paged_fwd.restype = i32
     lib.mha_paged_fwd.argtypes = [vp] * 7 + [i32] * 11 + [f32, i32, vp, sz, vp]
+    lib.mha_paged_tree_fwd.restype = i32
+    lib.mha_paged_tree_fwd.argtypes = [vp] * 8 + [i32] * 11 + [f32, i32, vp, sz, vp]
     lib.mha_paged_path.restype = i32
     lib.mha_paged_path.argtypes = [i32] * 8
 
@@ -49,6 +55,31 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, device="cuda"):
     import torch
     i = torch.arange(rotary_dim // 2, dtype=torch.float64)
     return (float(base) ** (-2.0 * i / rotary_dim)).float().to(device)
+
+
+def tree_mask(parents, words=None, device="cuda"):
+    """Rows of mha_paged_tree_fwd's ``tree_mask`` and depths of one tree of drafted tokens.
+
+    ``parents``: for each token the number of its parent, which comes before it, or -1
+    (a root).  Returns (int32 [n, words], int32 [n]): every token sees its ancestors and
+    itself, and its position is the cached length before the tree plus its depth.
+    ``words``: of a row (default: as many as the tree needs)."""
+    import torch
+    n = len(parents)
+    if words is None:
+        words = max(1, -(-n // 32))
+    if n > 32 * words:
+        raise ValueError("a tree of %d tokens needs rows of more than %d words" % (n, words))
+    sees, depth = [], []
+    for i, p in enumerate(parents):
+        if not -1 <= p < i:
+            raise ValueError("token %d: its parent must be -1 or a token before it, not %d" % (i, p))
+        sees.append(1 << i | (sees[p] if p >= 0 else 0))
+        depth.append(depth[p] + 1 if p >= 0 else 0)
+    rows = [[(s >> 32 * w & 0xffffffff) for w in range(words)] for s in sees]
+    rows = [[x - (1 << 32) if x >> 31 else x for x in r] for r in rows]
+    return (torch.tensor(rows, dtype=torch.int32).reshape(n, words).to(device),
+            torch.tensor(depth, dtype=torch.int32).to(device))
 
 
 _modules = {}
@@ -288,6 +319,24 @@ def mha_paged_append(q, k, v, k_cache, v_cache, q_out=None, *, q_starts, kv_leng
     [pages,page_size,H_kv,d].  Rows of no sequence keep what ``q_out`` held (zeros
     when it is allocated here); ``q_out`` may be q itself.
     """
+    return _append("mha_paged_append", (), q, k, v, k_cache, v_cache, q_out, q_starts, kv_lengths,
+                   block_table, q_weight, k_weight, inv_freq, layout, interleaved, eps, stream)
+
+
+def mha_paged_append_at(q, k, v, k_cache, v_cache, positions, q_out=None, *, q_starts, kv_lengths,
+                        block_table, q_weight=None, k_weight=None, inv_freq=None,
+                        layout: str = "bhsd", interleaved: bool = False, eps: float = 1e-6,
+                        stream=None):
+    """mha_paged_append whose tokens are rotated at ``positions`` (int32 [T]) instead of
+    their cells': those of a drafted tree lie behind one another in the cache, each at
+    the position of its depth (``tree_mask``)."""
+    return _append("mha_paged_append_at", (positions,), q, k, v, k_cache, v_cache, q_out, q_starts,
+                   kv_lengths, block_table, q_weight, k_weight, inv_freq, layout, interleaved, eps,
+                   stream)
+
+
+def _append(name, positions, q, k, v, k_cache, v_cache, q_out, q_starts, kv_lengths, block_table,
+            q_weight, k_weight, inv_freq, layout, interleaved, eps, stream):
     lay = _layout_of(layout)
     if k.dim() != 3:
         raise ValueError("q, k and v must have 3 dimensions")
@@ -305,9 +354,10 @@ def mha_paged_append(q, k, v, k_cache, v_cache, q_out=None, *, q_starts, kv_leng
     args = (_at("q", q, (T, H, d), dt, dev), _at("k", k, ks, dt, dev), _at("v", v, ks, dt, dev),
             _at("q_out", q_out, (T, H, d), dt, dev), kc, vc,
             _at("q_weight", q_weight, (d,), dt, dev), _at("k_weight", k_weight, (d,), dt, dev), freq,
+            *[_at("positions", t, (T,), _torch().int32, dev) for t in positions],
             *arrays, B, T, H, Hkv, d, pages, page, max_pages, rotary, lay, 1 if interleaved else 0,
             eps, dtype)
-    _call("mha_paged_append", dev, stream, args)
+    _call(name, dev, stream, args)
     return q_out
 
 
@@ -335,6 +385,24 @@ def mha_paged_fwd(q, k_cache, v_cache, out=None, *, q_starts, kv_lengths, block_
     1/sqrt(d).  ``workspace``: uint8 CUDA tensor of at least
     mha_paged_workspace_size(B, T, H, H_kv, d, max_q, q.dtype) bytes (allocated here
     when None)."""
+    return _attend("mha_paged_fwd", (), q, k_cache, v_cache, out, q_starts, kv_lengths, block_table,
+                   max_q, layout, (mask_kind,), scale, workspace, stream)
+
+
+def mha_paged_tree_fwd(q, k_cache, v_cache, tree_mask, out=None, *, q_starts, kv_lengths,
+                       block_table, max_q: int, layout: str = "bhsd", scale=None, workspace=None,
+                       stream=None):
+    """mha_paged_fwd for new tokens that form a drafted tree in each sequence: a token sees
+    every position before its sequence's new tokens, and of those the ones in its row
+    of ``tree_mask``, int32 [T, words]: bit m % 32 of word m // 32 for new token m of
+    its sequence (the module's ``tree_mask`` makes the rows of a tree).  Everything else,
+    the workspace too, as mha_paged_fwd's."""
+    return _attend("mha_paged_tree_fwd", (tree_mask,), q, k_cache, v_cache, out, q_starts,
+                   kv_lengths, block_table, max_q, layout, (), scale, workspace, stream)
+
+
+def _attend(name, tree, q, k_cache, v_cache, out, q_starts, kv_lengths, block_table, max_q, layout,
+            mask, scale, workspace, stream):
     lay = _layout_of(layout)
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must have 3 dimensions and the caches 4")
@@ -350,8 +418,14 @@ def mha_paged_fwd(q, k_cache, v_cache, out=None, *, q_starts, kv_lengths, block_
             if workspace is None:
                 n = mha_paged_workspace_size(B, T, H, Hkv, d, max_q, dtype)
                 workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
-    args = (_at("q", q, qs, dt, dev), kc, vc, _at("out", out, qs, dt, dev), *arrays, B, T, H, Hkv, d,
-            max_q, pages, page, max_pages, lay, mask_kind, d ** -0.5 if scale is None else scale,
-            dtype, *_scratch(workspace, dev))
-    _call("mha_paged_fwd", dev, stream, args)
+    words = ()
+    if tree:
+        if tree[0].dim() != 2 or not 1 <= tree[0].shape[1] <= _INT_MAX:
+            raise ValueError("tree_mask must have 2 dimensions, at least one word to a row")
+        words = (tree[0].shape[1],)
+        tree = (_at("tree_mask", tree[0], (T, *words), _torch().int32, dev),)
+    args = (_at("q", q, qs, dt, dev), kc, vc, _at("out", out, qs, dt, dev), *tree, *arrays, B, T, H,
+            Hkv, d, max_q, pages, page, max_pages, *words, lay, *mask,
+            d ** -0.5 if scale is None else scale, dtype, *_scratch(workspace, dev))
+    _call(name, dev, stream, args)
     return out
