@@ -10,10 +10,16 @@
  *   mha_paged_fwd          attention of the new tokens over the paged cache
  *   mha_paged_append_at    mha_paged_append with given positions: drafted trees
  *   mha_paged_tree_fwd     attention of trees of drafted tokens
+ *   mha_paged_compact      the tokens that stay, moved to the front or elsewhere
+ *   mha_paged_reserve      the page tables of the next step: sequences that grow,
+ *                          shrink, fork, end and begin
+ *   mha_paged_copy         pages copied to pages, in all layers
  *
  * A generation step is mha_linear_fwd (the projections), mha_paged_append,
  * mha_paged_fwd, mha_linear_fwd; one that verifies drafted trees takes
- * mha_paged_append_at and mha_paged_tree_fwd instead.  The pages that mha.h cites describe a decoder
+ * mha_paged_append_at and mha_paged_tree_fwd instead, and mha_paged_compact when
+ * it knows which drafted tokens it accepts.  mha_paged_reserve and mha_paged_copy
+ * come before either.  The pages that mha.h cites describe a decoder
  * that attends to every earlier position (alexdo.xyz, "How predictions are
  * generated"); paging, rotation and head norms are how present decoders carry
  * that out, and have no counterpart on the pages.
@@ -247,6 +253,109 @@ int mha_paged_tree_fwd(const void *q, const void *k_cache, const void *v_cache, 
    rows, (H / H_kv) * max_q, per key/value head), 3 = many-query tensor-core
    kernel; negative = -(mha_status) for arguments it would reject.  Host only. */
 int mha_paged_path(int B, int T, int H, int H_kv, int d, int max_q, int page_size, int dtype);
+
+/*
+ * The page pool
+ *
+ * The operators below work on the block tables themselves and, for the caches of
+ * `layers` layers that lie behind one another in memory, on [layers, num_pages, ...]
+ * with every layer's pages laid out as above.  A sequence has the same pages in every
+ * layer and in both caches.  All int32 arrays are 4-byte aligned; the caches 16-byte.
+ */
+
+/* Bytes of device workspace mha_paged_reserve needs; 0 for arguments it rejects. */
+size_t mha_paged_reserve_workspace_size(int B, int num_pages);
+
+/*
+ * mha_paged_reserve -- the block tables of the next step.  Row i of the new tables
+ * continues row parents[i] of the old ones: it keeps the first
+ * keep = min(kv_lengths[parents[i]], new_lengths[i]) positions and gets pages for
+ * new_lengths[i].  So a sequence grows (parents[i] = i, a larger length), gives
+ * back what rejected tokens took (a smaller one), ends (0), begins (parents[i] = -1)
+ * or forks (a parent that several rows name, as beams do).
+ *
+ * refs counts each page's references: one for every row that holds a position in
+ * it, and whatever the caller adds to hold on to a page (a cached prefix).  With
+ * whole pages shared, and a part-filled last page a row's own, because the row will
+ * write to it:
+ *
+ *   refs_out[p] = refs[p] - references of the old rows + whole pages of the new rows
+ *   Where keep is no multiple of page_size, row i keeps its last page p if
+ *   refs_out[p] is then 0 or less and i is the lowest row whose last page p is, and
+ *   refs_out[p] grows by one.  Other such rows need a copy: a new page in p's place,
+ *   and moves[i] = (p, new page) for mha_paged_copy (otherwise (-1, -1)).
+ *   Pages with refs_out <= 0 are free.  The rows in their order get the lowest-numbered
+ *   free ones: a row's copy first, then the pages its new positions need, ascending.
+ *   They get refs_out = 1.
+ *
+ * When the free pages run out, the remaining places hold -1 and lengths_out says
+ * how far the row's pages go: new_lengths[i] where it got them all (at most
+ * max_pages * page_size), else the positions in the pages it has (without its
+ * part-filled page when that one's copy is missing).  The inputs are left as they
+ * were, so the caller may choose other lengths and call again.
+ *
+ * block_table, kv_lengths  int32 [B_old, max_pages], [B_old]: the old tables; entries
+ *               outside [0, num_pages) name no page, and are -1 where they are kept
+ * new_lengths, parents  int32 [B], [B]; a parent outside [0, B_old) is none; NULL:
+ *               row i's is i.  Lengths below 0 count as 0, those past
+ *               max_pages * page_size as that
+ * refs, refs_out  int32 [num_pages]; refs_out may be refs itself
+ * table_out, lengths_out, moves  int32 [B, max_pages], [B], [B, 2], overwritten;
+ *               entries that hold no position are -1
+ * counts        int32 [2], or NULL: pages given out, pages free after it
+ * B_old, B, num_pages at most 2^31 - 2^20 - 1, rows * max_pages at most 2^31 - 1,
+ *               max_pages * page_size at most 2^31 - 1024
+ * workspace     device memory of at least mha_paged_reserve_workspace_size(B,
+ *               num_pages) bytes, 256-byte aligned, overlapping nothing
+ */
+int mha_paged_reserve(const int32_t *block_table, const int32_t *kv_lengths,
+                      const int32_t *new_lengths, const int32_t *parents, const int32_t *refs,
+                      int32_t *table_out, int32_t *lengths_out, int32_t *refs_out, int32_t *moves,
+                      int32_t *counts, int B_old, int B, int num_pages, int page_size,
+                      int max_pages, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * mha_paged_copy -- k_cache[l, moves[i][1]] = k_cache[l, moves[i][0]], and v_cache,
+ * for every layer l and pair i (those of mha_paged_reserve).
+ *
+ * k_cache, v_cache  [layers, num_pages, page_size * H_kv * d], either layout
+ * moves    int32 [n, 2]; a pair with a number outside [0, num_pages) is skipped.  A
+ *          page that is written is no other pair's page (it would hold one of what
+ *          the pairs say, or parts of both)
+ */
+int mha_paged_copy(void *k_cache, void *v_cache, const int32_t *moves, int n, int layers, int H_kv,
+                   int d, int num_pages, int page_size, int dtype, void *stream);
+
+/*
+ * mha_paged_compact -- the tokens that stay of each sequence: position
+ * starts[b] + keep[b][i] moves to position starts[b] + i, in every layer, and the
+ * sequence ends behind the last:
+ *
+ *     lengths_out[b] = starts[b] + the number of kept tokens
+ *
+ * An accepted path of a drafted tree (starts: the cached length before the tree,
+ * keep: its tokens' numbers), or what is left of a long sequence.
+ *
+ * keep        int32 [B, max_keep], keep_counts [B] (clamped to [0, max_keep]): a list
+ *             ascends, from 0 on, and stays below kv_lengths[b] - starts[b].  It ends
+ *             before the first entry that does not (an entry that is no larger than the
+ *             one before it, a position that the sequence does not have)
+ * starts      int32 [B], or NULL: 0.  Clamped to [0, kv_lengths[b]]
+ * kv_lengths  int32 [B]: the lengths before; negative: 0
+ * block_table int32 [B, max_pages]: the pages that are written
+ * src_table   like it: the pages that are read; NULL: block_table, in place.  Where the
+ *             tables differ, a page that is written is none that is read
+ * A position in no page is neither read nor written.  In place, what a cell held is read
+ * before it is written; cells that are written belong to one sequence (and one place of
+ * its table) only.  lengths_out overlaps nothing.
+ * 2 B H_kv layers is at most 2^31 - 1
+ */
+int mha_paged_compact(void *k_cache, void *v_cache, int32_t *lengths_out, const int32_t *keep,
+                      const int32_t *keep_counts, const int32_t *starts,
+                      const int32_t *kv_lengths, const int32_t *src_table,
+                      const int32_t *block_table, int B, int layers, int H_kv, int d,
+                      int num_pages, int page_size, int max_pages, int max_keep, int layout,
+                      int dtype, void *stream);
 
 #ifdef __cplusplus
 }

@@ -5,9 +5,9 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <initializer_list>
 
 #include "../../include/mha_paged.h"
+#include "buffers.cuh"
 #include "common.cuh"
 #include "host.cuh"
 #include "paged.cuh"
@@ -15,57 +15,12 @@
 namespace mha {
 namespace {
 
-constexpr size_t kAlign = 256;
-size_t round_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
-
-// One argument's memory: where, how much, the alignment it needs.
-struct Buffer {
-  const void *p;
-  size_t n;
-  size_t align;
-};
-
-// Whether every buffer with a size is there and aligned.
-template <size_t N>
-bool present(const Buffer (&bufs)[N]) {
-  for (const Buffer &b : bufs)
-    if (b.n > 0 && (b.p == nullptr || reinterpret_cast<uintptr_t>(b.p) % b.align != 0)) return false;
-  return true;
-}
-
-// Whether an output shares memory with an input or another output; output i may
-// be input in_place[i] itself (same address).
-template <size_t N, size_t M>
-bool clash(const Buffer (&outs)[N], const Buffer (&ins)[M], const int (&in_place)[N]) {
-  for (size_t o = 0; o < N; ++o) {
-    for (size_t i = 0; i < M; ++i) {
-      if (static_cast<int>(i) == in_place[o] && outs[o].p == ins[i].p) continue;
-      if (overlaps(outs[o].p, outs[o].n, ins[i].p, ins[i].n)) return true;
-    }
-    for (size_t o2 = o + 1; o2 < N; ++o2)
-      if (overlaps(outs[o].p, outs[o].n, outs[o2].p, outs[o2].n)) return true;
-  }
-  return false;
-}
-
-// Whether a product of counts (>= 0) stays below 2^56: sizes in bytes then fit.
-bool fits(std::initializer_list<long long> counts) {
-  long long n = 1;
-  for (const long long c : counts) {
-    if (c != 0 && n > (1LL << 56) / c) return false;
-    n *= c;
-  }
-  return true;
-}
-
 // tokens of the row operators, and a token's rows: their warps step through 32-bit numbers
 constexpr long long kMaxTokens = 0x7fffffffLL - (1 << 20);
 bool rows_fit(long long tokens, int H, int H_kv, int d) {
   return tokens <= kMaxTokens && H + 2LL * H_kv <= kMaxTokens && fits({tokens, H, d}) &&
          fits({tokens, H_kv, d});
 }
-
-size_t elem_size(int dtype) { return dtype == MHA_DTYPE_F32 ? 4 : 2; }
 
 // Checks shared by every operator here.
 int check_common(int d, int layout, int dtype) {
@@ -101,12 +56,6 @@ int check_batch(const int32_t *q_starts, const int32_t *kv_lengths, const int32_
   b->max_pages = max_pages;
   b->layout = layout;
   return MHA_OK;
-}
-
-// SMs of the current device; 0 on failure
-int current_sms() {
-  int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess ? sm_count(dev) : 0;
 }
 
 // ---- attention over the cache -------------------------------------------------

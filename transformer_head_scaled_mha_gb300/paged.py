@@ -2,7 +2,7 @@
 
 The per-head norm and position rotation of queries and keys with its gradients,
 the paged key/value cache and the attention over it, for trees of drafted tokens
-too.  Same library, same errors
+too, and the page pool under it.  Same library, same errors
 and same conventions as ``mha.py``: torch CUDA tensors in, nothing computed here.
 """
 from __future__ import annotations
@@ -20,7 +20,8 @@ _INT_MAX = 0x7fffffff
 
 EXPORTED = ("mha_qk_norm_rope_fwd", "mha_qk_norm_rope_bwd_workspace_size", "mha_qk_norm_rope_bwd",
             "mha_paged_append", "mha_paged_append_at", "mha_paged_workspace_size", "mha_paged_fwd",
-            "mha_paged_tree_fwd", "mha_paged_path")
+            "mha_paged_tree_fwd", "mha_paged_path", "mha_paged_reserve_workspace_size",
+            "mha_paged_reserve", "mha_paged_copy", "mha_paged_compact")
 
 
 def _declare() -> None:
@@ -44,6 +45,14 @@ def _declare() -> None:
     lib.mha_paged_tree_fwd.argtypes = [vp] * 8 + [i32] * 11 + [f32, i32, vp, sz, vp]
     lib.mha_paged_path.restype = i32
     lib.mha_paged_path.argtypes = [i32] * 8
+    lib.mha_paged_reserve_workspace_size.restype = sz
+    lib.mha_paged_reserve_workspace_size.argtypes = [i32] * 2
+    lib.mha_paged_reserve.restype = i32
+    lib.mha_paged_reserve.argtypes = [vp] * 10 + [i32] * 5 + [vp, sz, vp]
+    lib.mha_paged_copy.restype = i32
+    lib.mha_paged_copy.argtypes = [vp] * 3 + [i32] * 7 + [vp]
+    lib.mha_paged_compact.restype = i32
+    lib.mha_paged_compact.argtypes = [vp] * 9 + [i32] * 10 + [vp]
 
 
 _declare()
@@ -429,3 +438,118 @@ def _attend(name, tree, q, k_cache, v_cache, out, q_starts, kv_lengths, block_ta
             d ** -0.5 if scale is None else scale, dtype, *_scratch(workspace, dev))
     _call(name, dev, stream, args)
     return out
+
+
+def _counted(name, shape):
+    """A shape whose counts the C entry points take (ctypes would keep their low 32 bits)."""
+    if any(n > _INT_MAX for n in shape):
+        raise ValueError("%s has more than 2^31 - 1 rows or columns" % name)
+    return shape
+
+
+def mha_paged_reserve_workspace_size(B: int, num_pages: int) -> int:
+    return int(lib.mha_paged_reserve_workspace_size(int(B), int(num_pages)))
+
+
+def mha_paged_reserve(block_table, kv_lengths, new_lengths, refs, *, page_size: int, parents=None,
+                      table_out=None, lengths_out=None, refs_out=None, moves=None, counts=None,
+                      workspace=None, stream=None):
+    """The block tables of the next step: row i continues row ``parents[i]`` (int32 [B];
+    None: its own number; -1: a new sequence) with ``new_lengths[i]`` positions, sharing
+    whole pages with its parent and taking free ones as it needs them.  Sequences grow,
+    shrink, fork, end (length 0) and begin.
+
+    block_table int32 [B_old, max_pages], kv_lengths [B_old], new_lengths [B], refs
+    [num_pages] (references to each page; 0: free).  Returns (table_out, lengths_out,
+    refs_out, moves, counts): the new tables, how far each row's pages go (less than its
+    length where the free pages ran out), the new references (``refs_out`` may be refs),
+    the page copies that the rows need, [B, 2], for ``mha_paged_copy``, and int32 [2]: pages
+    given out and pages still free."""
+    torch = _torch()
+    i32, dev = torch.int32, _device_of(block_table)
+    if block_table.dim() != 2 or new_lengths.dim() != 1 or refs.dim() != 1:
+        raise ValueError("block_table must have 2 dimensions, new_lengths and refs 1")
+    B_old, width = _counted("block_table", block_table.shape)
+    (B,), (pages,) = _counted("new_lengths", new_lengths.shape), _counted("refs", refs.shape)
+    if any(t is None for t in (table_out, lengths_out, refs_out, moves, counts, workspace)):
+        with _on(stream, block_table.device):
+            new = lambda *n: torch.empty(n, dtype=i32, device=block_table.device)  # noqa: E731
+            table_out = new(B, width) if table_out is None else table_out
+            lengths_out = new(B) if lengths_out is None else lengths_out
+            refs_out = new(pages) if refs_out is None else refs_out
+            moves = new(B, 2) if moves is None else moves
+            counts = new(2) if counts is None else counts
+            if workspace is None:
+                workspace = torch.empty(max(mha_paged_reserve_workspace_size(B, pages), 1),
+                                        dtype=torch.uint8, device=block_table.device)
+    args = (_at("block_table", block_table, (B_old, width), i32, dev),
+            _at("kv_lengths", kv_lengths, (B_old,), i32, dev),
+            _at("new_lengths", new_lengths, (B,), i32, dev),
+            _at("parents", parents, (B,), i32, dev), _at("refs", refs, (pages,), i32, dev),
+            _at("table_out", table_out, (B, width), i32, dev),
+            _at("lengths_out", lengths_out, (B,), i32, dev),
+            _at("refs_out", refs_out, (pages,), i32, dev), _at("moves", moves, (B, 2), i32, dev),
+            _at("counts", counts, (2,), i32, dev), B_old, B, pages, page_size, width,
+            *_scratch(workspace, dev))
+    _call("mha_paged_reserve", dev, stream, args)
+    return table_out, lengths_out, refs_out, moves, counts
+
+
+def _stack(k_cache, v_cache):
+    """(layers, shape of one layer's cache, its dtype, device) of caches with or without a
+    dimension of layers in front."""
+    if k_cache.dim() not in (4, 5):
+        raise ValueError("the caches must have 4 dimensions, or 5 with the layers in front")
+    shape = _counted("k_cache", k_cache.shape)
+    layers = shape[0] if len(shape) == 5 else 1
+    return layers, shape[-4:], k_cache.dtype, _device_of(k_cache)
+
+
+def mha_paged_copy(k_cache, v_cache, moves, *, stream=None):
+    """Copies page moves[i][0] to page moves[i][1] (int32 [n, 2]; pairs with a number that
+    is no page's are skipped) in both caches, [pages, ...] or [layers, pages, ...] in either
+    layout.  What mha_paged_reserve leaves to be copied."""
+    layers, (pages, a, b, d), dt, dev = _stack(k_cache, v_cache)
+    if moves.dim() != 2:
+        raise ValueError("moves must have 2 dimensions")
+    n, _ = _counted("moves", moves.shape)
+    # (a page's bytes are copied whatever their order: which of its two inner dimensions is
+    # the page's and which the heads' does not matter, but a page's is a power of two)
+    page, heads = (a, b) if a >= 16 and a & (a - 1) == 0 else (b, a)
+    args = (_at("k_cache", k_cache, k_cache.shape, dt, dev),
+            _at("v_cache", v_cache, k_cache.shape, dt, dev),
+            _at("moves", moves, (n, 2), _torch().int32, dev), n, layers, heads, d, pages, page,
+            _dtype_of(k_cache))
+    _call("mha_paged_copy", dev, stream, args)
+
+
+def mha_paged_compact(k_cache, v_cache, keep, keep_counts, lengths_out=None, *, starts=None,
+                      kv_lengths, block_table, src_table=None, layout: str = "bhsd", stream=None):
+    """Moves the tokens that stay: position starts[b] + keep[b][i] to starts[b] + i for i <
+    keep_counts[b], in both caches, [pages, ...] or [layers, pages, ...].  Returns the new
+    lengths, starts[b] + keep_counts[b].
+
+    keep int32 [B, max_keep]: ascending lists, which end before an entry that is not; starts
+    int32 [B] (None: 0); kv_lengths [B]: the lengths before; ``block_table`` [B, max_pages]:
+    the pages written, ``src_table`` those read (None: the same, in place)."""
+    torch = _torch()
+    i32, lay = torch.int32, _layout_of(layout)
+    layers, (pages, a, b, d), dt, dev = _stack(k_cache, v_cache)
+    page, heads = (a, b) if lay == MHA_LAYOUT_BSHD else (b, a)
+    if keep.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("keep and block_table must have 2 dimensions")
+    B, most = _counted("keep", keep.shape)
+    _, width = _counted("block_table", block_table.shape)
+    if lengths_out is None:
+        with _on(stream, k_cache.device):
+            lengths_out = torch.empty(B, dtype=i32, device=k_cache.device)
+    args = (_at("k_cache", k_cache, k_cache.shape, dt, dev),
+            _at("v_cache", v_cache, k_cache.shape, dt, dev),
+            _at("lengths_out", lengths_out, (B,), i32, dev), _at("keep", keep, (B, most), i32, dev),
+            _at("keep_counts", keep_counts, (B,), i32, dev), _at("starts", starts, (B,), i32, dev),
+            _at("kv_lengths", kv_lengths, (B,), i32, dev),
+            _at("src_table", src_table, (B, width), i32, dev),
+            _at("block_table", block_table, (B, width), i32, dev), B, layers, heads, d, pages, page,
+            width, most, lay, _dtype_of(k_cache))
+    _call("mha_paged_compact", dev, stream, args)
+    return lengths_out
