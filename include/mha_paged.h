@@ -303,8 +303,9 @@ size_t mha_paged_reserve_workspace_size(int B, int num_pages);
  * table_out, lengths_out, moves  int32 [B, max_pages], [B], [B, 2], overwritten;
  *               entries that hold no position are -1
  * counts        int32 [2], or NULL: pages given out, pages free after it
- * B_old, B, num_pages at most 2^31 - 2^20 - 1, rows * max_pages at most 2^31 - 1,
- *               max_pages * page_size at most 2^31 - 1024
+ * B_old, B, num_pages at most 2^31 - 2^20 - 1, B_old * max_pages and
+ *               B * (max_pages + 1) at most 2^29 - 1, max_pages * page_size at most
+ *               2^31 - 1024
  * workspace     device memory of at least mha_paged_reserve_workspace_size(B,
  *               num_pages) bytes, 256-byte aligned, overlapping nothing
  */

@@ -21,16 +21,18 @@ struct ReserveArgs {
   // workspace
   int32_t *lowest;  // [num_pages] of a part-filled page: the lowest row that keeps it
   int32_t *given;   // [num_pages] pages given out, in order
-  int32_t *first;   // [B] which of them is the row's first
-  int32_t *copies;  // [B] 1: that one is a copy of the row's last kept page
-  int32_t *totals;  // [kReserveTotals]
+  int32_t *last;    // [B] the row's part-filled page
+  int32_t *need;    // [B] pages that the row needs (kReserve* bits), then its first one's number
+  uint32_t *free;   // [num_pages / 32, rounded up] free pages, a bit each
+  int32_t *totals;  // [kReserveTotals] pages given out, blocks that are done
   int B_old, B;
   int num_pages, page_shift, max_pages;
 };
-constexpr int kReserveMaxCtas = 8;  // of a cluster
-// totals: pages that each CTA's rows need, free pages that each CTA finds, pages given
-constexpr int kReserveTotals = 64;
-constexpr int kTotalNeed = 0, kTotalFree = 16, kTotalGiven = 32;
+constexpr int kReserveTotals = 2, kTotalGiven = 0, kTotalDone = 1;
+// bits of a row's word beside its number
+constexpr int kReserveCopied = 1;  // its part-filled page is replaced by a copy
+constexpr int kReserveStays = 2;   // ... stays the row's own
+constexpr int kReserveShift = 2;
 
 // What row i of the new tables keeps of its parent, and what it wants.
 struct ReserveRow {
@@ -101,13 +103,14 @@ struct PageCopyArgs {
 cudaError_t launch_page_copy(const PageCopyArgs &a, int num_sms, cudaStream_t stream);
 
 // A kernel launch that may begin before the one ahead of it has ended (its griddep_wait
-// waits for that), as a cluster of `cluster` CTAs (1: none).
+// waits for that), in clusters of `cluster` CTAs.
 template <typename... Args>
-cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, int cluster,
+cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, int smem, int cluster,
                           cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

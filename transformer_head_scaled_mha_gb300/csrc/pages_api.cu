@@ -16,6 +16,9 @@ namespace {
 
 // rows and pages that the kernels step through in 32 bits
 constexpr long long kMaxCount = 0x7fffffffLL - (1 << 20);
+// entries of a table, and pages that its rows may need: their numbers share a word with
+// two bits
+constexpr long long kMaxEntries = 0x1fffffffLL;
 
 // page_size: a power of two of at least 16, and tables whose positions fit 32 bits
 int check_pages(int num_pages, int page_size, int max_pages, int *shift) {
@@ -48,7 +51,7 @@ using namespace mha;
 
 extern "C" size_t mha_paged_reserve_workspace_size(int B, int num_pages) {
   if (B < 0 || num_pages < 0 || B > kMaxCount || num_pages > kMaxCount) return 0;
-  return round_up(ints(2LL * num_pages + 2LL * B + kReserveTotals));
+  return round_up(ints(2LL * num_pages + 2LL * B + (num_pages + 31LL) / 32 + kReserveTotals));
 }
 
 extern "C" int mha_paged_reserve(const int32_t *block_table, const int32_t *kv_lengths,
@@ -62,8 +65,8 @@ extern "C" int mha_paged_reserve(const int32_t *block_table, const int32_t *kv_l
   const int st = check_pages(num_pages, page_size, max_pages, &a.page_shift);
   if (st != MHA_OK) return st;
   if (B_old > kMaxCount || B > kMaxCount ||
-      static_cast<long long>(B_old) * max_pages > 0x7fffffffLL ||
-      static_cast<long long>(B) * max_pages > 0x7fffffffLL)
+      static_cast<long long>(B_old) * max_pages > kMaxEntries ||
+      static_cast<long long>(B) * (max_pages + 1LL) > kMaxEntries)
     return MHA_ERR_UNSUPPORTED;
   if (B_old == 0 && B == 0 && num_pages == 0 && counts == nullptr) return MHA_OK;
   const size_t nw = mha_paged_reserve_workspace_size(B, num_pages);
@@ -95,9 +98,10 @@ extern "C" int mha_paged_reserve(const int32_t *block_table, const int32_t *kv_l
   a.counts = counts;
   a.lowest = static_cast<int32_t *>(workspace);
   a.given = a.lowest + num_pages;
-  a.first = a.given + num_pages;
-  a.copies = a.first + B;
-  a.totals = a.copies + B;
+  a.last = a.given + num_pages;
+  a.need = a.last + B;
+  a.free = reinterpret_cast<uint32_t *>(a.need + B);
+  a.totals = reinterpret_cast<int32_t *>(a.free) + (num_pages + 31LL) / 32;
   a.B_old = B_old;
   a.B = B;
   a.num_pages = num_pages;

@@ -235,7 +235,7 @@ cudaError_t compact(const CompactArgs &a, bool in_place, int num_sms, cudaStream
     const int apart = static_cast<int>(
         std::max(1LL, std::min<long long>(a.layers, 8LL * num_sms / std::max(ctas, 1LL))));
     return launch_behind(compact_short_kernel<kCols>, dim3(static_cast<unsigned>(ctas), apart),
-                         kShortWarps * 32, 1, stream, a);
+                         kShortWarps * 32, 0, 1, stream, a);
   }
   const long long all = units * 2 * std::max(a.layers, 1);
   constexpr int kRound = kLongThreads / kCols * 8;
@@ -243,7 +243,7 @@ cudaError_t compact(const CompactArgs &a, bool in_place, int num_sms, cudaStream
   const int stretches =
       in_place ? 1 : static_cast<int>(std::max(1LL, std::min<long long>(rounds, 4LL * num_sms / all)));
   return launch_behind(compact_long_kernel<kCols>, dim3(static_cast<unsigned>(all * stretches)),
-                       kLongThreads, 1, stream, a, stretches);
+                       kLongThreads, 0, 1, stream, a, stretches);
 }
 
 }  // namespace
@@ -261,7 +261,7 @@ cudaError_t launch_page_copy(const PageCopyArgs &a, int num_sms, cudaStream_t st
   const long long pieces = (a.page_bytes + kPiece - 1) / kPiece;
   const long long units = std::min<long long>(a.n, kPairs) * 2 * a.layers * pieces;
   const int grid = static_cast<int>(std::min<long long>(units, 8LL * num_sms));
-  return launch_behind(page_copy_kernel, dim3(std::max(grid, 1)), kCopyThreads, 1, stream, a);
+  return launch_behind(page_copy_kernel, dim3(std::max(grid, 1)), kCopyThreads, 0, 1, stream, a);
 }
 
 }  // namespace mha

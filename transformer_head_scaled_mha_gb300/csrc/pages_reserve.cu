@@ -6,12 +6,14 @@
 // part-filled last page will be written, so it has to be the row's own:
 //
 //   refs'[p] = refs[p] - (old rows' references to p) + (new rows' whole pages that are p)
-//   row i keeps its part-filled page p where refs'[p] = 0 and i is the lowest row that
-//   keeps p so; then refs'[p] = 1.  Any other such row gets a copy: moves[i] = (p, page).
-//   Pages with refs' = 0 are free.  Rows take, in their order, the lowest free ones:
-//   the copy first, then those of the positions they grow by; these get refs' = 1.
+//   row i keeps its part-filled page p where refs'[p] <= 0 and i is the lowest row that
+//   keeps p so; then refs'[p] grows by one.  Any other such row gets a copy: moves[i] =
+//   (p, page).  Pages with refs' <= 0 are free.  Rows take, in their order, the lowest free
+//   ones: the copy first, then those of the positions they grow by; these get refs' = 1.
 //
-// All of it is integers, and sums that atomics form do not depend on their order.
+// All of it is integers, and sums and minima that atomics form do not depend on their
+// order.  A row that is its own parent keeps its whole pages without a word, so that a step
+// of growing sequences counts almost nothing.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,54 +28,52 @@ namespace {
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kChunk = 256;  // entries of a row that a warp takes at a time
 
-// All threads of the cluster; what they wrote before it is seen behind it.
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-
-// refs_out = refs, and the words that the rows' minima start from.
-__device__ void begin(const ReserveArgs &a, int thread, int threads) {
-  if (a.refs_out != a.refs)
-    for (int p = thread; p < a.num_pages; p += threads) a.refs_out[p] = a.refs[p];
-  for (int i = thread; i < a.B; i += threads) {
-    const ReserveRow r = reserve_row(a, i);
-    if (r.last >= 0) a.lowest[r.last] = 0x7fffffff;
-  }
-}
-
 __device__ __forceinline__ int row_chunks(const ReserveArgs &a) {
   return max(1, (a.max_pages + kChunk - 1) / kChunk);
 }
 
-// References given up and taken.  A row that is its own parent keeps its whole pages
-// without a word: a step of growing sequences touches none of them.
-__device__ void count(const ReserveArgs &a, int warp, int warps) {
-  const int lane = threadIdx.x & 31, chunks = row_chunks(a);
-  const long long tasks = static_cast<long long>(max(a.B_old, a.B)) * chunks;
-  for (long long t = warp; t < tasks; t += warps) {
-    const int row = static_cast<int>(t / chunks), from = static_cast<int>(t % chunks) * kChunk;
-    int kept = 0;  // whole pages of this row that it keeps itself
-    if (row < a.B) {
-      const ReserveRow r = reserve_row(a, row);
-      if (r.parent == row) {
-        kept = r.full;
-      } else if (r.parent >= 0) {
-        for (int x = from + lane; x < min(r.full, from + kChunk); x += 32) {
-          const int p = reserve_page(a, r.parent, x);
-          if (p >= 0) atomicAdd(&a.refs_out[p], 1);
-        }
-      }
-      if (from == 0 && lane == 0 && r.last >= 0) atomicMin(&a.lowest[r.last], row);
+// An entry that names no page is -1.
+__device__ __forceinline__ int named(const ReserveArgs &a, int id) {
+  return static_cast<unsigned>(id) < static_cast<unsigned>(a.num_pages) ? id : -1;
+}
+
+// References given up and taken in entries [from, from + kChunk) of old and new row `row`,
+// added to `refs`; by a warp.  A page that the row had at that place and keeps there (its
+// own, or one it shared with its parent) is given up and taken: no word.  `had`: pages of
+// the old row.
+__device__ __forceinline__ void count_chunk(const ReserveArgs &a, int row, const ReserveRow &r, int had,
+                                            int from, int *refs) {
+  const int lane = threadIdx.x & 31;
+  const bool same = r.parent == row;  // whole pages that the row keeps itself: none to look at
+  const int32_t *mine = a.table + static_cast<size_t>(row) * a.max_pages;
+  const int32_t *parents = a.table + static_cast<size_t>(max(r.parent, 0)) * a.max_pages;
+  constexpr int kDeep = 4;
+  for (int x0 = from + lane; x0 < min(max(had, r.full), from + kChunk); x0 += 32 * kDeep) {
+    int old[kDeep], now[kDeep];
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      const int x = x0 + 32 * k;
+      const bool in = x < from + kChunk;
+      old[k] = now[k] = -1;
+      if (in && x < had && !(same && x < r.full)) old[k] = __ldcg(mine + x);
+      if (in && x < r.full && !same) now[k] = __ldcg(parents + x);
     }
-    if (row < a.B_old) {
-      const int had = reserve_pages(a, reserve_clamp(a, a.lens[row]));
-      for (int x = max(from, kept) + lane; x < min(had, from + kChunk); x += 32) {
-        const int p = reserve_page(a, row, x);
-        if (p >= 0) atomicSub(&a.refs_out[p], 1);
-      }
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      if (old[k] == now[k]) continue;
+      const int gone = named(a, old[k]), taken = named(a, now[k]);
+      if (gone >= 0) atomicSub(&refs[gone], 1);
+      if (taken >= 0) atomicAdd(&refs[taken], 1);
     }
   }
+}
+
+// What row i needs: pages, and whether its part-filled page, with its references and the
+// lowest row that keeps it, stays or is copied.
+__device__ __forceinline__ int need_of(const ReserveRow &r, int i, int lowest, int refs) {
+  int bits = 0;
+  if (r.last >= 0) bits = lowest == i && refs <= 0 ? kReserveStays : kReserveCopied;
+  return (r.want - r.had + ((bits & kReserveCopied) != 0)) << kReserveShift | bits;
 }
 
 // Exclusive sum of a number per thread over the block; `total`: of all.
@@ -99,165 +99,374 @@ __device__ int block_scan(int x, int *scratch, int &total) {
   return inc - x + (warp > 0 ? before : 0);
 }
 
-// Which part-filled pages stay, how many pages each row needs, and which free ones it gets.
-// One cluster of `ctas`.
-__device__ void assign(const ReserveArgs &a, int cta, int ctas) {
-  __shared__ int scratch[kWarps];
+// Gives out the `total` lowest free pages, whose bits `free` tells by words, to `given`; refs[p] =
+// 1.  One block: runs of 32 words are counted by the warps in turn, summed, and those that
+// hold pages to give looked at again.  Returns how many there were to give; `all`: how many
+// were free.
+template <typename Page, typename Free>
+__device__ int give_pages(const ReserveArgs &a, const Free &free, int total, int *refs,
+                          Page *given, int *scratch, int *runs, int &all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // rows: a stretch per CTA, and of it one per thread
-  const int per_cta = (a.B + ctas - 1) / ctas, per = (per_cta + kThreads - 1) / kThreads;
-  const int stop = min(a.B, (cta + 1) * per_cta);
-  const int r0 = min(stop, cta * per_cta + static_cast<int>(threadIdx.x) * per);
-  const int r1 = min(stop, r0 + per);
-  int mine = 0;
-  for (int i = r0; i < r1; ++i) {
-    const ReserveRow r = reserve_row(a, i);
-    bool copied = false;
-    if (r.last >= 0) {
-      copied = true;
-      // (only the lowest row looks at the page's count, and only it changes it here)
-      if (__ldcg(&a.lowest[r.last]) == i) {
-        const int refs = __ldcg(&a.refs_out[r.last]);
-        if (refs <= 0) {
-          __stcg(&a.refs_out[r.last], refs + 1);
-          copied = false;
-        }
+  const int words = (a.num_pages + 31) / 32;
+  all = 0;  // so far
+  for (int base = 0; base < words; base += 32 * kThreads) {
+    __syncthreads();
+    constexpr int kDeep = 8;
+    for (int s = warp; s < kThreads && base + s * 32 < words; s += kDeep * kWarps) {
+      uint32_t bits[kDeep];
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int w = base + (s + k * kWarps) * 32 + lane;
+        bits[k] = s + k * kWarps < kThreads && w < words ? free(w) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int n = __reduce_add_sync(0xffffffffu, __popc(bits[k]));
+        if (lane == 0 && s + k * kWarps < kThreads) runs[s + k * kWarps] = n;
       }
     }
-    a.copies[i] = copied;
-    a.first[i] = mine;
-    mine += r.want - r.had + copied;
-  }
-  int need, total;
-  const int before = block_scan(mine, scratch, need);
-  if (threadIdx.x == 0) __stcg(&a.totals[kTotalNeed + cta], need);
-  cluster_barrier();
-  int at = before;
-  total = 0;
-  for (int c = 0; c < ctas; ++c) {
-    const int n = __ldcg(&a.totals[kTotalNeed + c]);
-    if (c < cta) at += n;
-    total += n;
-  }
-  for (int i = r0; i < r1; ++i) a.first[i] += at;
-  // free pages: a stretch per warp, whole words of 32
-  const int warps = ctas * kWarps;
-  const int words = (a.num_pages + 31) / 32, each = (words + warps - 1) / warps;
-  const int w0 = min(words, (cta * kWarps + warp) * each), w1 = min(words, w0 + each);
-  int found = 0;
-#pragma unroll 4
-  for (int w = w0; w < w1; ++w) {
-    const int p = w * 32 + lane;
-    const bool free = p < a.num_pages && __ldcg(&a.refs_out[p]) <= 0;
-    found += __popc(__ballot_sync(0xffffffffu, free));
-  }
-  int of_cta;
-  int rank = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? found : 0, scratch, of_cta), 0);
-  if (threadIdx.x == 0) __stcg(&a.totals[kTotalFree + cta], of_cta);
-  cluster_barrier();
-  int all = 0;
-  for (int c = 0; c < ctas; ++c) {
-    const int n = __ldcg(&a.totals[kTotalFree + c]);
-    if (c < cta) rank += n;
-    all += n;
-  }
-  for (int w = w0; w < w1 && rank < total; ++w) {
-    const int p = w * 32 + lane;
-    const bool free = p < a.num_pages && __ldcg(&a.refs_out[p]) <= 0;
-    const unsigned ballot = __ballot_sync(0xffffffffu, free);
-    const int to = rank + __popc(ballot & ((1u << lane) - 1));
-    if (free && to < total) {
-      a.given[to] = p;
-      a.refs_out[p] = 1;
+    __syncthreads();
+    int sum;
+    const bool is = base + static_cast<int>(threadIdx.x) * 32 < words;
+    const int before = all + block_scan(is ? runs[threadIdx.x] : 0, scratch, sum);
+    runs[threadIdx.x] = before;
+    all += sum;
+    __syncthreads();
+    for (int s = warp; s < kThreads && base + s * 32 < words && runs[s] < total; s += kWarps) {
+      const int w = base + s * 32 + lane;
+      uint32_t bits = w < words ? free(w) : 0u;
+      int inc = __popc(bits);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      for (int to = runs[s] + inc - __popc(bits); bits != 0 && to < total; bits &= bits - 1, ++to) {
+        const int p = w * 32 + __ffs(bits) - 1;
+        given[to] = static_cast<Page>(p);
+        refs[p] = 1;
+      }
     }
-    rank += __popc(ballot);
   }
-  if (cta == 0 && threadIdx.x == 0) {
-    const int given = min(total, all);
-    a.totals[kTotalGiven] = given;
-    if (a.counts != nullptr) {
-      a.counts[0] = given;
-      a.counts[1] = all - given;
-    }
+  return min(total, all);
+}
+__device__ __forceinline__ void write_counts(const ReserveArgs &a, int given, int all) {
+  if (a.counts == nullptr) return;
+  a.counts[0] = given;
+  a.counts[1] = all - given;
+}
+
+// Where a new row's entries come from: those before `end` from its parent's row, at `from`;
+// entry x from there to `want` is the (shift + x)-th of the pages given out.
+struct Source {
+  int from, end, want, shift;
+};
+__device__ __forceinline__ Source source_of(const ReserveArgs &a, const ReserveRow &r, int word) {
+  Source s;
+  s.from = max(r.parent, 0) * a.max_pages;
+  s.end = word & kReserveCopied ? r.full : r.had;
+  s.want = r.want;
+  s.shift = (word >> kReserveShift) - s.end;
+  return s;
+}
+// Entry x, a number of the parent's row as it is: loads that nothing looks at yet go out
+// one behind another.
+template <typename Page>
+__device__ __forceinline__ int entry(const ReserveArgs &a, const Source &s, int x, const Page *given,
+                                     int count) {
+  int id = -1;
+  if (x < s.end) id = __ldcg(a.table + s.from + x);
+  if (x >= s.end && x < s.want && s.shift + x < count) id = given[s.shift + x];
+  return id;
+}
+
+// A new row's other results; by one thread.
+template <typename Page>
+__device__ __forceinline__ void write_row(const ReserveArgs &a, int i, const ReserveRow &r, int word,
+                                          const Page *given, int count) {
+  const int first = word >> kReserveShift;
+  const bool copied = (word & kReserveCopied) != 0;
+  const int to = copied && first < count ? static_cast<int>(given[first]) : -1;
+  a.moves[2 * static_cast<size_t>(i)] = to >= 0 ? r.last : -1;
+  a.moves[2 * static_cast<size_t>(i) + 1] = to;
+  a.lens_out[i] = reserve_length(a, r, copied, max(count - first, 0));
+}
+
+// ---- one cluster -----------------------------------------------------------------
+// For pools and tables that one SM goes through in a moment: the references, the rows and
+// the pages given out live in shared memory, and barriers of a block stand between the
+// steps.  Every CTA of the cluster does all of it alike, in its own shared memory, and
+// writes a share of the results: copying the tables is most of the work, and that much
+// faster than telling the others.
+constexpr int kSmallRows = 1024, kSmallPages = 28672;
+constexpr int kSmallEntries = 65536;  // of the tables
+constexpr int kSmallCtas = 8;
+constexpr int kFew = 4;  // references that a thread counts alone
+struct SmallRow {
+  int parent, keep, next, last;
+};
+struct SmallShared {
+  SmallRow rows[kSmallRows];
+  Source sources[kSmallRows];
+  int had[kSmallRows], listed[kSmallRows], count;
+  int runs[kThreads];
+  uint32_t free[kSmallPages / 32];
+  int scratch[kWarps];
+  uint16_t given[kSmallPages];  // before: of a part-filled page, the lowest row that keeps it
+  int refs[kSmallPages];        // (only num_pages of them are there)
+};
+static_assert(kSmallRows < 0xffff && kSmallPages <= 0x10000 && sizeof(SmallShared) <= 232448, "sizes");
+
+// at[i] = min(at[i], x), others' at[i ^ 1] untouched
+__device__ __forceinline__ void atomic_min16(uint16_t *at, int i, uint32_t x) {
+  uint32_t *word = reinterpret_cast<uint32_t *>(at + (i & ~1));
+  const int shift = (i & 1) * 16;
+  uint32_t old = *reinterpret_cast<volatile uint32_t *>(word);
+  while (((old >> shift) & 0xffffu) > x) {
+    const uint32_t seen = old;
+    old = atomicCAS(word, seen, (seen & ~(0xffffu << shift)) | x << shift);
+    if (old == seen) break;
   }
 }
 
-__device__ void write_tables(const ReserveArgs &a, int warp, int warps) {
-  const int lane = threadIdx.x & 31, chunks = row_chunks(a);
+__device__ __forceinline__ ReserveRow unpack(const ReserveArgs &a, const SmallRow &s) {
+  ReserveRow r;
+  r.parent = s.parent;
+  r.keep = s.keep;
+  r.next = s.next;
+  r.last = s.last;
+  r.full = r.keep >> a.page_shift;
+  r.had = reserve_pages(a, r.keep);
+  r.want = reserve_pages(a, r.next);
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads) reserve_small_kernel(const ReserveArgs a) {
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  extern __shared__ __align__(16) uint8_t smem[];
+  SmallShared &sh = *reinterpret_cast<SmallShared *>(smem);
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, chunks = row_chunks(a);
+  const int mine = threadIdx.x;  // this thread's row
+#pragma unroll 8
+  for (int p = threadIdx.x; p < a.num_pages; p += kThreads) sh.refs[p] = a.refs[p];
+  ReserveRow r{};
+  r.parent = r.last = -1;
+  // pages of the old row of that number
+  const int had = mine < a.B_old ? reserve_pages(a, reserve_clamp(a, a.lens[mine])) : 0;
+  if (threadIdx.x == 0) sh.count = 0;
+  sh.had[mine] = had;
+  if (mine < a.B) r = reserve_row(a, mine);
+  sh.rows[mine] = SmallRow{r.parent, r.keep, r.next, r.last};
+  if (mine < a.B) {
+    if (r.last >= 0) sh.given[r.last] = 0xffff;
+  }
+  __syncthreads();
+  // every CTA has read refs, which refs_out may be (waited for below)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (r.last >= 0) atomic_min16(sh.given, r.last, mine);
+  // rows with few references to count, one to a thread; the others by warps
+  const int kept = r.parent == mine ? r.full : 0;  // whole pages that the row keeps itself
+  if (max(had - kept, 0) + (r.parent != mine ? r.full : 0) <= kFew) {
+    for (int x = kept; x < had; ++x) {
+      const int p = reserve_page(a, mine, x);
+      if (p >= 0) atomicSub(&sh.refs[p], 1);
+    }
+    for (int x = 0; r.parent != mine && x < r.full; ++x) {
+      const int p = reserve_page(a, r.parent, x);
+      if (p >= 0) atomicAdd(&sh.refs[p], 1);
+    }
+  } else {
+    sh.listed[atomicAdd(&sh.count, 1)] = mine;  // (in any order: sums)
+  }
+  __syncthreads();
+  for (int t = warp; t < sh.count * chunks; t += kWarps) {
+    const int row = sh.listed[t / chunks];
+    count_chunk(a, row, unpack(a, sh.rows[row]), sh.had[row], t % chunks * kChunk, sh.refs);
+  }
+  __syncthreads();
+  int word = 0, total, given;
+  if (mine < a.B)
+    word = r.last >= 0 ? need_of(r, mine, sh.given[r.last], sh.refs[r.last]) : need_of(r, mine, -1, 0);
+  const int before = block_scan(word >> kReserveShift, sh.scratch, total);
+  word = before << kReserveShift | (word & ((1 << kReserveShift) - 1));
+  sh.sources[mine] = source_of(a, r, word);
+  // (every row has looked at its page's references: the scan's barriers)
+  if (word & kReserveStays) ++sh.refs[r.last];
+  __syncthreads();
+  for (int w = warp; w < (a.num_pages + 31) / 32; w += kWarps) {
+    const int p = w * 32 + lane;
+    const unsigned free = __ballot_sync(0xffffffffu, p < a.num_pages && sh.refs[p] <= 0);
+    if (lane == 0) sh.free[w] = free;
+  }
+  __syncthreads();
+  int all;
+  given = give_pages(a, [&](int w) { return sh.free[w]; }, total, sh.refs, sh.given, sh.scratch, sh.runs, all);
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  __syncthreads();
+  for (int p = cta * kThreads + threadIdx.x; p < a.num_pages; p += ctas * kThreads)
+    a.refs_out[p] = sh.refs[p];
+  if (mine < a.B && mine % ctas == cta) write_row(a, mine, r, word, sh.given, given);
+  if (cta == 0 && threadIdx.x == 0) write_counts(a, given, all);
+  // the entries of all rows behind one another, some loads in flight to a thread
+  constexpr int kDeep = 8;
+  const int width = max(a.max_pages, 1), entries = a.B * a.max_pages, step = ctas * kThreads;
+  const int rows_on = step / width, cols_on = step % width;
+  const int first = cta * kThreads + threadIdx.x;
+  int row = first / width, x = first % width;
+  for (int e = first; e < entries; e += kDeep * step) {
+    int id[kDeep];
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      id[k] = e + k * step < entries ? entry(a, sh.sources[row], x, sh.given, given) : -1;
+      row += rows_on;
+      x += cols_on;
+      if (x >= width) {
+        x -= width;
+        ++row;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k)
+      if (e + k * step < entries) a.table_out[e + k * step] = named(a, id[k]);
+  }
+}
+
+// ---- larger ones: the whole GPU, a launch to a step -----------------------------------
+// (__ldcg: numbers that other SMs have just written)
+__device__ void begin_step(const ReserveArgs &a, int block, int blocks) {
+  const int thread = block * kThreads + threadIdx.x, threads = blocks * kThreads;
+  if (a.refs_out != a.refs) {
+#pragma unroll 4
+    for (int p = thread; p < a.num_pages; p += threads) a.refs_out[p] = __ldg(a.refs + p);
+  }
+  if (thread == 0) a.totals[kTotalDone] = 0;
+  for (int i = thread; i < a.B; i += threads) {
+    const ReserveRow r = reserve_row(a, i);
+    a.last[i] = r.last;
+    if (r.last >= 0) a.lowest[r.last] = 0x7fffffff;
+  }
+}
+
+__device__ void count_step(const ReserveArgs &a, int block, int blocks) {
+  const int chunks = row_chunks(a), warps = blocks * kWarps;
+  const long long tasks = static_cast<long long>(max(a.B_old, a.B)) * chunks;
+  for (long long t = block * kWarps + (threadIdx.x >> 5); t < tasks; t += warps) {
+    const int row = static_cast<int>(t / chunks), from = static_cast<int>(t % chunks) * kChunk;
+    ReserveRow r{};
+    r.parent = r.last = -1;
+    if (row < a.B) r = reserve_row(a, row);
+    const int had = row < a.B_old ? reserve_pages(a, reserve_clamp(a, a.lens[row])) : 0;
+    count_chunk(a, row, r, had, from, a.refs_out);
+    if (from == 0 && (threadIdx.x & 31) == 0 && r.last >= 0) atomicMin(&a.lowest[r.last], row);
+  }
+}
+
+// Pages that stay, the rows' first numbers, and the pages given out: by one block.
+__device__ void give_step(const ReserveArgs &a) {
+  __shared__ int scratch[kWarps], runs[kThreads];
+  int total = 0;
+  for (int base = 0; base < a.B; base += kThreads) {
+    const int i = base + threadIdx.x;
+    const int word = i < a.B ? __ldcg(&a.need[i]) : 0;
+    const int last = i < a.B ? __ldcg(&a.last[i]) : 0;
+    if (word & kReserveStays) {
+      atomicAdd(&a.refs_out[last], 1);  // (one row to a page)
+      atomicAnd(&a.free[last >> 5], ~(1u << (last & 31)));
+    }
+    int sum;
+    const int before = total + block_scan(word >> kReserveShift, scratch, sum);
+    if (i < a.B) a.need[i] = before << kReserveShift | (word & ((1 << kReserveShift) - 1));
+    total += sum;
+  }
+  __syncthreads();
+  int all;
+  const int given = give_pages(a, [&](int w) { return __ldcg(&a.free[w]); }, total, a.refs_out, a.given, scratch, runs, all);
+  if (threadIdx.x == 0) {
+    a.totals[kTotalGiven] = given;
+    write_counts(a, given, all);
+  }
+}
+
+// What rows need, and which pages are free but for those that stay; the block that is done
+// last gives them out.
+__device__ void need_step(const ReserveArgs &a, int block, int blocks) {
+  const int thread = block * kThreads + threadIdx.x, threads = blocks * kThreads;
+  for (int i = thread; i < a.B; i += threads) {
+    const ReserveRow r = reserve_row(a, i);
+    a.need[i] = r.last >= 0 ? need_of(r, i, __ldcg(&a.lowest[r.last]), __ldcg(&a.refs_out[r.last]))
+                            : need_of(r, i, -1, 0);
+  }
+  const int words = (a.num_pages + 31) / 32, lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int w = thread >> 5; w < words; w += threads >> 5) {
+    const int p = w * 32 + lane;
+    const unsigned free = __ballot_sync(0xffffffffu, p < a.num_pages && __ldcg(&a.refs_out[p]) <= 0);
+    if (lane == 0) a.free[w] = free;
+  }
+  __shared__ bool last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(&a.totals[kTotalDone], 1) == blocks - 1;
+  }
+  __syncthreads();
+  if (last) {
+    __threadfence();
+    give_step(a);
+  }
+}
+
+__device__ void tables_step(const ReserveArgs &a, int block, int blocks) {
+  const int chunks = row_chunks(a), warps = blocks * kWarps, given = __ldcg(&a.totals[kTotalGiven]);
+  const int lane = threadIdx.x & 31;
   const long long tasks = static_cast<long long>(a.B) * chunks;
-  const int given = __ldcg(&a.totals[kTotalGiven]);
-  for (long long t = warp; t < tasks; t += warps) {
+  for (long long t = block * kWarps + (threadIdx.x >> 5); t < tasks; t += warps) {
     const int i = static_cast<int>(t / chunks), from = static_cast<int>(t % chunks) * kChunk;
     const ReserveRow r = reserve_row(a, i);
-    const int first = __ldcg(&a.first[i]), copied = __ldcg(&a.copies[i]);
-    // the k-th of the row's new pages
-    auto page = [&](int k) { return first + k < given ? __ldcg(&a.given[first + k]) : -1; };
-    int32_t *out = a.table_out + static_cast<size_t>(i) * a.max_pages;
-#pragma unroll 4
-    for (int x = from + lane; x < min(a.max_pages, from + kChunk); x += 32) {
-      int id = -1;
-      if (x < r.had && !(copied && x == r.full)) id = reserve_page(a, r.parent, x);
-      else if (x < r.want) id = page(x < r.had ? 0 : x - r.had + copied);
-      out[x] = id;
-    }
-    if (from == 0 && lane == 0) {
-      const int to = copied ? page(0) : -1;
-      a.moves[2 * static_cast<size_t>(i)] = to >= 0 ? r.last : -1;
-      a.moves[2 * static_cast<size_t>(i) + 1] = to;
-      a.lens_out[i] = reserve_length(a, r, copied != 0, max(given - first, 0));
-    }
+    const int word = __ldcg(&a.need[i]);
+    const Source src = source_of(a, r, word);
+    int id[kChunk / 32];
+#pragma unroll
+    for (int k = 0; k < kChunk / 32; ++k) id[k] = entry(a, src, from + lane + 32 * k, a.given, given);
+    int32_t *out = a.table_out + static_cast<size_t>(i) * a.max_pages + from + lane;
+#pragma unroll
+    for (int k = 0; k < kChunk / 32; ++k)
+      if (from + lane + 32 * k < a.max_pages) out[32 * k] = named(a, id[k]);
+    if (from == 0 && lane == 0) write_row(a, i, r, word, a.given, given);
   }
 }
 
-// Everything, one cluster.
-__global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) {
+// The whole GPU, a launch to a step.
+template <void (*kStep)(const ReserveArgs &, int, int)>
+__global__ void __launch_bounds__(kThreads) reserve_step_kernel(const ReserveArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const int ctas = gridDim.x, cta = blockIdx.x;
-  const int thread = cta * kThreads + threadIdx.x, threads = ctas * kThreads;
-  begin(a, thread, threads);
-  cluster_barrier();
-  count(a, thread >> 5, threads >> 5);
-  cluster_barrier();
-  assign(a, cta, ctas);
-  cluster_barrier();
-  write_tables(a, thread >> 5, threads >> 5);
-}
-
-// The same in steps over the whole GPU.
-__global__ void __launch_bounds__(kThreads) reserve_begin_kernel(const ReserveArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  begin(a, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
-}
-__global__ void __launch_bounds__(kThreads) reserve_count_kernel(const ReserveArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  count(a, blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps);
-}
-__global__ void __launch_bounds__(kThreads) reserve_assign_kernel(const ReserveArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  assign(a, blockIdx.x, gridDim.x);
-}
-__global__ void __launch_bounds__(kThreads) reserve_tables_kernel(const ReserveArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  write_tables(a, blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps);
+  kStep(a, blockIdx.x, gridDim.x);
 }
 
 }  // namespace
 
 cudaError_t launch_reserve(const ReserveArgs &a, int num_sms, cudaStream_t stream) {
   const long long entries = static_cast<long long>(std::max(a.B_old, a.B)) * a.max_pages;
-  const int ctas = entries + a.num_pages <= 16384 ? 1 : kReserveMaxCtas;
-  if (entries <= 65536)
-    return launch_behind(reserve_kernel, dim3(ctas), kThreads, ctas, stream, a);
-  const dim3 grid(2 * num_sms);
-  cudaError_t e = launch_behind(reserve_begin_kernel, grid, kThreads, 1, stream, a);
-  if (e == cudaSuccess) e = launch_behind(reserve_count_kernel, grid, kThreads, 1, stream, a);
-  if (e == cudaSuccess) e = launch_behind(reserve_assign_kernel, dim3(ctas), kThreads, ctas, stream, a);
-  if (e == cudaSuccess) e = launch_behind(reserve_tables_kernel, grid, kThreads, 1, stream, a);
+  if (std::max(a.B_old, a.B) <= kSmallRows && a.num_pages <= kSmallPages && entries <= kSmallEntries) {
+    const int smem = static_cast<int>(sizeof(SmallShared) - sizeof(int) * kSmallPages) + 4 * a.num_pages;
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(reserve_small_kernel),
+                                        static_cast<int>(sizeof(SmallShared)));
+    if (e != cudaSuccess) return e;
+    // two entries to a thread
+    const int ctas = static_cast<int>(std::min<long long>(kSmallCtas, 1 + entries / (2 * kThreads)));
+    return launch_behind(reserve_small_kernel, dim3(ctas), kThreads, smem, ctas, stream, a);
+  }
+  const dim3 grid(num_sms);
+  cudaError_t e = launch_behind(reserve_step_kernel<begin_step>, grid, kThreads, 0, 1, stream, a);
+  if (e == cudaSuccess)
+    e = launch_behind(reserve_step_kernel<count_step>, grid, kThreads, 0, 1, stream, a);
+  if (e == cudaSuccess)
+    e = launch_behind(reserve_step_kernel<need_step>, grid, kThreads, 0, 1, stream, a);
+  if (e == cudaSuccess)
+    e = launch_behind(reserve_step_kernel<tables_step>, grid, kThreads, 0, 1, stream, a);
   return e;
 }
 
