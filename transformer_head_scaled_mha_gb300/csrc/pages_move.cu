@@ -111,11 +111,16 @@ __global__ void __launch_bounds__(kShortWarps * 32) compact_short_kernel(const C
 }
 
 // Longer lists: a CTA per sequence, head, layer and tensor (and, where nothing that is
-// written is read, stretch of the list), rounds as above.
-constexpr int kLongThreads = 256;
+// written is read, stretch of the list), rounds as above.  A round's rows are found, one to
+// a thread, while those of the round before are on their way.
+constexpr int kLongThreads = 256, kLongCtas = 4;  // CTAs per SM
 template <int kCols>
-__global__ void __launch_bounds__(kLongThreads) compact_long_kernel(const CompactArgs a, int stretches) {
+__global__ void __launch_bounds__(kLongThreads, kLongCtas)
+    compact_long_kernel(const CompactArgs a, int stretches) {
   constexpr int kRows = kLongThreads / kCols, kDeep = 8, kRound = kRows * kDeep;
+  static_assert(kRound <= kLongThreads, "a row to a thread");
+  // of this round, the next one, and the one before, whose rows may still be on their way out
+  __shared__ Move moves[3][kRound];
   __shared__ int stop;
   griddep_launch_dependents();
   griddep_wait();
@@ -140,23 +145,36 @@ __global__ void __launch_bounds__(kLongThreads) compact_long_kernel(const Compac
   if (a.Hkv == 0 || a.layers == 0) return;
   uint8_t *cache = (item & 1 ? a.v : a.k) + (item >> 1) * a.layer_bytes +
                    (threadIdx.x % kCols) * 16;
-  const int mine = threadIdx.x / kCols;
-  for (int r0 = stretch * kRound; r0 < n; r0 += stretches * kRound) {
-    Move m[kDeep];
+  const int mine = threadIdx.x / kCols, step = stretches * kRound;
+  const int my_row = static_cast<int>(threadIdx.x);
+  // entry of the list that this thread looks up, of the round at r0 (-1: none)
+  auto entry = [&](int r0) {
+    return my_row < kRound && r0 + my_row < n ? l.keep[r0 + my_row] : -1;
+  };
+  auto find = [&](Move *to, int r0, int k) {
+    if (my_row >= kRound) return;
+    to[my_row].src = -1;
+    if (k >= 0) to[my_row] = move_of(a, l, b, head, r0 + my_row, k);
+  };
+  int r0 = stretch * kRound, k = entry(r0), buffer = 0;
+  find(moves[0], r0, k);
+  k = entry(r0 + step);
+  __syncthreads();
+  for (; r0 < n; r0 += step) {
+    const int behind = buffer == 2 ? 0 : buffer + 1;
     uint4 x[kDeep];
-#pragma unroll
-    for (int u = 0; u < kDeep; ++u) {
-      const int i = r0 + u * kRows + mine;
-      m[u].src = -1;
-      if (i < n) m[u] = move_of(a, l, b, head, i, l.keep[i]);
-    }
+    const Move *m = moves[buffer] + mine;
 #pragma unroll
     for (int u = 0; u < kDeep; ++u)
-      if (m[u].src >= 0) x[u] = ld16(cache + m[u].src * (kCols * 16));
+      if (m[u * kRows].src >= 0) x[u] = ld16(cache + m[u * kRows].src * (kCols * 16));
+    const int next = entry(r0 + 2 * step);
+    find(moves[behind], r0 + step, k);
+    k = next;
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kDeep; ++u)
-      if (m[u].src >= 0) st_global_v4(cache + m[u].dst * (kCols * 16), x[u]);
+      if (m[u * kRows].src >= 0) st_global_v4(cache + m[u * kRows].dst * (kCols * 16), x[u]);
+    buffer = behind;
   }
 }
 
@@ -240,8 +258,10 @@ cudaError_t compact(const CompactArgs &a, bool in_place, int num_sms, cudaStream
   const long long all = units * 2 * std::max(a.layers, 1);
   constexpr int kRound = kLongThreads / kCols * 8;
   const int rounds = (a.max_keep + kRound - 1) / kRound;
-  const int stretches =
-      in_place ? 1 : static_cast<int>(std::max(1LL, std::min<long long>(rounds, 4LL * num_sms / all)));
+  // enough CTAs for several turns of all SMs, so that the last one leaves little idle
+  const int stretches = in_place ? 1
+                                 : static_cast<int>(std::max(
+                                       1LL, std::min<long long>(rounds, 8LL * kLongCtas * num_sms / all)));
   return launch_behind(compact_long_kernel<kCols>, dim3(static_cast<unsigned>(all * stretches)),
                        kLongThreads, 0, 1, stream, a, stretches);
 }
