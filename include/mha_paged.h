@@ -237,8 +237,9 @@ int mha_paged_fwd(const void *q, const void *k_cache, const void *v_cache, void 
  *            what a row sees need not be a path, and a row that sees nothing (and
  *            has nothing cached before the new tokens) is written as +0.0.
  * tree_words >= 1
- * The workspace is that of mha_paged_fwd, and mha_paged_path tells the kernel;
- * everything else as there (a new token's value must be finite where any other
+ * The workspace is that of mha_paged_fwd.  The kernel is the one that mha_paged_path
+ * tells, but where there is little work few rows are taken at a time, on the few-query
+ * kernel (BF16); everything else as there (a new token's value must be finite where any other
  * token of its sequence is in the call).
  */
 int mha_paged_tree_fwd(const void *q, const void *k_cache, const void *v_cache, void *out,

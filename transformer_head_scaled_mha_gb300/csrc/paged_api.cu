@@ -90,9 +90,10 @@ int paged_path(int B, int T, int H, int H_kv, int d, int max_q, int dtype) {
   return static_cast<long long>(H / H_kv) * max_q <= kFewRows ? kFew : kMany;
 }
 
-Units units_of(int path, int group, int max_q) {
+// `rows`: of a tile; 0: as many as the kernel takes.
+Units units_of(int path, int group, int max_q, int rows = 0) {
   Units u;
-  const int rows = path == kMany ? 128 : 16;  // of a tile
+  if (rows == 0) rows = path == kMany ? 128 : 16;
   u.hpu = std::min(group, rows);
   u.hblocks = (group + u.hpu - 1) / u.hpu;
   u.tb = path == kMany ? 2 * (rows / u.hpu) : std::min(rows / u.hpu, max_q);
@@ -100,6 +101,43 @@ Units units_of(int path, int group, int max_q) {
   u.ctas = path == kMany ? kPagedManyMaxCtas : kPagedMaxCtas;
   u.split = path == kMany ? kSplitMany : (path == kFew ? kSplitFew : kSplitSimt);
   return u;
+}
+
+// Trees of drafted tokens have many rows to a sequence, and where the sequences are few or
+// short most SMs would have nothing to do: units of fewer rows read the keys again, from
+// L2, but a row's softmax no longer waits for 15 others.  `path` and the answer: the rows of
+// a unit, 0 where the usual units are as good; `path` becomes the few-query kernel where
+// that is faster than the many-query one.
+//
+// Measured, usual units / these, by units x tiles of the longest sequence that the table
+// has room for (T4, T8: with 4 and 8 rows).  bf16, d 64, 16 tokens of 8 heads: T4 = 96 12.1
+// / 9.0 us, 384 14.9 / 12.9; T8 = 752 18.6 / 15.6; T4 = 1536 13.9 / 14.7; 8 tokens of 8
+// heads over 2 (many-query): T4 = 752 17.5 / 13.6, 768 11.6 / 10.4, 3072 17.0 / 21.4.  d
+// 128, 8 tokens of 32 heads over 8 (many-query): T4 = 192 12.4 / 9.5; T8 = 384 18.9 / 14.5,
+// 1536 20.2 / 23.4; 16 of 16 heads: T8 = 384 16.7 / 14.5, 1504 20.4 / 21.8.  fp32, d 64, 13
+// tokens of 8 heads over 2: T4 = 1248 18.7 / 14.7; 16 tokens of 8 heads: 1504 25.0 / 23.6,
+// 1536 23.9 / 23.9, 3072 48 / 66; d 128, 8 tokens of 32 over 8: 192 21.8 / 14.9, 384 23.4 /
+// 30.1.  fp32 with 5 to 8 rows takes the time of 16: 4 are as fast at any size (8 tokens of
+// 8 heads, 16 sequences of 6000: 129 / 120, of 300: 21.7 / 18.3).
+int tree_rows(int *path, int B, int T, int H_kv, int group, int max_q, int d, int dtype,
+              long long keys, int sms) {
+  const long long tiles = (keys + kPagedTile - 1) / kPagedTile;
+  const bool f32 = dtype == MHA_DTYPE_F32;
+  const long long ctas = (d == 64 ? 2LL : 1LL) * sms;
+  const Units usual = units_of(*path, group, max_q);
+  for (const int rows : {4, 8}) {
+    const Units u = units_of(kFew, group, max_q, rows);
+    if (u.rows >= usual.rows || (f32 && rows == 8)) continue;
+    const long long blocks =
+        std::min<long long>(T, static_cast<long long>(B) * ((max_q - 1LL) / u.tb + 1));
+    const long long work = blocks * H_kv * u.hblocks * tiles;
+    const long long most = d == 64 ? (f32 ? 5 : 4) : (rows == 4 ? 2 : 3);
+    if (work <= most * ctas || (f32 && usual.rows <= 8)) {
+      if (*path == kMany) *path = kFew;
+      return rows;
+    }
+  }
+  return 0;
 }
 
 size_t meta_bytes(const Units &u) {
@@ -368,7 +406,7 @@ static int attend(const void *q, const void *k_cache, const void *v_cache, void 
     st = check_batch(q_starts, kv_lengths, block_table, B, T, num_pages, page_size, max_pages,
                      layout, &p.batch);
   if (st != MHA_OK) return st;
-  const int path = paged_path(B, T, H, H_kv, d, max_q, dtype);
+  int path = paged_path(B, T, H, H_kv, d, max_q, dtype);
   if (path < 0) return -path;
   if (mask_kind != MHA_MASK_NONE && mask_kind != MHA_MASK_CAUSAL_TAIL)
     return MHA_ERR_INVALID_ARGUMENT;
@@ -379,7 +417,7 @@ static int attend(const void *q, const void *k_cache, const void *v_cache, void 
   if ((static_cast<long long>(max_pages) << p.batch.page_shift) > (1LL << 31) - 1024)
     return MHA_ERR_UNSUPPORTED;
   if (path == kNone) return MHA_OK;
-  const Units u = units_of(path, H / H_kv, max_q);
+  Units u = units_of(path, H / H_kv, max_q);
   const size_t e = elem_size(dtype);
   const size_t nq = static_cast<size_t>(T) * H * d * e;
   const size_t nc = static_cast<size_t>(num_pages) * page_size * H_kv * d * e;
@@ -398,6 +436,17 @@ static int attend(const void *q, const void *k_cache, const void *v_cache, void 
     return MHA_ERR_INVALID_ARGUMENT;
   const int sms = current_sms();
   if (sms <= 0) return MHA_ERR_CUDA;
+  if (of_tree) {
+    int small_path = path;
+    const int rows =
+        tree_rows(&small_path, B, T, H_kv, H / H_kv, max_q, d, dtype,
+                  static_cast<long long>(max_pages) << p.batch.page_shift, sms);
+    const Units small = units_of(small_path, H / H_kv, max_q, rows);
+    if (rows > 0 && workspace_bytes_of(small, d) <= nw) {
+      path = small_path;
+      u = small;
+    }
+  }
   p.H = H;
   p.Hkv = H_kv;
   p.group = H / H_kv;
