@@ -410,15 +410,21 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const Rope
   ang.frequencies(a.inv_freq, place.freq, place.on, group);
   Stretch stretch(static_cast<long long>(a.tokens) * rounds, w, warps);
   int t, lo, hi;
+  int seq = -1, end = -1, len = 0;  // the last token's sequence, where it ends, its length
   while (stretch.next(rounds, t, lo, hi)) {
-    int pos = 0, seq = 0;
+    int pos = 0;
     bool live = true;
     if (kAppend) {
-      seq = seq_of_row(a.batch, t, lane);
+      if (t >= end) {
+        seq = seq_of_row(a.batch, t, lane);
+        if (seq >= 0) {
+          end = min(a.batch.q_starts[seq + 1], a.tokens);
+          len = max(a.batch.kv_lengths[seq], 0);
+        }
+      }
       live = seq >= 0;
       // tokens up to the sequence's end count back from its length
-      if (live)
-        pos = max(a.batch.kv_lengths[seq], 0) - (min(a.batch.q_starts[seq + 1], a.tokens) - t);
+      if (live) pos = len - (end - t);
       // (drafted trees: the angle's position is not the cell's)
       ang.at(a.positions != nullptr ? a.positions[t] : pos, col);
     } else {
