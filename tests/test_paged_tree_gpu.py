@@ -43,9 +43,10 @@ def run_tree(q, kc, vc, mask, b, *, dt, layout, scale, max_q, fill=3.0, **kw):
 
 
 def check_tree(seqs, H, Hkv, d, dt, page, layout, how="tree", seed=0, scale=None, max_q=None,
-               behind=0, before=0, change=None, words=None, spoil=None, mask_of=None):
+               behind=0, before=0, change=None, words=None, spoil=None, mask_of=None,
+               max_pages=None):
     rng = np.random.default_rng(seed)
-    b = batch(rng, seqs, page, behind=behind, before=before)
+    b = batch(rng, seqs, page, behind=behind, before=before, max_pages=max_pages)
     if change is not None:  # (before the caches, whose cells without a position hold NaN)
         change(b)
     kc, vc = cache_of(rng, b, Hkv, page, d, dt, layout)
@@ -91,9 +92,13 @@ CASES = [
                                           for i, c in enumerate(CASES)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("how", ["tree", "any"])
-def test_tree_attention(c, dt, how):
+@pytest.mark.parametrize("room", [None, 200000], ids=["small_tables", "large_tables"])
+def test_tree_attention(c, dt, how, room):
+    """Small tables have units of few rows, on the few-query kernel; with room for long
+    sequences the units are the usual ones."""
     seqs, H, Hkv, d, page, layout = c
-    check_tree(seqs, H, Hkv, d, dt, page, layout, how, seed=len(seqs) + H)
+    check_tree(seqs, H, Hkv, d, dt, page, layout, how, seed=len(seqs) + H,
+               max_pages=None if room is None else room // page)
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])

@@ -135,7 +135,7 @@ def _at(name, t, shape, dtype, dev):
     here: plain attribute reads, the device by its number."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d, not %s of shape "
                          "%s on %s" % (name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape),
                                        t.device))
@@ -176,13 +176,22 @@ def _call(name, dev, stream, args):
         handle = _current_stream(dev)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == dev:
+    if _only_device() or torch.cuda.current_device() == dev:
         st = getattr(lib, name)(*args, handle)
     else:
         with torch.cuda.device(dev):
             st = getattr(lib, name)(*args, handle)
     if st != MHA_OK:
         raise MhaError(st, name)
+
+
+def _only_device() -> bool:
+    """Whether the process has one CUDA device, which then is the current one (asking for
+    that takes a quarter of a microsecond)."""
+    one = _modules.get("one device")
+    if one is None:
+        one = _modules["one device"] = _torch().cuda.device_count() == 1
+    return one
 
 
 def _current_stream(dev: int) -> int:
@@ -442,8 +451,9 @@ def _attend(name, tree, q, k_cache, v_cache, out, q_starts, kv_lengths, block_ta
 
 def _counted(name, shape):
     """A shape whose counts the C entry points take (ctypes would keep their low 32 bits)."""
-    if any(n > _INT_MAX for n in shape):
-        raise ValueError("%s has more than 2^31 - 1 rows or columns" % name)
+    for n in shape:
+        if n > _INT_MAX:
+            raise ValueError("%s has more than 2^31 - 1 rows or columns" % name)
     return shape
 
 
@@ -471,7 +481,8 @@ def mha_paged_reserve(block_table, kv_lengths, new_lengths, refs, *, page_size: 
         raise ValueError("block_table must have 2 dimensions, new_lengths and refs 1")
     B_old, width = _counted("block_table", block_table.shape)
     (B,), (pages,) = _counted("new_lengths", new_lengths.shape), _counted("refs", refs.shape)
-    if any(t is None for t in (table_out, lengths_out, refs_out, moves, counts, workspace)):
+    if (table_out is None or lengths_out is None or refs_out is None or moves is None or
+            counts is None or workspace is None):
         with _on(stream, block_table.device):
             new = lambda *n: torch.empty(n, dtype=i32, device=block_table.device)  # noqa: E731
             table_out = new(B, width) if table_out is None else table_out
