@@ -40,6 +40,14 @@
 // way to the first tile is 8 us, a part's beginning and end 3, the merge 8.  Up to 32 rows
 // (drafts of grouped heads) lie in one warp of a warpgroup, and the others wait for its
 // exponentials: 16 x 8 tokens over 4000 keys, 32 heads over 8, d 128: 65 us, 0.60 of HBM.
+// Trees of drafted tokens (kTree: the row's mask words are looked at in a sequence's last
+// tiles only): 16 of 9-25 tokens behind 1000-4096 keys, 32 heads over 8, d 128: 49 us, 3.5
+// TB/s (6 us to the first tile, then 1.67 a tile, 2 to 3 to a part's output, merge 5); 64 of
+// 64 tokens behind 4096-8192: 327 us, 1.25 PFLOP/s, 0.76 of HBM (1.76 us a pair of tiles,
+// which HBM brings in 1.47); 256 of 8 tokens behind 128-1024, 3 to 9 tiles to a unit: 175
+// us, 0.54 of HBM, 4 us between one part's last tile and the next part's first.  Two
+// warpgroups to a tile, 64 columns each, were slower (327 -> 383 us): 104 registers do not
+// hold a thread's scores, and every more wait for TMEM is 250 cycles.
 //
 // Warp roles (384 threads): warps 0-3 and 4-7 softmax, warp 8 producer (walks the
 // parts and hands their descriptions to the others), warp 9 TMEM owner and product

@@ -3,7 +3,12 @@
 // copies of pages that forked sequences may no longer share.
 //
 // Bound: HBM, twice the moved bytes; for few tokens the chain of loads that finds them
-// (count, list, tables, row).
+// (count, list, tables, row).  Measured, in captured graphs: the accepted paths (up to 9
+// tokens) of 64 trees, 16 layers, 8 heads, d 128: 6.8 us (29 MB moved: 0.63 of a copy's
+// rate); 8 sequences of 4096-8192 shortened to three quarters, 4 layers, into other pages:
+// 204 us (0.88; 329 with a round's places found behind one another and one turn of CTAs), in
+// place 214; one such sequence, one layer: 17, in place 55 (its rounds follow one another);
+// 128 pages of 128 KB copied in 16 layers: 165 us (0.96).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -13,7 +13,15 @@
 //
 // All of it is integers, and sums and minima that atomics form do not depend on their
 // order.  A row that is its own parent keeps its whole pages without a word, so that a step
-// of growing sequences counts almost nothing.
+// of growing sequences counts almost nothing, and a page that a beam shared with its parent
+// is given up and taken without one.
+//
+// Bound: the way from number to number (parents, lengths, tables, counts, ranks, pages), not
+// the few bytes.  Measured, in captured graphs: 256 sequences of 128-1024 positions, pages of
+// 16, one step: 8.9 us (15.2 as one cluster with the counts in L2, 13.2 as one block that
+// writes all tables); 8 of 300: 5.5; 64 beams of 2000-8000, 459 pages to a row: 14.1; 1024
+// beams of 2048-8192, 513 pages to a row, 350000 pages: 20.7 (54.7 as one cluster of 8 CTAs,
+// 34.6 of 16; five launches 19.4, but 2 us more of the host's time, which is as much).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -25,7 +25,9 @@
 // rows to a token are bound by latency, with neither the issue slots (54%) nor DRAM (31%)
 // full: 128 x 127 tokens of 8 + 8 heads, d 64, backward 28 us (0.53: a round at a time, its
 // sums six shuffles behind one another, and 5 us before the first row and for the weights'
-// last sums), forward 26 (0.38: two rounds of loads to a token's tensor).
+// last sums), forward 26 (0.38: two rounds of loads to a token's tensor), 256 trees of 64
+// tokens appended 26.7 (0.56: 57% of the issue slots, 170 instructions to a warp's round of
+// four rows; all of a token's rows loaded at once, 6 rounds in flight: 28.5, and prompts 53).
 //
 // Angles: with the frequency in turns as a 64-bit binary fraction F =
 // frac(f / 2 pi) 2^64, the position times F modulo 2^64 is the angle's fraction of
