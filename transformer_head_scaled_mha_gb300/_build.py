@@ -1,4 +1,5 @@
-"""Builds the CUDA library libmha.so in-tree with nvcc for sm_103a.
+"""Builds the CUDA library libmha.so in-tree with nvcc for sm_103a, and beside it
+the inner part of the Python binding (binding.cpp) with the host compiler.
 
 Each translation unit is compiled in parallel, then linked into one shared
 library against the shared CUDA runtime (the one PyTorch already loaded).
@@ -6,14 +7,19 @@ library against the shared CUDA runtime (the one PyTorch already loaded).
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmha.so")
+# of this interpreter's kind alone: another one does not find it, and does without
+BINDING = os.path.join(BUILD, "_mha_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["mha_api.cu", "attn_f32_simt.cu", "attn_short_tc.cu", "attn_long_tc.cu", "attn_decode_tc.cu",
@@ -39,11 +45,49 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _fresh(path: str) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= _deps_mtime()
+
+
+def build_binding(verbose: bool = False) -> bool:
+    """Compile binding.cpp against PyTorch's headers; False (and no file) where that is
+    not possible: the binding then makes its checks and calls in Python."""
+    spec = importlib.util.find_spec("torch")
+    cxx = shutil.which(os.environ.get("CXX", "g++"))
+    if os.path.exists(BINDING):
+        os.remove(BINDING)
+    if spec is None or not spec.submodule_search_locations or cxx is None:
+        return False
+    torch = spec.submodule_search_locations[0]
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch, "include"),
+           "-I", INCLUDE, os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        print("binding.cpp not built, calls are made through ctypes:\n" + res.stderr[-2000:],
+              file=sys.stderr)
+        return False
+    if verbose and res.stderr:
+        print(res.stderr)
+    os.replace(tmp, BINDING)
+    return True
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile (if stale) and return the path of libmha.so."""
     os.makedirs(BUILD, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
-        return LIB
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside the library's own files
+        binding = None if _fresh(BINDING) and not force else ex.submit(build_binding, verbose)
+        if force or not _fresh(LIB):
+            _build_library(verbose, extra_flags)
+        if binding is not None:
+            binding.result()
+    return LIB
+
+
+def _build_library(verbose: bool, extra_flags) -> None:
     cc = nvcc()
 
     def compile_one(src):
@@ -64,7 +108,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

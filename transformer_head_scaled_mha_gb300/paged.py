@@ -4,12 +4,18 @@ The per-head norm and position rotation of queries and keys with its gradients,
 the paged key/value cache and the attention over it, for trees of drafted tokens
 too, and the page pool under it.  Same library, same errors
 and same conventions as ``mha.py``: torch CUDA tensors in, nothing computed here.
+Where binding.cpp is built it checks the tensors and makes the calls; what is refused,
+and how, stays the same.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 
+from . import _build
 from .mha import (MHA_DTYPE_BF16, MHA_DTYPE_F32, MHA_LAYOUT_BHSD, MHA_LAYOUT_BSHD,
                   MHA_MASK_CAUSAL_TAIL, MHA_OK, MhaError, lib)
 
@@ -101,7 +107,31 @@ def _torch():
     if torch is None:
         import torch
         _modules["torch"] = torch
+        _use_binding()
     return torch
+
+
+_LIB = lib      # (a test may put another one in lib's place)
+_native = None  # binding.cpp's module
+
+
+def _use_binding() -> None:
+    """Takes binding.cpp's checks and calls, where it is built (torch is imported: it links
+    to it)."""
+    global _native, _at
+    if not os.path.exists(_build.BINDING):
+        return
+    loader = importlib.machinery.ExtensionFileLoader("_mha_binding", _build.BINDING)
+    try:
+        native = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_mha_binding", loader))
+        loader.exec_module(native)
+    except ImportError:  # built against another PyTorch
+        return
+    native.refuse_with(_at_plain)
+    for name in EXPORTED:
+        native.bind(name, ctypes.cast(getattr(_LIB, name), ctypes.c_void_p).value)
+    _native, _at = native, native.at
 
 
 def _dtype_of(t) -> int:
@@ -129,7 +159,7 @@ def _device_of(t) -> int:
     return dev
 
 
-def _at(name, t, shape, dtype, dev):
+def _at_plain(name, t, shape, dtype, dev):
     """Address of a tensor or array of the call (None: none): contiguous, of that
     shape, dtype and device.  Every tensor of every call of a generation step passes
     here: plain attribute reads, the device by its number."""
@@ -140,6 +170,9 @@ def _at(name, t, shape, dtype, dev):
                          "%s on %s" % (name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape),
                                        t.device))
     return t.data_ptr()
+
+
+_at = _at_plain
 
 
 def _scratch(t, dev):
@@ -176,11 +209,12 @@ def _call(name, dev, stream, args):
         handle = _current_stream(dev)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    entry = getattr(_native if _native is not None and lib is _LIB else lib, name)
     if _only_device() or torch.cuda.current_device() == dev:
-        st = getattr(lib, name)(*args, handle)
+        st = entry(*args, handle)
     else:
         with torch.cuda.device(dev):
-            st = getattr(lib, name)(*args, handle)
+            st = entry(*args, handle)
     if st != MHA_OK:
         raise MhaError(st, name)
 
