@@ -25,9 +25,11 @@
 // rows to a token are bound by latency, with neither the issue slots (54%) nor DRAM (31%)
 // full: 128 x 127 tokens of 8 + 8 heads, d 64, backward 28 us (0.53: a round at a time, its
 // sums six shuffles behind one another, and 5 us before the first row and for the weights'
-// last sums), forward 26 (0.38: two rounds of loads to a token's tensor), 256 trees of 64
-// tokens appended 26.7 (0.56: 57% of the issue slots, 170 instructions to a warp's round of
-// four rows; all of a token's rows loaded at once, 6 rounds in flight: 28.5, and prompts 53).
+// last sums), forward 26 (0.38: two rounds of loads to a token's tensor).  256 trees of 64
+// tokens of 8 + 8 + 8 heads appended: 22.7 us (0.66; 26.7 with a tensor's rows loaded after
+// the one before was done; 57% of the issue slots, 170 instructions to a warp's round of
+// four rows).  One loop over all tensors' rounds, six loads ahead, for any number of heads:
+// 28.5, and prompts 53.
 //
 // Angles: with the frequency in turns as a 64-bit binary fraction F =
 // frac(f / 2 pi) 2^64, the position times F modulo 2^64 is the angle's fraction of
@@ -315,6 +317,56 @@ struct Stretch {
   }
 };
 
+// What a token's rows of one tensor are multiplied by: y_a = r (a ca - b sb), y_b = r (a sa
+// + b cb), the weight in the factors.
+template <typename T, int D, int kStyle>
+struct Factors {
+  using P = Place<T, D, kStyle>;
+  static constexpr int kN = P::kN, kPairs = P::kPairs;
+  float ca[kPairs], sb[kPairs], sa[kPairs], cb[kPairs];
+  bool normed;
+  __device__ __forceinline__ void set(const Angles<T, D> &ang, const P &place, const T *weight) {
+    normed = weight != nullptr;
+    float w[kN];
+    if (normed) Vec<T>::unpack(place.load(weight), w);
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) {
+      float c0, c1, s0, s1;
+      f2_unpack(ang.c[e / 2], c0, c1);
+      f2_unpack(ang.s[e / 2], s0, s1);
+      const float c = e % 2 == 0 ? c0 : c1, s = e % 2 == 0 ? s0 : s1;
+      const float wa = normed ? w[P::a(e)] : 1.f, wb = normed ? w[P::b(e)] : 1.f;
+      ca[e] = c * wa;
+      sb[e] = s * wb;
+      sa[e] = s * wa;
+      cb[e] = c * wb;
+    }
+  }
+  __device__ __forceinline__ uint4 apply(uint4 raw, const P &place, float eps) const {
+    float y[kN];
+    Vec<T>::unpack(raw, y);
+    float r = 1.f;
+    if (normed) {
+      float sq = 0.f;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) sq = fmaf(y[e], y[e], sq);
+      r = rsqrtf(row_sum<Angles<T, D>::kLanes>(sq) * (1.f / D) + eps);
+    }
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) {
+      const float ya = y[P::a(e)], yb = y[P::b(e)];
+      float oa = ya * ca[e], ob = yb * cb[e];
+      if (place.on) {  // outside the rotation an infinity must not meet a factor of 0
+        oa = fmaf(-yb, sb[e], oa);
+        ob = fmaf(ya, sa[e], ob);
+      }
+      y[P::a(e)] = oa * r;
+      y[P::b(e)] = ob * r;
+    }
+    return Vec<T>::pack(y);
+  }
+};
+
 // Norms and rotates (or, kCopy, copies) rounds [from, to) of one tensor.  Row h lies
 // at src + h * in and goes to dst + h * out.
 template <typename T, int D, int kStyle, bool kCopy>
@@ -322,13 +374,9 @@ __device__ __forceinline__ void fwd_rows(const T *src, long long in, T *dst, lon
                                          int heads, int from, int to, int group, bool live,
                                          const Place<T, D, kStyle> &place, const T *weight, float eps,
                                          const Angles<T, D> &ang) {
-  using P = Place<T, D, kStyle>;
   using A = Angles<T, D>;
-  constexpr int kN = P::kN, kPairs = P::kPairs, kBatch = 4;
+  constexpr int kBatch = 4;
   if (from >= to) return;
-  // y_a = r (a ca - b sb), y_b = r (a sa + b cb), the weight in the factors
-  float ca[kPairs], sb[kPairs], sa[kPairs], cb[kPairs];
-  const bool normed = !kCopy && weight != nullptr;
   int h = from * A::kGroups + group;
   src += h * in;
   dst += h * out;
@@ -346,48 +394,12 @@ __device__ __forceinline__ void fwd_rows(const T *src, long long in, T *dst, lon
     src = row;
   };
   load(from);
-  if (!kCopy) {
-    float w[kN];
-    if (normed) Vec<T>::unpack(place.load(weight), w);
-#pragma unroll
-    for (int e = 0; e < kPairs; ++e) {
-      float c0, c1, s0, s1;
-      f2_unpack(ang.c[e / 2], c0, c1);
-      f2_unpack(ang.s[e / 2], s0, s1);
-      const float c = e % 2 == 0 ? c0 : c1, s = e % 2 == 0 ? s0 : s1;
-      const float wa = normed ? w[P::a(e)] : 1.f, wb = normed ? w[P::b(e)] : 1.f;
-      ca[e] = c * wa;
-      sb[e] = s * wb;
-      sa[e] = s * wa;
-      cb[e] = c * wb;
-    }
-  }
+  Factors<T, D, kStyle> f;
+  if (!kCopy) f.set(ang, place, weight);
   for (int j = from; j < to; j += kBatch) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (!kCopy) {
-        float y[kN];
-        Vec<T>::unpack(raw[i], y);
-        float r = 1.f;
-        if (normed) {
-          float sq = 0.f;
-#pragma unroll
-          for (int e = 0; e < kN; ++e) sq = fmaf(y[e], y[e], sq);
-          r = rsqrtf(row_sum<A::kLanes>(sq) * (1.f / D) + eps);
-        }
-#pragma unroll
-        for (int e = 0; e < kPairs; ++e) {
-          const float ya = y[P::a(e)], yb = y[P::b(e)];
-          float oa = ya * ca[e], ob = yb * cb[e];
-          if (place.on) {  // outside the rotation an infinity must not meet a factor of 0
-            oa = fmaf(-yb, sb[e], oa);
-            ob = fmaf(ya, sa[e], ob);
-          }
-          y[P::a(e)] = oa * r;
-          y[P::b(e)] = ob * r;
-        }
-        raw[i] = Vec<T>::pack(y);
-      }
+      if (!kCopy) raw[i] = f.apply(raw[i], place, eps);
       if (live && j + i < to && h + i * A::kGroups < heads) place.store(dst, raw[i]);
       dst += out;
     }
@@ -395,6 +407,33 @@ __device__ __forceinline__ void fwd_rows(const T *src, long long in, T *dst, lon
     if (j + kBatch < to) load(j + kBatch);
   }
 }
+
+// The sequence of a row that is appended, and its position, from row to row of a warp's
+// stretch.
+struct Cells {
+  int seq = -1, end = -1, len = 0;  // the last row's sequence, where it ends, its length
+  int pos;
+  __device__ __forceinline__ void at(const RopeArgs &a, int t, int lane) {
+    if (t >= end) {
+      seq = seq_of_row(a.batch, t, lane);
+      if (seq >= 0) {
+        end = min(a.batch.q_starts[seq + 1], a.tokens);
+        len = max(a.batch.kv_lengths[seq], 0);
+      }
+    }
+    // tokens up to the sequence's end count back from its length
+    pos = seq >= 0 ? len - (end - t) : 0;
+  }
+  __device__ __forceinline__ bool live() const { return seq >= 0; }
+  // row of head 0 in the cache; -1: none
+  __device__ __forceinline__ long long cell(const RopeArgs &a) const {
+    return seq >= 0 ? paged_cell(a.batch, seq, pos, 0, a.Hkv) : -1;
+  }
+  // (drafted trees: the angle's position is not the cell's)
+  __device__ __forceinline__ int angle(const RopeArgs &a, int t) const {
+    return a.positions != nullptr ? a.positions[t] : pos;
+  }
+};
 
 template <typename T, int D, int kStyle, bool kAppend>
 __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const RopeArgs a, int warps) {
@@ -412,26 +451,15 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const Rope
   ang.frequencies(a.inv_freq, place.freq, place.on, group);
   Stretch stretch(static_cast<long long>(a.tokens) * rounds, w, warps);
   int t, lo, hi;
-  int seq = -1, end = -1, len = 0;  // the last token's sequence, where it ends, its length
+  Cells cells;
   while (stretch.next(rounds, t, lo, hi)) {
-    int pos = 0;
     bool live = true;
     if (kAppend) {
-      if (t >= end) {
-        seq = seq_of_row(a.batch, t, lane);
-        if (seq >= 0) {
-          end = min(a.batch.q_starts[seq + 1], a.tokens);
-          len = max(a.batch.kv_lengths[seq], 0);
-        }
-      }
-      live = seq >= 0;
-      // tokens up to the sequence's end count back from its length
-      if (live) pos = len - (end - t);
-      // (drafted trees: the angle's position is not the cell's)
-      ang.at(a.positions != nullptr ? a.positions[t] : pos, col);
+      cells.at(a, t, lane);
+      live = cells.live();
+      ang.at(cells.angle(a, t), col);
     } else {
-      pos = a.positions != nullptr ? a.positions[t] : t % a.L;
-      ang.at(pos, col);
+      ang.at(a.positions != nullptr ? a.positions[t] : t % a.L, col);
     }
     const int layout = kAppend ? kLayoutBSHD : a.layout;
     const Rows q = rows_of(layout, t, a.H, a.L, D), k = rows_of(layout, t, a.Hkv, a.L, D);
@@ -441,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const Rope
                                   static_cast<const T *>(a.q_weight), a.eps, ang);
     Rows to = k;
     if (kAppend) {
-      const long long cell = live ? paged_cell(a.batch, seq, pos, 0, a.Hkv) : -1;
+      const long long cell = cells.cell(a);
       live = cell >= 0;
       to.base = cell * D;
       to.step = a.batch.layout == kLayoutBHSD ? static_cast<long long>(a.batch.page_size) * D : D;
@@ -455,6 +483,68 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const Rope
                                    static_cast<T *>(a.v_out) + to.base, to.step, a.Hkv,
                                    max(lo - rq - rk, 0), hi - rq - rk, group, live, place,
                                    nullptr, 0.f, ang);
+  }
+}
+
+// Appending where a token has at most kShortRounds rounds of each tensor (8 heads of 64 in
+// bf16): all its rows are loaded at once, ahead of the loads that find its sequence, position
+// and cell, which only the stores need.
+constexpr int kShortRounds = 2;
+template <typename T, int D, int kStyle>
+__global__ void __launch_bounds__(kThreads, kFwdCtas)
+    rope_append_short_kernel(const RopeArgs a, int warps) {
+  using A = Angles<T, D>;
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = lane % A::kLanes, group = lane / A::kLanes;
+  const Place<T, D, kStyle> place(col, a.rotary);
+  const int rq = (a.H + A::kGroups - 1) / A::kGroups, rk = (a.Hkv + A::kGroups - 1) / A::kGroups;
+  const int w = blockIdx.x * kWarps + warp;
+  griddep_wait();
+  if (w >= warps) return;
+  A ang;
+  ang.frequencies(a.inv_freq, place.freq, place.on, group);
+  const int rounds = rq + 2 * rk;
+  Stretch stretch(static_cast<long long>(a.tokens) * rounds, w, warps);
+  const long long step =
+      (a.batch.layout == kLayoutBHSD ? static_cast<long long>(a.batch.page_size) : 1) * D * A::kGroups;
+  int t, lo, hi;
+  Cells cells;
+  while (stretch.next(rounds, t, lo, hi)) {
+    const long long q0 = (static_cast<long long>(t) * a.H + group) * D;
+    const long long k0 = (static_cast<long long>(t) * a.Hkv + group) * D;
+    // which of the rounds are this warp's, and this lane's rows there
+    bool mine[3][kShortRounds];
+    uint4 raw[3][kShortRounds];
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      const T *src = static_cast<const T *>(x == 0 ? a.q : (x == 1 ? a.k : a.v)) + (x == 0 ? q0 : k0);
+#pragma unroll
+      for (int i = 0; i < kShortRounds; ++i) {
+        const int j = (x == 0 ? 0 : (x == 1 ? rq : rq + rk)) + i;
+        mine[x][i] = i < (x == 0 ? rq : rk) && j >= lo && j < hi &&
+                     group + i * A::kGroups < (x == 0 ? a.H : a.Hkv);
+        raw[x][i] = make_uint4(0, 0, 0, 0);
+        if (mine[x][i]) raw[x][i] = place.load(src + i * A::kGroups * D);
+      }
+    }
+    cells.at(a, t, lane);
+    const long long cell = cells.cell(a);
+    ang.at(cells.angle(a, t), col);
+    Factors<T, D, kStyle> f;
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      if (x < 2) f.set(ang, place, static_cast<const T *>(x == 0 ? a.q_weight : a.k_weight));
+      T *dst = static_cast<T *>(x == 0 ? a.q_out : (x == 1 ? a.k_out : a.v_out)) +
+               (x == 0 ? q0 : cell * D + group * (step / A::kGroups));
+      const bool live = x == 0 ? cells.live() : cell >= 0;
+#pragma unroll
+      for (int i = 0; i < kShortRounds; ++i) {
+        if (i >= (x == 0 ? rq : rk)) break;
+        if (x < 2) raw[x][i] = f.apply(raw[x][i], place, a.eps);
+        if (mine[x][i] && live) place.store(dst + (x == 0 ? i * A::kGroups * D : i * step), raw[x][i]);
+      }
+    }
   }
 }
 
@@ -750,6 +840,8 @@ cudaError_t fwd(const RopeArgs &a, bool append, int num_sms, cudaStream_t stream
       (rounds<T, D>(a.H) + (append ? 2 : 1) * rounds<T, D>(a.Hkv));
   const int warps = warps_of(total, kFwdCtas * kWarps * num_sms);
   const dim3 grid((warps + kWarps - 1) / kWarps);
+  if (append && rounds<T, D>(a.H) <= kShortRounds && rounds<T, D>(a.Hkv) <= kShortRounds)
+    return launch(rope_append_short_kernel<T, D, kStyle>, grid, kThreads, stream, a, warps);
   return append ? launch(rope_fwd_kernel<T, D, kStyle, true>, grid, kThreads, stream, a, warps)
                 : launch(rope_fwd_kernel<T, D, kStyle, false>, grid, kThreads, stream, a, warps);
 }
