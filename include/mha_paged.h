@@ -293,7 +293,8 @@ size_t mha_paged_reserve_workspace_size(int B, int num_pages);
  * how far the row's pages go: new_lengths[i] where it got them all (at most
  * max_pages * page_size), else the positions in the pages it has (without its
  * part-filled page when that one's copy is missing).  The inputs are left as they
- * were, so the caller may choose other lengths and call again.
+ * were (but for refs where refs_out is refs), so the caller may choose other lengths
+ * and call again.
  *
  * block_table, kv_lengths  int32 [B_old, max_pages], [B_old]: the old tables; entries
  *               outside [0, num_pages) name no page, and are -1 where they are kept
@@ -345,8 +346,9 @@ int mha_paged_copy(void *k_cache, void *v_cache, const int32_t *moves, int n, in
  * starts      int32 [B], or NULL: 0.  Clamped to [0, kv_lengths[b]]
  * kv_lengths  int32 [B]: the lengths before; negative: 0
  * block_table int32 [B, max_pages]: the pages that are written
- * src_table   like it: the pages that are read; NULL: block_table, in place.  Where the
- *             tables differ, a page that is written is none that is read
+ * src_table   like it: the pages that are read; NULL, or block_table itself: in place.
+ *             Otherwise no cell that is written is read as well, by any sequence (a token
+ *             whose cell is the same in both tables is neither read nor written)
  * A position in no page is neither read nor written.  In place, what a cell held is read
  * before it is written; cells that are written belong to one sequence (and one place of
  * its table) only.  lengths_out overlaps nothing.

@@ -576,7 +576,8 @@ def mha_paged_compact(k_cache, v_cache, keep, keep_counts, lengths_out=None, *, 
 
     keep int32 [B, max_keep]: ascending lists, which end before an entry that is not; starts
     int32 [B] (None: 0); kv_lengths [B]: the lengths before; ``block_table`` [B, max_pages]:
-    the pages written, ``src_table`` those read (None: the same, in place)."""
+    the pages written, ``src_table`` those read (None: the same, in place; else no cell is
+    both written and read)."""
     torch = _torch()
     i32, lay = torch.int32, _layout_of(layout)
     layers, (pages, a, b, d), dt, dev = _stack(k_cache, v_cache)
