@@ -352,7 +352,7 @@ int mha_paged_copy(void *k_cache, void *v_cache, const int32_t *moves, int n, in
  * A position in no page is neither read nor written.  In place, what a cell held is read
  * before it is written; cells that are written belong to one sequence (and one place of
  * its table) only.  lengths_out overlaps nothing.
- * 2 B H_kv layers is at most 2^31 - 1
+ * 2 B H_kv layers is at most 2^31 - 1, max_keep 2^30
  */
 int mha_paged_compact(void *k_cache, void *v_cache, int32_t *lengths_out, const int32_t *keep,
                       const int32_t *keep_counts, const int32_t *starts,

@@ -73,7 +73,7 @@ def test_compact_rejects_before_launch(mha):  # noqa: F811
         assert compact(mha, **kw) == mha.MHA_ERR_INVALID_ARGUMENT, kw
     for kw in (dict(page=8), dict(d=32), dict(B=2 ** 31 - 1), dict(layers=2 ** 30, pages=1),
                dict(page=1 << 20, max_pages=1 << 11), dict(B=1 << 30, Hkv=0, layers=0),
-               dict(pages=2 ** 31 - 1), dict(B=2 ** 31 - 1, Hkv=2 ** 31 - 1, layers=2 ** 31 - 1)):
+               dict(pages=2 ** 31 - 1), dict(most=(1 << 30) + 1), dict(B=2 ** 31 - 1, Hkv=2 ** 31 - 1, layers=2 ** 31 - 1)):
         assert compact(mha, **kw) == mha.MHA_ERR_UNSUPPORTED, kw
     assert compact(mha, B=0, k=None, v=None, out=None, keep=None, counts=None, lens=None,
                    table=None) == mha.MHA_OK

@@ -123,7 +123,8 @@ extern "C" int mha_paged_compact(void *k_cache, void *v_cache, int32_t *lengths_
   if (st != MHA_OK) return st;
   // one CTA to a sequence, head, layer and tensor
   const int heads = std::max(H_kv, 1), stack = std::max(layers, 1);
-  if (!fits({B, max_pages}) || !fits({B, max_keep}) || !fits({2, B, heads, stack}) ||
+  // (and a list in 32 bits, with rounds behind it)
+  if (max_keep > 1 << 30 || !fits({B, max_pages}) || !fits({B, max_keep}) || !fits({2, B, heads, stack}) ||
       2LL * B * heads * stack > 0x7fffffffLL)
     return MHA_ERR_UNSUPPORTED;
   if (B == 0) return MHA_OK;
