@@ -334,6 +334,79 @@ def test_moves_beyond_32_bit_offsets():
                 assert torch.equal(c[:, p], s[:, i])
 
 
+def test_moves_on_streams_and_in_graphs():
+    """A captured copy and compaction, replayed with other pairs and lists, and both at once on
+    streams of their own, each on caches of its own."""
+    import torch
+    import transformer_head_scaled_mha_gb300 as mha
+    rng = np.random.default_rng(5)
+    layers, pages, page, Hkv, d, B, width = 3, 40, 16, 2, 64, 4, 8
+    table = rng.permutation(pages)[:B * width].reshape(B, width).astype(np.int32)
+    spare = np.setdiff1d(np.arange(pages), table).astype(np.int32)
+    lens = np.array([100, 128, 7, 60], np.int32)
+    starts = np.array([3, 0, 0, 50], np.int32)
+    for most in (12, 90):
+        want, (kc, vc) = caches(rng, (layers, pages, page, Hkv, d), "bf16")
+        turns = []
+        for _ in range(3):
+            keep, counts = lists(rng, B, most, lens, starts, False)
+            moves = np.stack([rng.permutation(table.ravel())[:4], rng.permutation(spare)[:4]], -1)
+            turns.append((keep, counts, moves.astype(np.int32)))
+        keep, counts, moves = (up(x) for x in turns[0])
+        out, args = up(lens).clone(), dict(starts=up(starts), kv_lengths=up(lens), block_table=up(table),
+                                           layout="bshd")
+        other = [c.clone() for c in (kc, vc)]
+
+        def both(c, stream=None):
+            mha.mha_paged_copy(*c, moves, stream=stream)
+            mha.mha_paged_compact(*c, keep, counts, out, stream=stream, **args)
+        both([c.clone() for c in (kc, vc)])  # (warm)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            both((kc, vc))
+        side = torch.cuda.Stream()
+        for turn in turns:
+            for t, x in zip((keep, counts, moves), turn):
+                t.copy_(up(x))
+            torch.cuda.synchronize()
+            graph.replay()
+            both(other, side)
+            torch.cuda.synchronize()
+            for c in want:
+                c[:, turn[2][:, 1]] = c[:, turn[2][:, 0]]
+            want, length = pages_ref.compact(want, turn[0], turn[1], starts, lens, table, table, page,
+                                             "bshd")
+            assert np.array_equal(down(out), length)
+            for c, o, w in zip((kc, vc), other, want):
+                assert np.array_equal(bits_of(c), w) and torch.equal(c.view(torch.int16), o.view(torch.int16))
+
+
+@pytest.mark.parametrize("most", [3, 40])
+def test_thousands_of_sequences_and_none(most):
+    import torch
+    import transformer_head_scaled_mha_gb300 as mha
+    rng = np.random.default_rng(6)
+    B, width, page = 5000, 4, 16
+    table = rng.permutation(B * width).reshape(B, width).astype(np.int32)
+    lens = rng.integers(0, width * page + 1, B).astype(np.int32)
+    starts = np.array([rng.integers(0, n + 1) for n in lens], np.int32)
+    keep, counts = lists(rng, B, most, lens, starts, True)
+    start, (kc, vc) = caches(rng, (1, B * width, page, 1, 64), "bf16")
+    got = mha.mha_paged_compact(kc, vc, up(keep), up(counts), starts=up(starts), kv_lengths=up(lens),
+                                block_table=up(table), layout="bshd")
+    want, length = pages_ref.compact(start, keep, counts, starts, lens, table, table, page, "bshd")
+    torch.cuda.synchronize()
+    assert np.array_equal(down(got), length)
+    assert np.array_equal(bits_of(kc), want[0]) and np.array_equal(bits_of(vc), want[1])
+    none = torch.zeros(0, most, dtype=torch.int32, device="cuda")
+    got = mha.mha_paged_compact(kc, vc, none, none[:, 0], kv_lengths=none[:, 0].contiguous(),
+                                block_table=none, layout="bshd")
+    assert got.shape == (0,)
+    mha.mha_paged_copy(kc, vc, torch.zeros(0, 2, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert np.array_equal(bits_of(kc), want[0])
+
+
 # ---------------------------------------------------------------------------
 # a run of them together
 # ---------------------------------------------------------------------------
