@@ -19,9 +19,9 @@ struct ReserveArgs {
   int32_t *moves;   // [B, 2]
   int32_t *counts;  // [2] or nullptr
   // workspace
+  int4 *rows;       // [B] what a row keeps: parent, keep, next, last
   int32_t *lowest;  // [num_pages] of a part-filled page: the lowest row that keeps it
   int32_t *given;   // [num_pages] pages given out, in order
-  int32_t *last;    // [B] the row's part-filled page
   int32_t *need;    // [B] pages that the row needs (kReserve* bits), then its first one's number
   uint32_t *free;   // [num_pages / 32, rounded up] free pages, a bit each
   int32_t *totals;  // [kReserveTotals] pages given out, blocks that are done

@@ -51,7 +51,7 @@ using namespace mha;
 
 extern "C" size_t mha_paged_reserve_workspace_size(int B, int num_pages) {
   if (B < 0 || num_pages < 0 || B > kMaxCount || num_pages > kMaxCount) return 0;
-  return round_up(ints(2LL * num_pages + 2LL * B + (num_pages + 31LL) / 32 + kReserveTotals));
+  return round_up(ints(2LL * num_pages + 5LL * B + (num_pages + 31LL) / 32 + kReserveTotals));
 }
 
 extern "C" int mha_paged_reserve(const int32_t *block_table, const int32_t *kv_lengths,
@@ -96,10 +96,10 @@ extern "C" int mha_paged_reserve(const int32_t *block_table, const int32_t *kv_l
   a.refs_out = refs_out;
   a.moves = moves;
   a.counts = counts;
-  a.lowest = static_cast<int32_t *>(workspace);
+  a.rows = static_cast<int4 *>(workspace);
+  a.lowest = reinterpret_cast<int32_t *>(a.rows + B);
   a.given = a.lowest + num_pages;
-  a.last = a.given + num_pages;
-  a.need = a.last + B;
+  a.need = a.given + num_pages;
   a.free = reinterpret_cast<uint32_t *>(a.need + B);
   a.totals = reinterpret_cast<int32_t *>(a.free) + (num_pages + 31LL) / 32;
   a.B_old = B_old;

@@ -20,8 +20,9 @@
 // the few bytes.  Measured, in captured graphs: 256 sequences of 128-1024 positions, pages of
 // 16, one step: 8.9 us (15.2 as one cluster with the counts in L2, 13.2 as one block that
 // writes all tables); 8 of 300: 5.5; 64 beams of 2000-8000, 459 pages to a row: 14.1; 1024
-// beams of 2048-8192, 513 pages to a row, 350000 pages: 20.7 (54.7 as one cluster of 8 CTAs,
-// 34.6 of 16; five launches 19.4, but 2 us more of the host's time, which is as much).
+// beams of 2048-8192, 513 pages to a row, 350000 pages: 18 (54.7 as one cluster of 8 CTAs,
+// 34.6 of 16; 20.2 in blocks of 1024, which leave the next launch no room; a fifth launch in place
+// of the last block: 1.3 less, but 2 more of the host's time).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -38,6 +39,22 @@ constexpr int kChunk = 256;  // entries of a row that a warp takes at a time
 
 __device__ __forceinline__ int row_chunks(const ReserveArgs &a) {
   return max(1, (a.max_pages + kChunk - 1) / kChunk);
+}
+
+// A row in 16 bytes: what took loads behind one another to find.
+__device__ __forceinline__ int4 pack(const ReserveRow &r) {
+  return make_int4(r.parent, r.keep, r.next, r.last);
+}
+__device__ __forceinline__ ReserveRow unpack(const ReserveArgs &a, int4 s) {
+  ReserveRow r;
+  r.parent = s.x;
+  r.keep = s.y;
+  r.next = s.z;
+  r.last = s.w;
+  r.full = r.keep >> a.page_shift;
+  r.had = reserve_pages(a, r.keep);
+  r.want = reserve_pages(a, r.next);
+  return r;
 }
 
 // An entry that names no page is -1.
@@ -84,7 +101,8 @@ __device__ __forceinline__ int need_of(const ReserveRow &r, int i, int lowest, i
   return (r.want - r.had + ((bits & kReserveCopied) != 0)) << kReserveShift | bits;
 }
 
-// Exclusive sum of a number per thread over the block; `total`: of all.
+// Exclusive sum of a number per thread over a block of kT; `total`: of all.
+template <int kT>
 __device__ int block_scan(int x, int *scratch, int &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = x;
@@ -96,7 +114,7 @@ __device__ int block_scan(int x, int *scratch, int &total) {
   __syncthreads();
   if (lane == 31) scratch[warp] = inc;
   __syncthreads();
-  int w = scratch[lane];
+  int w = lane < kT / 32 ? scratch[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, w, o);
@@ -111,36 +129,36 @@ __device__ int block_scan(int x, int *scratch, int &total) {
 // 1.  One block: runs of 32 words are counted by the warps in turn, summed, and those that
 // hold pages to give looked at again.  Returns how many there were to give; `all`: how many
 // were free.
-template <typename Page, typename Free>
+template <int kT, typename Page, typename Free>
 __device__ int give_pages(const ReserveArgs &a, const Free &free, int total, int *refs,
                           Page *given, int *scratch, int *runs, int &all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int words = (a.num_pages + 31) / 32;
   all = 0;  // so far
-  for (int base = 0; base < words; base += 32 * kThreads) {
+  for (int base = 0; base < words; base += 32 * kT) {
     __syncthreads();
     constexpr int kDeep = 8;
-    for (int s = warp; s < kThreads && base + s * 32 < words; s += kDeep * kWarps) {
+    for (int s = warp; s < kT && base + s * 32 < words; s += kDeep * (kT / 32)) {
       uint32_t bits[kDeep];
 #pragma unroll
       for (int k = 0; k < kDeep; ++k) {
-        const int w = base + (s + k * kWarps) * 32 + lane;
-        bits[k] = s + k * kWarps < kThreads && w < words ? free(w) : 0u;
+        const int w = base + (s + k * (kT / 32)) * 32 + lane;
+        bits[k] = s + k * (kT / 32) < kT && w < words ? free(w) : 0u;
       }
 #pragma unroll
       for (int k = 0; k < kDeep; ++k) {
         const int n = __reduce_add_sync(0xffffffffu, __popc(bits[k]));
-        if (lane == 0 && s + k * kWarps < kThreads) runs[s + k * kWarps] = n;
+        if (lane == 0 && s + k * (kT / 32) < kT) runs[s + k * (kT / 32)] = n;
       }
     }
     __syncthreads();
     int sum;
     const bool is = base + static_cast<int>(threadIdx.x) * 32 < words;
-    const int before = all + block_scan(is ? runs[threadIdx.x] : 0, scratch, sum);
+    const int before = all + block_scan<kT>(is ? runs[threadIdx.x] : 0, scratch, sum);
     runs[threadIdx.x] = before;
     all += sum;
     __syncthreads();
-    for (int s = warp; s < kThreads && base + s * 32 < words && runs[s] < total; s += kWarps) {
+    for (int s = warp; s < kT && base + s * 32 < words && runs[s] < total; s += (kT / 32)) {
       const int w = base + s * 32 + lane;
       uint32_t bits = w < words ? free(w) : 0u;
       int inc = __popc(bits);
@@ -210,11 +228,8 @@ constexpr int kSmallRows = 1024, kSmallPages = 28672;
 constexpr int kSmallEntries = 65536;  // of the tables
 constexpr int kSmallCtas = 8;
 constexpr int kFew = 4;  // references that a thread counts alone
-struct SmallRow {
-  int parent, keep, next, last;
-};
 struct SmallShared {
-  SmallRow rows[kSmallRows];
+  int4 rows[kSmallRows];
   Source sources[kSmallRows];
   int had[kSmallRows], listed[kSmallRows], count;
   int runs[kThreads];
@@ -237,18 +252,6 @@ __device__ __forceinline__ void atomic_min16(uint16_t *at, int i, uint32_t x) {
   }
 }
 
-__device__ __forceinline__ ReserveRow unpack(const ReserveArgs &a, const SmallRow &s) {
-  ReserveRow r;
-  r.parent = s.parent;
-  r.keep = s.keep;
-  r.next = s.next;
-  r.last = s.last;
-  r.full = r.keep >> a.page_shift;
-  r.had = reserve_pages(a, r.keep);
-  r.want = reserve_pages(a, r.next);
-  return r;
-}
-
 __global__ void __launch_bounds__(kThreads) reserve_small_kernel(const ReserveArgs a) {
   const int cta = blockIdx.x, ctas = gridDim.x;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) reserve_small_kernel(const ReserveAr
   if (threadIdx.x == 0) sh.count = 0;
   sh.had[mine] = had;
   if (mine < a.B) r = reserve_row(a, mine);
-  sh.rows[mine] = SmallRow{r.parent, r.keep, r.next, r.last};
+  sh.rows[mine] = pack(r);
   if (mine < a.B) {
     if (r.last >= 0) sh.given[r.last] = 0xffff;
   }
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) reserve_small_kernel(const ReserveAr
   int word = 0, total, given;
   if (mine < a.B)
     word = r.last >= 0 ? need_of(r, mine, sh.given[r.last], sh.refs[r.last]) : need_of(r, mine, -1, 0);
-  const int before = block_scan(word >> kReserveShift, sh.scratch, total);
+  const int before = block_scan<kThreads>(word >> kReserveShift, sh.scratch, total);
   word = before << kReserveShift | (word & ((1 << kReserveShift) - 1));
   sh.sources[mine] = source_of(a, r, word);
   // (every row has looked at its page's references: the scan's barriers)
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) reserve_small_kernel(const ReserveAr
   }
   __syncthreads();
   int all;
-  given = give_pages(a, [&](int w) { return sh.free[w]; }, total, sh.refs, sh.given, sh.scratch, sh.runs, all);
+  given = give_pages<kThreads>(a, [&](int w) { return sh.free[w]; }, total, sh.refs, sh.given, sh.scratch, sh.runs, all);
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
   for (int p = cta * kThreads + threadIdx.x; p < a.num_pages; p += ctas * kThreads)
@@ -342,9 +345,12 @@ __global__ void __launch_bounds__(kThreads) reserve_small_kernel(const ReserveAr
 }
 
 // ---- larger ones: the whole GPU, a launch to a step -----------------------------------
-// (__ldcg: numbers that other SMs have just written)
+// (__ldcg: numbers that other SMs have just written.)  Blocks of 512 leave room on an SM for
+// the next launch's, which then wait there.
+constexpr int kStepThreads = 512, kStepWarps = kStepThreads / 32;
+
 __device__ void begin_step(const ReserveArgs &a, int block, int blocks) {
-  const int thread = block * kThreads + threadIdx.x, threads = blocks * kThreads;
+  const int thread = block * kStepThreads + threadIdx.x, threads = blocks * kStepThreads;
   if (a.refs_out != a.refs) {
 #pragma unroll 4
     for (int p = thread; p < a.num_pages; p += threads) a.refs_out[p] = __ldg(a.refs + p);
@@ -352,19 +358,19 @@ __device__ void begin_step(const ReserveArgs &a, int block, int blocks) {
   if (thread == 0) a.totals[kTotalDone] = 0;
   for (int i = thread; i < a.B; i += threads) {
     const ReserveRow r = reserve_row(a, i);
-    a.last[i] = r.last;
+    a.rows[i] = pack(r);
     if (r.last >= 0) a.lowest[r.last] = 0x7fffffff;
   }
 }
 
 __device__ void count_step(const ReserveArgs &a, int block, int blocks) {
-  const int chunks = row_chunks(a), warps = blocks * kWarps;
+  const int chunks = row_chunks(a), warps = blocks * kStepWarps;
   const long long tasks = static_cast<long long>(max(a.B_old, a.B)) * chunks;
-  for (long long t = block * kWarps + (threadIdx.x >> 5); t < tasks; t += warps) {
+  for (long long t = block * kStepWarps + (threadIdx.x >> 5); t < tasks; t += warps) {
     const int row = static_cast<int>(t / chunks), from = static_cast<int>(t % chunks) * kChunk;
     ReserveRow r{};
     r.parent = r.last = -1;
-    if (row < a.B) r = reserve_row(a, row);
+    if (row < a.B) r = unpack(a, __ldcg(&a.rows[row]));
     const int had = row < a.B_old ? reserve_pages(a, reserve_clamp(a, a.lens[row])) : 0;
     count_chunk(a, row, r, had, from, a.refs_out);
     if (from == 0 && (threadIdx.x & 31) == 0 && r.last >= 0) atomicMin(&a.lowest[r.last], row);
@@ -373,24 +379,24 @@ __device__ void count_step(const ReserveArgs &a, int block, int blocks) {
 
 // Pages that stay, the rows' first numbers, and the pages given out: by one block.
 __device__ void give_step(const ReserveArgs &a) {
-  __shared__ int scratch[kWarps], runs[kThreads];
+  __shared__ int scratch[kStepWarps], runs[kStepThreads];
   int total = 0;
-  for (int base = 0; base < a.B; base += kThreads) {
+  for (int base = 0; base < a.B; base += kStepThreads) {
     const int i = base + threadIdx.x;
     const int word = i < a.B ? __ldcg(&a.need[i]) : 0;
-    const int last = i < a.B ? __ldcg(&a.last[i]) : 0;
+    const int last = i < a.B ? __ldcg(&a.rows[i].w) : 0;
     if (word & kReserveStays) {
       atomicAdd(&a.refs_out[last], 1);  // (one row to a page)
       atomicAnd(&a.free[last >> 5], ~(1u << (last & 31)));
     }
     int sum;
-    const int before = total + block_scan(word >> kReserveShift, scratch, sum);
+    const int before = total + block_scan<kStepThreads>(word >> kReserveShift, scratch, sum);
     if (i < a.B) a.need[i] = before << kReserveShift | (word & ((1 << kReserveShift) - 1));
     total += sum;
   }
   __syncthreads();
   int all;
-  const int given = give_pages(a, [&](int w) { return __ldcg(&a.free[w]); }, total, a.refs_out, a.given, scratch, runs, all);
+  const int given = give_pages<kStepThreads>(a, [&](int w) { return __ldcg(&a.free[w]); }, total, a.refs_out, a.given, scratch, runs, all);
   if (threadIdx.x == 0) {
     a.totals[kTotalGiven] = given;
     write_counts(a, given, all);
@@ -400,9 +406,9 @@ __device__ void give_step(const ReserveArgs &a) {
 // What rows need, and which pages are free but for those that stay; the block that is done
 // last gives them out.
 __device__ void need_step(const ReserveArgs &a, int block, int blocks) {
-  const int thread = block * kThreads + threadIdx.x, threads = blocks * kThreads;
+  const int thread = block * kStepThreads + threadIdx.x, threads = blocks * kStepThreads;
   for (int i = thread; i < a.B; i += threads) {
-    const ReserveRow r = reserve_row(a, i);
+    const ReserveRow r = unpack(a, __ldcg(&a.rows[i]));
     a.need[i] = r.last >= 0 ? need_of(r, i, __ldcg(&a.lowest[r.last]), __ldcg(&a.refs_out[r.last]))
                             : need_of(r, i, -1, 0);
   }
@@ -427,12 +433,12 @@ __device__ void need_step(const ReserveArgs &a, int block, int blocks) {
 }
 
 __device__ void tables_step(const ReserveArgs &a, int block, int blocks) {
-  const int chunks = row_chunks(a), warps = blocks * kWarps, given = __ldcg(&a.totals[kTotalGiven]);
+  const int chunks = row_chunks(a), warps = blocks * kStepWarps, given = __ldcg(&a.totals[kTotalGiven]);
   const int lane = threadIdx.x & 31;
   const long long tasks = static_cast<long long>(a.B) * chunks;
-  for (long long t = block * kWarps + (threadIdx.x >> 5); t < tasks; t += warps) {
+  for (long long t = block * kStepWarps + (threadIdx.x >> 5); t < tasks; t += warps) {
     const int i = static_cast<int>(t / chunks), from = static_cast<int>(t % chunks) * kChunk;
-    const ReserveRow r = reserve_row(a, i);
+    const ReserveRow r = unpack(a, __ldcg(&a.rows[i]));
     const int word = __ldcg(&a.need[i]);
     const Source src = source_of(a, r, word);
     int id[kChunk / 32];
@@ -448,7 +454,7 @@ __device__ void tables_step(const ReserveArgs &a, int block, int blocks) {
 
 // The whole GPU, a launch to a step.
 template <void (*kStep)(const ReserveArgs &, int, int)>
-__global__ void __launch_bounds__(kThreads) reserve_step_kernel(const ReserveArgs a) {
+__global__ void __launch_bounds__(kStepThreads) reserve_step_kernel(const ReserveArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   kStep(a, blockIdx.x, gridDim.x);
@@ -467,14 +473,14 @@ cudaError_t launch_reserve(const ReserveArgs &a, int num_sms, cudaStream_t strea
     const int ctas = static_cast<int>(std::min<long long>(kSmallCtas, 1 + entries / (2 * kThreads)));
     return launch_behind(reserve_small_kernel, dim3(ctas), kThreads, smem, ctas, stream, a);
   }
-  const dim3 grid(num_sms);
-  cudaError_t e = launch_behind(reserve_step_kernel<begin_step>, grid, kThreads, 0, 1, stream, a);
+  const dim3 grid(2 * num_sms);
+  cudaError_t e = launch_behind(reserve_step_kernel<begin_step>, grid, kStepThreads, 0, 1, stream, a);
   if (e == cudaSuccess)
-    e = launch_behind(reserve_step_kernel<count_step>, grid, kThreads, 0, 1, stream, a);
+    e = launch_behind(reserve_step_kernel<count_step>, grid, kStepThreads, 0, 1, stream, a);
   if (e == cudaSuccess)
-    e = launch_behind(reserve_step_kernel<need_step>, grid, kThreads, 0, 1, stream, a);
+    e = launch_behind(reserve_step_kernel<need_step>, grid, kStepThreads, 0, 1, stream, a);
   if (e == cudaSuccess)
-    e = launch_behind(reserve_step_kernel<tables_step>, grid, kThreads, 0, 1, stream, a);
+    e = launch_behind(reserve_step_kernel<tables_step>, grid, kStepThreads, 0, 1, stream, a);
   return e;
 }
 
