@@ -305,23 +305,19 @@ __device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long l
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.batch.B + kThreads - 1) / kThreads;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch.B), b1 = min(b0 + per, p.batch.B);
-  long long mine = 0;  // of one head block
-  unsigned units = 0;  // (at most T)
-  // the last sequence looked at: the only one where there are no more than threads
-  PagedSeq own{};
-  int own_blocks = 0;
+  long long mine = 0, units = 0;  // of one head block
   for (int b = b0; b < b1; ++b) {
-    own = paged_seq(p.batch, b);
-    own_blocks = paged_blocks(p, own);
-    units += own_blocks;
-    mine += paged_cost_before(p, own, own_blocks, own_blocks);
+    const PagedSeq s = paged_seq(p.batch, b);
+    const long long nu = paged_blocks(p, s);
+    units += nu;
+    mine += paged_cost_before(p, s, static_cast<int>(nu), static_cast<int>(nu));
   }
-  units = __reduce_add_sync(0xffffffffu, units);
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
+    units += __shfl_xor_sync(0xffffffffu, units, o);
   }
   if (lane == 31) {
     scratch[warp] = inc;
@@ -348,9 +344,9 @@ __device__ PagedSpan paged_span(const PagedProblem &p, int cta, int grid, long l
   if (any && at >= first && at < first + mine) {  // one thread of the block
     long long s = first;
     for (int b = b0;; ++b) {
-      const PagedSeq q = per == 1 ? own : paged_seq(p.batch, b);
-      const int nu = per == 1 ? own_blocks : paged_blocks(p, q);
-      const long long whole = per == 1 ? mine : paged_cost_before(p, q, nu, nu);
+      const PagedSeq q = paged_seq(p.batch, b);
+      const int nu = paged_blocks(p, q);
+      const long long whole = paged_cost_before(p, q, nu, nu);
       if (at < s + whole || b + 1 >= b1) {
         long long before_u;
         scratch[34] = paged_unit_at(p, q, nu, at - s, before_u);
@@ -420,7 +416,7 @@ struct PagedWalk {
       }
       part.seq = seq;
       part.b = b;
-      part.kv = p.hblocks == 1 ? hb : hb / p.hblocks;
+      part.kv = hb / p.hblocks;
       const int hin = (hb - part.kv * p.hblocks) * p.hpu;
       part.h0 = part.kv * p.group + hin;
       part.heads = p.group - hin < p.hpu ? p.group - hin : p.hpu;

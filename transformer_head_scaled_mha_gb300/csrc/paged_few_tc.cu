@@ -8,11 +8,9 @@
 // paged_merge_kernel joins the cut ones.
 //
 // Measured, with the merge: one token, 64 sequences of 4096-8192 keys, 32 heads over 8,
-// d 128: 230 us, 7.0 TB/s (1.03 of a copy's rate; 234 with a part's queries asked for before
-// its first keys); 256 sequences of 128-1024 keys, 8 heads, d 64: 58 us, 5.2 TB/s (0.77; its
-// 2048 short units and the way to a CTA's first tile, 7 us); one sequence of 300 keys: 7.5
-// us, a chain of latencies (finding the stretch 3000 cycles, the part 1800, 16 copies of a
-// tile 2200, 1500 a tile, the output 2000).  Batches that do
+// d 128: 230-235 us, 6.9 TB/s (1.02 of a copy's rate); 256 sequences of 128-1024 keys, 8
+// heads, d 64: 59 us, 5.1 TB/s (0.76; its 2048 short units and the way to a CTA's first
+// tile, 7 us); one sequence of 300 keys: 8.2 us, a chain of latencies.  Batches that do
 // not fill the GPU for long pay 6 us to the first tile and 4 for the merge: 8 sequences of
 // 1000-4000 keys, 32 heads over 8, d 128: 24.6 us, 0.49 of a copy's rate.  From 9 rows on
 // the lone softmax warpgroup sets the pace, 16 exponentials and stores per key and thread:
@@ -274,80 +272,71 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
         return static_cast<unsigned>(id) < static_cast<unsigned>(pb.num_pages) ? id : -1;
       };
       int id = more ? page_of(part.t0) : -1;
+      ok = mbar_wait_warp(&sh->desc_empty[n % kDescs], ((n / kDescs) & 1) ^ 1, abort_flag,
+                          p.wait_ns);
+      if (!ok) break;
       const bool split = more && paged_split(part);
-      // The part's first tile, then its description and queries, then its other tiles: what
-      // takes longest to come is asked for first.
-      int j = more ? part.t0 : 0;
-      const int t1 = more ? part.t1 : 0;
-#pragma unroll 1
-      for (int phase = 0; phase < 2 && ok; ++phase) {
-        const int stop = phase == 0 ? min(j + 1, t1) : t1;
-        for (; j < stop; ++j) {
-          const int id_next = page_of(j + 1);
-          const int slot = issued % C::kSlots, round = issued / C::kSlots;
-          ok = mbar_wait_warp(&sh->kv_empty[slot], (round & 1) ^ 1, abort_flag, p.wait_ns);
-          if (!ok) break;
-          const uint32_t there = __ballot_sync(0xffffffffu, id >= 0) & ((1u << pieces) - 1);
-          if (lane == 0) {
-            sh->present[slot] = there;
-            mbar_arrive_expect_tx(&sh->kv_full[slot],
-                                  static_cast<uint32_t>(__popc(there) * box * 128 * 2 * C::kSlabs));
-          }
-          __syncwarp();
-          if (id >= 0)
-            tma_load_4d(ring + slot * C::kSlotBytes + dst0, map, &sh->kv_full[slot], slab * 64,
-                        (j * kBN + piece * box) & (pb.page_size - 1), part.kv, id);
-          ++issued;
-          id = id_next;
+      if (lane == 0) {
+        Desc d;
+        d.go = more;
+        d.tiles = part.t1 - part.t0;
+        d.key0 = part.t0 * kBN;
+        d.kv_end = part.kv_end;
+        // of a tree: where its tokens begin
+        d.lim0 = kTree ? part.seq.base : (p.causal ? part.seq.base + part.i0 + 1 : part.seq.len);
+        d.lim_step = p.causal;
+        d.row0 = part.seq.q0 + part.i0;
+        d.tokens = part.i1 - part.i0;
+        d.heads = part.heads;
+        d.h0 = part.h0;
+        d.slot = split ? paged_slot(part) : -1;
+        sh->desc[n % kDescs] = d;
+        mbar_arrive(&sh->desc_full[n % kDescs]);
+      }
+      __syncwarp();
+      ++n;
+      if (!more) break;
+      if (split) {
+        if (part.t0 > 0) {
+          flags |= kPartContinues | (part.t1 == part.nt ? kPartEnds : 0);
+          mrow = part.seq.q0 + part.i0;
+          mtokens = part.i1 - part.i0;
+          mhead = part.h0;
+          mheads = part.heads;
+        } else {
+          flags |= kPartBegins;
         }
-        if (phase == 1 || !ok) break;
-        ok = mbar_wait_warp(&sh->desc_empty[n % kDescs], ((n / kDescs) & 1) ^ 1, abort_flag,
-                            p.wait_ns);
+      }
+      if (part.nt == 0) continue;
+      const int qb = q_issued & 1;
+      ok = mbar_wait_warp(&sh->q_empty[qb], ((q_issued >> 1) & 1) ^ 1, abort_flag, p.wait_ns);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sh->q_full[qb], static_cast<uint32_t>(C::kSlabs * R * 128));
+        for (int blk = 0; blk < C::kSlabs; ++blk)
+          tma_load_4d(qbuf + qb * C::kQBytes + blk * C::kQBlk, &maps.q, &sh->q_full[qb], blk * 64,
+                      part.seq.q0 + part.i0, part.h0, 0);
+      }
+      ++q_issued;
+      for (int j = part.t0; j < part.t1; ++j) {
+        const int id_next = page_of(j + 1);
+        const int slot = issued % C::kSlots, round = issued / C::kSlots;
+        ok = mbar_wait_warp(&sh->kv_empty[slot], (round & 1) ^ 1, abort_flag, p.wait_ns);
         if (!ok) break;
+        const uint32_t there = __ballot_sync(0xffffffffu, id >= 0) & ((1u << pieces) - 1);
         if (lane == 0) {
-          Desc d;
-          d.go = more;
-          d.tiles = part.t1 - part.t0;
-          d.key0 = part.t0 * kBN;
-          d.kv_end = part.kv_end;
-          // of a tree: where its tokens begin
-          d.lim0 = kTree ? part.seq.base : (p.causal ? part.seq.base + part.i0 + 1 : part.seq.len);
-          d.lim_step = p.causal;
-          d.row0 = part.seq.q0 + part.i0;
-          d.tokens = part.i1 - part.i0;
-          d.heads = part.heads;
-          d.h0 = part.h0;
-          d.slot = split ? paged_slot(part) : -1;
-          sh->desc[n % kDescs] = d;
-          mbar_arrive(&sh->desc_full[n % kDescs]);
+          sh->present[slot] = there;
+          mbar_arrive_expect_tx(&sh->kv_full[slot],
+                                static_cast<uint32_t>(__popc(there) * box * 128 * 2 * C::kSlabs));
         }
         __syncwarp();
-        ++n;
-        if (!more) break;
-        if (split) {
-          if (part.t0 > 0) {
-            flags |= kPartContinues | (part.t1 == part.nt ? kPartEnds : 0);
-            mrow = part.seq.q0 + part.i0;
-            mtokens = part.i1 - part.i0;
-            mhead = part.h0;
-            mheads = part.heads;
-          } else {
-            flags |= kPartBegins;
-          }
-        }
-        if (part.nt == 0) break;
-        const int qb = q_issued & 1;
-        ok = mbar_wait_warp(&sh->q_empty[qb], ((q_issued >> 1) & 1) ^ 1, abort_flag, p.wait_ns);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sh->q_full[qb], static_cast<uint32_t>(C::kSlabs * R * 128));
-          for (int blk = 0; blk < C::kSlabs; ++blk)
-            tma_load_4d(qbuf + qb * C::kQBytes + blk * C::kQBlk, &maps.q, &sh->q_full[qb], blk * 64,
-                        part.seq.q0 + part.i0, part.h0, 0);
-        }
-        ++q_issued;
+        if (id >= 0)
+          tma_load_4d(ring + slot * C::kSlotBytes + dst0, map, &sh->kv_full[slot], slab * 64,
+                      (j * kBN + piece * box) & (pb.page_size - 1), part.kv, id);
+        ++issued;
+        id = id_next;
       }
-      if (!ok || !more) break;
+      if (!ok) break;
     }
     if (lane == 0) {
       int32_t *meta = p.meta + static_cast<size_t>(blockIdx.x) * kPagedMeta;
