@@ -16,7 +16,8 @@
 // the lone softmax warpgroup sets the pace, 16 exponentials and stores per key and thread:
 // 32 sequences of 500-2000 keys, 4 tokens of 32 heads over 8, d 64: 41 us, 0.30.  Trees of
 // drafted tokens where there is little work come in units of 4 or 8 rows: 16 tokens over 300
-// keys, 8 heads, d 64: 9.1 us (12.1 with 16 rows).
+// keys, 8 heads, d 64: 8.9 us (12.1 with 16 rows); 256 trees of 8 tokens, 128-1024 keys, 8
+// heads, d 64: 78 us, 0.58 (89 with a quotient to every row in every thread).
 //
 // Scores are computed transposed, keys on the 128 TMEM lanes, so that a thread
 // owns a key and the few rows cost a few exponentials per thread:
@@ -119,7 +120,7 @@ struct __align__(16) Shared {
     float4 red[2][RP];      // tile maxima of the four warps, double-buffered by tile
     long long scratch[40];  // before: where the span is found
   };
-  float lsum[4][RP];    // per-warp row sums
+  float4 lsum[RP];      // row sums of the four warps
   Desc desc[kDescs];
   uint32_t present[kMaxSlots];  // pages of the slot's tile that were loaded
   uint64_t desc_full[kDescs], desc_empty[kDescs];
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
         const float v = warp_sum(l[r]);
-        if (lane == 0) sh->lsum[warp][r] = v;
+        if (lane == 0) reinterpret_cast<float *>(&sh->lsum[r])[warp] = v;
       }
       const int u = t - 1;
       const bool oke =
@@ -636,22 +637,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RP>::kCtas)
       if (!ok) break;
       if (stores) {
         float *sums = d.slot >= 0 ? paged_slot_ptr(p, D, blockIdx.x, d.slot) : nullptr;
+        // Row r's sum, and what it is divided by, in lane r (and those r + RP, ...): one
+        // quotient to a warp.  (Row after row in every thread, the output of 8 rows took 3000
+        // cycles.)
+        const int own = lane & (RP - 1);
+        const float4 ls = sh->lsum[own];
+        float lt = (ls.x + ls.y) + (ls.z + ls.w), mt = m[0];
+#pragma unroll
+        for (int r = 1; r < RP; ++r) mt = own == r ? m[r] : mt;
+        if (sums == nullptr && mt == kLowestScore) lt = NAN;
+        const float inv = 1.f / lt;
+        const unsigned none = __ballot_sync(0xffffffffu, lt == 0.f);  // no allowed key: +0.0
+        float acc[RP];
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          acc[r] = __uint_as_float(o[r]);
+          if (D == 64) acc[r] += xo[r * 64 + vdim];
+        }
         int h = 0, i = 0;
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
+          const float f = __shfl_sync(0xffffffffu, inv, r);
           if (r < R && h < d.heads && i < d.tokens) {
-            float lt = (sh->lsum[0][r] + sh->lsum[1][r]) + (sh->lsum[2][r] + sh->lsum[3][r]);
-            float acc = __uint_as_float(o[r]);
-            if (D == 64) acc += xo[r * 64 + vdim];
             if (sums != nullptr) {
-              sums[r * D + vdim] = acc;
-              if (k == 0) {
-                sums[p.rows * D + 2 * r] = m[r];
+              sums[r * D + vdim] = acc[r];
+              if (k == r) {  // (of warp 0)
+                sums[p.rows * D + 2 * r] = mt;
                 sums[p.rows * D + 2 * r + 1] = lt;
               }
-            } else {  // a row with no allowed key is stored as +0.0
-              if (m[r] == kLowestScore) lt = NAN;
-              out[row_at(h, i) * D + vdim] = bf16_bits(lt == 0.f ? 0.f : acc * (1.f / lt));
+            } else {
+              out[row_at(h, i) * D + vdim] = bf16_bits((none >> r) & 1 ? 0.f : acc[r] * f);
             }
           }
           if (++i == p.tb) {
