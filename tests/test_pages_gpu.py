@@ -123,6 +123,24 @@ def test_tables_that_hold_anything(seed):
     check_reserve(table, lens, new, None, refs, page, in_place=True)
 
 
+@pytest.mark.parametrize("B,width,pool", [(1500, 9, 12000), (60, 1300, 30000), (40, 3, 60000),
+                                          (2500, 3, 900)])
+def test_large_tables_that_hold_anything(B, width, pool):
+    """The same, of the whole GPU's kernels; and pools that run out."""
+    rng = np.random.default_rng(B)
+    page = 16
+    wild = lambda a, lo, hi: np.where(rng.random(a.shape) < 0.1,  # noqa: E731
+                                      rng.choice([-2 ** 31, -1, hi, 2 ** 31 - 1], a.shape), a)
+    table = wild(rng.integers(0, pool, (B, width)), 0, pool).astype(np.int32)
+    lens = wild(rng.integers(0, width * page + 1, B), 0, width * page + 5).astype(np.int32)
+    new = wild(rng.integers(0, width * page + 1, B), 0, width * page + 5).astype(np.int32)
+    par = wild(rng.integers(0, B, B), 0, B).astype(np.int32)
+    for least in (-2, 0, 1):
+        refs = rng.integers(least, 4, pool).astype(np.int32)
+        check_reserve(table, lens, new, par, refs, page)
+        check_reserve(table, lens, new, None, refs, page, in_place=True)
+
+
 def test_empty_problems():
     z = lambda *s: np.zeros(s, dtype=np.int32)  # noqa: E731
     table, lens, refs = np.array([[1, 0]], np.int32), np.array([20], np.int32), np.ones(5, np.int32)

@@ -20,7 +20,7 @@
 // the few bytes.  Measured, in captured graphs: 256 sequences of 128-1024 positions, pages of
 // 16, one step: 8.9 us (15.2 as one cluster with the counts in L2, 13.2 as one block that
 // writes all tables); 8 of 300: 5.5; 64 beams of 2000-8000, 459 pages to a row: 14.1; 1024
-// beams of 2048-8192, 513 pages to a row, 350000 pages: 18 (54.7 as one cluster of 8 CTAs,
+// beams of 2048-8192, 513 pages to a row, 350000 pages: 19 (54.7 as one cluster of 8 CTAs,
 // 34.6 of 16; 20.2 in blocks of 1024, which leave the next launch no room; a fifth launch in place
 // of the last block: 1.3 less, but 2 more of the host's time).
 #include <cuda_runtime.h>
@@ -385,13 +385,13 @@ __device__ void give_step(const ReserveArgs &a) {
     const int i = base + threadIdx.x;
     const int word = i < a.B ? __ldcg(&a.need[i]) : 0;
     const int last = i < a.B ? __ldcg(&a.rows[i].w) : 0;
-    if (word & kReserveStays) {
-      atomicAdd(&a.refs_out[last], 1);  // (one row to a page)
-      atomicAnd(&a.free[last >> 5], ~(1u << (last & 31)));
-    }
+    int refs = -1;  // (one row to a page)
+    if (word & kReserveStays) refs = atomicAdd(&a.refs_out[last], 1);
     int sum;
     const int before = total + block_scan<kStepThreads>(word >> kReserveShift, scratch, sum);
     if (i < a.B) a.need[i] = before << kReserveShift | (word & ((1 << kReserveShift) - 1));
+    // (a page whose references were fewer than the old rows that held it stays free)
+    if (refs == 0) atomicAnd(&a.free[last >> 5], ~(1u << (last & 31)));
     total += sum;
   }
   __syncthreads();
