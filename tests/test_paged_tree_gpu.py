@@ -321,3 +321,22 @@ def test_append_at_its_own_positions_is_append():
     c = mha.mha_paged_append_at(q, k, v, *caches[1], dev(pos.astype(np.int32)), **kw)
     assert torch.equal(a, c)
     assert all(torch.equal(x, y) for x, y in zip(*caches))
+
+
+@pytest.mark.parametrize("room", [None, 200000], ids=["small_tables", "large_tables"])
+@pytest.mark.parametrize("n,H,Hkv,d", [(3, 2, 2, 64), (4, 8, 2, 128), (40, 4, 2, 128)])
+def test_a_wait_that_runs_out(room, n, H, Hkv, d):
+    """As test_paged_give_up_gpu.py: an issuer (of whichever kernel the call takes) waits for
+    what nothing signals, the kernel returns, the status tells, and the next call is right."""
+    import transformer_head_scaled_mha_gb300 as mha
+    from test_paged_give_up_gpu import STALL_FEW, STALL_MANY, stalled
+    rng = np.random.default_rng(n)
+    room = None if room is None else room // 64
+    for seqs in ([(n, 128 * t) for t in (1, 2, 3, 4, 5)] * 40, [(n, 20000)]):
+        b = batch(rng, seqs, 64, max_pages=room)
+        kc, vc = (dev(x, "bf16") for x in cache_of(rng, b, Hkv, 64, d, "bf16", "bshd"))
+        q, mask = dev(rnd(rng, (b["T"], H, d), "bf16"), "bf16"), dev(masks(rng, b, "tree"))
+        kw = dict(q_starts=dev(b["starts"]), kv_lengths=dev(b["lens"]), block_table=dev(b["table"]),
+                  max_q=n, layout="bshd")
+        stalled(STALL_FEW | STALL_MANY, lambda: mha.mha_paged_tree_fwd(q, kc, vc, mask, **kw))
+    check_tree([(n, 128), (n, 700)], H, Hkv, d, "bf16", 64, "bshd", seed=n, max_pages=room)
