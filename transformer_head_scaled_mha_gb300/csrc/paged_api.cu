@@ -114,11 +114,15 @@ Units units_of(int path, int group, int max_q, int rows = 0) {
 // / 9.0 us, 384 14.9 / 12.9; T8 = 752 18.6 / 15.6; T4 = 1536 13.9 / 14.7; 8 tokens of 8
 // heads over 2 (many-query): T4 = 752 17.5 / 13.6, 768 11.6 / 10.4, 3072 17.0 / 21.4.  d
 // 128, 8 tokens of 32 heads over 8 (many-query): T4 = 192 12.4 / 9.5; T8 = 384 18.9 / 14.5,
-// 1536 20.2 / 23.4; 16 of 16 heads: T8 = 384 16.7 / 14.5, 1504 20.4 / 21.8.  fp32, d 64, 13
-// tokens of 8 heads over 2: T4 = 1248 18.7 / 14.7; 16 tokens of 8 heads: 1504 25.0 / 23.6,
-// 1536 23.9 / 23.9, 3072 48 / 66; d 128, 8 tokens of 32 over 8: 192 21.8 / 14.9, 384 23.4 /
-// 30.1.  fp32 with 5 to 8 rows takes the time of 16: 4 are as fast at any size (8 tokens of
-// 8 heads, 16 sequences of 6000: 129 / 120, of 300: 21.7 / 18.3).
+// 1536 20.2 / 23.4; 16 of 16 heads: T8 = 384 16.7 / 14.5, 1504 20.4 / 21.8.  fp32, 4 / 8 /
+// 16 rows, sequences that fill their tables: d 64, 13 tokens of 8 heads over 2: T4 = 312 13.4 /
+// 13.6 / 13.8 us, 624 16.4 / 16.5 / 17.9, T8 = 1008 25.3 / 23.7 / 23.4; 16 tokens of 8 heads:
+// T4 = 96 10.3 / 11.7 / 11.5, 768 18.0 / 16.7 / 18.8, T8 = 768 25.5 / 22.4 / 21.9.  d 128,
+// 16 tokens of 8 heads: T4 = 96 11.3 / 16.1 / 15.1, T8 = 192 19.7 / 17.4 / 21.0, 384 28.4 /
+// 24.1 / 22.1.  Ragged ones, of an eighth to all of it: d 64, 4 tokens of 16 heads over 4: T4 =
+// 1024 12.4 / 14.4 / 18.3; 5-13 of 8 over 2: T4 = 1248 15.2 / 15.9 / 17.5, T8 = 1344 19.2 /
+// 17.4 / 19.7; 6-16 of 8: T8 = 1024 18.6 / 16.6 / 18.5, 1536 22.6 / 21.4 / 20.8; d 128, T4 =
+// 384 13.7 / 14.6 / 20.2, T8 = 672 22.8 / 20.5 / 21.6, 1344 31.3 / 28.2 / 27.0.
 int tree_rows(int *path, int B, int T, int H_kv, int group, int max_q, int d, int dtype,
               long long keys, int sms) {
   const long long tiles = (keys + kPagedTile - 1) / kPagedTile;
@@ -127,12 +131,13 @@ int tree_rows(int *path, int B, int T, int H_kv, int group, int max_q, int d, in
   const Units usual = units_of(*path, group, max_q);
   for (const int rows : {4, 8}) {
     const Units u = units_of(kFew, group, max_q, rows);
-    if (u.rows >= usual.rows || (f32 && rows == 8)) continue;
+    if (u.rows >= usual.rows) continue;
     const long long blocks =
         std::min<long long>(T, static_cast<long long>(B) * ((max_q - 1LL) / u.tb + 1));
     const long long work = blocks * H_kv * u.hblocks * tiles;
-    const long long most = d == 64 ? (f32 ? 5 : 4) : (rows == 4 ? 2 : 3);
-    if (work <= most * ctas || (f32 && usual.rows <= 8)) {
+    const long long most =
+        rows == 4 ? (d == 128 ? 2 : (f32 ? 3 : 4)) : (d == 128 && !f32 ? 3 : 4);
+    if (work <= most * ctas) {
       if (*path == kMany) *path = kFew;
       return rows;
     }

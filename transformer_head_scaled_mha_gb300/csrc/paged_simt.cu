@@ -3,10 +3,10 @@
 //
 // A CTA of four warps walks its parts (paged.cuh): R <= 16 query rows of one
 // key/value head against tiles of 128 keys.  Warp w takes keys 32 w .. 32 w + 31
-// of each tile: scores with a key per lane (keys staged in shared memory, rows padded
-// by 16 bytes so that lanes read without conflicts; queries broadcast), an online
+// of each tile: scores with up to 4 keys and 4 rows to a lane (keys staged in shared memory,
+// rows padded by 16 bytes so that lanes read without conflicts), an online
 // softmax with a row per lane, or 32 / R lanes to a row, through a small square of
-// shared memory, then the value rows, each lane owning d / 32 output columns.  Keys and
+// shared memory, then the value rows, up to 8 rows and d / 16 output columns to a lane.  Keys and
 // values are copied to shared memory without registers (cp.async): the next tile's keys
 // while this one's softmax and values are worked on, its values while the next scores
 // are, so a warp always has a tile in flight.  The warps' sums are joined once per part.
@@ -15,15 +15,19 @@
 // own way into the instruction caches; hence one copy loop for both ends of a tile
 // (the walk starts one tile early, with nothing to work on) and rows' places and
 // limits in shared memory, found once.  Measured, with the merge: 8 sequences of 90-700
-// keys, 5 tokens of 8 heads over 2, d 64: 17.5 us (44 with two tiles to a CTA and rows in
-// registers); one token, 16 sequences of 1000-4000 keys, 32 heads over 8, d 128: 69 us,
-// 4.8 TB/s; 4 tokens, 8 such sequences: 69 us, 2.4 TB/s.  Chunks and prompts take it as
+// keys, 5 tokens of 8 heads over 2, d 64: 17.0 us (44 with two tiles to a CTA and rows in
+// registers); one token, 16 sequences of 1000-4000 keys, 32 heads over 8, d 128: 62 us,
+// 5.4 TB/s; 4 tokens, 8 such sequences: 61 us, 2.7 TB/s.  Chunks and prompts take it as
 // well, 16 rows at a time, each of which reads the keys again: 4 x 2048 tokens of 16 heads,
-// d 64: 1391 us, 25 TFLOP/s; d 128: 3075 us, 22 TFLOP/s (0.3 of the CUDA cores' nominal
-// 80); 16 trees of 32 drafted tokens over 1000-2000 keys, 16 heads, d 64: 145 us, 21
-// TFLOP/s.  Bound there by the loads from shared memory (20 wavefronts to 64 FFMA in the
-// score loop) and, at d 128, by one CTA of four warps to an SM.  Small batches of trees come
-// in units of 4 rows: 8 of 5-13 tokens over 90-700 keys, 8 heads over 2, d 64: 15 us (19).
+// d 64: 1111 us, 31 TFLOP/s (1383 with one key and all rows to a lane in the scores and one
+// row of all in the output: a wide load takes 4 cycles to its registers even where all lanes
+// ask for the same); d 128: 2610 us, 26 TFLOP/s (0.3 of the CUDA cores' nominal
+// 80); 16 trees of 32 drafted tokens over 1000-2000 keys, 16 heads, d 64: 120 us, 25
+// TFLOP/s.  Bound there by latencies between two warps to a scheduler (at d 128 one), which
+// shared memory has no room to add to: 0.45 to 0.59 of the issue slots, 0.5 to 0.65 of the
+// loads' wavefronts.  Trees come in units of 4 or 8 rows where there is little work: 8 of 5-13
+// tokens over 90-700 keys, 8 heads over 2, d 64: 15 us (19); and of up to 8 where a tree has
+// no more: 16 of 8 tokens of 8 heads over 6000 keys, d 64: 80 us (105 as 16 rows).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -90,6 +94,39 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// N floats, as wide as they come
+template <int N>
+__device__ __forceinline__ void ld_vec(const float *p, float *x) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(p + i);
+      x[i] = v.x;
+      x[i + 1] = v.y;
+      x[i + 2] = v.z;
+      x[i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const float2 v = *reinterpret_cast<const float2 *>(p);
+    x[0] = v.x;
+    x[1] = v.y;
+  } else {
+    static_assert(N == 1, "widths");
+    x[0] = *p;
+  }
+}
+template <int N>
+__device__ __forceinline__ void st_vec(float *p, const float *x) {
+  if constexpr (N == 4) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+  } else {
+    static_assert(N == 1, "widths");
+    *p = x[0];
+  }
+}
+
 template <int D>
 struct Smem {
   float q[kRows][D];
@@ -107,7 +144,11 @@ struct Smem {
 
 template <int D, int RP, bool kTree>
 __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_constant__ PagedProblem p) {
-  constexpr int kC = D / 32;  // output columns of a lane
+  // A lane's squares: scores of kTR rows and kTK keys (kKg apart), output of kOR rows and kOC
+  // columns (pieces of kOV, kOg lanes side by side).
+  constexpr int kTR = RP == 16 ? 4 : (RP == 1 ? 1 : 2), kTK = RP / kTR, kKg = 32 / kTK;
+  constexpr int kOR = RP <= 4 ? RP : RP / 2, kOC = RP * D / 32 / kOR, kOV = kOC < 4 ? kOC : 4;
+  constexpr int kOg = D / kOC;
   constexpr int kPer = 32 / RP;  // lanes to a row in the softmax
   static_assert(kRows <= kKeys, "a warp's sums fit where its values were");
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -124,6 +165,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
   const float *kc = static_cast<const float *>(p.k), *vc = static_cast<const float *>(p.v);
   float *out = static_cast<float *>(p.out);
   float *kw = &sm.k[warp][0][0], *vw = &sm.v[warp][0][0];
+  const int key_at = lane % kKg, row_at = lane / kKg * kTR;           // of its scores
+  const int col_at = lane % kOg * kOV, orow_at = lane / kOg * kOR;  // of its output
   // copies a warp's 32 cache rows, one per lane's cell, zeros where there is none; 16
   // bytes per lane
   auto copy = [&](const float *cache, float *to, int stride, long long cell) {
@@ -158,11 +201,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
     const int mine = lane % RP, lim = sm.lim[mine];  // this lane's row in the softmax
     const uint32_t *tree = kTree && lim >= 0 ? p.tree + static_cast<size_t>(lim) * p.tree_words : nullptr;
     float m = -INFINITY, l = 0.f;                    // ... its maximum, and its share of the sum
-    float acc[RP][kC];
+    float acc[kOR][kOC];
 #pragma unroll
-    for (int r = 0; r < RP; ++r)
+    for (int r = 0; r < kOR; ++r)
 #pragma unroll
-      for (int c = 0; c < kC; ++c) acc[r][c] = 0.f;
+      for (int c = 0; c < kOC; ++c) acc[r][c] = 0.f;
     __syncthreads();
     long long cell = -1;
 #pragma unroll 1
@@ -177,22 +220,35 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
       if (work) {
         cp_async_wait<1>();  // this tile's keys (its values may be on their way)
         __syncwarp();
-        float s[RP];
+        float s[kTK][kTR];
 #pragma unroll
-        for (int r = 0; r < RP; ++r) s[r] = 0.f;
-#pragma unroll 2
+        for (int x = 0; x < kTK; ++x)
+#pragma unroll
+          for (int r = 0; r < kTR; ++r) s[x][r] = 0.f;
+#pragma unroll 8
         for (int c = 0; c < D; c += 4) {
-          const float4 kv = *reinterpret_cast<const float4 *>(&sm.k[warp][lane][c]);
+          float4 kv[kTK];
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[r][c]);
-            s[r] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[r]))));
+          for (int x = 0; x < kTK; ++x)
+            kv[x] = *reinterpret_cast<const float4 *>(&sm.k[warp][key_at + x * kKg][c]);
+#pragma unroll
+          for (int r = 0; r < kTR; ++r) {
+            const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[row_at + r][c]);
+#pragma unroll
+            for (int x = 0; x < kTK; ++x)
+              s[x][r] = fmaf(qv.x, kv[x].x,
+                             fmaf(qv.y, kv[x].y, fmaf(qv.z, kv[x].z, fmaf(qv.w, kv[x].w, s[x][r]))));
           }
         }
+        const unsigned there = __ballot_sync(0xffffffffu, cell >= 0);
 #pragma unroll
-        for (int r = 0; r < RP; ++r)
-          sm.p[warp][lane][r] =
-              cell >= 0 ? max_nan(s[r] * p.scale_log2, kLowestScore) : -INFINITY;
+        for (int x = 0; x < kTK; ++x) {
+          const int key = key_at + x * kKg;
+#pragma unroll
+          for (int r = 0; r < kTR; ++r)
+            s[x][r] = (there >> key) & 1 ? max_nan(s[x][r] * p.scale_log2, kLowestScore) : -INFINITY;
+          st_vec<kTR>(&sm.p[warp][key][row_at], s[x]);
+        }
         __syncwarp();
       }
       copy(kc, kw, D + 4, next);
@@ -232,22 +288,22 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
         cp_async_wait<1>();  // this tile's values
         __syncwarp();
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          const float shrink = sm.alpha[warp][r];
+        for (int r = 0; r < kOR; ++r) {
+          const float shrink = sm.alpha[warp][orow_at + r];
 #pragma unroll
-          for (int c = 0; c < kC; ++c) acc[r][c] *= shrink;
+          for (int c = 0; c < kOC; ++c) acc[r][c] *= shrink;
         }
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < kKeys; ++j) {
-          float v[kC];
+          float v[kOC], pr[kOR];
 #pragma unroll
-          for (int c = 0; c < kC; ++c) v[c] = sm.v[warp][j][c * 32 + lane];
+          for (int c = 0; c < kOC; c += kOV)
+            ld_vec<kOV>(&sm.v[warp][j][c * kOg + col_at], v + c);
+          ld_vec<kOR>(&sm.p[warp][j][orow_at], pr);
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            const float pr = sm.p[warp][j][r];
+          for (int r = 0; r < kOR; ++r)
 #pragma unroll
-            for (int c = 0; c < kC; ++c) acc[r][c] = fmaf(pr, v[c], acc[r][c]);
-          }
+            for (int c = 0; c < kOC; ++c) acc[r][c] = fmaf(pr[r], v[c], acc[r][c]);
         }
         __syncwarp();
       }
@@ -264,9 +320,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
       sm.l[warp][lane] = l;
     }
 #pragma unroll
-    for (int r = 0; r < RP; ++r)
+    for (int r = 0; r < kOR; ++r)
 #pragma unroll
-      for (int c = 0; c < kC; ++c) vw[r * D + c * 32 + lane] = acc[r][c];
+      for (int c = 0; c < kOC; c += kOV)
+        st_vec<kOV>(vw + (orow_at + r) * D + c * kOg + col_at, &acc[r][c]);
     __syncthreads();
     const bool split = paged_split(part);
     float *slot = split ? paged_slot_ptr(p, D, blockIdx.x, paged_slot(part)) : nullptr;
@@ -513,6 +570,8 @@ cudaError_t simt_rows(const PagedProblem &p, int grid, cudaStream_t stream) {
   const int R = p.hpu * p.tb;
   if (R <= 1) return simt<D, 1>(p, grid, stream);
   if (R <= 4) return simt<D, 4>(p, grid, stream);
+  // (causal rows keep the order of their sums, which differs with the lanes to a row)
+  if (R <= 8 && p.tree != nullptr) return simt_as<D, 8, true>(p, grid, stream);
   return simt<D, 16>(p, grid, stream);
 }
 
