@@ -484,6 +484,6 @@ cudaError_t launch_paged_many(const CUtensorMap &q, const CUtensorMap &k, const 
 cudaError_t launch_paged_simt(const PagedProblem &p, int d, int grid, cudaStream_t stream);
 // joins the parts of split units; `many`: of launch_paged_many
 cudaError_t launch_paged_merge(const PagedProblem &p, int d, int dtype, bool many, int grid,
-                               cudaStream_t stream);
+                               int num_sms, cudaStream_t stream);
 
 }  // namespace mha

@@ -504,7 +504,7 @@ static int attend(const void *q, const void *k_cache, const void *v_cache, void 
   // table has no room for them
   const long long most = static_cast<long long>(max_pages) * page_size;
   if (err == cudaSuccess && most > (2 * u.split.min_part - 1) * kPagedTile)
-    err = launch_paged_merge(p, d, dtype, path == kMany, grid, stream);
+    err = launch_paged_merge(p, d, dtype, path == kMany, grid, sms, stream);
   return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
 

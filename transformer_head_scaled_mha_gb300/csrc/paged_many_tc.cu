@@ -37,9 +37,9 @@
 // thread's two passes over 128 columns (0.85 us), then its two products, which have to
 // wait because P_w lies in S_w's columns.  d = 64 has columns for P of its own, but scores
 // formed before the products then cost more in waits than they gain (215 -> 227 us).  The
-// way to the first tile is 8 us, a part's beginning and end 3, the merge 8.  Up to 32 rows
+// way to the first tile is 8 us, a part's beginning and end 3, the merge 6.  Up to 32 rows
 // (drafts of grouped heads) lie in one warp of a warpgroup, and the others wait for its
-// exponentials: 16 x 8 tokens over 4000 keys, 32 heads over 8, d 128: 65 us, 0.60 of HBM.
+// exponentials: 16 x 8 tokens over 4000 keys, 32 heads over 8, d 128: 63 us, 0.62 of HBM.
 // Trees of drafted tokens (kTree: the row's mask words are looked at in a sequence's last
 // tiles only): 16 of 9-25 tokens behind 1000-4096 keys, 32 heads over 8, d 128: 49 us, 3.5
 // TB/s (6 us to the first tile, then 1.67 a tile, 2 to 3 to a part's output, merge 5); 64 of

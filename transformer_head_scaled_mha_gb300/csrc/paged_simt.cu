@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
 // A unit to join, as its second part's CTA c describes it.
 struct Joined {
   int row0, tokens, h0, heads;
-  int last;  // CTA of its last part
+  int c, last;  // CTAs of its second part and of its last
   // false: CTA c holds no unit's second part.  (Whole warp; the words are loaded at
   // once, for the merge is a chain of loads.)
   __device__ __forceinline__ bool find(const PagedProblem &p, int c, int ctas, int lane) {
@@ -401,6 +401,7 @@ struct Joined {
     int flags = p.meta[static_cast<size_t>(min(c + lane, ctas - 1)) * kPagedMeta + kMetaFlags];
     heads = meta[kMetaHeads];
     static_assert(kMetaFlags == 0 && kMetaRow == 1 && kMetaTokens == 2 && kMetaHead == 3, "int4");
+    this->c = c;
     row0 = own.y;
     tokens = own.z;
     h0 = own.w;
@@ -425,9 +426,9 @@ struct Joined {
 // each takes every eighth part, its lanes d / 32 columns each.  A unit may have as many
 // parts as there are CTAs, and a warp that went through them alone would wait for
 // memory over and over (13 of then 22 us of one token over 8192 keys, d 128; 16 now).
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 8, kMergeThreads = kMergeWarps * 32;
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeWarps * 32)
+__global__ void __launch_bounds__(kMergeThreads)
     paged_merge_kernel(const PagedProblem p, int ctas) {
   constexpr int kC = D / 32;
   __shared__ float sums[kMergeWarps][D];
@@ -482,56 +483,139 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
           o);
 }
 
-// The same for the slots of paged_many_tc_kernel, [d / 4][rows][4] of up to 256 rows and
-// few parts: CTA (c, y) takes rows 32 y + lane, warp w an eighth of the columns, so that
-// a warp reads 512 bytes in a stretch.
+// All units to join of the many-query kernel, found by every CTA of the merge for itself, in
+// blocks of 32 of their rows (the tokens and heads that there are, which lie apart in a slot),
+// dealt out by warps.  (1208 CTAs, each for 32 rows of a slot that may hold a part, came in
+// turns, most of them for nothing, with two parts in flight to a warp: one tree of 16 tokens
+// over 8192 keys, 32 heads over 8, d 128: 32.7 us, 21.3 so; of 64 tokens 37.7, 26.0; 16 of 9-25
+// over 1000-4096 50.0, 48.6.  The few-query kernel's units are more and smaller: 2 us slower so.)
+constexpr int kMergeRowsCtas = 2;  // to an SM
+struct JoinedList {
+  static constexpr int kWords = kMergeWarps;  // CTAs, a bit each
+  static constexpr int kBlocks = 256 / 32;    // 32 rows of a unit, at most
+  Joined unit[kPagedManyMaxCtas];             // by the CTA of its second part
+  uint16_t block[kPagedManyMaxCtas * kBlocks];  // kBlocks times the unit, and which of its blocks
+  uint32_t begins[kWords], ends[kWords];
+  int count[kWords];
+
+  // How many blocks there are.
+  __device__ __forceinline__ int find(const PagedProblem &p, int ctas) {
+    static_assert(kPagedManyMaxCtas <= kMergeThreads, "a CTA to a thread");
+    const int c = threadIdx.x, lane = c & 31, warp = c >> 5;
+    int4 own = make_int4(0, 0, 0, 0);
+    int heads = 0;
+    if (c < ctas) {
+      const int32_t *meta = p.meta + static_cast<size_t>(c) * kPagedMeta;
+      own = *reinterpret_cast<const int4 *>(meta);
+      heads = meta[kMetaHeads];
+    }
+    const unsigned b = __ballot_sync(0xffffffffu, (own.x & kPartBegins) != 0);
+    const unsigned e = __ballot_sync(0xffffffffu, (own.x & kPartEnds) != 0);
+    if (lane == 0) {
+      begins[warp] = b;
+      ends[warp] = e;
+    }
+    __syncthreads();
+    const bool start = c > 0 && (own.x & kPartContinues) != 0 &&
+                       ((begins[(c - 1) >> 5] >> ((c - 1) & 31)) & 1) != 0;
+    const int blocks = start ? min((own.z * heads + 31) / 32, kBlocks) : 0;
+    int at = blocks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += x;
+    }
+    if (lane == 31) count[warp] = at;
+    at -= blocks;
+    if (start) {
+      int word = warp;
+      uint32_t left = ends[word] & (0xffffffffu << lane);
+      while (left == 0 && ++word < kWords) left = ends[word];
+      Joined &u = unit[c];
+      u.row0 = own.y;
+      u.tokens = own.z;
+      u.h0 = own.w;
+      u.heads = heads;
+      u.c = c;
+      u.last = left != 0 ? word * 32 + __ffs(left) - 1 : c;
+    }
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      total += count[w];
+      if (w < warp) at += count[w];
+    }
+    for (int x = 0; x < blocks; ++x) block[at + x] = static_cast<uint16_t>(c * kBlocks + x);
+    __syncthreads();
+    return total;
+  }
+};
+
+// The same for the slots of paged_many_tc_kernel, [d / 4][rows][4] of up to 256 rows: a warp
+// takes 32 of a unit's rows, one to a lane, and kC4 fours of columns, so that it reads 512
+// bytes in a stretch, kDeep parts at once.
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32)
+__global__ void __launch_bounds__(kMergeThreads)
     paged_merge_rows_kernel(const PagedProblem p, int ctas) {
-  constexpr int kC4 = D / 4 / kMergeWarps;  // fours of columns of a thread
+  constexpr int kC4 = 4, kPieces = D / 4 / kC4, kDeep = 4;
+  __shared__ JoinedList list;
   griddep_launch_dependents();
   griddep_wait();
-  const int c = blockIdx.x + 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Joined u;
-  if (!u.find(p, c, ctas, lane)) return;
-  const int r = blockIdx.y * 32 + lane, h = r / p.tb, i = r - h * p.tb;
-  if (r >= p.rows || h >= u.heads || i >= u.tokens) return;
-  float o[kC4][4], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < kC4; ++e)
-#pragma unroll
-    for (int x = 0; x < 4; ++x) o[e][x] = 0.f;
-#pragma unroll 2
-  for (int k = c - 1; k <= u.last; ++k) {
-    const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
-    float part[kC4][4];
-#pragma unroll
-    for (int e = 0; e < kC4; ++e)
-      ld_cols(slot + (static_cast<size_t>(warp * kC4 + e) * p.rows + r) * 4, part[e]);
-    const float2 ml = *reinterpret_cast<const float2 *>(slot + static_cast<size_t>(p.rows) * D + 2 * r);
-    const float mn = fmaxf(m, ml.x), use = mn == -INFINITY ? 0.f : mn;
-    const float older = ex2_approx(m - use), f = ex2_approx(ml.x - use);
-    m = mn;
-    l = fmaf(l, older, ml.y * f);
+  const int tasks = list.find(p, ctas) * kPieces;
+  // (neighbours in different CTAs)
+  for (int task = warp * gridDim.x + blockIdx.x; task < tasks; task += kMergeWarps * gridDim.x) {
+    const int block = list.block[task / kPieces], piece = task % kPieces;
+    const Joined &u = list.unit[block / JoinedList::kBlocks];
+    const int row = block % JoinedList::kBlocks * 32 + lane, h = row / u.tokens, i = row - h * u.tokens;
+    if (h >= u.heads) continue;
+    const int c = u.c, last = u.last, r = h * p.tb + i;  // row in a slot
+    float o[kC4][4], m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int e = 0; e < kC4; ++e)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) o[e][x] = fmaf(o[e][x], older, part[e][x] * f);
-  }
-  __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.out) +
-                      (static_cast<long long>(u.row0 + i) * p.H + u.h0 + h) * D + warp * kC4 * 4;
-  if (m == kLowestScore) l = NAN;
-  const float inv = 1.f / l;
+      for (int x = 0; x < 4; ++x) o[e][x] = 0.f;
+    for (int k0 = c - 1; k0 <= last; k0 += kDeep) {
+      float part[kDeep][kC4][4];
+      float2 ml[kDeep];
 #pragma unroll
-  for (int e = 0; e < kC4; e += 2) {
-    uint32_t v[4];
+      for (int j = 0; j < kDeep; ++j) {
+        const int k = k0 + j;
+        if (k > last) break;
+        const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
+        ml[j] = *reinterpret_cast<const float2 *>(slot + static_cast<size_t>(p.rows) * D + 2 * r);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const float a = o[e + x / 2][2 * (x % 2)], b = o[e + x / 2][2 * (x % 2) + 1];
-      v[x] = l == 0.f ? 0u : pack_bf16x2(a * inv, b * inv);
+        for (int e = 0; e < kC4; ++e)
+          ld_cols(slot + (static_cast<size_t>(piece * kC4 + e) * p.rows + r) * 4, part[j][e]);
+      }
+#pragma unroll
+      for (int j = 0; j < kDeep; ++j) {
+        if (k0 + j > last) break;
+        const float mn = fmaxf(m, ml[j].x), use = mn == -INFINITY ? 0.f : mn;
+        const float older = ex2_approx(m - use), f = ex2_approx(ml[j].x - use);
+        m = mn;
+        l = fmaf(l, older, ml[j].y * f);
+#pragma unroll
+        for (int e = 0; e < kC4; ++e)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[e][x] = fmaf(o[e][x], older, part[j][e][x] * f);
+      }
     }
-    st_global_v4(to + e * 4, make_uint4(v[0], v[1], v[2], v[3]));
+    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.out) +
+                        (static_cast<long long>(u.row0 + i) * p.H + u.h0 + h) * D + piece * kC4 * 4;
+    if (m == kLowestScore) l = NAN;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int e = 0; e < kC4; e += 2) {
+      uint32_t v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float a = o[e + x / 2][2 * (x % 2)], b = o[e + x / 2][2 * (x % 2) + 1];
+        v[x] = l == 0.f ? 0u : pack_bf16x2(a * inv, b * inv);
+      }
+      st_global_v4(to + e * 4, make_uint4(v[0], v[1], v[2], v[3]));
+    }
   }
 }
 
@@ -586,22 +670,24 @@ namespace {
 
 template <typename T, int D>
 cudaError_t merge(const PagedProblem &p, int grid, cudaStream_t stream) {
-  return launch(paged_merge_kernel<T, D>, dim3(grid - 1, p.rows), kMergeWarps * 32, 0, stream, p,
-                grid);
+  return launch(paged_merge_kernel<T, D>, dim3(grid - 1, p.rows), kMergeThreads, 0, stream, p, grid);
 }
 
 template <int D>
-cudaError_t merge_rows(const PagedProblem &p, int grid, cudaStream_t stream) {
-  return launch(paged_merge_rows_kernel<D>, dim3(grid - 1, (p.rows + 31) / 32), kMergeWarps * 32, 0,
-                stream, p, grid);
+cudaError_t merge_rows(const PagedProblem &p, int grid, int num_sms, cudaStream_t stream) {
+  if (grid > kPagedManyMaxCtas) return cudaErrorInvalidValue;
+  return launch(paged_merge_rows_kernel<D>, dim3(kMergeRowsCtas * num_sms), kMergeThreads, 0, stream,
+                p, grid);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_merge(const PagedProblem &p, int d, int dtype, bool many, int grid,
-                               cudaStream_t stream) {
+                               int num_sms, cudaStream_t stream) {
   if (grid < 2) return cudaSuccess;
-  if (many) return d == 64 ? merge_rows<64>(p, grid, stream) : merge_rows<128>(p, grid, stream);
+  if (many)
+    return d == 64 ? merge_rows<64>(p, grid, num_sms, stream)
+                   : merge_rows<128>(p, grid, num_sms, stream);
   if (dtype == 0)
     return d == 64 ? merge<float, 64>(p, grid, stream) : merge<float, 128>(p, grid, stream);
   return d == 64 ? merge<__nv_bfloat16, 64>(p, grid, stream)
