@@ -426,61 +426,94 @@ struct Joined {
 // each takes every eighth part, its lanes d / 32 columns each.  A unit may have as many
 // parts as there are CTAs, and a warp that went through them alone would wait for
 // memory over and over (13 of then 22 us of one token over 8192 keys, d 128; 16 now).
+// With more than 8 rows kSide rows to a CTA: the CTAs, most of which have nothing to do, come in
+// fewer turns (16 rows, 32 sequences of 500-2000, d 64: 37.9 -> 36.5 us; 8 rows: 24.6, 24.7; 4
+// rows 15.0, 15.2).
 constexpr int kMergeWarps = 8, kMergeThreads = kMergeWarps * 32;
-template <typename T, int D>
+template <typename T, int D, int kSide>
 __global__ void __launch_bounds__(kMergeThreads)
     paged_merge_kernel(const PagedProblem p, int ctas) {
   constexpr int kC = D / 32;
-  __shared__ float sums[kMergeWarps][D];
+  __shared__ float sums[kSide][kMergeWarps][D];
   griddep_launch_dependents();
   griddep_wait();
   const int c = blockIdx.x + 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Joined u;
   if (!u.find(p, c, ctas, lane)) return;
-  const int r = blockIdx.y, h = r / p.tb, i = r - h * p.tb;
-  if (h >= u.heads || i >= u.tokens) return;
-  float o[kC], m = -INFINITY, l = 0.f;
+  float o[kSide][kC], m[kSide], l[kSide], use[kSide];
+  int at[kSide];  // row in a slot
+  T *to[kSide];   // nullptr: no row
 #pragma unroll
-  for (int e = 0; e < kC; ++e) o[e] = 0.f;
-  const size_t ml = static_cast<size_t>(p.rows) * D + 2 * r;  // (max, sum) in a slot
-  for (int k = c - 1 + lane; k <= u.last; k += 32) {
-    const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
-    const float mk = slot[ml], lk = slot[ml + 1];
-    const float mn = fmaxf(m, mk), to = mn == -INFINITY ? 0.f : mn;
-    l = l * ex2_approx(m - to) + lk * ex2_approx(mk - to);
-    m = mn;
+  for (int s = 0; s < kSide; ++s) {
+    const int r = blockIdx.y * kSide + s, h = r / p.tb, i = r - h * p.tb;
+    const bool there = r < p.rows && h < u.heads && i < u.tokens;
+    at[s] = there ? r : 0;
+    to[s] = there ? static_cast<T *>(p.out) +
+                        (static_cast<long long>(u.row0 + i) * p.H + u.h0 + h) * D + lane * kC
+                  : nullptr;
+    m[s] = -INFINITY;
+    l[s] = 0.f;
+#pragma unroll
+    for (int e = 0; e < kC; ++e) o[s][e] = 0.f;
   }
-  const float top = warp_max(m), use = top == -INFINITY ? 0.f : top;
-  l = warp_sum(l * ex2_approx(m - use));
-  if (top == kLowestScore) l = NAN;
-#pragma unroll 4
+  const size_t sums_at = static_cast<size_t>(p.rows) * D;  // (max, sum) of rows in a slot
+  for (int k = c - 1 + lane; k <= u.last; k += 32) {
+    const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0) + sums_at;
+    float2 part[kSide];
+#pragma unroll
+    for (int s = 0; s < kSide; ++s) part[s] = *reinterpret_cast<const float2 *>(slot + 2 * at[s]);
+#pragma unroll
+    for (int s = 0; s < kSide; ++s) {
+      const float mn = fmaxf(m[s], part[s].x), be = mn == -INFINITY ? 0.f : mn;
+      l[s] = l[s] * ex2_approx(m[s] - be) + part[s].y * ex2_approx(part[s].x - be);
+      m[s] = mn;
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < kSide; ++s) {
+    const float top = warp_max(m[s]);
+    use[s] = top == -INFINITY ? 0.f : top;
+    l[s] = warp_sum(l[s] * ex2_approx(m[s] - use[s]));
+    if (top == kLowestScore) l[s] = NAN;
+  }
+#pragma unroll 2
   for (int k = c - 1 + warp; k <= u.last; k += kMergeWarps) {
     const float *slot = paged_slot_ptr(p, D, k, k < c ? 1 : 0);
-    const float f = ex2_approx(slot[ml] - use);
-    float part[kC];  // this lane's kC columns
-    ld_cols(slot + static_cast<size_t>(r) * D + lane * kC, part);
+    float part[kSide][kC], top[kSide];  // this lane's kC columns
 #pragma unroll
-    for (int e = 0; e < kC; ++e) o[e] = fmaf(part[e], f, o[e]);
+    for (int s = 0; s < kSide; ++s) {
+      top[s] = slot[sums_at + 2 * at[s]];
+      ld_cols(slot + static_cast<size_t>(at[s]) * D + lane * kC, part[s]);
+    }
+#pragma unroll
+    for (int s = 0; s < kSide; ++s) {
+      const float f = ex2_approx(top[s] - use[s]);
+#pragma unroll
+      for (int e = 0; e < kC; ++e) o[s][e] = fmaf(part[s][e], f, o[s][e]);
+    }
   }
-  st_cols(&sums[warp][lane * kC], o);
+#pragma unroll
+  for (int s = 0; s < kSide; ++s) st_cols(&sums[s][warp][lane * kC], o[s]);
   __syncthreads();
-  if (warp != 0) return;
 #pragma unroll
-  for (int e = 0; e < kC; ++e) o[e] = 0.f;
+  for (int s = 0; s < kSide; ++s) {  // a warp to a row
+    if (warp != s || to[s] == nullptr) continue;
+    float x[kC];
 #pragma unroll
-  for (int g = 0; g < kMergeWarps; ++g) {
-    float part[kC];
-    ld_cols(&sums[g][lane * kC], part);
+    for (int e = 0; e < kC; ++e) x[e] = 0.f;
 #pragma unroll
-    for (int e = 0; e < kC; ++e) o[e] += part[e];
+    for (int g = 0; g < kMergeWarps; ++g) {
+      float part[kC];
+      ld_cols(&sums[s][g][lane * kC], part);
+#pragma unroll
+      for (int e = 0; e < kC; ++e) x[e] += part[e];
+    }
+    const float inv = 1.f / l[s];
+#pragma unroll
+    for (int e = 0; e < kC; ++e) x[e] = l[s] == 0.f ? 0.f : x[e] * inv;
+    st_cols(to[s], x);
   }
-  const float inv = 1.f / l;
-#pragma unroll
-  for (int e = 0; e < kC; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-  st_cols(static_cast<T *>(p.out) + (static_cast<long long>(u.row0 + i) * p.H + u.h0 + h) * D +
-              lane * kC,
-          o);
 }
 
 // All units to join of the many-query kernel, found by every CTA of the merge for itself, in
@@ -670,7 +703,11 @@ namespace {
 
 template <typename T, int D>
 cudaError_t merge(const PagedProblem &p, int grid, cudaStream_t stream) {
-  return launch(paged_merge_kernel<T, D>, dim3(grid - 1, p.rows), kMergeThreads, 0, stream, p, grid);
+  if (p.rows <= 8)
+    return launch(paged_merge_kernel<T, D, 1>, dim3(grid - 1, p.rows), kMergeThreads, 0, stream, p,
+                  grid);
+  return launch(paged_merge_kernel<T, D, 2>, dim3(grid - 1, (p.rows + 1) / 2), kMergeThreads, 0, stream,
+                p, grid);
 }
 
 template <int D>
