@@ -6,8 +6,9 @@
 // (count, list, tables, row).  Measured, in captured graphs: the accepted paths (up to 9
 // tokens) of 64 trees, 16 layers, 8 heads, d 128: 6.8 us (29 MB moved: 0.63 of a copy's
 // rate); 8 sequences of 4096-8192 shortened to three quarters, 4 layers, into other pages:
-// 204 us (0.88; 329 with a round's places found behind one another and one turn of CTAs), in
-// place 214; one such sequence, one layer: 17, in place 55 (its rounds follow one another);
+// 187 us (0.96; 204 with the lists' entries looked at one behind another, 329 with a round's
+// places too and one turn of CTAs), in place 214; one such sequence, one layer: 14, in place 26
+// (its rounds follow one another);
 // 128 pages of 128 KB copied in 16 layers: 165 us (0.96).
 #include <cuda_runtime.h>
 
@@ -116,14 +117,16 @@ __global__ void __launch_bounds__(kShortWarps * 32) compact_short_kernel(const C
 }
 
 // Longer lists: a CTA per sequence, head, layer and tensor (and, where nothing that is
-// written is read, stretch of the list), rounds as above.  A round's rows are found, one to
-// a thread, while those of the round before are on their way.
+// written is read, stretch of the list), rounds as above.  A round's rows are found while
+// those of the round before are on their way.  A CTA may take kPart of a row's kCols columns
+// of 16 bytes: its rounds are that much longer, and fewer.
 constexpr int kLongThreads = 256, kLongCtas = 4;  // CTAs per SM
-template <int kCols>
+template <int kCols, int kPart>
 __global__ void __launch_bounds__(kLongThreads, kLongCtas)
     compact_long_kernel(const CompactArgs a, int stretches) {
-  constexpr int kRows = kLongThreads / kCols, kDeep = 8, kRound = kRows * kDeep;
-  static_assert(kRound <= kLongThreads, "a row to a thread");
+  constexpr int kRows = kLongThreads / kPart, kDeep = 8, kRound = kRows * kDeep;
+  constexpr int kFind = (kRound + kLongThreads - 1) / kLongThreads;  // rows that a thread finds
+  static_assert(kCols % kPart == 0, "whole parts");
   // of this round, the next one, and the one before, whose rows may still be on their way out
   __shared__ Move moves[3][kRound];
   __shared__ int stop;
@@ -133,37 +136,57 @@ __global__ void __launch_bounds__(kLongThreads, kLongCtas)
   long long unit = blockIdx.x;
   const int stretch = static_cast<int>(unit % stretches);
   unit /= stretches;
+  const int part = static_cast<int>(unit % (kCols / kPart));
+  unit /= kCols / kPart;
   const int head = static_cast<int>(unit % heads);
   unit /= heads;
   const int item = static_cast<int>(unit % items), b = static_cast<int>(unit / items);
   const List l(a, b);
   if (threadIdx.x == 0) stop = l.count;
   __syncthreads();
-  for (int i = threadIdx.x; i < l.count; i += kLongThreads)
-    if (!compact_stands(i > 0 ? l.keep[i - 1] : -1, l.keep[i], l.start, l.len)) {
-      atomicMin(&stop, i);
-      break;
+  constexpr int kScan = 8;  // entries in flight
+  for (int i0 = threadIdx.x; i0 < l.count; i0 += kScan * kLongThreads) {
+    int here[kScan], before[kScan];
+#pragma unroll
+    for (int s = 0; s < kScan; ++s) {
+      const int i = i0 + s * kLongThreads;
+      here[s] = i < l.count ? l.keep[i] : 0;
+      before[s] = i > 0 && i < l.count ? l.keep[i - 1] : -1;
     }
+#pragma unroll
+    for (int s = 0; s < kScan; ++s) {
+      const int i = i0 + s * kLongThreads;
+      if (i < l.count && !compact_stands(before[s], here[s], l.start, l.len)) atomicMin(&stop, i);
+    }
+  }
   __syncthreads();
   const int n = stop;
-  if (head == 0 && item == 0 && stretch == 0 && threadIdx.x == 0) a.lens_out[b] = l.start + n;
+  if (head == 0 && item == 0 && stretch == 0 && part == 0 && threadIdx.x == 0) a.lens_out[b] = l.start + n;
   if (a.Hkv == 0 || a.layers == 0) return;
   uint8_t *cache = (item & 1 ? a.v : a.k) + (item >> 1) * a.layer_bytes +
-                   (threadIdx.x % kCols) * 16;
-  const int mine = threadIdx.x / kCols, step = stretches * kRound;
-  const int my_row = static_cast<int>(threadIdx.x);
-  // entry of the list that this thread looks up, of the round at r0 (-1: none)
-  auto entry = [&](int r0) {
-    return my_row < kRound && r0 + my_row < n ? l.keep[r0 + my_row] : -1;
+                   (part * kPart + threadIdx.x % kPart) * 16;
+  const int mine = threadIdx.x / kPart, step = stretches * kRound;
+  // entries of the list that this thread looks up, of the round at r0 (-1: none)
+  auto entries = [&](int r0, int (&k)[kFind]) {
+#pragma unroll
+    for (int f = 0; f < kFind; ++f) {
+      const int row = f * kLongThreads + static_cast<int>(threadIdx.x);
+      k[f] = row < kRound && r0 + row < n ? l.keep[r0 + row] : -1;
+    }
   };
-  auto find = [&](Move *to, int r0, int k) {
-    if (my_row >= kRound) return;
-    to[my_row].src = -1;
-    if (k >= 0) to[my_row] = move_of(a, l, b, head, r0 + my_row, k);
+  auto find = [&](Move *to, int r0, const int (&k)[kFind]) {
+#pragma unroll
+    for (int f = 0; f < kFind; ++f) {
+      const int row = f * kLongThreads + static_cast<int>(threadIdx.x);
+      if (row >= kRound) break;
+      to[row].src = -1;
+      if (k[f] >= 0) to[row] = move_of(a, l, b, head, r0 + row, k[f]);
+    }
   };
-  int r0 = stretch * kRound, k = entry(r0), buffer = 0;
+  int r0 = stretch * kRound, k[kFind], buffer = 0;
+  entries(r0, k);
   find(moves[0], r0, k);
-  k = entry(r0 + step);
+  entries(r0 + step, k);
   __syncthreads();
   for (; r0 < n; r0 += step) {
     const int behind = buffer == 2 ? 0 : buffer + 1;
@@ -172,9 +195,11 @@ __global__ void __launch_bounds__(kLongThreads, kLongCtas)
 #pragma unroll
     for (int u = 0; u < kDeep; ++u)
       if (m[u * kRows].src >= 0) x[u] = ld16(cache + m[u * kRows].src * (kCols * 16));
-    const int next = entry(r0 + 2 * step);
+    int next[kFind];
+    entries(r0 + 2 * step, next);
     find(moves[behind], r0 + step, k);
-    k = next;
+#pragma unroll
+    for (int f = 0; f < kFind; ++f) k[f] = next[f];
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kDeep; ++u)
@@ -261,13 +286,21 @@ cudaError_t compact(const CompactArgs &a, bool in_place, int num_sms, cudaStream
                          kShortWarps * 32, 0, 1, stream, a);
   }
   const long long all = units * 2 * std::max(a.layers, 1);
+  // In place the rounds of a CTA follow one another, and few CTAs leave SMs idle: parts of 64
+  // bytes of a row to each while the CTAs all run at once.  One sequence of 8192, 8 heads: d 128
+  // bf16 60 -> 29 us, fp32 115 -> 45; 8 of 4096: 54 -> 45; 8 of 4096-8192, 4 layers: 213 -> 219.
+  constexpr int kPart = 4;
+  if (in_place && all * (kCols / kPart) <= 1LL * kLongCtas * num_sms)
+    return launch_behind(compact_long_kernel<kCols, kPart>,
+                         dim3(static_cast<unsigned>(all * (kCols / kPart))), kLongThreads, 0, 1,
+                         stream, a, 1);
   constexpr int kRound = kLongThreads / kCols * 8;
   const int rounds = (a.max_keep + kRound - 1) / kRound;
   // enough CTAs for several turns of all SMs, so that the last one leaves little idle
   const int stretches = in_place ? 1
                                  : static_cast<int>(std::max(
                                        1LL, std::min<long long>(rounds, 8LL * kLongCtas * num_sms / all)));
-  return launch_behind(compact_long_kernel<kCols>, dim3(static_cast<unsigned>(all * stretches)),
+  return launch_behind(compact_long_kernel<kCols, kCols>, dim3(static_cast<unsigned>(all * stretches)),
                        kLongThreads, 0, 1, stream, a, stretches);
 }
 
