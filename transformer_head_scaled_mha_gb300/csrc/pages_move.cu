@@ -4,7 +4,7 @@
 //
 // Bound: HBM, twice the moved bytes; for few tokens the chain of loads that finds them
 // (count, list, tables, row).  Measured, in captured graphs: the accepted paths (up to 9
-// tokens) of 64 trees, 16 layers, 8 heads, d 128: 6.8 us (29 MB moved: 0.63 of a copy's
+// tokens) of 64 trees, 16 layers, 8 heads, d 128: 6.6 us (29 MB moved: 0.65 of a copy's
 // rate); 8 sequences of 4096-8192 shortened to three quarters, 4 layers, into other pages:
 // 187 us (0.96; 204 with the lists' entries looked at one behind another, 329 with a round's
 // places too and one turn of CTAs), in place 214; one such sequence, one layer: 14, in place 26
@@ -75,7 +75,8 @@ __global__ void __launch_bounds__(kShortWarps * 32) compact_short_kernel(const C
   const int b = static_cast<int>(unit / heads), head = static_cast<int>(unit % heads);
   if (b >= a.from.B) return;
   const List l(a, b);
-  const int k = lane < l.count ? l.keep[lane] : -1;
+  // (asked for beside the count)
+  const int listed = lane < a.max_keep ? l.keep[lane] : -1, k = lane < l.count ? listed : -1;
   const int before = __shfl_up_sync(0xffffffffu, k, 1);
   const unsigned stands = __ballot_sync(
       0xffffffffu, lane < l.count && compact_stands(lane > 0 ? before : -1, k, l.start, l.len));
