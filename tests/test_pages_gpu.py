@@ -425,6 +425,28 @@ def test_thousands_of_sequences_and_none(most):
     assert np.array_equal(bits_of(kc), want[0])
 
 
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 128)])
+@pytest.mark.parametrize("B", [3, 90])
+def test_long_lists_in_place(dt, d, B):
+    """Few sequences, whose rows are split over CTAs, and so many that they are not; some
+    rounds to a list."""
+    import torch
+    import transformer_head_scaled_mha_gb300 as mha
+    rng = np.random.default_rng(B + d)
+    Hkv, page, width = 5, 32, 45
+    table = rng.permutation(B * width).reshape(B, width).astype(np.int32)
+    lens = rng.integers(width * page // 2, width * page + 1, B).astype(np.int32)
+    starts = np.where(rng.random(B) < 0.5, 0, rng.integers(0, 400, B)).astype(np.int32)
+    keep, counts = lists(rng, B, width * page, lens, starts, False)
+    start, (kc, vc) = caches(rng, (1, B * width, page, Hkv, d), dt)
+    got = mha.mha_paged_compact(kc, vc, up(keep), up(counts), starts=up(starts), kv_lengths=up(lens),
+                                block_table=up(table), layout="bshd")
+    want, length = pages_ref.compact(start, keep, counts, starts, lens, table, table, page, "bshd")
+    torch.cuda.synchronize()
+    assert np.array_equal(down(got), length)
+    assert np.array_equal(bits_of(kc), want[0]) and np.array_equal(bits_of(vc), want[1])
+
+
 # ---------------------------------------------------------------------------
 # a run of them together
 # ---------------------------------------------------------------------------
