@@ -7,6 +7,8 @@ library against the shared CUDA runtime (the one PyTorch already loaded).
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -18,8 +20,18 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmha.so")
-# of this interpreter's kind alone: another one does not find it, and does without
-BINDING = os.path.join(BUILD, "_mha_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+def _torch_version() -> str:
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return "unknown"
+
+
+# of this PyTorch and interpreter alone: others do not find it, and do without
+BINDING = os.path.join(BUILD, "_mha_binding.torch-%s%s" % (
+    _torch_version(), sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["mha_api.cu", "attn_f32_simt.cu", "attn_short_tc.cu", "attn_long_tc.cu", "attn_decode_tc.cu",
@@ -54,7 +66,7 @@ def build_binding(verbose: bool = False) -> bool:
     not possible: the binding then makes its checks and calls in Python."""
     spec = importlib.util.find_spec("torch")
     cxx = shutil.which(os.environ.get("CXX", "g++"))
-    if os.path.exists(BINDING):
+    with contextlib.suppress(FileNotFoundError):
         os.remove(BINDING)
     if spec is None or not spec.submodule_search_locations or cxx is None:
         return False
