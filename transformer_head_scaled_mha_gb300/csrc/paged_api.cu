@@ -98,7 +98,7 @@ Units units_of(int path, int group, int max_q, int rows = 0) {
   u.hblocks = (group + u.hpu - 1) / u.hpu;
   u.tb = path == kMany ? 2 * (rows / u.hpu) : std::min(rows / u.hpu, max_q);
   u.rows = u.hpu * u.tb;
-  u.ctas = path == kMany ? kPagedManyMaxCtas : kPagedMaxCtas;
+  u.ctas = path == kMany ? kPagedManyMaxCtas : (rows > 16 ? kPagedMaxCtas / 2 : kPagedMaxCtas);
   u.split = path == kMany ? kSplitMany : (path == kFew ? kSplitFew : kSplitSimt);
   return u;
 }
@@ -123,24 +123,38 @@ Units units_of(int path, int group, int max_q, int rows = 0) {
 // 1024 12.4 / 14.4 / 18.3; 5-13 of 8 over 2: T4 = 1248 15.2 / 15.9 / 17.5, T8 = 1344 19.2 /
 // 17.4 / 19.7; 6-16 of 8: T8 = 1024 18.6 / 16.6 / 18.5, 1536 22.6 / 21.4 / 20.8; d 128, T4 =
 // 384 13.7 / 14.6 / 20.2, T8 = 672 22.8 / 20.5 / 21.6, 1344 31.3 / 28.2 / 27.0.
+//
+// Large fp32 trees at d 128 take 32 rows to a unit, where that makes for fewer units of the
+// mean tree.  16 / 32 rows, by T32: 8 of 32 tokens of 8 heads, 1000 keys, 512: 59.0 / 50.3 us;
+// 64 of 500 keys, 2560: 196 / 151; 13 tokens of 8 heads over 2, 256: 33.5 / 28.7, ragged 384
+// 27.3 / 28.9; 32 tokens, ragged, 192: 26.7 / 28.1; 8-20 tokens of 8 heads (one unit either
+// way), 4096: 123 / 157.
 int tree_rows(int *path, int B, int T, int H_kv, int group, int max_q, int d, int dtype,
               long long keys, int sms) {
   const long long tiles = (keys + kPagedTile - 1) / kPagedTile;
   const bool f32 = dtype == MHA_DTYPE_F32;
   const long long ctas = (d == 64 ? 2LL : 1LL) * sms;
+  const auto work = [&](const Units &u) {
+    const long long blocks =
+        std::min<long long>(T, static_cast<long long>(B) * ((max_q - 1LL) / u.tb + 1));
+    return blocks * H_kv * u.hblocks * tiles;
+  };
   const Units usual = units_of(*path, group, max_q);
   for (const int rows : {4, 8}) {
     const Units u = units_of(kFew, group, max_q, rows);
     if (u.rows >= usual.rows) continue;
-    const long long blocks =
-        std::min<long long>(T, static_cast<long long>(B) * ((max_q - 1LL) / u.tb + 1));
-    const long long work = blocks * H_kv * u.hblocks * tiles;
     const long long most =
         rows == 4 ? (d == 128 ? 2 : (f32 ? 3 : 4)) : (d == 128 && !f32 ? 3 : 4);
-    if (work <= most * ctas) {
+    if (work(u) <= most * ctas) {
       if (*path == kMany) *path = kFew;
       return rows;
     }
+  }
+  if (f32 && d == 128) {
+    const Units u = units_of(*path, group, max_q, 32);
+    const long long mean = (T - 1LL) / B + 1;  // tokens of a sequence
+    const auto units = [&](const Units &x) { return ((mean - 1) / x.tb + 1) * x.hblocks; };
+    if (3 * units(u) <= 2 * units(usual) && 2 * work(u) > 3 * ctas) return 32;
   }
   return 0;
 }

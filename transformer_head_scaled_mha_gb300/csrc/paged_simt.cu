@@ -25,7 +25,10 @@
 // 80); 16 trees of 32 drafted tokens over 1000-2000 keys, 16 heads, d 64: 120 us, 25
 // TFLOP/s.  Bound there by latencies between two warps to a scheduler (at d 128 one), which
 // shared memory has no room to add to: 0.45 to 0.59 of the issue slots, 0.5 to 0.65 of the
-// loads' wavefronts.  Trees come in units of 4 or 8 rows where there is little work: 8 of 5-13
+// loads' wavefronts.  Hence units of 32 rows for larger trees at d 128, whose second 16 have
+// four warps of their own over the same keys: 16 trees of 150 tokens of 12 heads over 4, 300
+// keys: 282 us, 211 so (d 64, where the registers no longer suffice: 122, 116, and smaller
+// ones slower).  Trees come in units of 4 or 8 rows where there is little work: 8 of 5-13
 // tokens over 90-700 keys, 8 heads over 2, d 64: 15 us (19); and of up to 8 where a tree has
 // no more: 16 of 8 tokens of 8 heads over 6000 keys, d 64: 80 us (105 as 16 rows).
 #include <cuda_bf16.h>
@@ -127,36 +130,41 @@ __device__ __forceinline__ void st_vec(float *p, const float *x) {
   }
 }
 
-template <int D>
+template <int D, int kSets>
 struct Smem {
-  float q[kRows][D];
+  float q[kSets * kRows][D];
   float k[kWarps][kKeys][D + 4];
-  float v[kWarps][kKeys][D];          // at a part's end the warps' sums
-  float p[kWarps][kKeys][kRows + 4];  // scores, then their powers
-  float alpha[kWarps][kRows];         // what the older sums shrink to
-  float m[kWarps][kRows], l[kWarps][kRows];
-  float f[kWarps][kRows], total[kRows];  // the warps' weights when joined, and the sum
-  long long row[kRows];                  // where a row's query and output begin (-1: no row)
-  int lim[kRows];                        // keys below this are allowed (of a tree: the row's
-                                         // token, -1: no row)
+  float v[kWarps][kKeys][D];                  // at a part's end the warps' sums
+  float p[kSets * kWarps][kKeys][kRows + 4];  // scores, then their powers
+  float alpha[kSets * kWarps][kRows];         // what the older sums shrink to
+  float m[kSets * kWarps][kRows], l[kSets * kWarps][kRows];
+  float f[kSets * kWarps][kRows], total[kSets * kRows];  // the warps' weights when joined, the sum
+  long long row[kSets * kRows];  // where a row's query and output begin (-1: no row)
+  int lim[kSets * kRows];        // keys below this are allowed (of a tree: the row's token, -1:
+                                 // no row)
   long long scratch[40];
 };
 
-template <int D, int RP, bool kTree>
-__global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_constant__ PagedProblem p) {
+// kSets: of RP rows, each with four warps of its own over the same keys and values.
+template <int D, int RP, bool kTree, int kSets>
+__global__ void __launch_bounds__(kSets * kThreads, kSets == 1 ? 2 : 1)
+    paged_simt_kernel(const __grid_constant__ PagedProblem p) {
   // A lane's squares: scores of kTR rows and kTK keys (kKg apart), output of kOR rows and kOC
   // columns (pieces of kOV, kOg lanes side by side).
   constexpr int kTR = RP == 16 ? 4 : (RP == 1 ? 1 : 2), kTK = RP / kTR, kKg = 32 / kTK;
   constexpr int kOR = RP <= 4 ? RP : RP / 2, kOC = RP * D / 32 / kOR, kOV = kOC < 4 ? kOC : 4;
   constexpr int kOg = D / kOC;
   constexpr int kPer = 32 / RP;  // lanes to a row in the softmax
-  static_assert(kRows <= kKeys, "a warp's sums fit where its values were");
+  constexpr int kAll = kSets * RP;  // rows of a unit
+  static_assert(kSets * kRows <= kKeys && (kSets == 1 || RP == kRows),
+                "the warps' sums fit where their values were");
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+  Smem<D, kSets> &sm = *reinterpret_cast<Smem<D, kSets> *>(smem_raw);
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const PagedSpan span = paged_span<kThreads>(p, blockIdx.x, gridDim.x, sm.scratch);
+  const int slice = warp % kWarps, set = warp / kWarps;  // whose keys, whose rows
+  const PagedSpan span = paged_span<kSets * kThreads>(p, blockIdx.x, gridDim.x, sm.scratch);
   PagedWalk walk;
   walk.begin(p, span);
   PagedPart part;
@@ -164,17 +172,25 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
   const float *q = static_cast<const float *>(p.q);
   const float *kc = static_cast<const float *>(p.k), *vc = static_cast<const float *>(p.v);
   float *out = static_cast<float *>(p.out);
-  float *kw = &sm.k[warp][0][0], *vw = &sm.v[warp][0][0];
+  float *kw = &sm.k[slice][0][0], *vw = &sm.v[slice][0][0];
   const int key_at = lane % kKg, row_at = lane / kKg * kTR;           // of its scores
   const int col_at = lane % kOg * kOV, orow_at = lane / kOg * kOR;  // of its output
-  // copies a warp's 32 cache rows, one per lane's cell, zeros where there is none; 16
-  // bytes per lane
+  // the warps of a slice wait for one another
+  auto slice_sync = [&]() {
+    if constexpr (kSets == 1) {
+      __syncwarp();
+    } else {
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + slice), "n"(kSets * 32) : "memory");
+    }
+  };
+  // copies the slice's 32 cache rows, one per lane's cell, zeros where there is none; 16
+  // bytes per lane, a share of the rows to each of its warps
   auto copy = [&](const float *cache, float *to, int stride, long long cell) {
     constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;  // lanes per row, rows at once
     const int c = (lane % kLanes) * 4;
 #pragma unroll 4
-    for (int j = 0; j < kKeys; j += kAtOnce) {
-      const int row = j + lane / kLanes;
+    for (int j = 0; j < kKeys / kSets; j += kAtOnce) {
+      const int row = set * (kKeys / kSets) + j + lane / kLanes;
       const long long at = __shfl_sync(0xffffffffu, cell, row);
       cp_async16_or_zero(smem_addr(to + row * stride + c), cache + (at < 0 ? 0 : at) * D + c,
                          at >= 0);
@@ -183,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
   };
   while (walk.next(p, part)) {
     __syncthreads();  // the part before has read q and the warps' sums
-    if (threadIdx.x < RP) {
+    if (threadIdx.x < kAll) {
       const int r = threadIdx.x, h = r / p.tb, i = part.i0 + r - h * p.tb;
       sm.row[r] = h < part.heads && i < part.i1
                       ? (static_cast<long long>(part.seq.q0 + i) * p.H + part.h0 + h) * D
@@ -193,12 +209,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
                         : paged_kv_end(part.seq, i + 1, p.causal);
     }
     __syncthreads();
-    for (int e = threadIdx.x * 4; e < RP * D; e += kThreads * 4) {
+    for (int e = threadIdx.x * 4; e < kAll * D; e += kSets * kThreads * 4) {
       const long long row = sm.row[e / D];
       *reinterpret_cast<float4 *>(&sm.q[0][e]) =
           row >= 0 ? *reinterpret_cast<const float4 *>(q + row + e % D) : make_float4(0, 0, 0, 0);
     }
-    const int mine = lane % RP, lim = sm.lim[mine];  // this lane's row in the softmax
+    const int mine = lane % RP, lim = sm.lim[set * RP + mine];  // this lane's row in the softmax
     const uint32_t *tree = kTree && lim >= 0 ? p.tree + static_cast<size_t>(lim) * p.tree_words : nullptr;
     float m = -INFINITY, l = 0.f;                    // ... its maximum, and its share of the sum
     float acc[kOR][kOC];
@@ -211,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
 #pragma unroll 1
     for (int t = part.t0 - 1; t < part.t1; ++t) {
       const bool work = t >= part.t0;
-      const int first = t * kPagedTile + warp * kKeys;  // this warp's keys
+      const int first = t * kPagedTile + slice * kKeys;  // this warp's keys
       // the next tile's cache row, one per lane (-1: none)
       const int ahead = first + kPagedTile + lane;
       const long long next = t + 1 < part.t1 && ahead < part.kv_end
@@ -219,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
                                  : -1;
       if (work) {
         cp_async_wait<1>();  // this tile's keys (its values may be on their way)
-        __syncwarp();
+        slice_sync();
         float s[kTK][kTR];
 #pragma unroll
         for (int x = 0; x < kTK; ++x)
@@ -230,10 +246,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
           float4 kv[kTK];
 #pragma unroll
           for (int x = 0; x < kTK; ++x)
-            kv[x] = *reinterpret_cast<const float4 *>(&sm.k[warp][key_at + x * kKg][c]);
+            kv[x] = *reinterpret_cast<const float4 *>(&sm.k[slice][key_at + x * kKg][c]);
 #pragma unroll
           for (int r = 0; r < kTR; ++r) {
-            const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[row_at + r][c]);
+            const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[set * RP + row_at + r][c]);
 #pragma unroll
             for (int x = 0; x < kTK; ++x)
               s[x][r] = fmaf(qv.x, kv[x].x,
@@ -249,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
             s[x][r] = (there >> key) & 1 ? max_nan(s[x][r] * p.scale_log2, kLowestScore) : -INFINITY;
           st_vec<kTR>(&sm.p[warp][key][row_at], s[x]);
         }
-        __syncwarp();
+        slice_sync();
       }
       copy(kc, kw, D + 4, next);
       if (work) {
@@ -286,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
         m = mn;
         if (lane < RP) sm.alpha[warp][lane] = alpha;
         cp_async_wait<1>();  // this tile's values
-        __syncwarp();
+        slice_sync();
 #pragma unroll
         for (int r = 0; r < kOR; ++r) {
           const float shrink = sm.alpha[warp][orow_at + r];
@@ -298,14 +314,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
           float v[kOC], pr[kOR];
 #pragma unroll
           for (int c = 0; c < kOC; c += kOV)
-            ld_vec<kOV>(&sm.v[warp][j][c * kOg + col_at], v + c);
+            ld_vec<kOV>(&sm.v[slice][j][c * kOg + col_at], v + c);
           ld_vec<kOR>(&sm.p[warp][j][orow_at], pr);
 #pragma unroll
           for (int r = 0; r < kOR; ++r)
 #pragma unroll
             for (int c = 0; c < kOC; ++c) acc[r][c] = fmaf(pr[r], v[c], acc[r][c]);
         }
-        __syncwarp();
+        slice_sync();
       }
       copy(vc, vw, D, next);
       cell = next;
@@ -323,21 +339,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
     for (int r = 0; r < kOR; ++r)
 #pragma unroll
       for (int c = 0; c < kOC; c += kOV)
-        st_vec<kOV>(vw + (orow_at + r) * D + c * kOg + col_at, &acc[r][c]);
+        st_vec<kOV>(vw + (set * RP + orow_at + r) * D + c * kOg + col_at, &acc[r][c]);
     __syncthreads();
     const bool split = paged_split(part);
     float *slot = split ? paged_slot_ptr(p, D, blockIdx.x, paged_slot(part)) : nullptr;
-    if (threadIdx.x < RP) {
-      const int r = threadIdx.x;
+    if (threadIdx.x < kAll) {
+      const int r = threadIdx.x, of = r / RP * kWarps, in = r % RP;  // the row's warps, its place there
       float mt = -INFINITY, lt = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, sm.m[w][r]);
+      for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, sm.m[of + w][in]);
       const float use = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2_approx(sm.m[w][r] - use);
-        lt = fmaf(sm.l[w][r], f, lt);
-        sm.f[w][r] = f;
+        const float f = ex2_approx(sm.m[of + w][in] - use);
+        lt = fmaf(sm.l[of + w][in], f, lt);
+        sm.f[of + w][in] = f;
       }
       sm.total[r] = mt == kLowestScore ? NAN : lt;
       if (split && sm.row[r] >= 0) {
@@ -346,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
       }
     }
     __syncthreads();
-    for (int e = threadIdx.x * 4; e < RP * D; e += kThreads * 4) {
+    for (int e = threadIdx.x * 4; e < kAll * D; e += kSets * kThreads * 4) {
       const int r = e / D;
       const long long row = sm.row[r];
       if (row < 0) continue;
@@ -355,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(const __grid_co
       for (int w = 0; w < kWarps; ++w) {
         ld_cols(&sm.v[w][0][e], v);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = fmaf(v[c], sm.f[w][r], o[c]);
+        for (int c = 0; c < 4; ++c) o[c] = fmaf(v[c], sm.f[r / RP * kWarps + w][r % RP], o[c]);
       }
       if (split) {
         st_cols(slot + e, o);
@@ -668,12 +684,14 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, int smem, cu
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, int RP, bool kTree>
+template <int D, int RP, bool kTree, int kSets = 1>
 cudaError_t simt_as(const PagedProblem &p, int grid, cudaStream_t stream) {
-  const cudaError_t e =
-      set_smem_once(reinterpret_cast<const void *>(paged_simt_kernel<D, RP, kTree>), sizeof(Smem<D>));
+  constexpr int kSmem = sizeof(Smem<D, kSets>);
+  static_assert(kSmem <= 232448, "shared memory budget");
+  const auto kernel = paged_simt_kernel<D, RP, kTree, kSets>;
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), kSmem);
   if (e != cudaSuccess) return e;
-  return launch(paged_simt_kernel<D, RP, kTree>, dim3(grid), kThreads, sizeof(Smem<D>), stream, p);
+  return launch(kernel, dim3(grid), kSets * kThreads, kSmem, stream, p);
 }
 
 template <int D, int RP>
@@ -689,13 +707,16 @@ cudaError_t simt_rows(const PagedProblem &p, int grid, cudaStream_t stream) {
   if (R <= 4) return simt<D, 4>(p, grid, stream);
   // (causal rows keep the order of their sums, which differs with the lanes to a row)
   if (R <= 8 && p.tree != nullptr) return simt_as<D, 8, true>(p, grid, stream);
-  return simt<D, 16>(p, grid, stream);
+  if (R <= kRows) return simt<D, 16>(p, grid, stream);
+  if constexpr (D == 128) {
+    if (R <= 2 * kRows && p.tree != nullptr) return simt_as<D, 16, true, 2>(p, grid, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_paged_simt(const PagedProblem &p, int d, int grid, cudaStream_t stream) {
-  if (p.hpu * p.tb > kRows) return cudaErrorInvalidValue;
   return d == 64 ? simt_rows<64>(p, grid, stream) : simt_rows<128>(p, grid, stream);
 }
 
