@@ -112,7 +112,7 @@ Units units_of(int path, int group, int max_q, int rows = 0) {
 // Measured, usual units / these, by units x tiles of the longest sequence that the table
 // has room for (T4, T8: with 4 and 8 rows).  bf16, d 64, 16 tokens of 8 heads: T4 = 96 12.1
 // / 9.0 us, 384 14.9 / 12.9; T8 = 752 18.6 / 15.6; T4 = 1536 13.9 / 14.7; 8 tokens of 8
-// heads over 2 (many-query): T4 = 752 17.5 / 13.6, 768 11.6 / 10.4, 3072 17.0 / 21.4.  d
+// heads over 2 (many-query): T4 = 752 17.5 / 13.6, 768 11.6 / 10.4.  d
 // 128, 8 tokens of 32 heads over 8 (many-query): T4 = 192 12.4 / 9.5; T8 = 384 18.9 / 14.5,
 // 1536 20.2 / 23.4; 16 of 16 heads: T8 = 384 16.7 / 14.5, 1504 20.4 / 21.8.  fp32, 4 / 8 /
 // 16 rows, sequences that fill their tables: d 64, 13 tokens of 8 heads over 2: T4 = 312 13.4 /
