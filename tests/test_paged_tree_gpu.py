@@ -101,6 +101,18 @@ def test_tree_attention(c, dt, how, room):
                max_pages=None if room is None else room // page)
 
 
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (5, 1), (18, 2), (12, 1), (40, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_larger_units_of_fp32(H, Hkv, d):
+    """Trees of more rows than 16 to a key/value head, fp32: at d 128 units of 32 rows where
+    that makes for fewer, with groups of heads that fill them and that do not; keys split over
+    CTAs, too."""
+    for seqs in ([(40, 700), (33, 33), (1, 129), (0, 50), (35, 128)], [(70, 3000), (64, 70)]):
+        for how in ("tree", "any"):
+            check_tree(seqs, H, Hkv, d, "f32", 32, "bshd", how, seed=H, max_pages=200000 // 32,
+                       behind=3)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("words", [1, 2, 7])
 def test_rows_of_fewer_or_more_words_than_tokens(dt, words):
