@@ -4,8 +4,9 @@ The per-head norm and position rotation of queries and keys with its gradients,
 the paged key/value cache and the attention over it, for trees of drafted tokens
 too, and the page pool under it.  Same library, same errors
 and same conventions as ``mha.py``: torch CUDA tensors in, nothing computed here.
-Where binding.cpp is built it checks the tensors and makes the calls; what is refused,
-and how, stays the same.
+Where binding.cpp is built it checks the tensors and makes the calls, those of a
+generation step whole where the caller brings the results along; what is refused, and
+how, stays the same.
 """
 from __future__ import annotations
 
@@ -129,6 +130,9 @@ def _use_binding() -> None:
     except ImportError:  # built against another PyTorch
         return
     native.refuse_with(_at_plain)
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        native.stream_with(raw)
     for name in EXPORTED:
         native.bind(name, ctypes.cast(getattr(_LIB, name), ctypes.c_void_p).value)
     _native, _at = native, native.at
@@ -217,6 +221,22 @@ def _call(name, dev, stream, args):
             st = entry(*args, handle)
     if st != MHA_OK:
         raise MhaError(st, name)
+
+
+def _whole():
+    """binding.cpp's module where it may make whole calls, else None: it knows no other
+    device than the current one, and no other library than its own."""
+    return _native if _native is not None and lib is _LIB and _only_device() else None
+
+
+def _made(status, name) -> bool:
+    """Whether a whole call has been made (None: its arguments are not all as they should
+    be, and Python says how, or brings along what is missing)."""
+    if status is None:
+        return False
+    if status != MHA_OK:
+        raise MhaError(status, name)
+    return True
 
 
 def _only_device() -> bool:
@@ -389,6 +409,12 @@ def mha_paged_append_at(q, k, v, k_cache, v_cache, positions, q_out=None, *, q_s
 
 def _append(name, positions, q, k, v, k_cache, v_cache, q_out, q_starts, kv_lengths, block_table,
             q_weight, k_weight, inv_freq, layout, interleaved, eps, stream):
+    native = _whole()
+    if native is not None and _made(native.append(
+            len(positions) == 1, q, k, v, k_cache, v_cache, q_out, positions[0] if positions else None,
+            q_starts, kv_lengths, block_table, q_weight, k_weight, inv_freq, layout, interleaved, eps,
+            stream), name):
+        return q_out
     lay = _layout_of(layout)
     if k.dim() != 3:
         raise ValueError("q, k and v must have 3 dimensions")
@@ -455,6 +481,11 @@ def mha_paged_tree_fwd(q, k_cache, v_cache, tree_mask, out=None, *, q_starts, kv
 
 def _attend(name, tree, q, k_cache, v_cache, out, q_starts, kv_lengths, block_table, max_q, layout,
             mask, scale, workspace, stream):
+    native = _whole()
+    if native is not None and (not tree or tree[0] is not None) and _made(native.attend(
+            q, k_cache, v_cache, out, tree[0] if tree else None, q_starts, kv_lengths, block_table,
+            max_q, layout, mask[0] if mask else 0, scale, workspace, stream), name):
+        return out
     lay = _layout_of(layout)
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must have 3 dimensions and the caches 4")
@@ -509,6 +540,11 @@ def mha_paged_reserve(block_table, kv_lengths, new_lengths, refs, *, page_size: 
     length where the free pages ran out), the new references (``refs_out`` may be refs),
     the page copies that the rows need, [B, 2], for ``mha_paged_copy``, and int32 [2]: pages
     given out and pages still free."""
+    native = _whole()
+    if native is not None and _made(native.reserve(
+            block_table, kv_lengths, new_lengths, parents, refs, table_out, lengths_out, refs_out,
+            moves, counts, page_size, workspace, stream), "mha_paged_reserve"):
+        return table_out, lengths_out, refs_out, moves, counts
     torch = _torch()
     i32, dev = torch.int32, _device_of(block_table)
     if block_table.dim() != 2 or new_lengths.dim() != 1 or refs.dim() != 1:
@@ -554,6 +590,9 @@ def mha_paged_copy(k_cache, v_cache, moves, *, stream=None):
     """Copies page moves[i][0] to page moves[i][1] (int32 [n, 2]; pairs with a number that
     is no page's are skipped) in both caches, [pages, ...] or [layers, pages, ...] in either
     layout.  What mha_paged_reserve leaves to be copied."""
+    native = _whole()
+    if native is not None and _made(native.copy(k_cache, v_cache, moves, stream), "mha_paged_copy"):
+        return
     layers, (pages, a, b, d), dt, dev = _stack(k_cache, v_cache)
     if moves.dim() != 2:
         raise ValueError("moves must have 2 dimensions")
@@ -578,6 +617,11 @@ def mha_paged_compact(k_cache, v_cache, keep, keep_counts, lengths_out=None, *, 
     int32 [B] (None: 0); kv_lengths [B]: the lengths before; ``block_table`` [B, max_pages]:
     the pages written, ``src_table`` those read (None: the same, in place; else no cell is
     both written and read)."""
+    native = _whole()
+    if native is not None and _made(native.compact(
+            k_cache, v_cache, keep, keep_counts, lengths_out, starts, kv_lengths, block_table,
+            src_table, layout, stream), "mha_paged_compact"):
+        return lengths_out
     torch = _torch()
     i32, lay = torch.int32, _layout_of(layout)
     layers, (pages, a, b, d), dt, dev = _stack(k_cache, v_cache)
