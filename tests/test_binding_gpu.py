@@ -106,6 +106,24 @@ def test_the_same_results(paged, monkeypatch, name, layout, q, extra):
         assert torch.equal(x, y), k
 
 
+@pytest.mark.parametrize("name", ["append", "append_at", "fwd", "tree_fwd"])
+@pytest.mark.parametrize("native", [True, False])
+def test_results_made_by_the_call(paged, monkeypatch, name, native):
+    import torch
+    f, args = entries("bshd")[name]
+    want = f(**args).clone()
+    if not native:
+        monkeypatch.setattr(paged, "_whole", lambda: None)
+    for key in ("q_out", "out", "workspace"):
+        args.pop(key, None)
+    got = f(**args)
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    with pytest.raises((ValueError, AttributeError)):
+        f(**dict(args, kv_lengths=args["kv_lengths"].float()))
+    with pytest.raises(ValueError):
+        f(**dict(args, layout="sbhd"))
+
+
 def changes(x):
     """Other values of an argument, none of which a call would take for what it is not."""
     import torch

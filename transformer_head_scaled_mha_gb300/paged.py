@@ -426,6 +426,9 @@ def _append(name, positions, q, k, v, k_cache, v_cache, q_out, q_starts, kv_leng
     elif q_out is None:
         with _on(stream, k.device):
             q_out = _torch().zeros_like(q)
+        if native is not None:  # (now that it is there)
+            return _append(name, positions, q, k, v, k_cache, v_cache, q_out, q_starts, kv_lengths,
+                           block_table, q_weight, k_weight, inv_freq, layout, interleaved, eps, stream)
     kc, vc, pages, page = _cache(k_cache, v_cache, d, Hkv, lay, dt, dev)
     arrays, B, max_pages = _batch(q_starts, kv_lengths, block_table, dev)
     freq, rotary = _rotary(inv_freq, dev)
@@ -501,6 +504,9 @@ def _attend(name, tree, q, k_cache, v_cache, out, q_starts, kv_lengths, block_ta
             if workspace is None:
                 n = mha_paged_workspace_size(B, T, H, Hkv, d, max_q, dtype)
                 workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        if native is not None:  # (now that they are there)
+            return _attend(name, tree, q, k_cache, v_cache, out, q_starts, kv_lengths, block_table,
+                           max_q, layout, mask, scale, workspace, stream)
     words = ()
     if tree:
         if tree[0].dim() != 2 or not 1 <= tree[0].shape[1] <= _INT_MAX:
