@@ -1,0 +1,46 @@
+"""What the entry points of include/mha_paged.h hand to their kernels, recorded on the host
+(paged_launches_host.cu)."""
+import ctypes
+import os
+import shutil
+import subprocess
+import types
+
+import pytest
+
+from test_paged_cpu import CSRC, P, ROOT, append, mha  # noqa: F401 (fixture)
+from test_paged_tree_cpu import append_at
+
+
+@pytest.fixture(scope="module")
+def launches(mha, tmp_path_factory):  # noqa: F811
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    out = str(tmp_path_factory.mktemp("launches") / "launches.so")
+    subprocess.run([nvcc, "-O1", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-Xlinker",
+                    "-Bsymbolic", "--expt-relaxed-constexpr", "-I", CSRC, "-o", out,
+                    os.path.join(ROOT, "tests", "paged_launches_host.cu")], check=True,
+                   capture_output=True)
+    lib = ctypes.CDLL(out)
+    for name in ("mha_paged_append", "mha_paged_append_at", "mha_paged_tree_fwd",
+                 "mha_paged_workspace_size"):
+        entry, known = getattr(lib, name), getattr(mha.lib, name)
+        entry.argtypes, entry.restype = known.argtypes, known.restype
+    for name in ("rope_q_weight", "rope_k_weight"):
+        getattr(lib, name).restype = ctypes.c_void_p
+    lib.attention_slots_end.restype = ctypes.c_longlong
+    return types.SimpleNamespace(lib=lib)
+
+
+@pytest.mark.parametrize("call", [append, append_at], ids=["append", "append_at"])
+def test_queries_without_heads_have_no_weight(launches, call):
+    """With H = 0 the queries' weight is not an argument that is checked, so no kernel may get
+    hold of it."""
+    assert call(launches) == 0
+    assert launches.lib.rope_q_weight() and launches.lib.rope_k_weight()
+    if call is append:
+        for weight in (None, P[6], P[6] + 2, P[3], P[4]):  # any address, misaligned, another's
+            assert append(launches, q=None, qo=None, H=0, qw=weight) == 0
+            assert launches.lib.rope_q_weight() is None and launches.lib.rope_k_weight() == P[7]
+    else:
+        assert append_at(launches, q=None, qo=None, H=0) == 0
+        assert launches.lib.rope_q_weight() is None and launches.lib.rope_k_weight() == P[7]

@@ -340,7 +340,8 @@ static int append(const void *q, const void *k, const void *v, void *q_out, void
   a.q_out = q_out;
   a.k_out = k_cache;
   a.v_out = v_cache;
-  a.q_weight = q_weight;
+  // (a weight of no queries has not been looked at, and the kernels form every weight's factors)
+  a.q_weight = nq > 0 ? q_weight : nullptr;
   a.k_weight = k_weight;
   a.inv_freq = inv_freq;
   a.positions = at ? positions : nullptr;
