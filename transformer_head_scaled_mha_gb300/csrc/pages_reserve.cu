@@ -345,15 +345,16 @@ __global__ void __launch_bounds__(kThreads) reserve_small_kernel(const ReserveAr
 }
 
 // ---- larger ones: the whole GPU, a launch to a step -----------------------------------
-// (__ldcg: numbers that other SMs have just written.)  Blocks of 512 leave room on an SM for
-// the next launch's, which then wait there.
+// (__ldcg: numbers that other SMs have just written, or the launch ahead, which may still run
+// when this one begins.)  Blocks of 512 leave room on an SM for the next launch's, which then
+// wait there.
 constexpr int kStepThreads = 512, kStepWarps = kStepThreads / 32;
 
 __device__ void begin_step(const ReserveArgs &a, int block, int blocks) {
   const int thread = block * kStepThreads + threadIdx.x, threads = blocks * kStepThreads;
   if (a.refs_out != a.refs) {
 #pragma unroll 4
-    for (int p = thread; p < a.num_pages; p += threads) a.refs_out[p] = __ldg(a.refs + p);
+    for (int p = thread; p < a.num_pages; p += threads) a.refs_out[p] = __ldcg(a.refs + p);
   }
   if (thread == 0) a.totals[kTotalDone] = 0;
   for (int i = thread; i < a.B; i += threads) {
