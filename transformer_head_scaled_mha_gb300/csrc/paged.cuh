@@ -43,6 +43,12 @@ struct RopeArgs {
   float *dq_weight, *dk_weight;
 };
 
+// The position whose angles appended row t takes, of sequence `seq` (-1: none) and at `pos` of
+// it: the given one (drafted trees: it is not the cell's), unread where the row has no sequence.
+MHA_HD int append_angle(const RopeArgs &a, int t, int seq, int pos) {
+  return a.positions != nullptr && seq >= 0 ? a.positions[t] : pos;
+}
+
 // CTAs of the backward kernel at most (rows of RopeArgs::partial)
 constexpr int kRopeBwdMaxCtas = 1216;
 

@@ -429,9 +429,8 @@ struct Cells {
   __device__ __forceinline__ long long cell(const RopeArgs &a) const {
     return seq >= 0 ? paged_cell(a.batch, seq, pos, 0, a.Hkv) : -1;
   }
-  // (drafted trees: the angle's position is not the cell's)
   __device__ __forceinline__ int angle(const RopeArgs &a, int t) const {
-    return a.positions != nullptr ? a.positions[t] : pos;
+    return append_angle(a, t, seq, pos);
   }
 };
 
