@@ -19,7 +19,8 @@
  * mha_paged_fwd, mha_linear_fwd; one that verifies drafted trees takes
  * mha_paged_append_at and mha_paged_tree_fwd instead, and mha_paged_compact when
  * it knows which drafted tokens it accepts.  mha_paged_reserve and mha_paged_copy
- * come before either.  The pages that mha.h cites describe a decoder
+ * come before either, and once more behind mha_paged_compact, to give back the pages
+ * that only rejected tokens took.  The pages that mha.h cites describe a decoder
  * that attends to every earlier position (alexdo.xyz, "How predictions are
  * generated"); paging, rotation and head norms are how present decoders carry
  * that out, and have no counterpart on the pages.
@@ -275,6 +276,16 @@ size_t mha_paged_reserve_workspace_size(int B, int num_pages);
  * back what rejected tokens took (a smaller one), ends (0), begins (parents[i] = -1)
  * or forks (a parent that several rows name, as beams do).
  *
+ * kv_lengths say how far the old tables reach: pages that hold positions below them are
+ * given up, what a table names behind them is not.  They are the lengths_out of the call
+ * that made the tables, also when the sequences have become shorter since: with the lengths
+ * that mha_paged_compact leaves, the pages behind those would be held for ever.  So a step
+ * whose drafted tokens are decided ends with a call that has the reach as kv_lengths, the
+ * lengths that are left as new_lengths and no parents.  Where no row forks, the call that
+ * begins the next step can do it as well: the reach as kv_lengths, the next lengths as
+ * new_lengths (the rows keep pages of rejected tokens as far as they need them, and write over
+ * them; rows that fork would share those pages).
+ *
  * refs counts each page's references: one for every row that holds a position in
  * it, and whatever the caller adds to hold on to a page (a cached prefix).  With
  * whole pages shared, and a part-filled last page a row's own, because the row will
@@ -296,8 +307,9 @@ size_t mha_paged_reserve_workspace_size(int B, int num_pages);
  * were (but for refs where refs_out is refs), so the caller may choose other lengths
  * and call again.
  *
- * block_table, kv_lengths  int32 [B_old, max_pages], [B_old]: the old tables; entries
- *               outside [0, num_pages) name no page, and are -1 where they are kept
+ * block_table, kv_lengths  int32 [B_old, max_pages], [B_old]: the old tables and how far
+ *               they reach; entries outside [0, num_pages) name no page, and are -1 where
+ *               they are kept
  * new_lengths, parents  int32 [B], [B]; a parent outside [0, B_old) is none; NULL:
  *               row i's is i.  Lengths below 0 count as 0, those past
  *               max_pages * page_size as that
@@ -337,7 +349,8 @@ int mha_paged_copy(void *k_cache, void *v_cache, const int32_t *moves, int n, in
  *     lengths_out[b] = starts[b] + the number of kept tokens
  *
  * An accepted path of a drafted tree (starts: the cached length before the tree,
- * keep: its tokens' numbers), or what is left of a long sequence.
+ * keep: its tokens' numbers), or what is left of a long sequence.  The sequence holds its
+ * pages as far as kv_lengths until mha_paged_reserve, told those, gives them back.
  *
  * keep        int32 [B, max_keep], keep_counts [B] (clamped to [0, max_keep]): a list
  *             ascends, from 0 on, and stays below kv_lengths[b] - starts[b].  It ends

@@ -540,8 +540,10 @@ def mha_paged_reserve(block_table, kv_lengths, new_lengths, refs, *, page_size: 
     whole pages with its parent and taking free ones as it needs them.  Sequences grow,
     shrink, fork, end (length 0) and begin.
 
-    block_table int32 [B_old, max_pages], kv_lengths [B_old], new_lengths [B], refs
-    [num_pages] (references to each page; 0: free).  Returns (table_out, lengths_out,
+    block_table int32 [B_old, max_pages], kv_lengths [B_old]: how far those tables reach (the
+    ``lengths_out`` they came with: after mha_paged_compact more than the sequences' lengths,
+    which go into ``new_lengths`` to give back the pages of rejected tokens before rows fork),
+    new_lengths [B], refs [num_pages] (references to each page; 0: free).  Returns (table_out, lengths_out,
     refs_out, moves, counts): the new tables, how far each row's pages go (less than its
     length where the free pages ran out), the new references (``refs_out`` may be refs),
     the page copies that the rows need, [B, 2], for ``mha_paged_copy``, and int32 [2]: pages
@@ -617,7 +619,8 @@ def mha_paged_compact(k_cache, v_cache, keep, keep_counts, lengths_out=None, *, 
                       kv_lengths, block_table, src_table=None, layout: str = "bhsd", stream=None):
     """Moves the tokens that stay: position starts[b] + keep[b][i] to starts[b] + i for i <
     keep_counts[b], in both caches, [pages, ...] or [layers, pages, ...].  Returns the new
-    lengths, starts[b] + keep_counts[b].
+    lengths, starts[b] + keep_counts[b]; the pages behind them are held until
+    mha_paged_reserve(block_table, kv_lengths, those lengths, ...) gives them back.
 
     keep int32 [B, max_keep]: ascending lists, which end before an entry that is not; starts
     int32 [B] (None: 0); kv_lengths [B]: the lengths before; ``block_table`` [B, max_pages]:
