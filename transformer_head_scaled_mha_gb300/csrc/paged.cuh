@@ -59,7 +59,7 @@ cudaError_t launch_rope_bwd(const RopeArgs &a, int d, int dtype, int num_sms, cu
 // ---- attention over the cache ----------------------------------------------
 constexpr int kPagedTile = 128;     // keys per tile: the unit that work is split by
 constexpr int kPagedMaxCtas = 608;      // CTAs that may hold partial sums, at most 16 rows per unit
-constexpr int kPagedManyMaxCtas = 192;  // ... 256 rows per unit
+constexpr int kPagedManyMaxCtas = 192;  // ... 256 rows per unit, or 32 in fp32: one CTA to an SM
 
 // What a visible score counts as at least.  A score that is not seen is -infinity, and a
 // visible one of -infinity this, so that a row with nothing to attend to (maximum
@@ -486,7 +486,7 @@ cudaError_t launch_paged_few(const CUtensorMap &q, const CUtensorMap &k, const C
 // as above
 cudaError_t launch_paged_many(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                               const PagedProblem &p, int d, int grid, cudaStream_t stream);
-// fp32, at most 16 rows per unit
+// fp32, at most 16 rows per unit, of trees at d = 128 32
 cudaError_t launch_paged_simt(const PagedProblem &p, int d, int grid, cudaStream_t stream);
 // joins the parts of split units; `many`: of launch_paged_many
 cudaError_t launch_paged_merge(const PagedProblem &p, int d, int dtype, bool many, int grid,

@@ -98,7 +98,7 @@ Units units_of(int path, int group, int max_q, int rows = 0) {
   u.hblocks = (group + u.hpu - 1) / u.hpu;
   u.tb = path == kMany ? 2 * (rows / u.hpu) : std::min(rows / u.hpu, max_q);
   u.rows = u.hpu * u.tb;
-  u.ctas = path == kMany ? kPagedManyMaxCtas : (rows > 16 ? kPagedMaxCtas / 2 : kPagedMaxCtas);
+  u.ctas = path == kMany || rows > 16 ? kPagedManyMaxCtas : kPagedMaxCtas;
   u.split = path == kMany ? kSplitMany : (path == kFew ? kSplitFew : kSplitSimt);
   return u;
 }
@@ -128,7 +128,11 @@ Units units_of(int path, int group, int max_q, int rows = 0) {
 // mean tree.  16 / 32 rows, by T32: 8 of 32 tokens of 8 heads, 1000 keys, 512: 59.0 / 50.3 us;
 // 64 of 500 keys, 2560: 196 / 151; 13 tokens of 8 heads over 2, 256: 33.5 / 28.7, ragged 384
 // 27.3 / 28.9; 32 tokens, ragged, 192: 26.7 / 28.1; 8-20 tokens of 8 heads (one unit either
-// way), 4096: 123 / 157.
+// way), 4096: 123 / 157.  One CTA of them fits an SM, so there are as few slots for their sums
+// as the many-query kernel has; with twice as many, the workspace, which is that of the usual
+// units, had no room for the 27 or 30 rows of groups of 6, 9 and 10 heads: 16 of 64 tokens of 12
+// heads over 2, 1000 keys: 328 / 213 us; of 18: 638 / 343; 2 of 150 tokens of 10 heads over 1,
+// 4000 keys: 351 / 194.
 int tree_rows(int *path, int B, int T, int H_kv, int group, int max_q, int d, int dtype,
               long long keys, int sms) {
   const long long tiles = (keys + kPagedTile - 1) / kPagedTile;
