@@ -239,9 +239,11 @@ int mha_paged_fwd(const void *q, const void *k_cache, const void *v_cache, void 
  *            has nothing cached before the new tokens) is written as +0.0.
  * tree_words >= 1
  * The workspace is that of mha_paged_fwd.  The kernel is the one that mha_paged_path
- * tells, but where there is little work few rows are taken at a time, on the few-query
- * kernel (BF16); everything else as there (a new token's value must be finite where any other
- * token of its sequence is in the call).
+ * tells, but where there is little work for what the block table has room for, 4 or 8 rows are
+ * taken at a time, with BF16 on the few-query kernel (no call tells; a wider table may take
+ * longer over the same lengths); everything else as there (a new token's value must be finite
+ * where any other token of its sequence is in the call).  With BF16 the softmax weights are
+ * kept to 2^-17 where 8 rows or fewer are taken at a time, else to 2^-8, as there.
  */
 int mha_paged_tree_fwd(const void *q, const void *k_cache, const void *v_cache, void *out,
                        const int32_t *tree_mask, const int32_t *q_starts,

@@ -1,6 +1,7 @@
-"""The generation step that README.md shows, taken from there and run over and over, with the
-page pool watched: every page's references are those of the rows that reach it, no row writes
-to a page that another one holds, and the cache holds what the accepted tokens left."""
+"""The generation step that the project's overview shows, taken from there and run over and
+over, with the page pool watched: every page's references are those of the rows that reach it,
+no row writes to a page that another one holds, and the cache holds what the accepted tokens
+left."""
 import os
 import re
 
@@ -9,8 +10,8 @@ import numpy as np
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
-def readme_step() -> str:
-    """The block of README.md with a step of drafted trees."""
+def shown_step() -> str:
+    """The overview's block with a step of drafted trees."""
     blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(ROOT, "README.md")).read(), re.S)
     (block,) = [b for b in blocks if "mha_paged_reserve" in b]
     return block
@@ -98,7 +99,7 @@ class Pool:
 
 def run(pool, steps, seed, forks):
     rng = np.random.default_rng(seed)
-    code = readme_step() if forks is not None else ONE_CALL
+    code = shown_step() if forks is not None else ONE_CALL
     pool.step(code, rng, 70, prompt=True)
     for i in range(steps):
         parents = None

@@ -1,4 +1,5 @@
-"""The generation step that README.md shows, on the plain forms of the page pool's operators."""
+"""The generation step that the project's overview shows, on the plain forms of the page
+pool's operators."""
 import types
 
 import numpy as np

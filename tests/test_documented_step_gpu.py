@@ -1,4 +1,4 @@
-"""The generation step that README.md shows, as it stands there, on the GPU."""
+"""The generation step that the project's overview shows, as it stands there, on the GPU."""
 import numpy as np
 import pytest
 

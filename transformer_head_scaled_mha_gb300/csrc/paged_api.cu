@@ -61,12 +61,11 @@ int check_batch(const int32_t *q_starts, const int32_t *kv_lengths, const int32_
 // ---- attention over the cache -------------------------------------------------
 // Expected query rows per key/value head up to which the few-query kernel is taken.
 // Measured at 16 rows, few / many: one token of 16 heads over 1, 8 sequences of 1000-8000
-// keys, d 128: 17 / 32 us; of 64 over 4, 16 such sequences: 38 / 49; 4 tokens of 32 heads
-// over 8, 32 sequences of 500-2000, d 128: 44 / 50.  Units short beside their number go the
-// other way: the same 32 sequences at d 64: 41 / 36; 256 of 200-600, d 128: 144 / 129 (12
-// rows: 141 / 129).  8 rows, 16 x 2 tokens of 32 heads over 8, 4000 keys, d 128: 52 / 66.
-// A few-query kernel of 32 rows, 64 sequences of 1000-4000: 101 / 84 us, 128 of 300-900:
-// 160 / 87.
+// keys, d 128: 15.8 / 21.7 us; of 64 over 4, 16 such sequences: 36.7 / 46.6; 4 tokens of 32
+// heads over 8, 8 of 1000-4000: 27.0 / 30.6, 32 sequences of 500-2000: 41.4 / 47.1, d 64 36.3 /
+// 35.0; 256 of 200-600, d 128: 125.8 / 126.4 (12 rows: 129.3 / 126.2).  8 rows, 16 x 2 tokens of
+// 32 heads over 8, 4000 keys, d 128: 51.5 / 62.7.  A few-query kernel of 32 rows (with the
+// merges that both had before), 64 sequences of 1000-4000: 101 / 84 us, 128 of 300-900: 160 / 87.
 constexpr int kFewRows = 16;
 
 enum PagedPath { kNone = 0, kSimt = 1, kFew = 2, kMany = 3 };
@@ -107,7 +106,11 @@ Units units_of(int path, int group, int max_q, int rows = 0) {
 // short most SMs would have nothing to do: units of fewer rows read the keys again, from
 // L2, but a row's softmax no longer waits for 15 others.  `path` and the answer: the rows of
 // a unit, 0 where the usual units are as good; `path` becomes the few-query kernel where
-// that is faster than the many-query one.
+// that is faster than the many-query one.  How much work there is is known on the device alone:
+// here it is what the table has room for, so short sequences in wide tables count as long ones
+// (16 tokens over 300 keys, 8 heads, d 64, with room for 320: 8.9 us, 4096: 11.0, 8192: 13.0,
+// 16384 and more: 14.2; the fp32 trees of 5-13 tokens over 90-700 keys, room for 736: 14.4, 2048
+// and more: 16.4).
 //
 // Measured, usual units / these, by units x tiles of the longest sequence that the table
 // has room for (T4, T8: with 4 and 8 rows).  bf16, d 64, 16 tokens of 8 heads: T4 = 96 12.1

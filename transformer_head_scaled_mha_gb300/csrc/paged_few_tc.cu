@@ -14,10 +14,11 @@
 // not fill the GPU for long pay 6 us to the first tile and 4 for the merge: 8 sequences of
 // 1000-4000 keys, 32 heads over 8, d 128: 24.6 us, 0.49 of a copy's rate.  From 9 rows on
 // the lone softmax warpgroup sets the pace, 16 exponentials and stores per key and thread:
-// 32 sequences of 500-2000 keys, 4 tokens of 32 heads over 8, d 64: 41 us, 0.30.  Trees of
+// 32 sequences of 500-2000 keys, 4 tokens of 32 heads over 8, d 64: 36 us, 0.33.  Trees of
 // drafted tokens where there is little work come in units of 4 or 8 rows: 16 tokens over 300
-// keys, 8 heads, d 64: 8.9 us (12.1 with 16 rows); 256 trees of 8 tokens, 128-1024 keys, 8
-// heads, d 64: 78 us, 0.58 (89 with a quotient to every row in every thread).
+// keys, 8 heads, d 64: 8.9 us (12.1 with 16 rows; 14 where the table has room for 16384
+// positions); 256 trees of 8 tokens, 128-1024 keys, 8 heads, d 64: 78 us, 0.58 (89 with a
+// quotient to every row in every thread).
 //
 // Scores are computed transposed, keys on the 128 TMEM lanes, so that a thread
 // owns a key and the few rows cost a few exponentials per thread:

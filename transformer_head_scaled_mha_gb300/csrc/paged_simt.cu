@@ -2,7 +2,8 @@
 // the joining of split units that every paged attention kernel uses.
 //
 // A CTA of four warps walks its parts (paged.cuh): R <= 16 query rows of one
-// key/value head against tiles of 128 keys.  Warp w takes keys 32 w .. 32 w + 31
+// key/value head against tiles of 128 keys (large trees at d 128: 32 rows, the second
+// 16 by four warps of their own).  Warp w takes keys 32 w .. 32 w + 31
 // of each tile: scores with up to 4 keys and 4 rows to a lane (keys staged in shared memory,
 // rows padded by 16 bytes so that lanes read without conflicts), an online
 // softmax with a row per lane, or 32 / R lanes to a row, through a small square of
@@ -538,6 +539,8 @@ __global__ void __launch_bounds__(kMergeThreads)
 // turns, most of them for nothing, with two parts in flight to a warp: one tree of 16 tokens
 // over 8192 keys, 32 heads over 8, d 128: 32.7 us, 21.3 so; of 64 tokens 37.7, 26.0; 16 of 9-25
 // over 1000-4096 50.0, 48.6.  The few-query kernel's units are more and smaller: 2 us slower so.)
+// Where many units of all rows are cut it is a little slower than those CTAs were (8 chunks of up
+// to 512 tokens, 1000-4096 keys: 75.4, 76.4); one CTA to an SM: 80.4, three 78.3, four 77.7.
 constexpr int kMergeRowsCtas = 2;  // to an SM
 struct JoinedList {
   static constexpr int kWords = kMergeWarps;  // CTAs, a bit each

@@ -18,11 +18,11 @@
 //
 // Bound: the way from number to number (parents, lengths, tables, counts, ranks, pages), not
 // the few bytes.  Measured, in captured graphs: 256 sequences of 128-1024 positions, pages of
-// 16, one step: 8.9 us (15.2 as one cluster with the counts in L2, 13.2 as one block that
-// writes all tables); 8 of 300: 5.5; 64 beams of 2000-8000, 459 pages to a row: 14.1; 1024
-// beams of 2048-8192, 513 pages to a row, 350000 pages: 19 (54.7 as one cluster of 8 CTAs,
-// 34.6 of 16; 20.2 in blocks of 1024, which leave the next launch no room; a fifth launch in place
-// of the last block: 1.3 less, but 2 more of the host's time).
+// 16, one step: 8.9 us, with tables for 8192 and more 11.1 to 11.6 (15.2 as one cluster with the
+// counts in L2, 13.2 as one block that writes all tables); 8 of 300: 5.5; 64 beams of 2000-8000,
+// 459 pages to a row: 14.1; 1024 beams of 2048-8192, 513 pages to a row, 350000 pages: 19 (54.7
+// as one cluster of 8 CTAs, 34.6 of 16; 20.2 in blocks of 1024, which leave the next launch no
+// room; a fifth launch in place of the last block: 1.3 less, but 2 more of the host's time).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -224,6 +224,14 @@ __device__ __forceinline__ void write_row(const ReserveArgs &a, int i, const Res
 // steps.  Every CTA of the cluster does all of it alike, in its own shared memory, and
 // writes a share of the results: copying the tables is most of the work, and that much
 // faster than telling the others.
+//
+// Rows and pages by what fits shared memory; entries, with the rows' empty places, by the time
+// that they take.  Measured, one cluster / the whole GPU: one step of 256 sequences of 128-1024,
+// pages of 16, room for 2048: 9.1 / 11.1 us, 4096 (65536 entries): 9.7 / 11.0, 8192: 12.0 / 11.3,
+// 32768: 23.9 / 11.6; of 64: 65536 entries 8.8 / 10.8, 131072 10.6 / 10.6, 262144 14.5 / 10.6; of
+// 1024 of 100-400: 65536 13.9 / 14.1, 131072 15.6 / 13.8.  Beams, which count all their pages,
+// would go to the whole GPU earlier: 64 of 2000-4000, 32768 entries: 13.6 / 11.6, 65536 18.0 /
+// 11.7; 32 of 1000-8000, 16384: 9.9 / 11.1, 32768 12.2 / 10.7.
 constexpr int kSmallRows = 1024, kSmallPages = 28672;
 constexpr int kSmallEntries = 65536;  // of the tables
 constexpr int kSmallCtas = 8;

@@ -27,9 +27,10 @@
 // sums six shuffles behind one another, and 5 us before the first row and for the weights'
 // last sums), forward 26 (0.38: two rounds of loads to a token's tensor).  256 trees of 64
 // tokens of 8 + 8 + 8 heads appended: 22.7 us (0.66; 26.7 with a tensor's rows loaded after
-// the one before was done; 57% of the issue slots, 170 instructions to a warp's round of
-// four rows).  One loop over all tensors' rounds, six loads ahead, for any number of heads:
-// 28.5, and prompts 53.
+// the one before was done), latency as well: a token's loads, lookups and stores follow one
+// another, 20 warps to an SM, with DRAM 33% busy, the issue slots 57% while an SM works and 43%
+// of the whole launch.  One loop over all tensors' rounds, six loads ahead, for any number of
+// heads: 28.5, and prompts 53.
 //
 // Angles: with the frequency in turns as a 64-bit binary fraction F =
 // frac(f / 2 pi) 2^64, the position times F modulo 2^64 is the angle's fraction of
